@@ -146,6 +146,68 @@ int moe_route_topk_bwd(const float* gates, const float* dgates, const int32_t* t
  * null pointer. */
 int moe_route_stats(const int32_t* counts, int32_t E, int32_t* stats, void* stream);
 
+/* Balance loss and z loss of the router, with the per-expert counts
+ * ("Scaling to the trillion-parameter range": experts' load is kept even during
+ * training; the pages give no formula, these are the usual ones).  With p the
+ * softmax of a token's E logits and lse their log-sum-exp, over the tokens that
+ * count in sequence s (n_s of them; S' sequences have any; N = sum n_s):
+ *   counts[s,e] = chosen slots of expert e, probs[s,e] = mean of p[e] (0 if n_s = 0)
+ *   loss[0] = alpha / S' sum_s E sum_e counts[s,e] / (k n_s) probs[s,e]
+ *   loss[1] = zeta / N sum_t lse_t^2                         (both 0 if N = 0)
+ *   lse [T]: 0 for a token that does not count
+ *   norm [S + 2] fp32: S', N, then n_s, kept for the backward
+ * seq_offsets [S+1] int32 (device, non-decreasing, within [0, T]): sequence s
+ * holds tokens [seq_offsets[s], seq_offsets[s+1]); empty sequences are allowed,
+ * and tokens before the first or behind the last one do not count.  NULL (then
+ * S = 1): one sequence of all T tokens.  A token counts when it is in a sequence,
+ * token_mask [T] (uint8, NULL: all) is nonzero and some logit is above -inf (a
+ * token of -inf only chooses nothing).  A counted token with a NaN or +inf logit
+ * makes the losses NaN; what masked tokens hold does not matter.
+ * topk_idx [T, k] from moe_route_topk; logits [T, E] fp32; counts [S, E] int32;
+ * probs [S, E], lse, loss [2] fp32.  Sums are fp32 in a fixed order.
+ * The backward writes
+ *   dlogits[t,e] = p_e (a_e - sum_j a_j p_j) + dloss[1] 2 zeta / N lse_t p_e,
+ *   a_e = dloss[0] alpha E counts[s,e] / (k n_s^2 S')       (no gradient through counts)
+ * and zero for tokens that do not count; with gates and dgates (both or
+ * neither; then topk_idx too) the gates' gradient of moe_route_topk_bwd is
+ * added for every token in the same pass, so that call is not needed.
+ * dloss [2] fp32 on the device: upstream gradients of the two losses (NULL: 1).
+ * Errors as for moe_route_topk; MOE_EINVAL also for a non-finite alpha or zeta,
+ * S < 1, and S > 1 without seq_offsets.  T = 0 is allowed (losses 0). */
+size_t moe_balance_loss_workspace(int64_t T, int32_t E, int64_t S);
+int moe_balance_loss(const float* logits, const int32_t* topk_idx, int64_t T, int32_t E, int32_t k,
+                     const int32_t* seq_offsets, int64_t S, const uint8_t* token_mask, float alpha, float zeta,
+                     float* loss, int32_t* counts, float* probs, float* lse, float* norm, void* ws,
+                     size_t ws_bytes, void* stream);
+int moe_balance_loss_bwd(const float* logits, const float* lse, const int32_t* counts, const float* norm, int64_t T,
+                         int32_t E, int32_t k, const int32_t* seq_offsets, int64_t S, const uint8_t* token_mask,
+                         float alpha, float zeta, const float* dloss, const int32_t* topk_idx, const float* gates,
+                         const float* dgates, float* dlogits, void* stream);
+
+/* ---------------------------------------------------------------------------
+ * Layer norm of the token rows, the norm before the router and the experts (no
+ * page defines it; the usual formula).  x [T, d] in `dtype` (MOE_F32 or
+ * MOE_BF16), any d from 1 to 2^20.
+ *   forward:  s = x, or x + residual rounded to `dtype` (stored in `sum` unless
+ *             NULL; sum without residual is MOE_EINVAL);
+ *             mean, rstd = 1 / sqrt(var + eps) of each row of s, fp32 [T] (each
+ *             may be NULL); y = (s - mean) rstd weight + bias
+ *   backward: of y for upstream dy, with x the rows that were normalised (s):
+ *             dx = rstd (v - avg(v) - h avg(v h)) (+ dres), v = dy weight,
+ *             h = (x - mean) rstd; dw = sum_t dy h, db = sum_t dy
+ * weight, bias, residual, dres, dw, db may be NULL (weight 1, bias 0, none);
+ * weight, bias, dw, db [d] in `dtype`.  dres [T, d] is a gradient that reaches
+ * s by another way (the residual stream's).  Statistics and sums are fp32.
+ * T = 0 is allowed: dw and db become zero.  The workspace is needed for dw and
+ * db only.  MOE_EINVAL for d < 1 and for an eps that is negative or not finite,
+ * MOE_EUNSUPPORTED for d > 2^20. */
+int moe_layernorm(const void* x, const void* residual, const void* weight, const void* bias, int dtype, int64_t T,
+                  int32_t d, float eps, void* y, void* sum, float* mean, float* rstd, void* stream);
+size_t moe_layernorm_bwd_workspace(int64_t T, int32_t d);
+int moe_layernorm_bwd(const void* dy, const void* x, const void* weight, const float* mean, const float* rstd,
+                      const void* dres, int dtype, int64_t T, int32_t d, void* dx, void* dw, void* db, void* ws,
+                      size_t ws_bytes, void* stream);
+
 /* ---------------------------------------------------------------------------
  * Row-wise dispatch and weighted combine ("Scaling and optimizing MoE
  * training": routed data goes directly into the experts' input buffers).
@@ -322,6 +384,35 @@ int moe_mx_weight_cache_build(const void* w_gate, const void* w_up, const void* 
 int mx_quantize(const void* src, int src_dtype, int64_t batch, int64_t rows, int64_t cols,
                 int32_t axis, const int32_t* seg_offsets, int32_t nseg, uint8_t* q,
                 uint8_t* scales, void* stream);
+
+/* ---------------------------------------------------------------------------
+ * Orthogonalised updates of the expert weights (no page gives an optimiser
+ * formula; Newton-Schulz orthogonalisation as in the published Muon optimiser).
+ * For each of E matrices U [rows, cols] on its own:
+ *   X = U / (|U|_F + eps);  `steps` times:  X <- a X + (b A + c A^2) X, A = X X^T
+ * moe_orthogonalize: U = g; out = X.
+ * moe_muon_step:     mom_out = momentum mom + g (fp32);
+ *                    U = g + momentum mom_out (nesterov != 0) or mom_out;
+ *                    w_out = (1 - lr weight_decay) w - lr scale X.
+ * g, out, w, w_out [E, rows, cols] in `dtype` (MOE_F32 or MOE_BF16); mom, mom_out
+ * [E, rows, cols] fp32.  mom_out may be mom and w_out may be w (in place); no other
+ * overlap.  coef: HOST array [steps][3] of a, b, c, read before the call returns;
+ * NULL: 3.4445, -4.7750, 2.0315 in every step.
+ * Accuracy: fp32 sums; products on matrix cores, with operands of 22 mantissa bits
+ * for MOE_F32, and for MOE_BF16 of 11 bits with the iterate itself kept to 22.  A
+ * zero matrix gives zeros; a non-finite element makes its own matrix NaN only.
+ * Limits: rows, cols <= 32768 with rows x cols (rounded up to 64) < 2^30,
+ * E <= 65535, 1 <= steps <= 16, and coefficients whose polynomial keeps singular
+ * values and its own terms within 15 over all steps (fp16 operands), else
+ * MOE_EUNSUPPORTED; MOE_EINVAL for non-finite scalars and negative eps.  E = 0 is a
+ * no-op.  One workspace size serves both calls. */
+size_t moe_orthogonalize_workspace(int32_t E, int32_t rows, int32_t cols, int dtype);
+int moe_orthogonalize(const void* g, int dtype, int32_t E, int32_t rows, int32_t cols, int32_t steps,
+                      const float* coef, float eps, void* out, void* ws, size_t ws_bytes, void* stream);
+int moe_muon_step(const void* g, int dtype, int32_t E, int32_t rows, int32_t cols, const float* mom, float momentum,
+                  int nesterov, int32_t steps, const float* coef, float eps, const void* w, float lr,
+                  float weight_decay, float scale, float* mom_out, void* w_out, void* ws, size_t ws_bytes,
+                  void* stream);
 
 /* ---------------------------------------------------------------------------
  * Diagnostics: per-kernel timing for benchmarks and profiling (no page

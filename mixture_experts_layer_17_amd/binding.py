@@ -22,6 +22,7 @@ MOE_F32, MOE_BF16, MOE_MXFP8 = 0, 1, 2
 _PREC = {"f32": MOE_F32, "bf16": MOE_BF16, "mxfp8": MOE_MXFP8}
 
 _c_void_p, _i64, _i32, _sz, _int = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int32, ctypes.c_size_t, ctypes.c_int
+_f32 = ctypes.c_float
 
 _SIGS = {
     "moe_abi_version": (_int, []),
@@ -55,6 +56,19 @@ _SIGS = {
     "moe_mx_weight_cache_build": (_int, [_c_void_p] * 3 + [_i32, _i32, _i32, _c_void_p, _sz, _c_void_p]),
     "mx_quantize": (_int, [_c_void_p, _int, _i64, _i64, _i64, _i32, _c_void_p, _i32, _c_void_p, _c_void_p,
                            _c_void_p]),
+    "moe_balance_loss_workspace": (_sz, [_i64, _i32, _i64]),
+    "moe_balance_loss": (_int, [_c_void_p, _c_void_p, _i64, _i32, _i32, _c_void_p, _i64, _c_void_p, _f32, _f32]
+                         + [_c_void_p] * 6 + [_sz, _c_void_p]),
+    "moe_balance_loss_bwd": (_int, [_c_void_p] * 4 + [_i64, _i32, _i32, _c_void_p, _i64, _c_void_p, _f32, _f32]
+                             + [_c_void_p] * 6),
+    "moe_layernorm": (_int, [_c_void_p] * 4 + [_int, _i64, _i32, _f32] + [_c_void_p] * 5),
+    "moe_layernorm_bwd_workspace": (_sz, [_i64, _i32]),
+    "moe_layernorm_bwd": (_int, [_c_void_p] * 6 + [_int, _i64, _i32] + [_c_void_p] * 4 + [_sz, _c_void_p]),
+    "moe_orthogonalize_workspace": (_sz, [_i32, _i32, _i32, _int]),
+    "moe_orthogonalize": (_int, [_c_void_p, _int, _i32, _i32, _i32, _i32, _c_void_p, _f32, _c_void_p, _c_void_p, _sz,
+                                 _c_void_p]),
+    "moe_muon_step": (_int, [_c_void_p, _int, _i32, _i32, _i32, _c_void_p, _f32, _int, _i32, _c_void_p, _f32,
+                             _c_void_p, _f32, _f32, _f32, _c_void_p, _c_void_p, _c_void_p, _sz, _c_void_p]),
     "moe_timing_enable": (_int, [_int]),
     "moe_timing_report": (_int, [ctypes.c_char_p, _sz]),
 }
@@ -375,6 +389,167 @@ def mx_quantize(src, axis, seg_offsets=None, nseg=0, q=None, scales=None):
     _check(lib().mx_quantize(_p(s3), _dtype_code(src), B, rows, cols, axis, _p(seg_offsets), nseg, _p(q), _p(scales),
                              _stream()), "mx_quantize")
     return q, scales
+
+
+# --------------------------------------------------------------------------- norm, balance loss, weight update
+
+def _arg(what, name, t, shape, dtypes, dev):
+    """A device tensor as the C ABI reads it: this shape and type, contiguous, on the current device (whose current
+    stream the call is enqueued on)."""
+    if t is None:
+        return
+    dtypes = dtypes if isinstance(dtypes, tuple) else (dtypes,)
+    if tuple(t.shape) != tuple(shape) or t.dtype not in dtypes:
+        raise MoeError(f"{what}: {name} is {t.dtype} {list(t.shape)}, expected "
+                       f"{' or '.join(str(d) for d in dtypes)} {list(shape)}")
+    if not t.is_contiguous():
+        raise MoeError(f"{what}: {name} is not contiguous")
+    if t.device != dev or dev.type != "cuda" or dev.index != torch.cuda.current_device():
+        raise MoeError(f"{what}: {name} is on {t.device}, not on the current GPU")
+
+
+_STORAGE = (torch.float32, torch.bfloat16)
+
+
+def moe_layernorm(x, weight=None, bias=None, eps=1e-5, residual=None, out=None):
+    """Layer norm of the rows of x [T, d] (of x + residual, also returned as "sum"); {"y", "mean", "rstd"[, "sum"]}."""
+    what, dev = "moe_layernorm", x.device
+    T, d = x.shape
+    _arg(what, "x", x, (T, d), _STORAGE, dev)
+    for name, t, shape in (("weight", weight, (d,)), ("bias", bias, (d,)), ("residual", residual, (T, d))):
+        _arg(what, name, t, shape, x.dtype, dev)
+    if out is None:
+        out = {"y": torch.empty_like(x), "mean": torch.empty(T, dtype=torch.float32, device=dev),
+               "rstd": torch.empty(T, dtype=torch.float32, device=dev)}
+        if residual is not None:
+            out["sum"] = torch.empty_like(x)
+    for name in ("y", "sum"):
+        _arg(what, name, out.get(name), (T, d), x.dtype, dev)
+    for name in ("mean", "rstd"):
+        _arg(what, name, out.get(name), (T,), torch.float32, dev)
+    _check(lib().moe_layernorm(_p(x), _p(residual), _p(weight), _p(bias), _dtype_code(x), T, d, eps, _p(out["y"]),
+                               _p(out.get("sum")), _p(out.get("mean")), _p(out.get("rstd")), _stream()), what)
+    return out
+
+
+def moe_layernorm_bwd(dy, x, weight, mean, rstd, dres=None, out=None, ws=None):
+    """Gradients of moe_layernorm; x: the rows that were normalised ("sum" with a residual), dres: added to dx.
+    {"dx", "dw", "db"}; an out without "dw" or "db" leaves that sum out."""
+    what, dev = "moe_layernorm_bwd", x.device
+    T, d = x.shape
+    _arg(what, "x", x, (T, d), _STORAGE, dev)
+    for name, t, shape in (("dy", dy, (T, d)), ("weight", weight, (d,)), ("dres", dres, (T, d))):
+        _arg(what, name, t, shape, x.dtype, dev)
+    for name, t in (("mean", mean), ("rstd", rstd)):
+        _arg(what, name, t, (T,), torch.float32, dev)
+    if out is None:
+        out = {"dx": torch.empty_like(x), "dw": torch.empty(d, dtype=x.dtype, device=dev),
+               "db": torch.empty(d, dtype=x.dtype, device=dev)}
+    _arg(what, "dx", out["dx"], (T, d), x.dtype, dev)
+    for name in ("dw", "db"):
+        _arg(what, name, out.get(name), (d,), x.dtype, dev)
+    ws = _ws(lib().moe_layernorm_bwd_workspace(T, d), dev) if ws is None else ws
+    _check(lib().moe_layernorm_bwd(_p(dy), _p(x), _p(weight), _p(mean), _p(rstd), _p(dres), _dtype_code(x), T, d,
+                                   _p(out["dx"]), _p(out.get("dw")), _p(out.get("db")), _p(ws), ws.numel(),
+                                   _stream()), what)
+    return out
+
+
+def _balance_args(what, logits, k, topk_idx, seq_offsets, token_mask):
+    dev = logits.device
+    T, E = logits.shape
+    S = 1 if seq_offsets is None else seq_offsets.numel() - 1
+    _arg(what, "logits", logits, (T, E), torch.float32, dev)
+    _arg(what, "topk_idx", topk_idx, (T, k), torch.int32, dev)
+    _arg(what, "seq_offsets", seq_offsets, (S + 1,), torch.int32, dev)
+    _arg(what, "token_mask", token_mask, (T,), (torch.uint8, torch.bool), dev)
+    return T, E, S, dev
+
+
+def moe_balance_loss(logits, topk_idx, alpha, zeta, seq_offsets=None, token_mask=None, out=None, ws=None):
+    """Balance and z loss of a routing: {"loss" [2], "counts" [S, E], "probs" [S, E], "lse" [T], "norm" [S + 2]}."""
+    what = "moe_balance_loss"
+    k = topk_idx.shape[1]
+    T, E, S, dev = _balance_args(what, logits, k, topk_idx, seq_offsets, token_mask)
+    f32 = dict(dtype=torch.float32, device=dev)
+    if out is None:
+        out = {"loss": torch.empty(2, **f32), "counts": torch.empty((S, E), dtype=torch.int32, device=dev),
+               "probs": torch.empty((S, E), **f32), "lse": torch.empty(T, **f32), "norm": torch.empty(S + 2, **f32)}
+    for name, shape in (("loss", (2,)), ("probs", (S, E)), ("lse", (T,)), ("norm", (S + 2,))):
+        _arg(what, name, out[name], shape, torch.float32, dev)
+    _arg(what, "counts", out["counts"], (S, E), torch.int32, dev)
+    ws = _ws(lib().moe_balance_loss_workspace(T, E, S), dev) if ws is None else ws
+    _check(lib().moe_balance_loss(_p(logits), _p(topk_idx), T, E, k, _p(seq_offsets), S, _p(token_mask), alpha, zeta,
+                                  _p(out["loss"]), _p(out["counts"]), _p(out["probs"]), _p(out["lse"]),
+                                  _p(out["norm"]), _p(ws), ws.numel(), _stream()), what)
+    return out
+
+
+def moe_balance_loss_bwd(logits, fwd, k, alpha, zeta, dloss=None, seq_offsets=None, token_mask=None, topk_idx=None,
+                         gates=None, dgates=None, out=None):
+    """dlogits [T, E] of the two losses (fwd: what moe_balance_loss returned for the same arguments), plus the gates'
+    gradient when gates, dgates and topk_idx are given."""
+    what = "moe_balance_loss_bwd"
+    T, E, S, dev = _balance_args(what, logits, k, topk_idx, seq_offsets, token_mask)
+    for name, shape in (("lse", (T,)), ("norm", (S + 2,))):
+        _arg(what, name, fwd[name], shape, torch.float32, dev)
+    _arg(what, "counts", fwd["counts"], (S, E), torch.int32, dev)
+    _arg(what, "dloss", dloss, (2,), torch.float32, dev)
+    _arg(what, "gates", gates, (T, k), torch.float32, dev)
+    _arg(what, "dgates", dgates, (T, k), torch.float32, dev)
+    out = torch.empty((T, E), dtype=torch.float32, device=dev) if out is None else out
+    _arg(what, "out", out, (T, E), torch.float32, dev)
+    _check(lib().moe_balance_loss_bwd(_p(logits), _p(fwd["lse"]), _p(fwd["counts"]), _p(fwd["norm"]), T, E, k,
+                                      _p(seq_offsets), S, _p(token_mask), alpha, zeta, _p(dloss), _p(topk_idx),
+                                      _p(gates), _p(dgates), _p(out), _stream()), what)
+    return out
+
+
+def moe_orthogonalize_workspace(E, rows, cols, dtype):
+    code = {torch.float32: MOE_F32, torch.bfloat16: MOE_BF16}.get(dtype)
+    if code is None:
+        raise MoeError(f"unsupported dtype {dtype}")
+    return lib().moe_orthogonalize_workspace(E, rows, cols, code)
+
+
+def _coef(steps, coef):
+    """Per-step (a, b, c): one triple for all steps, a list of `steps` triples, or None."""
+    if coef is None:
+        return None
+    rows = [coef] * steps if not hasattr(coef[0], "__len__") else list(coef)
+    if len(rows) != steps or any(len(r) != 3 for r in rows):
+        raise MoeError(f"coef: expected three coefficients, or {steps} triples")
+    return (ctypes.c_float * (3 * steps))(*[float(v) for r in rows for v in r])
+
+
+def moe_orthogonalize(g, steps=5, coef=None, eps=1e-7, out=None, ws=None):
+    """Newton-Schulz orthogonalisation of each matrix of g [E, rows, cols]."""
+    what, dev = "moe_orthogonalize", g.device
+    E, rows, cols = g.shape
+    _arg(what, "g", g, (E, rows, cols), _STORAGE, dev)
+    out = torch.empty_like(g) if out is None else out
+    _arg(what, "out", out, (E, rows, cols), g.dtype, dev)
+    ws = _ws(moe_orthogonalize_workspace(E, rows, cols, g.dtype), dev) if ws is None else ws
+    _check(lib().moe_orthogonalize(_p(g), _dtype_code(g), E, rows, cols, steps, _coef(steps, coef), eps, _p(out),
+                                   _p(ws), ws.numel(), _stream()), what)
+    return out
+
+
+def moe_muon_step(g, mom, w, lr, momentum=0.95, nesterov=True, weight_decay=0.0, scale=1.0, steps=5, coef=None,
+                  eps=1e-7, inplace=True, ws=None):
+    """One Muon step of the weights w [E, rows, cols] with momentum mom (fp32); returns (w, mom): the tensors given,
+    updated, or with inplace=False new ones."""
+    what, dev = "moe_muon_step", g.device
+    E, rows, cols = g.shape
+    _arg(what, "g", g, (E, rows, cols), _STORAGE, dev)
+    _arg(what, "w", w, (E, rows, cols), g.dtype, dev)
+    _arg(what, "mom", mom, (E, rows, cols), torch.float32, dev)
+    w_out, mom_out = (w, mom) if inplace else (torch.empty_like(w), torch.empty_like(mom))
+    ws = _ws(moe_orthogonalize_workspace(E, rows, cols, g.dtype), dev) if ws is None else ws
+    _check(lib().moe_muon_step(_p(g), _dtype_code(g), E, rows, cols, _p(mom), momentum, int(bool(nesterov)), steps,
+                               _coef(steps, coef), eps, _p(w), lr, weight_decay, scale, _p(mom_out), _p(w_out),
+                               _p(ws), ws.numel(), _stream()), what)
+    return w_out, mom_out
 
 
 # --------------------------------------------------------------------------- diagnostics

@@ -1,0 +1,412 @@
+"""Layer norm, balance loss, orthogonalisation and the Muon step on the GPU
+against the fp64 oracle.
+
+Tolerances.  A stored value is off by at most half a step of its type
+(finfo.eps / 2, relative) from the fp32 result; fp32 sums in the kernels run
+over chains of at most a few hundred terms, so a sum is off by less than
+1e-5 of the sum of its absolute terms (2^-24 per addition).  Products: see
+ORTH_TOL.
+"""
+import numpy as np
+import pytest
+import torch
+
+from mixture_experts_layer_17_amd import binding as B
+from oracle import train_ops_oracle as to
+
+import gpu_util as gu
+
+pytestmark = pytest.mark.gpu
+
+DT = {"f32": torch.float32, "bf16": torch.bfloat16}
+
+
+def half(dtype):
+    return torch.finfo(DT[dtype]).eps / 2
+
+
+def dev(a, dtype=None):
+    t = torch.from_numpy(np.ascontiguousarray(a))
+    return t.to("cuda", dtype=dtype) if dtype is not None else t.cuda()
+
+
+def draw(rng, shape, dtype, scale=1.0, shift=0.0):
+    """A device tensor of the storage type and its exact values in fp64."""
+    t = torch.from_numpy((rng.standard_normal(shape) * scale + shift).astype(np.float32)).to(DT[dtype])
+    return t.cuda(), t.double().numpy()
+
+
+def h64(t):
+    return t.detach().cpu().double().numpy()
+
+
+def close(name, got, ref, rel, absolute):
+    """|got - ref| <= rel |ref| + absolute, elementwise."""
+    got = h64(got)
+    assert got.shape == np.shape(ref), name
+    bound = rel * np.abs(ref) + absolute
+    over = np.abs(got - ref) - bound
+    assert np.isfinite(got).all(), name
+    if over.size and over.max() > 0:
+        i = np.unravel_index(over.argmax(), over.shape)
+        raise AssertionError(f"{name}{list(i)}: {got[i]:.8e} for {np.asarray(ref)[i]:.8e}, {over[i]:.2e} past the bound")
+
+
+# ------------------------------------------------------------------- layer norm
+
+LN_SIZES = [(1, 1), (3, 2), (1, 64), (5, 7), (130, 512), (67, 513), (33, 777), (9, 1024), (17, 2048), (5, 2049),
+            (600, 96), (3, 4096), (4, 4100), (2, 8191), (2, 8192), (3, 8193), (2, 20001)]
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("T,d", LN_SIZES)
+def test_layernorm(gpu, T, d, dtype):
+    gu.say(f"case layernorm T={T} d={d} {dtype}")
+    rng = np.random.default_rng(T * 31 + d)
+    x, x64 = draw(rng, (T, d), dtype, 2.0, 0.5)
+    res, _ = draw(rng, (T, d), dtype)
+    w, w64 = draw(rng, (d,), dtype, 0.2, 1.0)
+    b, b64 = draw(rng, (d,), dtype, 0.3)
+    for use in ("plain", "affine", "residual"):
+        kw, ref = {}, x64
+        if use != "plain":
+            kw = dict(weight=w, bias=b)
+        if use == "residual":
+            s = (x.float() + res.float()).to(x.dtype)
+            kw["residual"], ref = res, h64(s)
+        got = B.moe_layernorm(x, eps=1e-5, **kw)
+        torch.cuda.synchronize()
+        if use == "residual":
+            assert torch.equal(got["sum"], s)
+        y, mu, rstd = to.layernorm(ref, w64 if "weight" in kw else None, b64 if "bias" in kw else None)
+        # statistics: one sum of d terms each
+        close("mean", got["mean"], mu, 1e-6, 1e-5 * np.abs(ref).mean(1))
+        close("rstd", got["rstd"], rstd, 1e-5, 0.0)
+        # (s - mean) rstd w: the error of the mean and of rstd, at most 1e-5 of the row's scale
+        scale = (np.abs(ref).max(1) * rstd).max() * np.abs(w64).max() + np.abs(b64).max()
+        close("y", got["y"], y, half(dtype), 1e-5 * scale)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("T,d", LN_SIZES + [(4000, 64)])
+def test_layernorm_bwd(gpu, T, d, dtype):
+    gu.say(f"case layernorm_bwd T={T} d={d} {dtype}")
+    rng = np.random.default_rng(T * 37 + d)
+    x, x64 = draw(rng, (T, d), dtype, 2.0, 0.5)
+    dy, dy64 = draw(rng, (T, d), dtype)
+    dres, dres64 = draw(rng, (T, d), dtype)
+    w, w64 = draw(rng, (d,), dtype, 0.2, 1.0)
+    _, mu, rstd = to.layernorm(x64)
+    mean, rs = dev(mu.astype(np.float32)), dev(rstd.astype(np.float32))
+    for use_w, use_res in ((True, True), (False, False)):
+        ws = B._ws(B.lib().moe_layernorm_bwd_workspace(T, d), "cuda").fill_(255)  # NaNs: nothing stale is read
+        got = B.moe_layernorm_bwd(dy, x, w if use_w else None, mean, rs, dres=dres if use_res else None, ws=ws)
+        torch.cuda.synchronize()
+        dx, dw, db, aw, ab = to.layernorm_bwd(dy64, x64, w64 if use_w else None, dres=dres64 if use_res else None)
+        big = rstd.max() * np.abs(dy64).max() * np.abs(w64).max() * (1 + np.sqrt(d))
+        close("dx", got["dx"], dx, half(dtype), 1e-6 * big + 1e-5 * np.abs(dx).max())
+        hmax = 1e-6 * np.abs(dy64).sum(0) * np.sqrt(d)  # mean and rstd are given in fp32
+        close("dw", got["dw"], dw, half(dtype), 1e-5 * aw + hmax)
+        close("db", got["db"], db, half(dtype), 1e-5 * ab)
+        only = B.moe_layernorm_bwd(dy, x, w if use_w else None, mean, rs, dres=dres if use_res else None,
+                                   out={"dx": torch.empty_like(x)})
+        close("dx alone", only["dx"], dx, half(dtype), 1e-6 * big + 1e-5 * np.abs(dx).max())
+
+
+def test_layernorm_no_rows(gpu):
+    x = torch.empty((0, 40), device="cuda")
+    st = torch.empty(0, device="cuda")
+    assert B.moe_layernorm(x)["y"].shape == (0, 40)
+    out = {"dx": torch.empty_like(x), "dw": torch.full((40,), 7.0, device="cuda"),
+           "db": torch.full((40,), 7.0, device="cuda")}
+    B.moe_layernorm_bwd(x, x, None, st, st, out=out)
+    assert not out["dw"].any() and not out["db"].any()
+
+
+def test_layernorm_leaves_other_rows(gpu):
+    for d in (33, 512, 8200):
+        for dtype in (torch.float32, torch.bfloat16):
+            buf = torch.full((12 * d,), 3.0, device="cuda", dtype=dtype)
+            x = torch.randn((4, d), device="cuda").to(dtype)
+            B.moe_layernorm(x, out={"y": buf[:4 * d].view(4, d)})
+            assert bool((buf[4 * d:] == 3.0).all())
+
+
+# ------------------------------------------------------------------- balance loss
+
+def routing_case(T, E, k, S, seed, masked, zipf=False, pad=0):
+    rng = np.random.default_rng(seed)
+    lg = rng.standard_normal((T, E)).astype(np.float32)
+    if zipf:
+        lg += (-3.0 * np.log(rng.permutation(E) + 1.0)).astype(np.float32)
+    idx = np.argsort(-lg, axis=1, kind="stable")[:, :k].astype(np.int32)
+    seq = None
+    if S:
+        cut = np.sort(rng.integers(0, T - pad + 1, S - 1))
+        seq = np.concatenate([[0], cut, [T - pad]]).astype(np.int32)
+    mask = (rng.random(T) > 0.3).astype(np.uint8) if masked else None
+    return lg, idx, seq, mask, rng
+
+
+def check_balance(lg, idx, seq, mask, rng, alpha=0.02, zeta=0.003, gates=True):
+    T, E = lg.shape
+    k = idx.shape[1]
+    d_lg, d_idx = dev(lg), dev(idx)
+    d_seq = None if seq is None else dev(seq)
+    d_mask = None if mask is None else dev(mask)
+    S = 1 if seq is None else len(seq) - 1
+    ws = B._ws(B.lib().moe_balance_loss_workspace(T, E, S), "cuda").fill_(255)
+    got = B.moe_balance_loss(d_lg, d_idx, alpha, zeta, seq_offsets=d_seq, token_mask=d_mask, ws=ws)
+    up = np.array([0.7, -1.3], np.float32)
+    g = rng.random((T, k)).astype(np.float32) if gates else None
+    dg = rng.standard_normal((T, k)).astype(np.float32) if gates else None
+    dl = B.moe_balance_loss_bwd(d_lg, got, k, alpha, zeta, dloss=dev(up), seq_offsets=d_seq, token_mask=d_mask,
+                                topk_idx=d_idx, gates=None if g is None else dev(g),
+                                dgates=None if dg is None else dev(dg))
+    torch.cuda.synchronize()
+    with np.errstate(invalid="ignore"):
+        loss, cnt, probs, lse = to.balance_loss(lg, idx, alpha, zeta, seq, mask)
+        ref = to.balance_loss_bwd(lg, idx, alpha, zeta, seq, mask, up.astype(np.float64), g, dg)
+    np.testing.assert_array_equal(got["counts"].cpu().numpy(), cnt)
+    close("loss", got["loss"], loss, 1e-5, 1e-12)
+    close("probs", got["probs"], probs, 1e-5, 1e-8)
+    close("lse", got["lse"], lse, 1e-6, 1e-6)
+    close("dlogits", dl, ref, 1e-5, 1e-5 * max(np.abs(ref).max() if ref.size else 0.0, 1e-12))
+    return got, dl
+
+
+@pytest.mark.parametrize("T,E,k,S,masked", [
+    (1, 1, 1, 0, False), (1, 8, 2, 0, False), (31, 5, 3, 0, True), (32, 8, 2, 1, False), (33, 16, 4, 3, True),
+    (256, 8, 2, 0, False), (300, 12, 1, 7, True), (1000, 33, 5, 40, True), (513, 64, 8, 2, False),
+    (700, 100, 4, 9, True), (2048, 128, 4, 24, True), (2050, 129, 4, 5, True), (999, 256, 8, 3, False),
+    (64, 7, 2, 64, False), (70, 4, 4, 300, True)])
+def test_balance_loss(gpu, T, E, k, S, masked):
+    gu.say(f"case balance T={T} E={E} k={k} S={S} masked={masked}")
+    for zipf, gates in ((False, True), (True, False)):
+        check_balance(*routing_case(T, E, k, S, T + E, masked, zipf, pad=T // 5 if S else 0), gates=gates)
+
+
+def test_balance_loss_large(gpu):
+    gu.say("case balance T=16384 E=128 S=1 and 24")
+    for S in (0, 24):
+        check_balance(*routing_case(16384, 128, 4, S, 5, S > 0, True, pad=300 if S else 0))
+
+
+def test_balance_loss_rows_that_do_not_count(gpu):
+    gu.say("case balance masked NaN / inf rows, rows of -inf, no row at all")
+    lg, idx, seq, mask, rng = routing_case(200, 24, 3, 6, 3, True)
+    mask[[7, 60, 100, 105, 120]] = 1
+    lg[mask == 0] = np.nan
+    lg[np.flatnonzero(mask == 0)[::2]] = np.inf
+    lg[7], lg[60:90] = -np.inf, -np.inf          # empty rows, a block of them
+    lg[100:110, ::2] = -np.inf                   # masked experts
+    lg[105, 1::2] = np.finfo(np.float32).min     # and none but the type's lowest value left
+    lg[120, :20] = np.finfo(np.float32).min
+    lg[105, 1] = 2.0
+    got, dl = check_balance(lg, idx, seq, mask, rng, gates=False)
+    assert not dl[dev((mask == 0))].any() and not dl[7].any()
+    lg[120] = np.finfo(np.float32).min           # a uniform row; its lse squared is past fp32: without the z loss
+    check_balance(lg, idx, seq, mask, rng, zeta=0.0, gates=False)
+    none = np.zeros(200, np.uint8)
+    got, dl = check_balance(lg, idx, seq, none, rng, gates=False)
+    assert not got["loss"].any() and not dl.any()
+    # a counted NaN reaches the losses
+    lg[np.flatnonzero(mask)[3], 2] = np.nan
+    bad = B.moe_balance_loss(dev(lg), dev(idx), 0.1, 0.1, seq_offsets=dev(seq), token_mask=dev(mask))
+    assert bool(torch.isnan(bad["loss"]).all()) or seq[0] > 0
+
+
+def test_balance_loss_no_tokens(gpu):
+    lg = torch.empty((0, 8), device="cuda")
+    idx = torch.empty((0, 2), dtype=torch.int32, device="cuda")
+    got = B.moe_balance_loss(lg, idx, 0.1, 0.1)
+    assert not got["loss"].any() and not got["counts"].any() and not got["probs"].any()
+    assert B.moe_balance_loss_bwd(lg, got, 2, 0.1, 0.1).shape == (0, 8)
+
+
+def test_balance_bwd_gates_match_route_topk_bwd(gpu):
+    """alpha = zeta = 0: exactly the gates' gradient of moe_route_topk_bwd, in its values."""
+    T, E, k = 500, 20, 3
+    lg = torch.randn((T, E), device="cuda")
+    r = B.moe_route_topk(lg, k)
+    dg = torch.randn((T, k), device="cuda")
+    f = B.moe_balance_loss(lg, r["topk_idx"], 0.0, 0.0)
+    np.testing.assert_array_equal(f["counts"][0].cpu().numpy(), r["counts"].cpu().numpy())
+    got = B.moe_balance_loss_bwd(lg, f, k, 0.0, 0.0, topk_idx=r["topk_idx"], gates=r["gates"], dgates=dg)
+    ref = B.moe_route_topk_bwd(r["gates"], dg, r["topk_idx"], E)
+    close("dlogits", got, h64(ref), 1e-6, 1e-6)
+
+
+# ------------------------------------------------------------------- orthogonalisation
+
+# max error over max |ref|.  fp32: operands carry 22 bits (2^-23 per rounding), and a step multiplies noise in
+# directions of small singular values by at most a = 3.4445: 5 steps by 485, summed over the steps' roundings by
+# 485 (1 + 1/3.44 + ...) < 690, and 690 x 2^-23 < 1e-4; the norm and the fp32 sums add less.  bf16: A and B are
+# rounded to 11 bits (2^-12 each of an entry); B acts on X with |b| A + 2 |c| A^2 <= 9 in the worst direction, three
+# such roundings over five steps whose errors mostly do not grow (they lie in X's own range, where singular values
+# are held near 1): 15 x 9 x 2^-12 / sqrt(15) < 9e-3, plus the output's half step 2^-8.
+ORTH_TOL = {"f32": 1e-4, "bf16": 9e-3 + 2.0 ** -8}
+
+ORTH_SIZES = [(1, 1, 1), (2, 1, 5), (2, 5, 1), (3, 2, 2), (2, 7, 33), (8, 64, 128), (2, 65, 64), (2, 64, 65),
+              (1, 128, 128), (3, 129, 100), (2, 31, 700), (2, 700, 31), (1, 257, 513), (2, 300, 190), (1, 512, 512)]
+
+
+def gradients(rng, E, rows, cols, kind):
+    if kind == "noise":
+        g = rng.standard_normal((E, rows, cols))
+    else:  # few tokens, columns of different scale
+        t = max(1, min(rows, cols) // 3)
+        g = rng.standard_normal((E, rows, t)) @ (rng.standard_normal((E, t, cols)) * 2.0 ** (-6 * rng.random(cols)))
+    return (g * 1e-3).astype(np.float32)
+
+
+def orth_err(got, ref):
+    got = h64(got)
+    assert np.isfinite(got).all()
+    return max(np.abs(g - r).max() / max(np.abs(r).max(), 1e-30) for g, r in zip(got, ref))
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("E,rows,cols", ORTH_SIZES)
+def test_orthogonalize(gpu, E, rows, cols, dtype):
+    rng = np.random.default_rng(E + rows * 7 + cols)
+    for kind in ("noise", "lowrank"):
+        g = torch.from_numpy(gradients(rng, E, rows, cols, kind)).to(DT[dtype])
+        ws = B._ws(B.moe_orthogonalize_workspace(E, rows, cols, DT[dtype]), "cuda").fill_(255)
+        gu.say(f"case orthogonalize E={E} {rows}x{cols} {dtype} {kind}")
+        out = B.moe_orthogonalize(g.cuda(), ws=ws)
+        torch.cuda.synchronize()
+        err = orth_err(out, to.orthogonalize(g.double().numpy()))
+        gu.say(f"  error {err:.2e}")
+        assert err <= ORTH_TOL[dtype]
+
+
+@pytest.mark.parametrize("E,rows,cols", [(32, 512, 1100), (32, 1100, 520), (300, 250, 256)])
+def test_orthogonalize_many(gpu, E, rows, cols):
+    """Enough matrices for the large tiles; every matrix checked against its own fp64 iteration on the GPU."""
+    rng = np.random.default_rng(rows)
+    for dtype in ("bf16", "f32"):
+        g = torch.from_numpy(gradients(rng, E, rows, cols, "lowrank")).to(DT[dtype]).cuda()
+        gu.say(f"case orthogonalize many E={E} {rows}x{cols} {dtype}")
+        out = B.moe_orthogonalize(g)
+        torch.cuda.synchronize()
+        a, b, c = to.QUINTIC
+        for e in range(E):
+            x = g[e].double()
+            x = x / (x.norm() + 1e-7)
+            for _ in range(5):
+                y = x @ (x.T.contiguous() @ x) if rows > cols else (x @ x.T.contiguous()) @ x
+                q = y @ (x.T.contiguous() @ x) if rows > cols else (x @ x.T.contiguous()) @ y
+                x = a * x + b * y + c * q
+            err = float((out[e].double() - x).abs().max() / x.abs().max())
+            assert err <= ORTH_TOL[dtype], (e, err)
+
+
+def test_orthogonalize_steps_and_coefficients(gpu):
+    rng = np.random.default_rng(3)
+    g = gradients(rng, 2, 96, 160, "noise")
+    cubic = [(1.5, -0.5, 0.0)] * 9
+    mixed = [(4.0848, -6.8946, 2.9270), (3.9505, -6.3029, 2.6377), (3.7418, -5.5913, 2.3037)]
+    for steps, coef in ((1, None), (9, cubic), (3, mixed), (2, [(1.0, 0.0, 0.0)] * 2)):
+        gu.say(f"case orthogonalize steps={steps}")
+        ref = to.orthogonalize(g, steps, None if coef is None else np.float64(np.float32(coef)))
+        assert orth_err(B.moe_orthogonalize(dev(g), steps=steps, coef=coef), ref) <= ORTH_TOL["f32"]
+    with pytest.raises(B.MoeError):
+        B.moe_orthogonalize(dev(g), steps=3, coef=[(1.0, 0.0, 0.0)] * 2)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_orthogonalize_special_matrices(gpu, dtype):
+    """Zero, tiny, huge, NaN and inf matrices side by side: each on its own."""
+    rng = np.random.default_rng(4)
+    g = gradients(rng, 7, 40, 72, "noise")
+    g[1] = 0.0
+    g[2] *= 1e-9                       # norm far below eps
+    g[3] *= 1e-30                      # squares below fp32's range
+    g[4] *= 1e30                       # squares above it
+    g[5, 3, 4] = np.nan
+    g[6, 0, 0] = np.inf
+    t = torch.from_numpy(g).to(DT[dtype])
+    gu.say(f"case orthogonalize special {dtype}")
+    for eps in (1e-7, 0.0):
+        out = B.moe_orthogonalize(t.cuda(), eps=eps)
+        torch.cuda.synchronize()
+        assert bool(torch.isnan(out[5:]).all()) and not out[1].any()
+        ref = to.orthogonalize(t[:5].double().numpy(), eps=eps)
+        for e in (0, 2, 3, 4):
+            err = np.abs(h64(out[e]) - ref[e]).max() / np.abs(ref[e]).max()
+            # 1e-30 scaled by a^5 / eps is representable in both types
+            assert err <= ORTH_TOL[dtype], (eps, e, err)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("E,rows,cols", [(1, 1, 3), (3, 70, 33), (2, 33, 70), (2, 128, 260)])
+def test_muon_step(gpu, E, rows, cols, dtype):
+    rng = np.random.default_rng(rows * 3 + cols)
+    g = torch.from_numpy(gradients(rng, E, rows, cols, "lowrank")).to(DT[dtype])
+    mom = gradients(rng, E, rows, cols, "noise") * 3
+    w = torch.from_numpy((rng.standard_normal((E, rows, cols)) * 0.02).astype(np.float32)).to(DT[dtype])
+    for nesterov in (True, False):
+        kw = dict(lr=0.02, momentum=0.9, nesterov=nesterov, weight_decay=0.1, scale=1.5)
+        gu.say(f"case muon E={E} {rows}x{cols} {dtype} nesterov={nesterov}")
+        dw, dm = w.cuda(), dev(mom)
+        w2, m2 = B.moe_muon_step(g.cuda(), dm, dw, inplace=False, **kw)
+        torch.cuda.synchronize()
+        assert torch.equal(dw, w.cuda()) and torch.equal(dm, dev(mom))  # untouched
+        rw, rm, o = to.muon_step(g.double().numpy(), mom, w.double().numpy(), **kw)
+        close("mom", m2, rm, 2.0 ** -22, 1e-9)
+        # the orthogonalised update's error times lr scale, the fp32 arithmetic, and the weight's own rounding
+        orth = (ORTH_TOL["f32"] if dtype == "f32" else 9e-3) * np.abs(o).max() * 0.03
+        close("w", w2, rw, half(dtype) + 2.0 ** -22, orth)
+        B.moe_muon_step(g.cuda(), dm, dw, **kw)  # in place: the same bits
+        assert torch.equal(dw, w2) and torch.equal(dm, m2)
+
+
+# ------------------------------------------------------------------- how the calls are used
+
+def test_calls_are_deterministic_and_capturable(gpu):
+    """Eager results repeat bit for bit; a graph of all calls gives them too, replayed with eager work in between."""
+    T, d, E, k, f = 300, 192, 12, 2, 320
+    x = torch.randn((T, d), device="cuda").bfloat16()
+    dy = torch.randn((T, d), device="cuda").bfloat16()
+    w = torch.randn(d, device="cuda").bfloat16()
+    lg = torch.randn((T, E), device="cuda")
+    r = B.moe_route_topk(lg, k)
+    dg = torch.randn((T, k), device="cuda")
+    g = torch.randn((E, d, f), device="cuda").bfloat16()
+    wt = torch.randn((E, d, f), device="cuda").bfloat16()
+    mom = torch.randn((E, d, f), device="cuda")
+
+    def all_calls():
+        o = {}
+        fw = B.moe_layernorm(x, w, w, residual=dy)
+        o.update({"y": fw["y"], "mean": fw["mean"]})
+        o.update(B.moe_layernorm_bwd(dy, fw["sum"], w, fw["mean"], fw["rstd"], dres=dy))
+        bl = B.moe_balance_loss(lg, r["topk_idx"], 0.01, 0.001)
+        o.update({"loss": bl["loss"], "counts": bl["counts"], "probs": bl["probs"]})
+        o["dl"] = B.moe_balance_loss_bwd(lg, bl, k, 0.01, 0.001, topk_idx=r["topk_idx"], gates=r["gates"], dgates=dg)
+        o["orth"] = B.moe_orthogonalize(g)
+        o["w"], o["mom"] = B.moe_muon_step(g, mom, wt, lr=0.1, inplace=False)
+        return o
+
+    gu.say("case eager and captured")
+    ref = {key: v.clone() for key, v in all_calls().items()}
+    again = all_calls()
+    for key in ref:
+        assert torch.equal(ref[key], again[key]), key
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        all_calls()
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = all_calls()
+    for _ in range(3):
+        for v in out.values():
+            v.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        for key in ref:
+            assert torch.equal(ref[key], out[key]), key
+        all_calls()

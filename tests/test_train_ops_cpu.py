@@ -1,0 +1,154 @@
+"""Host-side validation of the layer norm, balance loss, orthogonalisation and
+Muon calls, and the oracle's gradients against finite differences (CPU only: no
+call here reaches a launch)."""
+import ctypes
+import os
+
+import numpy as np
+import pytest
+
+from mixture_experts_layer_17_amd import binding as B
+from oracle import train_ops_oracle as to
+
+EINVAL, EUNSUP, EWS = 1, 2, 3
+FAKE = ctypes.c_void_p(0x10000)
+ODD = ctypes.c_void_p(0x10004)
+BIG = 1 << 50
+
+
+@pytest.fixture(scope="module")
+def L():
+    if not os.path.exists(B.LIB_PATH):
+        pytest.fail("libmoe.so not built: run __graft_entry__.build()")
+    return B.lib()
+
+
+def test_layernorm_validation(L):
+    def fwd(x=FAKE, res=None, w=FAKE, b=FAKE, dt=1, T=4, d=64, eps=1e-5, y=FAKE, s=None, m=FAKE, r=FAKE):
+        return L.moe_layernorm(x, res, w, b, dt, T, d, eps, y, s, m, r, None)
+
+    assert fwd(T=0, x=None, y=None) == 0
+    assert fwd(x=None) == fwd(y=None) == fwd(T=-1) == fwd(d=0) == fwd(dt=2) == fwd(eps=-1.0) == EINVAL
+    assert fwd(eps=float("nan")) == fwd(eps=float("inf")) == EINVAL
+    assert fwd(s=FAKE) == EINVAL                       # a sum without a residual
+    assert fwd(d=(1 << 20) + 1) == EUNSUP
+    for name in ("x", "res", "w", "b", "y", "m", "r"):
+        assert fwd(**{name: ODD}) == EINVAL, name
+
+    def bwd(dy=FAKE, x=FAKE, w=FAKE, m=FAKE, r=FAKE, res=None, dt=1, T=4, d=64, dx=FAKE, dw=FAKE, db=FAKE, ws=FAKE,
+            n=BIG):
+        return L.moe_layernorm_bwd(dy, x, w, m, r, res, dt, T, d, dx, dw, db, ws, n, None)
+
+    for name in ("dy", "x", "m", "r", "dx", "ws"):
+        assert bwd(**{name: None}) == EINVAL, name
+    for name in ("dy", "x", "w", "m", "r", "res", "dx", "dw", "db", "ws"):
+        assert bwd(**{name: ODD}) == EINVAL, name
+    need = L.moe_layernorm_bwd_workspace(4, 64)
+    assert need == 2 * 4 * 64 * 4 and bwd(n=need - 1) == EWS
+    assert L.moe_layernorm_bwd_workspace(-1, 64) == 0 and L.moe_layernorm_bwd_workspace(4, 0) == 0
+    assert bwd(d=0) == bwd(dt=5) == EINVAL and bwd(d=1 << 21) == EUNSUP
+
+
+def test_balance_validation(L):
+    def fwd(lg=FAKE, idx=FAKE, T=10, E=8, k=2, seq=FAKE, S=3, mask=None, a=0.1, z=0.1, loss=FAKE, c=FAKE, p=FAKE,
+            lse=FAKE, norm=FAKE, ws=FAKE, n=BIG):
+        return L.moe_balance_loss(lg, idx, T, E, k, seq, S, mask, a, z, loss, c, p, lse, norm, ws, n, None)
+
+    for name in ("lg", "idx", "loss", "c", "p", "lse", "norm", "ws"):
+        assert fwd(**{name: None}) == EINVAL, name
+        assert fwd(**{name: ODD}) == EINVAL, name
+    assert fwd(seq=ODD) == fwd(mask=ODD) == EINVAL
+    assert fwd(seq=None) == EINVAL                     # S > 1 without offsets
+    assert fwd(S=0) == fwd(T=-1) == fwd(k=9, E=8) == EINVAL or fwd(k=9) == EUNSUP
+    assert fwd(k=0) == fwd(E=0, k=0) == fwd(k=5, E=4) == EINVAL
+    assert fwd(E=257) == fwd(k=9, E=16) == EUNSUP
+    assert fwd(a=float("nan")) == fwd(z=float("inf")) == EINVAL
+    need = L.moe_balance_loss_workspace(10, 8, 3)
+    assert need > 0 and fwd(n=need - 1) == EWS
+    assert L.moe_balance_loss_workspace(10, 300, 3) == 0 and L.moe_balance_loss_workspace(10, 8, 0) == 0
+
+    def bwd(lg=FAKE, lse=FAKE, c=FAKE, norm=FAKE, T=10, E=8, k=2, seq=FAKE, S=3, mask=None, a=0.1, z=0.1, up=None,
+            idx=FAKE, g=FAKE, dg=FAKE, out=FAKE):
+        return L.moe_balance_loss_bwd(lg, lse, c, norm, T, E, k, seq, S, mask, a, z, up, idx, g, dg, out, None)
+
+    for name in ("lg", "lse", "c", "norm", "out", "idx", "g", "dg"):
+        assert bwd(**{name: None}) == EINVAL, name     # gates without dgates or indices, too
+    for name in ("lg", "lse", "c", "norm", "seq", "mask", "up", "idx", "g", "dg", "out"):
+        assert bwd(**{name: ODD}) == EINVAL, name
+    assert bwd(seq=None) == EINVAL and bwd(E=257) == EUNSUP
+    assert bwd(T=0, lg=None, out=None) == 0
+
+
+def test_orthogonalize_validation(L):
+    def orth(g=FAKE, dt=1, E=2, r=64, c=96, steps=5, coef=None, eps=1e-7, out=FAKE, ws=FAKE, n=BIG):
+        arr = None if coef is None else (ctypes.c_float * len(coef))(*coef)
+        return L.moe_orthogonalize(g, dt, E, r, c, steps, arr, eps, out, ws, n, None)
+
+    for name in ("g", "out", "ws"):
+        assert orth(**{name: None}) == EINVAL and orth(**{name: ODD}) == EINVAL, name
+    assert orth(E=0, g=None) == 0
+    assert orth(E=-1) == orth(r=0) == orth(c=0) == orth(dt=2) == orth(steps=0) == orth(eps=-1.0) == EINVAL
+    assert orth(steps=17) == orth(r=40000) == orth(E=70000) == orth(r=32768, c=32768) == EUNSUP
+    assert orth(steps=1, coef=[float("nan"), 0, 0]) == EINVAL
+    # steps that leave the operands' range: 20 x at once, and growth that adds up over the steps
+    assert orth(steps=1, coef=[20.0, 0.0, 0.0]) == EUNSUP
+    assert orth(steps=3, coef=[3.0, 0.0, 0.0] * 3) == EUNSUP
+    need = L.moe_orthogonalize_workspace(2, 64, 96, 1)
+    assert need > 0 and orth(n=need - 1) == EWS
+    assert L.moe_orthogonalize_workspace(2, 64, 96, 0) > need  # fp32 keeps pairs
+    assert L.moe_orthogonalize_workspace(2, 0, 96, 1) == 0
+
+    def muon(g=FAKE, mom=FAKE, b=0.9, w=FAKE, lr=0.1, wd=0.0, sc=1.0, mo=FAKE, wo=FAKE, ws=FAKE, n=BIG, E=2):
+        return L.moe_muon_step(g, 1, E, 64, 96, mom, b, 1, 5, None, 1e-7, w, lr, wd, sc, mo, wo, ws, n, None)
+
+    for name in ("g", "mom", "w", "mo", "wo", "ws"):
+        assert muon(**{name: None}) == EINVAL and muon(**{name: ODD}) == EINVAL, name
+    for name in ("b", "lr", "wd", "sc"):
+        assert muon(**{name: float("nan")}) == EINVAL, name
+    assert muon(n=need - 1) == EWS and muon(E=0, g=None) == 0
+
+
+def test_oracle_layernorm_gradient_against_differences():
+    rng = np.random.default_rng(0)
+    x, dy, w, b = rng.standard_normal((3, 11)), rng.standard_normal((3, 11)), rng.standard_normal(11), rng.standard_normal(11)
+    dx, dw, db, _, _ = to.layernorm_bwd(dy, x, w)
+    f = lambda x_, w_, b_: (to.layernorm(x_, w_, b_)[0] * dy).sum()
+    h = 1e-6
+    for grad, arr, at in ((dx, x, 0), (dw, w, 1), (db, b, 2)):
+        for i in np.ndindex(arr.shape):
+            args = [[x.copy(), w.copy(), b.copy()] for _ in range(2)]
+            args[0][at][i] += h
+            args[1][at][i] -= h
+            # central differences: h^2 truncation, 1e-16 / h rounding of values of order 10
+            assert abs((f(*args[0]) - f(*args[1])) / (2 * h) - grad[i]) < 1e-7
+
+
+def test_oracle_balance_gradient_against_differences():
+    rng = np.random.default_rng(1)
+    lg = rng.standard_normal((14, 6))
+    lg[5] = -np.inf
+    idx = np.argsort(-lg, axis=1, kind="stable")[:, :2]
+    seq, mask = [1, 4, 4, 12], (rng.random(14) > 0.2).astype(np.uint8)
+    up = (0.7, -1.3)
+    dl = to.balance_loss_bwd(lg, idx, 0.3, 0.2, seq, mask, up)
+    _, cnt, _, _ = to.balance_loss(lg, idx, 0.3, 0.2, seq, mask)
+    f = lambda v: float(np.dot(to.balance_loss(v, idx, 0.3, 0.2, seq, mask, counts=cnt)[0], up))
+    h = 1e-6
+    for i in np.ndindex(lg.shape):
+        if not np.isfinite(lg[i]):
+            assert dl[i] == 0
+            continue
+        a, b = lg.copy(), lg.copy()
+        a[i] += h
+        b[i] -= h
+        assert abs((f(a) - f(b)) / (2 * h) - dl[i]) < 1e-8
+
+
+def test_oracle_orthogonalize_flattens_singular_values():
+    rng = np.random.default_rng(2)
+    g = rng.standard_normal((2, 9, 14)), rng.standard_normal((1, 14, 9))
+    for m in g:
+        s = np.linalg.svd(to.orthogonalize(m, steps=10, coef=[(1.5, -0.5, 0.0)] * 10), compute_uv=False)
+        assert np.all(np.abs(s - 1) < 0.2)              # the cubic iteration converges to 1 from below
+        q = np.linalg.svd(to.orthogonalize(m), compute_uv=False)
+        assert np.all((q > 0.3) & (q < 1.3))            # the quintic keeps them in a band
