@@ -16,8 +16,10 @@
 // rounding noise outside the matrix's own range (a gradient's rank is at most
 // its token count).  So X is held as an fp16 pair hi + lo.  bf16 gradients: the
 // products use hi only (their error stays inside X's range, where it does not
-// grow), the a X term uses both; measured against fp64, the result is off by
-// 0.07-0.16% (rms), less than its rounding to bf16 (0.17%).  fp32 gradients
+// grow), the a X term uses both.  The diagonals of A and B, which outweigh the
+// other entries, are kept apart in fp32 and applied in the epilogues.  Against
+// fp64 the result is off by 0.06-0.11% (rms; without the split diagonals up to
+// 0.17%), less than its rounding to bf16 (0.17%).  fp32 gradients
 // need the products too at fp32 accuracy: X, A and B are pairs and every
 // product is hi hi + hi lo + lo hi (22 bits; lo lo is below fp32's last bit).
 //
@@ -68,10 +70,37 @@ __device__ __forceinline__ void split8(const float* v, uint4& hi, uint4& lo) {
   hi = __builtin_bit_cast(uint4, h);
   lo = __builtin_bit_cast(uint4, l);
 }
-__device__ __forceinline__ void add8(const uint4& u, float* o) {
-  const f16x8 h = __builtin_bit_cast(f16x8, u);
+
+// The same with lo in 8 bits (E4M3, times 16: a hi of up to 15 kS leaves at most
+// 16, and steps of 2^-13 are far below what lo has to carry).
+constexpr float kLoScale = 16.0f;
+typedef float f32x2 __attribute__((ext_vector_type(2)));
+__device__ __forceinline__ void split8_fp8(const float* v, uint4& hi, uint2& lo) {
+  f16x8 h;
+  float l[8];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) o[i] += static_cast<float>(h[i]);
+  for (int i = 0; i < 8; ++i) {
+    h[i] = static_cast<_Float16>(v[i]);
+    l[i] = (v[i] - static_cast<float>(h[i])) * kLoScale;
+  }
+  hi = __builtin_bit_cast(uint4, h);
+  int a = 0, b = 0;
+  a = __builtin_amdgcn_cvt_pk_fp8_f32(l[0], l[1], a, false);
+  a = __builtin_amdgcn_cvt_pk_fp8_f32(l[2], l[3], a, true);
+  b = __builtin_amdgcn_cvt_pk_fp8_f32(l[4], l[5], b, false);
+  b = __builtin_amdgcn_cvt_pk_fp8_f32(l[6], l[7], b, true);
+  lo = make_uint2(static_cast<uint32_t>(a), static_cast<uint32_t>(b));
+}
+__device__ __forceinline__ void lo_fp8(const uint2& u, float* l) {
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const int w = static_cast<int>(i ? u.y : u.x);
+    const f32x2 a = __builtin_amdgcn_cvt_pk_f32_fp8(w, false), b = __builtin_amdgcn_cvt_pk_f32_fp8(w, true);
+    l[4 * i] = a[0];
+    l[4 * i + 1] = a[1];
+    l[4 * i + 2] = b[0];
+    l[4 * i + 3] = b[1];
+  }
 }
 
 // Up to 8 elements at p (element alignment) as floats, and back.
@@ -118,7 +147,8 @@ struct PreArgs {
   int nesterov;
   double* part;       // [E][chunks] sums of squares
   float* cs;          // [E][steps + 1]
-  uint16_t *xh, *xl;  // [E][rp][cp]
+  uint16_t* xh;       // [E][rp][cp]
+  void* xl;           // lo: fp16 for fp32 gradients, else 8 bits; nullptr: not needed
   int rows, cols, rp, cp, chunks, steps;
   float eps, growth[kMaxSteps];
 };
@@ -214,11 +244,18 @@ __global__ __launch_bounds__(kNormThreads) void orth_scale_kernel(PreArgs a) {
         if (j >= k) u[j] = 0.f;
       }
     }
-    uint4 hi, lo;
-    split8(u, hi, lo);
     const int64_t o = e * np + i * 8;
+    uint4 hi;
+    if constexpr (sizeof(T) == 4) {
+      uint4 lo;
+      split8(u, hi, lo);
+      *reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.xl) + o) = lo;
+    } else {
+      uint2 lo;
+      split8_fp8(u, hi, lo);
+      if (a.xl) *reinterpret_cast<uint2*>(static_cast<uint8_t*>(a.xl) + o) = lo;
+    }
     *reinterpret_cast<uint4*>(a.xh + o) = hi;
-    *reinterpret_cast<uint4*>(a.xl + o) = lo;
   }
 }
 
@@ -233,8 +270,13 @@ struct MmArgs {
   int tm, tn;                         // output tiles (symmetric kinds: tn = 1, tm = all lower tiles)
   int64_t tiles;                      // tm * tn * E
   // epilogue
-  const uint16_t *eh, *el;            // A (poly) or X (apply) at the output's place
-  uint16_t *oh, *ol;                  // fp16 pair output
+  const uint16_t* eh;                 // A (poly) or X (apply) at the output's place
+  const void* el;                     // and its lo part; apply without split operands: 8 bits, or none (zero)
+  const float* din;                   // diagonal of A (poly) or of B (apply)
+  float* dout;                        // of A (gram) or of B (poly)
+  int64_t sd;
+  uint16_t* oh;                       // outputs; ol as el, nullptr: not wanted
+  void* ol;
   int64_t so;
   int ldo;
   const float* cs;
@@ -247,65 +289,88 @@ struct MmArgs {
   float keep, gain;                   // w' = keep w - gain O
 };
 
-// BT x BT outputs per workgroup by four waves of WT x WT; K step BK; a ring of
+// BM x BN outputs per workgroup by 2 x 2 waves of WM x WN; K step BK; a ring of
 // kRing K steps of both operands in LDS.
-template <int BT_, int BK_>
+template <int BM_, int BN_, int BK_, int RING_>
 struct Tile {
-  static constexpr int BT = BT_, BK = BK_, WT = BT / 2, TM = WT / 32;
-  static constexpr int kRing = 4;
-  static constexpr int kOp = BT * BK;          // elements of one operand's K step
-  static constexpr int kLoads = kOp / 512 / 4; // LDS-DMA instructions per wave, operand and step
-  static constexpr int kLds = kRing * 2 * kOp;
-  static_assert(kOp % 2048 == 0 && BT * BT <= kLds, "the output tile is mirrored through the ring's LDS");
+  static constexpr int BM = BM_, BN = BN_, BK = BK_, kRing = RING_;
+  static constexpr int WM = BM / 2, WN = BN / 2, TM = WM / 32, TN = WN / 32;
+  static constexpr int kA = BM * BK, kSlot = (BM + BN) * BK;  // elements: the A tile, then the B tile
+  static constexpr int kLoads = kSlot / 512 / 4;              // LDS-DMA instructions per wave and step
+  static constexpr int kLds = kRing * kSlot;
+  static_assert(kA % 2048 == 0 && kSlot % 2048 == 0, "whole LDS-DMA instructions per wave");
 };
 
 // 16-byte chunk swizzles against bank conflicts.  K-contiguous tiles (BK
 // elements per row): a fragment read takes one chunk column of 16 consecutive
-// rows at a time.  M/N-contiguous tiles (BT elements per k-row): a transposing
+// rows at a time.  M/N-contiguous tiles (W elements per k-row): a transposing
 // read takes 4 consecutive k-rows times 4 chunks.
 template <int BK>
 __device__ __forceinline__ int kc_swz(int row) {
   return BK == 64 ? (row >> 1) & 7 : (row >> 2) & 3;
 }
-template <int BT>
+template <int W>
 __device__ __forceinline__ int mc_swz(int k) {
-  return BT >= 128 ? 4 * (k & 3) : 4 * ((k >> 1) & 1);
+  return W >= 128 ? 4 * (k & 3) : 4 * ((k >> 1) & 1);
 }
 
-template <class C, bool KC>
+// MFMA fragment from a tile whose rows (RS elements, one k each) run along M/N,
+// with 16-byte chunks swizzled by swz(k): two transposing reads.  In each group
+// G of 16 lanes, lane L points at k-row 16 ks + 8 (G/2) + L/4 (then 4 further)
+// and columns base + 16 (G%2) + 4 (L%4), and receives the four k values of
+// column base + 16 (G%2) + L.
+template <int RS, class F>
+__device__ __forceinline__ f16x8 frag_tr(const uint16_t* t, int base, int ks, int lane, F&& swz) {
+  const int G = lane >> 4, L = lane & 15;
+  const int k = ks * 16 + 8 * (G >> 1) + (L >> 2);
+  const int c = base + 16 * (G & 1) + 4 * (L & 3);
+  const uint16_t* p = t + k * RS + ((c >> 3) ^ swz(k)) * 8 + (c & 7);
+  const uint16_t* q = t + (k + 4) * RS + ((c >> 3) ^ swz(k + 4)) * 8 + (c & 7);
+  typedef __attribute__((address_space(3))) i16x4 lds_i16x4;
+  const i16x4 a = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_i16x4*)(p));
+  const i16x4 b = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_i16x4*)(q));
+  const short v[8] = {a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]};
+  f16x8 r;
+  __builtin_memcpy(&r, v, 16);
+  return r;
+}
+
+// One operand of a tile: W rows (KC: stored with K contiguous) or columns.
+template <int W, int BK, bool KC>
 struct Operand {
+  static constexpr int kLoads = W * BK / 512 / 4;  // LDS-DMA instructions per wave and step
   __amdgpu_buffer_rsrc_t hi, lo;
   int voff, vstep, kstep;  // this lane's byte offset, per load, and per K step
 
-  // rows0: first row (KC) or column of the tile; valid: rows (KC) of the operand
+  // mn0: first row or column of the tile, of mn
   __device__ __forceinline__ void init(const uint16_t* h, const uint16_t* l, int ld, int mn0, int mn, int K, int wave,
                                        int lane) {
     if constexpr (KC) {
-      const int rows = mn - mn0 < C::BT ? mn - mn0 : C::BT;
+      const int rows = mn - mn0 < W ? mn - mn0 : W;
       const int64_t o = static_cast<int64_t>(mn0) * ld, bytes = static_cast<int64_t>(rows) * ld * 2;
       hi = rsrc(h + o, bytes);
       lo = rsrc(l ? l + o : h + o, bytes);
-      constexpr int CPR = C::BK / 8, RPI = 64 / CPR;
+      constexpr int CPR = BK / 8, RPI = 64 / CPR;
       const int row = wave * RPI + lane / CPR;
       // rows advance by 4 RPI per load: a multiple of the swizzle's period
-      voff = (row * ld + ((lane % CPR) ^ kc_swz<C::BK>(row)) * 8) * 2;
+      voff = (row * ld + ((lane % CPR) ^ kc_swz<BK>(row)) * 8) * 2;
       vstep = 4 * RPI * ld * 2;
-      kstep = C::BK * 2;
+      kstep = BK * 2;
     } else {
       const int64_t bytes = (static_cast<int64_t>(K) * ld - mn0) * 2;
       hi = rsrc(h + mn0, bytes);
       lo = rsrc(l ? l + mn0 : h + mn0, bytes);
-      constexpr int CPR = C::BT / 8, KPI = 64 / CPR;
+      constexpr int CPR = W / 8, KPI = 64 / CPR;
       const int k = wave * KPI + lane / CPR;
-      voff = (k * ld + ((lane % CPR) ^ mc_swz<C::BT>(k)) * 8) * 2;
+      voff = (k * ld + ((lane % CPR) ^ mc_swz<W>(k)) * 8) * 2;
       vstep = 4 * KPI * ld * 2;
-      kstep = C::BK * ld * 2;
+      kstep = BK * ld * 2;
     }
   }
-  // Loads of the K step at byte offset soff into dst (this operand's ring slot).
+  // Loads of the K step at byte offset soff into dst (this operand's part of a ring slot).
   __device__ __forceinline__ void issue(bool low, int soff, uint16_t* dst, int wave) const {
 #pragma unroll
-    for (int u = 0; u < C::kLoads; ++u)
+    for (int u = 0; u < kLoads; ++u)
       __builtin_amdgcn_raw_ptr_buffer_load_lds(low ? lo : hi, (lds_void*)(dst + (wave + 4 * u) * 512), 16,
                                                voff + u * vstep, soff, 0, 0);
   }
@@ -313,29 +378,11 @@ struct Operand {
   __device__ static __forceinline__ f16x8 frag(const uint16_t* t, int base, int ks, int lane) {
     if constexpr (KC) {
       const int row = base + (lane & 31);
-      const int ph = (ks * 2 + (lane >> 5)) ^ kc_swz<C::BK>(row);
-      return *reinterpret_cast<const f16x8*>(t + row * C::BK + ph * 8);
+      const int ph = (ks * 2 + (lane >> 5)) ^ kc_swz<BK>(row);
+      return *reinterpret_cast<const f16x8*>(t + row * BK + ph * 8);
     } else {
-      return frag_tr<C::BT>(t, base, ks, lane);
+      return frag_tr<W>(t, base, ks, lane, [](int k) { return mc_swz<W>(k); });
     }
-  }
-  // The same from a tile whose rows (RS elements) run along M/N: two transposing
-  // reads.  In each group G of 16 lanes, lane L points at k-row 16 ks + 8 (G/2) +
-  // L/4 (then 4 further) and columns base + 16 (G%2) + 4 (L%4), and receives
-  // the four k values of column base + 16 (G%2) + L.
-  template <int RS>
-  __device__ static __forceinline__ f16x8 frag_tr(const uint16_t* t, int base, int ks, int lane) {
-    const int G = lane >> 4, L = lane & 15;
-    const int k = ks * 16 + 8 * (G >> 1) + (L >> 2);
-    const int c = base + 16 * (G & 1) + 4 * (L & 3);
-    const uint16_t* p = t + k * RS + ((c >> 3) ^ mc_swz<RS>(k)) * 8 + (c & 7);  // k + 4 swizzles alike
-    typedef __attribute__((address_space(3))) i16x4 lds_i16x4;
-    const i16x4 a = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_i16x4*)(p));
-    const i16x4 b = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_i16x4*)(p + 4 * RS));
-    const short v[8] = {a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]};
-    f16x8 r;
-    __builtin_memcpy(&r, v, 16);
-    return r;
   }
 };
 
@@ -344,23 +391,358 @@ struct Operand {
 // that LDS-DMA loads in flight write; without them every read waits for all loads.
 template <class C, bool AKC, bool BKC>
 __device__ __forceinline__ void read_frags(const uint16_t* __restrict__ as, const uint16_t* __restrict__ bs, int wm,
-                                           int wn, int ks, int lane, f16x8 (&fa)[C::TM], f16x8 (&fb)[C::TM]) {
+                                           int wn, int ks, int lane, f16x8 (&fa)[C::TM], f16x8 (&fb)[C::TN]) {
 #pragma unroll
-  for (int i = 0; i < C::TM; ++i) fa[i] = Operand<C, AKC>::frag(as, wm * C::WT + i * 32, ks, lane);
+  for (int i = 0; i < C::TM; ++i) fa[i] = Operand<C::BM, C::BK, AKC>::frag(as, wm * C::WM + i * 32, ks, lane);
 #pragma unroll
-  for (int j = 0; j < C::TM; ++j) fb[j] = Operand<C, BKC>::frag(bs, wn * C::WT + j * 32, ks, lane);
+  for (int j = 0; j < C::TN; ++j) fb[j] = Operand<C::BN, C::BK, BKC>::frag(bs, wn * C::WN + j * 32, ks, lane);
 }
 
-// Lower-triangle tile of index i in row order: (r, c) with c <= r.
+// Tile i of those that meet the lower triangle, in row order: row r of tiles
+// BM = R BN high has R (r + 1) of them.
+template <int R>
 __device__ __forceinline__ void tri_tile(int i, int& r, int& c) {
-  r = static_cast<int>((__builtin_sqrtf(8.0f * static_cast<float>(i) + 1.0f) - 1.0f) * 0.5f);
-  while (r * (r + 1) / 2 > i) --r;
-  while ((r + 1) * (r + 2) / 2 <= i) ++r;
-  c = i - r * (r + 1) / 2;
+  r = static_cast<int>((__builtin_sqrtf(8.0f / R * static_cast<float>(i) + 1.0f) - 1.0f) * 0.5f);
+  while (R * (r * (r + 1) / 2) > i) --r;
+  while (R * ((r + 1) * (r + 2) / 2) <= i) ++r;
+  c = i - R * (r * (r + 1) / 2);
 }
 
-template <class C, int KIND, bool AKC, bool BKC, bool SPLIT>
-__global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(C::BT == 256 ? 1 : 2)))
+// ---------------------------------------------------------------------------
+// Epilogue.  Each wave handles its WM x WN outputs in blocks of 32 rows, alone
+// (no barriers), through two buffers of its own in the ring's LDS.  A buffer
+// holds the block's hi and lo parts (32 rows of WN fp16 values each).  What the
+// epilogue reads of X or A comes by LDS-DMA, a block ahead, as whole row
+// pieces; the results go back into the same places and leave as whole row
+// pieces too, and for the symmetric outputs once more transposed.  (Straight
+// from registers, where a lane holds 16 bytes of its row at a time, the apply
+// launch of 128 matrices of 4096 x 1536 took 4.07 ms.)
+// ---------------------------------------------------------------------------
+
+// Chunk swizzle of a block's rows: free of conflicts for 16 consecutive rows at
+// one chunk (the accumulators' order) and for the transposing reads' 4 rows
+// times 2 chunks.
+template <int WT>
+__device__ __forceinline__ int ep_swz(int r) {
+  if constexpr (WT == 128) return ((r & 3) << 2) | ((r >> 2) & 3);
+  else if constexpr (WT == 64) return (((r >> 1) & 1) << 2) | ((r >> 2) & 3);
+  else return (r >> 2) & 3;
+}
+
+// A block's 8-bit lo part: rows of WT bytes, in 16-byte chunks (what LDS-DMA
+// moves) swizzled likewise.  lo8_at: the 8 bytes of columns 8 q .. 8 q + 7.
+template <int WT>
+__device__ __forceinline__ int lo8_swz(int r) {
+  return WT == 64 ? (r >> 2) & 3 : (r >> 3) & 1;
+}
+template <int WT>
+__device__ __forceinline__ uint2* lo8_at(uint16_t* lo, int r, int q) {
+  return reinterpret_cast<uint2*>(reinterpret_cast<uint8_t*>(lo) + r * WT + (((q >> 1) ^ lo8_swz<WT>(r)) * 16) +
+                                  (q & 1) * 8);
+}
+
+// LDS accesses of one wave are in order; this keeps the compiler's order too.
+__device__ __forceinline__ void wave_lds_fence() {
+  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+}
+
+// Linear combination that makes a stored value (times kS) from hi x, lo y of
+// the staged input and the accumulator v, per row or per column:
+//   gram   v' = kv v
+//   poly   o = (b + c (D_r + D_c)) (x + y) + kv v            (A A = O O + (D_r + D_c) O off the diagonal)
+//   apply  o = f ((a + D) x + (a + theta D) y + kv v)
+// (D: the diagonal in fp32; O: A without it.)  In apply the diagonal acts on
+// what the product saw of X: for pairs on all of it.  For hi-only products half
+// of lo measured best over full-rank and rank-deficient matrices (the product
+// leaves out B lo, which the diagonal's lo completes in part).
+template <class C, int KIND, bool SPLIT, bool BYROW>
+struct Coef {
+  static constexpr float kTheta = SPLIT ? 1.0f : 0.5f;
+  static constexpr float kLo = SPLIT ? 1.0f : 1.0f / kLoScale;  // stored lo to lo
+  static constexpr bool kCols = KIND == kPoly || (KIND == kApply && !BYROW);
+  float dr[C::TM];                                // at this lane's rows
+  float dc[kCols ? C::TN : 1][2][8];              // at its columns
+  float a, b, c, v, f;
+
+  __device__ __forceinline__ void init(const MmArgs& p, int64_t e, int mw, int nw, int lane) {
+    const float* cs = p.cs + e * (p.steps + 1) + p.step;
+    const int rl = lane & 31, g = lane >> 5;
+    a = p.ca;
+    b = p.cb;
+    c = p.cc;
+    f = KIND != kApply ? 1.0f : p.out == kOutX ? cs[0] / cs[1] : cs[0] / kS;
+    v = KIND == kGram ? cs[0] * cs[0] / kS : (KIND == kPoly ? p.cc : f) / kS;
+    if constexpr (KIND != kGram) {
+      const float* d = p.din + e * p.sd;
+#pragma unroll
+      for (int i = 0; i < C::TM; ++i) {
+        const int row = mw + 32 * i + rl;
+        dr[i] = (KIND == kPoly || BYROW) && row < p.M ? d[row] : 0.f;
+      }
+      if constexpr (kCols)
+#pragma unroll
+        for (int i = 0; i < C::TN; ++i)
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const int col = nw + 32 * i + 16 * h + 8 * g;
+#pragma unroll
+            for (int q = 0; q < 8; q += 4) {
+              const float4 t = col < p.N ? *reinterpret_cast<const float4*>(d + col + q) : make_float4(0.f, 0.f, 0.f, 0.f);
+              dc[i][h][q] = t.x;
+              dc[i][h][q + 1] = t.y;
+              dc[i][h][q + 2] = t.z;
+              dc[i][h][q + 3] = t.w;
+            }
+          }
+    }
+  }
+};
+
+// Block i: accumulators -> stored values, in place of the staged hi / lo.
+template <class C, int KIND, bool SPLIT, bool BYROW, bool FINAL, bool HASLO>
+__device__ __forceinline__ void epi_block(const f32x16 (&acc)[C::TN], uint16_t* __restrict__ hi,
+                                          uint16_t* __restrict__ lo, const Coef<C, KIND, SPLIT, BYROW>& k, int i,
+                                          int lane) {
+  using K = Coef<C, KIND, SPLIT, BYROW>;
+  const int rl = lane & 31, g = lane >> 5;
+  float ax = 0.f, ay = 0.f;  // coefficients of x and y where they go by rows
+  if constexpr (KIND == kPoly) ax = k.b + k.c * k.dr[i];
+  if constexpr (KIND == kApply && BYROW) {
+    ax = k.f * (k.a + k.dr[i]);
+    ay = k.f * (k.a + K::kTheta * k.dr[i]) * K::kLo;
+  }
+#pragma unroll
+  for (int j = 0; j < C::TN; ++j) {
+    float v[2][8];
+    to_chunks(acc[j], v);
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int at = rl * C::WN + ((4 * j + 2 * h + g) ^ ep_swz<C::WN>(rl)) * 8;
+      f16x8 x, ys;
+      float y[8];
+      uint2* const at8 = lo8_at<C::WN>(lo, rl, 4 * j + 2 * h + g);
+      if constexpr (KIND != kGram) x = *reinterpret_cast<const f16x8*>(hi + at);
+      if constexpr (HASLO && SPLIT) ys = *reinterpret_cast<const f16x8*>(lo + at);
+      if constexpr (HASLO && !SPLIT) {
+        typedef unsigned u32x2 __attribute__((ext_vector_type(2)));
+        const u32x2 t = *reinterpret_cast<const u32x2*>(at8);
+        lo_fp8(make_uint2(t[0], t[1]), y);
+      } else if constexpr (HASLO) {
+#pragma unroll
+        for (int q = 0; q < 8; ++q) y[q] = static_cast<float>(ys[q]);
+      }
+      float o[8];
+#pragma unroll
+      for (int q = 0; q < 8; ++q) {
+        o[q] = k.v * v[h][q];
+        if constexpr (KIND == kPoly) {
+          const float t = ax + k.c * k.dc[j][h][q];
+          o[q] += t * static_cast<float>(x[q]);
+          if constexpr (HASLO) o[q] += t * y[q];
+        } else if constexpr (KIND == kApply) {
+          if constexpr (!BYROW) {
+            ax = k.f * (k.a + k.dc[j][h][q]);
+            ay = k.f * (k.a + K::kTheta * k.dc[j][h][q]) * K::kLo;
+          }
+          o[q] += ax * static_cast<float>(x[q]);
+          if constexpr (HASLO) o[q] += ay * y[q];
+        }
+      }
+      if constexpr (FINAL) {  // fp32: the chunk's first half in hi's place, the second in lo's
+        lds_put16(hi + at, Elem<float>::pack(o));
+        lds_put16(lo + at, Elem<float>::pack(o + 4));
+      } else if constexpr (SPLIT) {
+        uint4 uh, ul;
+        split8(o, uh, ul);
+        lds_put16(hi + at, uh);
+        lds_put16(lo + at, ul);
+      } else if constexpr (KIND == kApply) {
+        uint4 uh;
+        uint2 ul;
+        split8_fp8(o, uh, ul);
+        lds_put16(hi + at, uh);
+        typedef unsigned u32x2 __attribute__((ext_vector_type(2)));
+        const u32x2 t = {ul.x, ul.y};
+        *reinterpret_cast<u32x2*>(at8) = t;
+      } else {
+        f16x8 r;
+#pragma unroll
+        for (int q = 0; q < 8; ++q) r[q] = static_cast<_Float16>(o[q]);
+        *reinterpret_cast<f16x8*>(hi + at) = r;
+      }
+    }
+  }
+}
+
+// The diagonal of a symmetric output within block i and its 32 columns j:
+// written in fp32, and zero in the matrix.
+template <class C, int KIND, bool SPLIT>
+__device__ __forceinline__ void epi_diagonal(const f32x16& acc, uint16_t* hi, uint16_t* lo,
+                                             const Coef<C, KIND, SPLIT, true>& k, int i, int j, float* dout,
+                                             bool in, int lane) {
+  const int rl = lane & 31, g = lane >> 5;
+  float v[2][8];
+  to_chunks(acc, v);
+  float t = 0.f;
+#pragma unroll
+  for (int h = 0; h < 2; ++h)
+#pragma unroll
+    for (int q = 0; q < 8; ++q) t = 16 * h + 8 * g + q == rl ? v[h][q] : t;
+  if (((rl >> 3) & 1) == g) {
+    float d = k.v * t / kS;  // poly: O's diagonal is zero
+    if constexpr (KIND == kPoly) d += k.dr[i] * (k.b + k.c * k.dr[i]);
+    if (in) *dout = d;
+    const int at = rl * C::WN + ((4 * j + (rl >> 3)) ^ ep_swz<C::WN>(rl)) * 8 + (rl & 7);
+    hi[at] = 0;
+    if constexpr (SPLIT) lo[at] = 0;
+  }
+}
+
+template <class C, int KIND, bool SPLIT, bool BYROW, bool FINAL, bool HASLO>
+__device__ __forceinline__ void epilogue(const f32x16 (&acc)[C::TM][C::TN], const MmArgs& p, uint16_t* lds, int64_t e,
+                                         int m0, int n0, int wm, int wn, int wave, int lane) {
+  constexpr int WN = C::WN, kPart = 32 * WN, CPR = WN / 8, RPI = 64 / CPR, kPieces = 32 / RPI;
+  constexpr bool kLo8 = KIND == kApply && !SPLIT;
+  constexpr int CPR8 = WN / 16, RPI8 = 64 / CPR8, kPieces8 = 32 / RPI8;  // the same for an 8-bit lo part
+  constexpr int kStage = kPieces + (HASLO ? (kLo8 ? kPieces8 : kPieces) : 0);
+  static_assert(WN == 64 || WN == 32, "row piece layouts");
+  static_assert(4 * 4 * kPart <= C::kLds, "two buffers of hi and lo per wave");
+  const int rl = lane & 31, g = lane >> 5;
+  const int mw = m0 + wm * C::WM, nw = n0 + wn * WN;  // this wave's outputs
+  const int64_t ob = e * p.so;
+  uint16_t* mine = lds + wave * 4 * kPart;
+  Coef<C, KIND, SPLIT, BYROW> k;
+  k.init(p, e, mw, nw, lane);
+
+  const int64_t eo = ob + static_cast<int64_t>(mw) * p.ldo + nw;
+  const int64_t left = mw < p.M && nw < p.N ? (static_cast<int64_t>(p.M - mw) * p.ldo - nw) * 2 : 0;
+  __amdgpu_buffer_rsrc_t rh, rlo;
+  if constexpr (KIND != kGram) rh = rsrc(p.eh + eo, left);
+  if constexpr (HASLO)
+    rlo = kLo8 ? rsrc(static_cast<const uint8_t*>(p.el) + eo, left / 2)
+               : rsrc(static_cast<const uint16_t*>(p.el) + eo, left);
+  // row pieces: piece u of a block is rows [u RPI, (u + 1) RPI), 16 bytes per lane; the
+  // swizzle's column term repeats every 16 rows
+  const int pr = lane / CPR, pr8 = lane / CPR8;
+  auto piece_col = [&](int u) { return ((lane % CPR) ^ ep_swz<WN>(u * RPI + pr)) * 8; };
+  auto stage = [&](int i) {
+    uint16_t* b = mine + (i & 1) * 2 * kPart;
+#pragma unroll
+    for (int u = 0; u < kPieces; ++u) {
+      const int voff = ((32 * i + u * RPI + pr) * p.ldo + piece_col(u)) * 2;
+      dma16(rh, b + u * 512, voff);
+      if constexpr (HASLO && !kLo8) dma16(rlo, b + kPart + u * 512, voff);
+    }
+    if constexpr (HASLO && kLo8)
+#pragma unroll
+      for (int u = 0; u < kPieces8; ++u) {
+        const int r = u * RPI8 + pr8;
+        dma16(rlo, b + kPart + u * 512, (32 * i + r) * p.ldo + ((lane % CPR8) ^ lo8_swz<WN>(r)) * 16);
+      }
+  };
+  // symmetric outputs, in squares of BN = WM: above the diagonal there is nothing
+  // to do, squares on it are computed whole, those below are written twice
+  const bool below = KIND != kApply && mw / C::BN > nw / C::BN;
+  __syncthreads();  // the ring is no longer read
+  if (KIND != kApply && mw / C::BN < nw / C::BN) return;
+  if constexpr (KIND != kGram) {
+    stage(0);
+    if constexpr (C::TM > 1) stage(1);
+  }
+#pragma unroll
+  for (int i = 0; i < C::TM; ++i) {
+    uint16_t* hi = mine + (i & 1) * 2 * kPart;
+    uint16_t* lo = hi + kPart;
+    if constexpr (KIND != kGram) {  // block i has landed; block i + 1 may be in flight
+      if (i + 1 < C::TM) wait_vm<kStage>();
+      else wait_vm<0>();
+    }
+    epi_block<C, KIND, SPLIT, BYROW, FINAL, HASLO>(acc[i], hi, lo, k, i, lane);
+    if constexpr (KIND != kApply) {
+      const int row = mw + 32 * i + rl;
+#pragma unroll
+      for (int j = 0; j < C::TN; ++j)
+        if (mw + 32 * i == nw + 32 * j) {
+          wave_lds_fence();
+          epi_diagonal<C, KIND, SPLIT>(acc[i][j], hi, lo, k, i, j, p.dout + e * p.sd + row, row < p.M, lane);
+        }
+    }
+    wave_lds_fence();
+    if constexpr (FINAL) {
+      using T = typename std::conditional<SPLIT, float, uint16_t>::type;
+#pragma unroll 1
+      for (int u = 0; u < kPieces; ++u) {
+        float o[8];
+        Elem<float>::unpack(lds_get16(hi + u * 512 + lane * 8), o);
+        Elem<float>::unpack(lds_get16(lo + u * 512 + lane * 8), o + 4);
+        const int orow = mw + 32 * i + u * RPI + pr, col = nw + piece_col(u);
+        if (orow < p.rows && col < p.cols) {
+          const int64_t off = (e * p.rows + orow) * p.cols + col;
+          const int n = p.cols - col;
+          if (p.out == kOutW) {
+            float w[8];
+            ld8(static_cast<const T*>(p.w) + off, n, w);
+#pragma unroll
+            for (int q = 0; q < 8; ++q) o[q] = p.keep * w[q] - p.gain * o[q];
+          }
+          st8(static_cast<T*>(p.o) + off, n, o);
+        }
+      }
+    } else {
+#pragma unroll
+      for (int u = 0; u < kPieces; ++u) {
+        const int orow = 32 * i + u * RPI + pr, col = piece_col(u);
+        const uint4 vh = lds_get16(hi + u * 512 + lane * 8);
+        uint4 vl;
+        if constexpr (SPLIT) vl = lds_get16(lo + u * 512 + lane * 8);
+        if (mw + orow < p.M && nw + col < p.N) {
+          const int64_t off = eo + orow * p.ldo + col;
+          *reinterpret_cast<uint4*>(p.oh + off) = vh;
+          if constexpr (SPLIT) *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.ol) + off) = vl;
+        }
+      }
+      if (kLo8 && p.ol)
+#pragma unroll
+        for (int u = 0; u < kPieces8; ++u) {
+          const int r = u * RPI8 + pr8, orow = 32 * i + r, col = ((lane % CPR8) ^ lo8_swz<WN>(r)) * 16;
+          const uint4 vl = lds_get16(lo + u * 512 + lane * 8);
+          if (mw + orow < p.M && nw + col < p.N)
+            *reinterpret_cast<uint4*>(static_cast<uint8_t*>(p.ol) + eo + orow * p.ldo + col) = vl;
+        }
+    }
+    if constexpr (KIND != kApply) {
+      if (below) {  // the mirror image: 8 of the block's rows at one column per lane
+        auto swz = [](int r) { return ep_swz<WN>(r); };
+        const int64_t mo = ob + static_cast<int64_t>(nw + rl) * p.ldo + mw + 8 * g;
+#pragma unroll
+        for (int t = 0; t < WN / 32 * 2; ++t) {
+          const int cb = (t >> 1) * 32, ks = t & 1;
+          const f16x8 vh = frag_tr<WN>(hi, cb, ks, lane, swz);
+          f16x8 vl;
+          if constexpr (SPLIT) vl = frag_tr<WN>(lo, cb, ks, lane, swz);
+          if (nw + cb + rl < p.N && mw + 32 * i + ks * 16 + 8 * g < p.M) {
+            const int64_t off = mo + cb * p.ldo + 32 * i + ks * 16;
+            *reinterpret_cast<uint4*>(p.oh + off) = __builtin_bit_cast(uint4, vh);
+            if constexpr (SPLIT)
+              *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.ol) + off) = __builtin_bit_cast(uint4, vl);
+          }
+        }
+      }
+    }
+    wave_lds_fence();
+    if constexpr (KIND != kGram)
+      if (i + 2 < C::TM) {
+        __builtin_amdgcn_s_waitcnt(0xC07F);  // lgkmcnt(0): the buffer has been read out
+        stage(i + 2);
+      }
+  }
+}
+
+// FINAL: apply's last step, which writes the result instead of the next X.
+template <class C, int KIND, bool AKC, bool BKC, bool SPLIT, bool FINAL>
+__global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2)))
 void orth_mm_kernel(MmArgs p) {
   __shared__ __attribute__((aligned(16))) uint16_t lds[C::kLds];
   const int tid = threadIdx.x, lane = tid & 63;
@@ -377,29 +759,33 @@ void orth_mm_kernel(MmArgs p) {
     if (p.tm <= p.tn) { c = t / p.tm; r = t - c * p.tm; }
     else { r = t / p.tn; c = t - r * p.tn; }
   } else {
-    tri_tile(t, r, c);
+    tri_tile<C::BM / C::BN>(t, r, c);
   }
-  const int m0 = __builtin_amdgcn_readfirstlane(r * C::BT), n0 = __builtin_amdgcn_readfirstlane(c * C::BT);
+  const int m0 = __builtin_amdgcn_readfirstlane(r * C::BM), n0 = __builtin_amdgcn_readfirstlane(c * C::BN);
 
-  Operand<C, AKC> A;
-  Operand<C, BKC> B;
+  Operand<C::BM, C::BK, AKC> A;
+  Operand<C::BN, C::BK, BKC> B;
   A.init(p.ah + e * p.sa, SPLIT ? p.al + e * p.sa : nullptr, p.lda, m0, p.M, p.K, wave, lane);
   B.init(p.bh + e * p.sb, SPLIT ? p.bl + e * p.sb : nullptr, p.ldb, n0, p.N, p.K, wave, lane);
   const int nk1 = (p.K + C::BK - 1) / C::BK;
   const int nk = SPLIT ? 3 * nk1 : nk1;  // hi hi, hi lo, lo hi
-  auto issue = [&](int kt) {
-    uint16_t* dst = lds + (kt % C::kRing) * 2 * C::kOp;
-    const int part = SPLIT ? (kt >= nk1) + (kt >= 2 * nk1) : 0;
-    const int k = kt - part * nk1;
+  int head = 0;  // K step to load next, and its ring slot
+  int head_slot = 0;
+  auto issue = [&]() {
+    uint16_t* dst = lds + head_slot * C::kSlot;
+    const int part = SPLIT ? (head >= nk1) + (head >= 2 * nk1) : 0;
+    const int k = head - part * nk1;
     A.issue(SPLIT && part == 2, k * A.kstep, dst, wave);
-    B.issue(SPLIT && part == 1, k * B.kstep, dst + C::kOp, wave);
+    B.issue(SPLIT && part == 1, k * B.kstep, dst + C::kA, wave);
+    ++head;
+    head_slot = head_slot + 1 == C::kRing ? 0 : head_slot + 1;
   };
 
-  f32x16 acc[C::TM][C::TM];
+  f32x16 acc[C::TM][C::TN];
 #pragma unroll
   for (int i = 0; i < C::TM; ++i)
 #pragma unroll
-    for (int j = 0; j < C::TM; ++j)
+    for (int j = 0; j < C::TN; ++j)
 #pragma unroll
       for (int q = 0; q < 16; ++q) acc[i][j][q] = 0.f;
 
@@ -408,164 +794,55 @@ void orth_mm_kernel(MmArgs p) {
   // there the waves meet, the next step's loads are known to have landed, and the
   // step's own ring slot is free for the loads of step kt + kRing.
   constexpr int NS = C::BK / 16;
-  constexpr int kLoads2 = 2 * C::kLoads;
-  f16x8 fa[2][C::TM], fb[2][C::TM];
-  auto read = [&](int kt, int ks, int buf) {
-    const uint16_t* as = lds + (kt % C::kRing) * 2 * C::kOp;
-    read_frags<C, AKC, BKC>(as, as + C::kOp, wm, wn, ks, lane, fa[buf], fb[buf]);
+  static_assert(NS % 2 == 0, "slice buffers alternate");
+  f16x8 fa[2][C::TM], fb[2][C::TN];
+  auto read = [&](int slot, int ks, int buf) {
+    const uint16_t* as = lds + slot * C::kSlot;
+    read_frags<C, AKC, BKC>(as, as + C::kA, wm, wn, ks, lane, fa[buf], fb[buf]);
   };
+  // a wave whose outputs lie above the diagonal only helps with the loads
+  const bool idle = KIND != kApply && (m0 + wm * C::WM) / C::BN < (n0 + wn * C::WN) / C::BN;
   auto mma = [&](int buf) {
+    if (KIND != kApply && idle) return;
 #pragma unroll
     for (int i = 0; i < C::TM; ++i)
 #pragma unroll
-      for (int j = 0; j < C::TM; ++j)
+      for (int j = 0; j < C::TN; ++j)
         acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(fb[buf][j], fa[buf][i], acc[i][j], 0, 0, 0);
   };
-  // at most `ahead` steps' loads outstanding
-  auto wait_ahead = [&](int ahead) {
-    if (ahead >= 2) wait_vm<2 * kLoads2>();
-    else if (ahead == 1) wait_vm<kLoads2>();
-    else wait_vm<0>();
-  };
-  for (int s = 0; s < C::kRing && s < nk; ++s) issue(s);
-  if (nk >= C::kRing) wait_vm<3 * kLoads2>();
+  for (int s = 0; s < C::kRing && s < nk; ++s) issue();
+  if (nk >= C::kRing) wait_vm<(C::kRing - 1) * C::kLoads>();
   else wait_vm<0>();
   __syncthreads();
   read(0, 0, 0);
+  int slot = 0;
   for (int kt = 0; kt < nk; ++kt) {
+    const int next = slot + 1 == C::kRing ? 0 : slot + 1;
 #pragma unroll
     for (int ks = 0; ks < NS; ++ks) {
       if (ks + 1 < NS) {
-        read(kt, ks + 1, (ks + 1) & 1);
+        read(slot, ks + 1, (ks + 1) & 1);
       } else if (kt + 1 < nk) {
-        wait_ahead(nk - 2 - kt);
+        const int ahead = nk - 2 - kt;  // steps whose loads may stay outstanding
+        if (ahead >= C::kRing - 2) wait_vm<(C::kRing - 2) * C::kLoads>();
+        else if (C::kRing > 3 && ahead == 1) wait_vm<C::kLoads>();
+        else wait_vm<0>();
         __syncthreads();
-        if (kt + C::kRing < nk) issue(kt + C::kRing);
-        read(kt + 1, 0, 0);
+        if (head < nk) issue();
+        read(next, 0, 0);
       }
       mma(ks & 1);
     }
+    slot = next;
   }
-  static_assert(NS % 2 == 0, "slice buffers alternate");
-
-  // ---- epilogue: 8-column chunks of one row per lane
-  const float* cs = p.cs + e * (p.steps + 1) + p.step;
-  const float ci = cs[0], cn = cs[1];
-  const int64_t ob = e * p.so;
-  const bool mirror = KIND != kApply && m0 != n0;
-  if (mirror) __syncthreads();  // the ring's LDS becomes the mirror tile
-  const int rl = lane & 31, hc = 8 * (lane >> 5);
-  auto finish = [&](int i, int j, int cch, const float* v, float* o) {  // the stored (scaled) values of a chunk
-    const int row = m0 + wm * C::WT + i * 32 + rl, col = n0 + wn * C::WT + j * 32 + 16 * cch + hc;
-    if constexpr (KIND == kGram) {
-      const float f = ci * ci / kS;
-#pragma unroll
-      for (int q = 0; q < 8; ++q) o[q] = v[q] * f;
-    } else {
-      float x[8];
-#pragma unroll
-      for (int q = 0; q < 8; ++q) x[q] = 0.f;
-      if (row < p.M && col < p.N) {
-        const int64_t off = ob + static_cast<int64_t>(row) * p.ldo + col;
-        add8(*reinterpret_cast<const uint4*>(p.eh + off), x);
-        if (SPLIT || KIND == kApply) add8(*reinterpret_cast<const uint4*>(p.el + off), x);
-      }
-      const float fx = KIND == kPoly ? p.cb : p.ca, fv = (KIND == kPoly ? p.cc : 1.0f) / kS;
-#pragma unroll
-      for (int q = 0; q < 8; ++q) o[q] = fx * x[q] + fv * v[q];
-    }
-  };
-  if constexpr (KIND == kApply) {
-    const float f = p.out == kOutX ? ci / cn : ci / kS;
-#pragma unroll
-    for (int i = 0; i < C::TM; ++i)
-#pragma unroll
-      for (int j = 0; j < C::TM; ++j) {
-        float v[2][8];
-        to_chunks(acc[i][j], v);
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const int row = m0 + wm * C::WT + i * 32 + rl, col = n0 + wn * C::WT + j * 32 + 16 * h + hc;
-          float o[8];
-          finish(i, j, h, v[h], o);
-#pragma unroll
-          for (int q = 0; q < 8; ++q) o[q] *= f;
-          if (p.out == kOutX) {
-            if (row < p.M && col < p.N) {
-              uint4 hi, lo;
-              split8(o, hi, lo);
-              const int64_t off = ob + static_cast<int64_t>(row) * p.ldo + col;
-              *reinterpret_cast<uint4*>(p.oh + off) = hi;
-              *reinterpret_cast<uint4*>(p.ol + off) = lo;
-            }
-          } else if (row < p.rows && col < p.cols) {
-            using T = typename std::conditional<SPLIT, float, uint16_t>::type;
-            const int64_t off = (e * p.rows + row) * p.cols + col;
-            const int n = p.cols - col;
-            if (p.out == kOutW) {
-              float w[8];
-              ld8(static_cast<const T*>(p.w) + off, n, w);
-#pragma unroll
-              for (int q = 0; q < 8; ++q) o[q] = p.keep * w[q] - p.gain * o[q];
-            }
-            st8(static_cast<T*>(p.o) + off, n, o);
-          }
-        }
-      }
-  } else {
-    // symmetric outputs: the tile, and its mirror image through LDS (row-major
-    // there, read back with the transposing reads)
-    uint4 keep_lo[SPLIT ? C::TM : 1][SPLIT ? C::TM : 1][2];
-#pragma unroll
-    for (int i = 0; i < C::TM; ++i)
-#pragma unroll
-      for (int j = 0; j < C::TM; ++j) {
-        float v[2][8];
-        to_chunks(acc[i][j], v);
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const int rr = wm * C::WT + i * 32 + rl, cc = wn * C::WT + j * 32 + 16 * h + hc;
-          float o[8];
-          finish(i, j, h, v[h], o);
-          uint4 hi, lo;
-          split8(o, hi, lo);
-          if (m0 + rr < p.M && n0 + cc < p.N) {
-            const int64_t off = ob + static_cast<int64_t>(m0 + rr) * p.ldo + n0 + cc;
-            *reinterpret_cast<uint4*>(p.oh + off) = hi;
-            if constexpr (SPLIT) *reinterpret_cast<uint4*>(p.ol + off) = lo;
-          }
-          if (mirror) lds_put16(lds + rr * C::BT + ((cc >> 3) ^ mc_swz<C::BT>(rr)) * 8, hi);
-          if constexpr (SPLIT) keep_lo[i][j][h] = lo;
-        }
-      }
-    if (mirror) {
-      auto flush = [&](uint16_t* out) {
-        __syncthreads();
-        for (int i = wave; i < (C::BT / 32) * (C::BT / 16); i += 4) {
-          const int cb = (i % (C::BT / 32)) * 32, ks = i / (C::BT / 32);
-          const f16x8 v = Operand<C, false>::template frag_tr<C::BT>(lds, cb, ks, lane);
-          const int row = n0 + cb + rl, col = m0 + ks * 16 + hc;
-          if (row < p.N && col < p.M)
-            *reinterpret_cast<uint4*>(out + ob + static_cast<int64_t>(row) * p.ldo + col) =
-                __builtin_bit_cast(uint4, v);
-        }
-      };
-      flush(p.oh);
-      if constexpr (SPLIT) {
-        __syncthreads();
-#pragma unroll
-        for (int i = 0; i < C::TM; ++i)
-#pragma unroll
-          for (int j = 0; j < C::TM; ++j)
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              const int rr = wm * C::WT + i * 32 + rl, cc = wn * C::WT + j * 32 + 16 * h + hc;
-              lds_put16(lds + rr * C::BT + ((cc >> 3) ^ mc_swz<C::BT>(rr)) * 8, keep_lo[i][j][h]);
-            }
-        flush(p.ol);
-      }
-    }
-  }
+  if constexpr (KIND != kApply)
+    epilogue<C, KIND, SPLIT, true, false, KIND == kPoly && SPLIT>(acc, p, lds, e, m0, n0, wm, wn, wave, lane);
+  else if constexpr (SPLIT || FINAL)
+    epilogue<C, KIND, SPLIT, !BKC, FINAL, SPLIT>(acc, p, lds, e, m0, n0, wm, wn, wave, lane);
+  else if (p.el)
+    epilogue<C, KIND, SPLIT, !BKC, FINAL, true>(acc, p, lds, e, m0, n0, wm, wn, wave, lane);
+  else
+    epilogue<C, KIND, SPLIT, !BKC, FINAL, false>(acc, p, lds, e, m0, n0, wm, wn, wave, lane);
 }
 
 // ---------------------------------------------------------------------------
@@ -594,13 +871,14 @@ Sizes sizes_of(int E, int rows, int cols, bool split) {
 
 struct Ws {
   double* part;
-  float* cs;
-  uint16_t *xh[2], *xl[2], *ah, *al, *bh, *bl;
+  float *cs, *da, *db;  // scales; diagonals of A and B
+  uint16_t *xh[2], *ah, *al, *bh, *bl;
+  void* xl[2];
 };
 
-// X as two buffers of pairs (a product reads one and writes the other; without
-// split operands lo is only read where it is written, so one buffer serves), A
-// and B (pairs when split).
+// X as two buffers (a product reads one and writes the other), with its lo parts
+// (without split operands in 8 bits, and read only where it is written: one
+// buffer serves); A and B (pairs when split).
 size_t ws_layout(const Sizes& z, char* base, Ws* w) {
   size_t o = 0;
   auto take = [&](size_t bytes) {
@@ -611,10 +889,12 @@ size_t ws_layout(const Sizes& z, char* base, Ws* w) {
   Ws t;
   t.part = reinterpret_cast<double*>(take(static_cast<size_t>(z.E) * z.chunks * 8));
   t.cs = reinterpret_cast<float*>(take(static_cast<size_t>(z.E) * (kMaxSteps + 1) * 4));
+  t.da = reinterpret_cast<float*>(take(static_cast<size_t>(z.E) * z.mp * 4));
+  t.db = reinterpret_cast<float*>(take(static_cast<size_t>(z.E) * z.mp * 4));
   const size_t xb = static_cast<size_t>(z.E) * z.x * 2, ab = static_cast<size_t>(z.E) * z.a * 2;
   t.xh[0] = take(xb);
   t.xh[1] = take(xb);
-  t.xl[0] = take(xb);
+  t.xl[0] = take(z.split ? xb : xb / 2);
   t.xl[1] = z.split ? take(xb) : t.xl[0];
   t.ah = take(ab);
   t.bh = take(ab);
@@ -627,15 +907,24 @@ size_t ws_layout(const Sizes& z, char* base, Ws* w) {
 template <class C, int KIND, bool AKC, bool BKC>
 void launch_mm(const char* name, const MmArgs& a, bool split, hipStream_t s) {
   const dim3 grid(xcd_grid(a.tiles));
-  if (split) MOE_LAUNCH(name, (orth_mm_kernel<C, KIND, AKC, BKC, true>), grid, dim3(256), 0, s, a);
-  else MOE_LAUNCH(name, (orth_mm_kernel<C, KIND, AKC, BKC, false>), grid, dim3(256), 0, s, a);
+  const bool last = KIND == kApply && a.out != kOutX;
+  auto go = [&](auto sp, auto fin) {
+    MOE_LAUNCH(name, (orth_mm_kernel<C, KIND, AKC, BKC, decltype(sp)::value, decltype(fin)::value>), grid, dim3(256),
+               0, s, a);
+  };
+  constexpr std::integral_constant<bool, KIND == kApply> fin{};
+  constexpr std::false_type no{};
+  if (split) last ? go(std::true_type{}, fin) : go(std::true_type{}, no);
+  else last ? go(std::false_type{}, fin) : go(std::false_type{}, no);
 }
 
 template <class C>
-void run_products(const Sizes& z, const Ws& w, MmArgs a, const float (*coef)[3], int out, hipStream_t s) {
-  const int64_t nm = cdiv(z.mp, C::BT), sym = nm * (nm + 1) / 2;
-  const int64_t nr = cdiv(z.rp, C::BT), nc = cdiv(z.cp, C::BT);
+void run_products(const Sizes& z, const Ws& w, MmArgs a, const float (*coef)[3], int out, bool exact0,
+                  hipStream_t s) {
+  const int64_t nm = cdiv(z.mp, C::BM), sym = C::BM / C::BN * nm * (nm + 1) / 2;
+  const int64_t nr = cdiv(z.rp, C::BM), nc = cdiv(z.cp, C::BN);
   a.cs = w.cs;
+  a.sd = z.mp;
   for (int i = 0; i < a.steps; ++i) {
     const int cur = i & 1, nxt = cur ^ 1;
     a.step = i;
@@ -645,7 +934,7 @@ void run_products(const Sizes& z, const Ws& w, MmArgs a, const float (*coef)[3],
     a.out = kOutX;
     // Gram: the shorter side's inner products
     a.ah = a.bh = w.xh[cur];
-    a.al = a.bl = w.xl[cur];
+    a.al = a.bl = static_cast<const uint16_t*>(w.xl[cur]);  // read with split operands only, like the other lo operands
     a.sa = a.sb = z.x;
     a.lda = a.ldb = z.cp;
     a.K = z.tall ? z.rp : z.cp;
@@ -655,17 +944,20 @@ void run_products(const Sizes& z, const Ws& w, MmArgs a, const float (*coef)[3],
     a.tiles = sym * z.E;
     a.oh = w.ah;
     a.ol = w.al;
+    a.dout = w.da;
     a.so = z.a;
     a.ldo = z.mp;
     if (z.tall) launch_mm<C, kGram, false, false>("orth_gram", a, z.split, s);
     else launch_mm<C, kGram, true, true>("orth_gram", a, z.split, s);
     // polynomial
     a.ah = a.bh = a.eh = w.ah;
-    a.al = a.bl = a.el = w.al;
+    a.el = a.al = a.bl = w.al;
     a.sa = a.sb = z.a;
     a.lda = a.ldb = a.K = z.mp;
     a.oh = w.bh;
     a.ol = w.bl;
+    a.din = w.da;
+    a.dout = w.db;
     launch_mm<C, kPoly, true, true>("orth_poly", a, z.split, s);
     // apply
     a.M = z.rp;
@@ -674,15 +966,18 @@ void run_products(const Sizes& z, const Ws& w, MmArgs a, const float (*coef)[3],
     a.tn = static_cast<int>(nc);
     a.tiles = nr * nc * z.E;
     a.eh = w.xh[cur];
-    a.el = w.xl[cur];
+    // without split operands the last step does without X's lo part (noise in it
+    // is multiplied by a once more only), and the first of a bf16 gradient has none
+    a.el = !z.split && (i + 1 == a.steps || (i == 0 && exact0)) ? nullptr : w.xl[cur];
+    a.din = w.db;
     a.oh = w.xh[nxt];
-    a.ol = w.xl[nxt];
+    a.ol = !z.split && i + 2 >= a.steps ? nullptr : w.xl[nxt];
     a.so = z.x;
     a.ldo = z.cp;
     a.out = i + 1 < a.steps ? static_cast<int>(kOutX) : out;
     if (z.tall) {  // X B, B symmetric
       a.ah = w.xh[cur];
-      a.al = w.xl[cur];
+      a.al = static_cast<const uint16_t*>(w.xl[cur]);
       a.sa = z.x;
       a.lda = z.cp;
       a.bh = w.bh;
@@ -696,7 +991,7 @@ void run_products(const Sizes& z, const Ws& w, MmArgs a, const float (*coef)[3],
       a.sa = z.a;
       a.lda = z.mp;
       a.bh = w.xh[cur];
-      a.bl = w.xl[cur];
+      a.bl = static_cast<const uint16_t*>(w.xl[cur]);
       a.sb = z.x;
       a.ldb = z.cp;
       launch_mm<C, kApply, true, false>("orth_apply", a, z.split, s);
@@ -806,7 +1101,10 @@ int run(const void* g, int dtype, int E, int rows, int cols, int steps, const fl
   pre.part = w.part;
   pre.cs = w.cs;
   pre.xh = w.xh[0];
-  pre.xl = w.xl[0];
+  // a bf16 gradient has its 8 mantissa bits in hi (its smallest elements, below
+  // 2^-26 of the norm, lose bits far below the result's accuracy)
+  const bool exact0 = !z.split && (!st.mom || steps == 1);
+  pre.xl = exact0 ? nullptr : w.xl[0];
   pre.rows = rows;
   pre.cols = cols;
   pre.rp = z.rp;
@@ -832,8 +1130,8 @@ int run(const void* g, int dtype, int E, int rows, int cols, int steps, const fl
   a.gain = st.gain;
   const int kind = st.w ? kOutW : kOutO;
   const int64_t big = cdiv(z.rp, 256) * cdiv(z.cp, 256) * E;
-  if (big >= 256) run_products<Tile<256, 32>>(z, w, a, plan.coef, kind, s);
-  else run_products<Tile<128, 32>>(z, w, a, plan.coef, kind, s);
+  if (big >= 256) run_products<Tile<256, 128, 32, 3>>(z, w, a, plan.coef, kind, exact0, s);
+  else run_products<Tile<128, 128, 32, 4>>(z, w, a, plan.coef, kind, exact0, s);
   return launch_status();
 }
 
