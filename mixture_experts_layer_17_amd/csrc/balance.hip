@@ -268,6 +268,9 @@ __global__ __launch_bounds__(kSumThreads) void balance_sum_kernel(FwdArgs a) {
   __shared__ int s_c[G][kCols + 1], s_i[W], s_last;
   const int tid = threadIdx.x, cl = tid % kCols, g = tid / kCols, E = a.E;
   const int e = blockIdx.x * kCols + cl;
+  // partials cross workgroups as device-scope atomics, ordered by waiting for the
+  // stores: a device-scope fence would write back a whole L2 per workgroup
+  auto st = [](float* p, float v) { __hip_atomic_store(p, v, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT); };
   for (int64_t s = blockIdx.y; s < a.S; s += gridDim.y) {
     const int64_t lo = seq_at(a.seq, s, a.S, a.T), hi = seq_at(a.seq, s + 1, a.S, a.T);
     const int64_t f = lo < hi ? lo / kTok + s : 0, end = lo < hi ? (hi - 1) / kTok + s + 1 : 0;
@@ -315,19 +318,18 @@ __global__ __launch_bounds__(kSumThreads) void balance_sum_kernel(FwdArgs a) {
       }
 #pragma unroll
       for (int o = kCols / 2; o >= 1; o >>= 1) term += __shfl_xor(term, o, 64);
-      if (cl == 0) a.ws.bal[s * gridDim.x + blockIdx.x] = term;
+      if (cl == 0) st(a.ws.bal + s * gridDim.x + blockIdx.x, term);
       if (cl == 0 && blockIdx.x == 0) {
-        a.norm[2 + s] = static_cast<float>(n);
-        a.ws.zs[s] = z;
+        st(a.norm + 2 + s, static_cast<float>(n));
+        st(a.ws.zs + s, z);
       }
     }
     __syncthreads();
   }
-  if (tid == 0) {  // releases this workgroup's partials, acquires the others'
-    __threadfence();
+  __builtin_amdgcn_s_waitcnt(0x0F70);  // vmcnt(0): thread 0 wrote this workgroup's partials
+  if (tid == 0) {
     const int total = static_cast<int>(gridDim.x * gridDim.y);
-    s_last = __hip_atomic_fetch_add(a.ws.ticket, 1, __ATOMIC_ACQ_REL, __HIP_MEMORY_SCOPE_AGENT) == total - 1;
-    __threadfence();
+    s_last = __hip_atomic_fetch_add(a.ws.ticket, 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) == total - 1;
   }
   __syncthreads();
   if (!s_last) return;

@@ -71,17 +71,16 @@ __device__ __forceinline__ void split8(const float* v, uint4& hi, uint4& lo) {
   lo = __builtin_bit_cast(uint4, l);
 }
 
-// The same with lo in 8 bits (E4M3, times 16: a hi of up to 15 kS leaves at most
-// 16, and steps of 2^-13 are far below what lo has to carry).
-constexpr float kLoScale = 16.0f;
+// The same with lo in 8 bits: E4M3, times a power of two `scale` that takes the
+// largest possible lo (2^-11 of a value, see make_plan) to at most 448.
 typedef float f32x2 __attribute__((ext_vector_type(2)));
-__device__ __forceinline__ void split8_fp8(const float* v, uint4& hi, uint2& lo) {
+__device__ __forceinline__ void split8_fp8(const float* v, float scale, uint4& hi, uint2& lo) {
   f16x8 h;
   float l[8];
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
     h[i] = static_cast<_Float16>(v[i]);
-    l[i] = (v[i] - static_cast<float>(h[i])) * kLoScale;
+    l[i] = (v[i] - static_cast<float>(h[i])) * scale;
   }
   hi = __builtin_bit_cast(uint4, h);
   int a = 0, b = 0;
@@ -149,8 +148,10 @@ struct PreArgs {
   float* cs;          // [E][steps + 1]
   uint16_t* xh;       // [E][rp][cp]
   void* xl;           // lo: fp16 for fp32 gradients, else 8 bits; nullptr: not needed
+  int32_t* ticket;    // zeroed here
+  int tickets;        // per matrix
   int rows, cols, rp, cp, chunks, steps;
-  float eps, growth[kMaxSteps];
+  float eps, lo_scale, growth[kMaxSteps];
 };
 
 template <class T, bool MOM>
@@ -225,6 +226,8 @@ __global__ __launch_bounds__(kNormThreads) void orth_scale_kernel(PreArgs a) {
       cs[i + 1] = static_cast<float>(c);
     }
   }
+  if (blockIdx.x == 0)
+    for (int i = threadIdx.x; i < a.tickets; i += kNormThreads) a.ticket[e * a.tickets + i] = 0;
   const int64_t n = static_cast<int64_t>(a.rows) * a.cols;
   const int64_t np = static_cast<int64_t>(a.rp) * a.cp;
   const int cv = a.cp / 8;
@@ -252,7 +255,7 @@ __global__ __launch_bounds__(kNormThreads) void orth_scale_kernel(PreArgs a) {
       *reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.xl) + o) = lo;
     } else {
       uint2 lo;
-      split8_fp8(u, hi, lo);
+      split8_fp8(u, a.lo_scale, hi, lo);
       if (a.xl) *reinterpret_cast<uint2*>(static_cast<uint8_t*>(a.xl) + o) = lo;
     }
     *reinterpret_cast<uint4*>(a.xh + o) = hi;
@@ -282,18 +285,25 @@ struct MmArgs {
   const float* cs;
   int steps, step, out;
   float ca, cb, cc;                   // the step's coefficients
+  float lo_scale;
   // result / weight
   void* o;
   const void* w;
   int rows, cols;
   float keep, gain;                   // w' = keep w - gain O
+  // K split over `ks` workgroups per tile (symmetric kinds on the smallest tiles)
+  int ks;
+  float* part;                        // [tile][ks] accumulators
+  int32_t* ticket;                    // [tile], zero before and after a launch
 };
 
 // BM x BN outputs per workgroup by 2 x 2 waves of WM x WN; K step BK; a ring of
-// kRing K steps of both operands in LDS.
-template <int BM_, int BN_, int BK_, int RING_>
+// kRing K steps of both operands in LDS; fragments of KG 16-deep slices (a phase)
+// in registers at a time, twice.
+template <int BM_, int BN_, int BK_, int RING_, int KG_>
 struct Tile {
-  static constexpr int BM = BM_, BN = BN_, BK = BK_, kRing = RING_;
+  static constexpr int BM = BM_, BN = BN_, BK = BK_, kRing = RING_, KG = KG_;
+  static constexpr int kPhases = BK / 16 / KG;
   static constexpr int WM = BM / 2, WN = BN / 2, TM = WM / 32, TN = WN / 32;
   static constexpr int kA = BM * BK, kSlot = (BM + BN) * BK;  // elements: the A tile, then the B tile
   static constexpr int kLoads = kSlot / 512 / 4;              // LDS-DMA instructions per wave and step
@@ -441,6 +451,14 @@ __device__ __forceinline__ uint2* lo8_at(uint16_t* lo, int r, int q) {
                                   (q & 1) * 8);
 }
 
+// Barrier of the K loop: LDS accesses are ordered across it, the LDS-DMA loads in
+// flight are left alone (a full fence may wait for all of them).
+__device__ __forceinline__ void lds_barrier() {
+  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup", "local");
+  __builtin_amdgcn_s_barrier();
+  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
+}
+
 // LDS accesses of one wave are in order; this keeps the compiler's order too.
 __device__ __forceinline__ void wave_lds_fence() {
   __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
@@ -460,11 +478,10 @@ __device__ __forceinline__ void wave_lds_fence() {
 template <class C, int KIND, bool SPLIT, bool BYROW>
 struct Coef {
   static constexpr float kTheta = SPLIT ? 1.0f : 0.5f;
-  static constexpr float kLo = SPLIT ? 1.0f : 1.0f / kLoScale;  // stored lo to lo
   static constexpr bool kCols = KIND == kPoly || (KIND == kApply && !BYROW);
   float dr[C::TM];                                // at this lane's rows
   float dc[kCols ? C::TN : 1][2][8];              // at its columns
-  float a, b, c, v, f;
+  float a, b, c, v, f, lo_scale, lo_inv;
 
   __device__ __forceinline__ void init(const MmArgs& p, int64_t e, int mw, int nw, int lane) {
     const float* cs = p.cs + e * (p.steps + 1) + p.step;
@@ -472,6 +489,8 @@ struct Coef {
     a = p.ca;
     b = p.cb;
     c = p.cc;
+    lo_scale = p.lo_scale;
+    lo_inv = SPLIT ? 1.0f : 1.0f / p.lo_scale;
     f = KIND != kApply ? 1.0f : p.out == kOutX ? cs[0] / cs[1] : cs[0] / kS;
     v = KIND == kGram ? cs[0] * cs[0] / kS : (KIND == kPoly ? p.cc : f) / kS;
     if constexpr (KIND != kGram) {
@@ -511,7 +530,7 @@ __device__ __forceinline__ void epi_block(const f32x16 (&acc)[C::TN], uint16_t* 
   if constexpr (KIND == kPoly) ax = k.b + k.c * k.dr[i];
   if constexpr (KIND == kApply && BYROW) {
     ax = k.f * (k.a + k.dr[i]);
-    ay = k.f * (k.a + K::kTheta * k.dr[i]) * K::kLo;
+    ay = k.f * (k.a + K::kTheta * k.dr[i]) * k.lo_inv;
   }
 #pragma unroll
   for (int j = 0; j < C::TN; ++j) {
@@ -544,7 +563,7 @@ __device__ __forceinline__ void epi_block(const f32x16 (&acc)[C::TN], uint16_t* 
         } else if constexpr (KIND == kApply) {
           if constexpr (!BYROW) {
             ax = k.f * (k.a + k.dc[j][h][q]);
-            ay = k.f * (k.a + K::kTheta * k.dc[j][h][q]) * K::kLo;
+            ay = k.f * (k.a + K::kTheta * k.dc[j][h][q]) * k.lo_inv;
           }
           o[q] += ax * static_cast<float>(x[q]);
           if constexpr (HASLO) o[q] += ay * y[q];
@@ -561,7 +580,7 @@ __device__ __forceinline__ void epi_block(const f32x16 (&acc)[C::TN], uint16_t* 
       } else if constexpr (KIND == kApply) {
         uint4 uh;
         uint2 ul;
-        split8_fp8(o, uh, ul);
+        split8_fp8(o, k.lo_scale, uh, ul);
         lds_put16(hi + at, uh);
         typedef unsigned u32x2 __attribute__((ext_vector_type(2)));
         const u32x2 t = {ul.x, ul.y};
@@ -740,6 +759,56 @@ __device__ __forceinline__ void epilogue(const f32x16 (&acc)[C::TM][C::TN], cons
   }
 }
 
+// Joins the workgroups that share a tile's K: each writes its accumulators to
+// the workspace, and the last to arrive adds them all, in order, whichever it
+// is.  True in that one.  Accumulators and tickets are device-scope atomics
+// (they meet behind the XCDs' caches) ordered by waiting for the stores, not by
+// fences: a device-scope fence writes back a whole L2, which with some hundred
+// workgroups took 60 us.
+template <class C>
+__device__ __forceinline__ bool join_k(f32x16 (&acc)[C::TM][C::TN], const MmArgs& p, int64_t lid, int ks_i,
+                                       uint16_t* lds, int tid) {
+  constexpr int kVec = C::TM * C::TN * 8;  // pairs of floats per thread
+  uint64_t* part = reinterpret_cast<uint64_t*>(p.part) + lid * p.ks * kVec * 256 + tid;
+  uint64_t* mine = part + static_cast<int64_t>(ks_i) * kVec * 256;
+#pragma unroll
+  for (int v = 0; v < kVec; ++v) {
+    const f32x16& t = acc[v / 8 / C::TN][v / 8 % C::TN];
+    const uint64_t lo = __float_as_uint(t[2 * (v % 8)]), hi = __float_as_uint(t[2 * (v % 8) + 1]);
+    __hip_atomic_store(mine + v * 256, lo | hi << 32, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  }
+  int* last = reinterpret_cast<int*>(lds);
+  wait_vm<0>();
+  __syncthreads();  // all partials are out; the ring is no longer read
+  if (tid == 0) {
+    const int n = __hip_atomic_fetch_add(p.ticket + lid, 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    *last = n == p.ks - 1;
+    if (n == p.ks - 1) __hip_atomic_store(p.ticket + lid, 0, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  }
+  __syncthreads();
+  const bool is_last = *last != 0;
+  __syncthreads();  // before the epilogue uses this LDS
+  if (!is_last) return false;
+#pragma unroll
+  for (int i = 0; i < C::TM; ++i)
+#pragma unroll
+    for (int j = 0; j < C::TN; ++j)
+#pragma unroll
+      for (int q = 0; q < 16; ++q) acc[i][j][q] = 0.f;
+#pragma unroll 2
+  for (int k = 0; k < p.ks; ++k) {
+#pragma unroll
+    for (int v = 0; v < kVec; ++v) {
+      const uint64_t u = __hip_atomic_load(part + (static_cast<int64_t>(k) * kVec + v) * 256, __ATOMIC_RELAXED,
+                                           __HIP_MEMORY_SCOPE_AGENT);
+      f32x16& t = acc[v / 8 / C::TN][v / 8 % C::TN];
+      t[2 * (v % 8)] += __uint_as_float(static_cast<uint32_t>(u));
+      t[2 * (v % 8) + 1] += __uint_as_float(static_cast<uint32_t>(u >> 32));
+    }
+  }
+  return true;
+}
+
 // FINAL: apply's last step, which writes the result instead of the next X.
 template <class C, int KIND, bool AKC, bool BKC, bool SPLIT, bool FINAL>
 __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2)))
@@ -749,8 +818,12 @@ void orth_mm_kernel(MmArgs p) {
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int wm = wave >> 1, wn = wave & 1;
   // consecutive tiles of a matrix on one XCD (workgroups go to the 8 XCDs in turn)
-  const int64_t lid = xcd_tile(blockIdx.x, p.tiles);
-  if (lid < 0) return;
+  constexpr bool kKSplit = C::BM == 64 && KIND != kApply;
+  const int ks_n = kKSplit ? p.ks : 1;
+  const int64_t wid = xcd_tile(blockIdx.x, p.tiles * ks_n);
+  if (wid < 0) return;
+  const int64_t lid = kKSplit ? wid / ks_n : wid;
+  const int ks_i = kKSplit ? static_cast<int>(wid - lid * ks_n) : 0;
   const int per = p.tm * p.tn;
   const int64_t e = lid / per;
   const int t = static_cast<int>(lid - e * per);
@@ -768,13 +841,16 @@ void orth_mm_kernel(MmArgs p) {
   A.init(p.ah + e * p.sa, SPLIT ? p.al + e * p.sa : nullptr, p.lda, m0, p.M, p.K, wave, lane);
   B.init(p.bh + e * p.sb, SPLIT ? p.bl + e * p.sb : nullptr, p.ldb, n0, p.N, p.K, wave, lane);
   const int nk1 = (p.K + C::BK - 1) / C::BK;
-  const int nk = SPLIT ? 3 * nk1 : nk1;  // hi hi, hi lo, lo hi
-  int head = 0;  // K step to load next, and its ring slot
+  const int nk_all = SPLIT ? 3 * nk1 : nk1;  // hi hi, hi lo, lo hi
+  const int k_lo = kKSplit ? static_cast<int>(static_cast<int64_t>(nk_all) * ks_i / ks_n) : 0;
+  const int nk = (kKSplit ? static_cast<int>(static_cast<int64_t>(nk_all) * (ks_i + 1) / ks_n) : nk_all) - k_lo;
+  int head = 0;  // K step (from k_lo) to load next, and its ring slot
   int head_slot = 0;
   auto issue = [&]() {
     uint16_t* dst = lds + head_slot * C::kSlot;
-    const int part = SPLIT ? (head >= nk1) + (head >= 2 * nk1) : 0;
-    const int k = head - part * nk1;
+    const int at = k_lo + head;
+    const int part = SPLIT ? (at >= nk1) + (at >= 2 * nk1) : 0;
+    const int k = at - part * nk1;
     A.issue(SPLIT && part == 2, k * A.kstep, dst, wave);
     B.issue(SPLIT && part == 1, k * B.kstep, dst + C::kA, wave);
     ++head;
@@ -789,51 +865,72 @@ void orth_mm_kernel(MmArgs p) {
 #pragma unroll
       for (int q = 0; q < 16; ++q) acc[i][j][q] = 0.f;
 
-  // K loop.  The fragments of a slice are read while the MFMAs of the one before
-  // it run.  Before a step's last slice all its fragments are in registers:
+  // K loop.  The fragments of a phase are read while the MFMAs of the one before
+  // it run.  Before a step's last phase all its fragments are in registers:
   // there the waves meet, the next step's loads are known to have landed, and the
   // step's own ring slot is free for the loads of step kt + kRing.
-  constexpr int NS = C::BK / 16;
-  static_assert(NS % 2 == 0, "slice buffers alternate");
-  f16x8 fa[2][C::TM], fb[2][C::TN];
-  auto read = [&](int slot, int ks, int buf) {
+  f16x8 fa[2][C::KG][C::TM], fb[2][C::KG][C::TN];
+  auto read = [&](int slot, int ph, int buf) {
     const uint16_t* as = lds + slot * C::kSlot;
-    read_frags<C, AKC, BKC>(as, as + C::kA, wm, wn, ks, lane, fa[buf], fb[buf]);
+#pragma unroll
+    for (int g = 0; g < C::KG; ++g)
+      read_frags<C, AKC, BKC>(as, as + C::kA, wm, wn, ph * C::KG + g, lane, fa[buf][g], fb[buf][g]);
   };
   // a wave whose outputs lie above the diagonal only helps with the loads
   const bool idle = KIND != kApply && (m0 + wm * C::WM) / C::BN < (n0 + wn * C::WN) / C::BN;
   auto mma = [&](int buf) {
     if (KIND != kApply && idle) return;
 #pragma unroll
-    for (int i = 0; i < C::TM; ++i)
+    for (int g = 0; g < C::KG; ++g)
 #pragma unroll
-      for (int j = 0; j < C::TN; ++j)
-        acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(fb[buf][j], fa[buf][i], acc[i][j], 0, 0, 0);
+      for (int i = 0; i < C::TM; ++i)
+#pragma unroll
+        for (int j = 0; j < C::TN; ++j)
+          acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(fb[buf][g][j], fa[buf][g][i], acc[i][j], 0, 0, 0);
   };
   for (int s = 0; s < C::kRing && s < nk; ++s) issue();
   if (nk >= C::kRing) wait_vm<(C::kRing - 1) * C::kLoads>();
   else wait_vm<0>();
-  __syncthreads();
+  lds_barrier();
   read(0, 0, 0);
   int slot = 0;
-  for (int kt = 0; kt < nk; ++kt) {
+  // the step's end: wait for step kt + 1, refill the slot, read on
+  auto advance = [&](int kt, int buf) {
     const int next = slot + 1 == C::kRing ? 0 : slot + 1;
-#pragma unroll
-    for (int ks = 0; ks < NS; ++ks) {
-      if (ks + 1 < NS) {
-        read(slot, ks + 1, (ks + 1) & 1);
-      } else if (kt + 1 < nk) {
-        const int ahead = nk - 2 - kt;  // steps whose loads may stay outstanding
-        if (ahead >= C::kRing - 2) wait_vm<(C::kRing - 2) * C::kLoads>();
-        else if (C::kRing > 3 && ahead == 1) wait_vm<C::kLoads>();
-        else wait_vm<0>();
-        __syncthreads();
-        if (head < nk) issue();
-        read(next, 0, 0);
-      }
-      mma(ks & 1);
+    if (kt + 1 < nk) {
+      const int ahead = nk - 2 - kt;  // steps whose loads may stay outstanding
+      if (ahead >= C::kRing - 2) wait_vm<(C::kRing - 2) * C::kLoads>();
+      else if (C::kRing > 3 && ahead == 1) wait_vm<C::kLoads>();
+      else wait_vm<0>();
+      lds_barrier();
+      if (head < nk) issue();
+      read(next, 0, buf);
     }
     slot = next;
+  };
+  static_assert(C::kRing >= 2 && C::kRing <= 4, "ring waits");
+  if constexpr (C::kPhases == 1) {
+    for (int kt = 0; kt < nk; kt += 2) {
+      advance(kt, 1);
+      mma(0);
+      if (kt + 1 < nk) {
+        advance(kt + 1, 0);
+        mma(1);
+      }
+    }
+  } else {
+    static_assert(C::kPhases % 2 == 0, "phase buffers alternate");
+    for (int kt = 0; kt < nk; ++kt) {
+#pragma unroll
+      for (int ph = 0; ph < C::kPhases; ++ph) {
+        if (ph + 1 < C::kPhases) read(slot, ph + 1, (ph + 1) & 1);
+        else advance(kt, 0);
+        mma(ph & 1);
+      }
+    }
+  }
+  if constexpr (kKSplit) {
+    if (ks_n > 1 && !join_k<C>(acc, p, lid, ks_i, lds, tid)) return;
   }
   if constexpr (KIND != kApply)
     epilogue<C, KIND, SPLIT, true, false, KIND == kPoly && SPLIT>(acc, p, lds, e, m0, n0, wm, wn, wave, lane);
@@ -869,9 +966,46 @@ Sizes sizes_of(int E, int rows, int cols, bool split) {
   return z;
 }
 
+// Tile sizes, chosen per product by how many tiles there are for the 256 compute
+// units.  64 x 64 while they all fit at once, three to a unit (one matrix of 2048
+// x 1024: Gram 15 us against 26 us with 128 x 128 and 46 us with 256 x 128);
+// 256 x 128, two to a unit, once they fill the chip (8 of 1024 x 2048, 512 tiles:
+// apply 51 us against 54 and 72); 128 x 128 between (one of 2048 x 2048, 256
+// tiles: apply 33 us against 45 with 256 x 128 and 42 with 64 x 64).
+using Big = Tile<256, 128, 32, 3, 1>;
+using Mid = Tile<128, 128, 64, 2, 2>;
+using Small = Tile<64, 64, 64, 3, 2>;
+
+// Tiles of a symmetric m x m output, and of an r x c one, in E matrices.
+template <class C>
+int64_t sym_tiles(int64_t m, int64_t E) {
+  const int64_t n = cdiv(m, C::BM);
+  return C::BM / C::BN * (n * (n + 1) / 2) * E;
+}
+template <class C>
+int64_t rect_tiles(int64_t r, int64_t c, int64_t E) {
+  return cdiv(r, C::BM) * cdiv(c, C::BN) * E;
+}
+
+// Workgroups that share the K steps of a symmetric product's tile (Small tiles):
+// enough to occupy the chip, each with at least eight of the steps of 64.
+int k_split(int64_t tiles, int64_t steps) {
+  int64_t n = 512 / tiles;
+  if (n > steps / 8) n = steps / 8;
+  return static_cast<int>(n < 1 ? 1 : (n > 16 ? 16 : n));
+}
+// of the Gram (K = the longer side) or the polynomial (the shorter side); 1 where other tiles are used
+int k_split(const Sizes& z, int64_t K) {
+  const int64_t tiles = sym_tiles<Small>(z.mp, z.E);
+  return tiles > 256 ? 1 : k_split(tiles, cdiv(K, Small::BK) * (z.split ? 3 : 1));
+}
+
 struct Ws {
   double* part;
   float *cs, *da, *db;  // scales; diagonals of A and B
+  float* kpart;         // split-K accumulators
+  int32_t* ticket;      // and their tickets: `tickets` per matrix
+  int tickets;
   uint16_t *xh[2], *ah, *al, *bh, *bl;
   void* xl[2];
 };
@@ -891,6 +1025,11 @@ size_t ws_layout(const Sizes& z, char* base, Ws* w) {
   t.cs = reinterpret_cast<float*>(take(static_cast<size_t>(z.E) * (kMaxSteps + 1) * 4));
   t.da = reinterpret_cast<float*>(take(static_cast<size_t>(z.E) * z.mp * 4));
   t.db = reinterpret_cast<float*>(take(static_cast<size_t>(z.E) * z.mp * 4));
+  const int64_t tiles = sym_tiles<Small>(z.mp, z.E);
+  const int kg = k_split(z, z.rp > z.cp ? z.rp : z.cp), kp = k_split(z, z.mp), ks = kg > kp ? kg : kp;
+  t.kpart = reinterpret_cast<float*>(take(ks > 1 ? static_cast<size_t>(tiles) * ks * Small::BM * Small::BN * 4 : 0));
+  t.ticket = reinterpret_cast<int32_t*>(take(ks > 1 ? static_cast<size_t>(tiles) * 4 : 0));
+  t.tickets = ks > 1 ? static_cast<int>(tiles / z.E) : 0;
   const size_t xb = static_cast<size_t>(z.E) * z.x * 2, ab = static_cast<size_t>(z.E) * z.a * 2;
   t.xh[0] = take(xb);
   t.xh[1] = take(xb);
@@ -906,7 +1045,7 @@ size_t ws_layout(const Sizes& z, char* base, Ws* w) {
 
 template <class C, int KIND, bool AKC, bool BKC>
 void launch_mm(const char* name, const MmArgs& a, bool split, hipStream_t s) {
-  const dim3 grid(xcd_grid(a.tiles));
+  const dim3 grid(xcd_grid(a.tiles * a.ks));
   const bool last = KIND == kApply && a.out != kOutX;
   auto go = [&](auto sp, auto fin) {
     MOE_LAUNCH(name, (orth_mm_kernel<C, KIND, AKC, BKC, decltype(sp)::value, decltype(fin)::value>), grid, dim3(256),
@@ -918,15 +1057,36 @@ void launch_mm(const char* name, const MmArgs& a, bool split, hipStream_t s) {
   else last ? go(std::false_type{}, fin) : go(std::false_type{}, no);
 }
 
-template <class C>
+template <int KIND, bool AKC, bool BKC>
+void launch_any(const char* name, MmArgs& a, const Sizes& z, hipStream_t s) {
+  auto go = [&](auto tile) {
+    using C = decltype(tile);
+    if constexpr (KIND == kApply) {
+      a.tm = static_cast<int>(cdiv(a.M, C::BM));
+      a.tn = static_cast<int>(cdiv(a.N, C::BN));
+    } else {
+      a.tm = static_cast<int>(sym_tiles<C>(a.M, 1));
+      a.tn = 1;
+    }
+    a.tiles = static_cast<int64_t>(a.tm) * a.tn * z.E;
+    a.ks = C::BM == 64 && !(KIND == kApply) ? k_split(z, a.K) : 1;
+    launch_mm<C, KIND, AKC, BKC>(name, a, z.split, s);
+  };
+  const bool ap = KIND == kApply;
+  if ((ap ? rect_tiles<Small>(a.M, a.N, z.E) : sym_tiles<Small>(a.M, z.E)) <= 768) go(Small{});
+  else if ((ap ? rect_tiles<Big>(a.M, a.N, z.E) : sym_tiles<Big>(a.M, z.E)) >= 480) go(Big{});
+  else go(Mid{});
+}
+
 void run_products(const Sizes& z, const Ws& w, MmArgs a, const float (*coef)[3], int out, bool exact0,
                   hipStream_t s) {
-  const int64_t nm = cdiv(z.mp, C::BM), sym = C::BM / C::BN * nm * (nm + 1) / 2;
-  const int64_t nr = cdiv(z.rp, C::BM), nc = cdiv(z.cp, C::BN);
   a.cs = w.cs;
   a.sd = z.mp;
+  a.part = w.kpart;
+  a.ticket = w.ticket;
   for (int i = 0; i < a.steps; ++i) {
     const int cur = i & 1, nxt = cur ^ 1;
+    const uint16_t* xl = static_cast<const uint16_t*>(w.xl[cur]);  // as an operand: with split operands only
     a.step = i;
     a.ca = coef[i][0];
     a.cb = coef[i][1];
@@ -934,37 +1094,32 @@ void run_products(const Sizes& z, const Ws& w, MmArgs a, const float (*coef)[3],
     a.out = kOutX;
     // Gram: the shorter side's inner products
     a.ah = a.bh = w.xh[cur];
-    a.al = a.bl = static_cast<const uint16_t*>(w.xl[cur]);  // read with split operands only, like the other lo operands
+    a.al = a.bl = xl;
     a.sa = a.sb = z.x;
     a.lda = a.ldb = z.cp;
     a.K = z.tall ? z.rp : z.cp;
     a.M = a.N = z.mp;
-    a.tm = static_cast<int>(sym);
-    a.tn = 1;
-    a.tiles = sym * z.E;
     a.oh = w.ah;
     a.ol = w.al;
     a.dout = w.da;
     a.so = z.a;
     a.ldo = z.mp;
-    if (z.tall) launch_mm<C, kGram, false, false>("orth_gram", a, z.split, s);
-    else launch_mm<C, kGram, true, true>("orth_gram", a, z.split, s);
+    if (z.tall) launch_any<kGram, false, false>("orth_gram", a, z, s);
+    else launch_any<kGram, true, true>("orth_gram", a, z, s);
     // polynomial
     a.ah = a.bh = a.eh = w.ah;
-    a.el = a.al = a.bl = w.al;
+    a.al = a.bl = w.al;
+    a.el = w.al;
     a.sa = a.sb = z.a;
     a.lda = a.ldb = a.K = z.mp;
     a.oh = w.bh;
     a.ol = w.bl;
     a.din = w.da;
     a.dout = w.db;
-    launch_mm<C, kPoly, true, true>("orth_poly", a, z.split, s);
+    launch_any<kPoly, true, true>("orth_poly", a, z, s);
     // apply
     a.M = z.rp;
     a.N = z.cp;
-    a.tm = static_cast<int>(nr);
-    a.tn = static_cast<int>(nc);
-    a.tiles = nr * nc * z.E;
     a.eh = w.xh[cur];
     // without split operands the last step does without X's lo part (noise in it
     // is multiplied by a once more only), and the first of a bf16 gradient has none
@@ -977,24 +1132,24 @@ void run_products(const Sizes& z, const Ws& w, MmArgs a, const float (*coef)[3],
     a.out = i + 1 < a.steps ? static_cast<int>(kOutX) : out;
     if (z.tall) {  // X B, B symmetric
       a.ah = w.xh[cur];
-      a.al = static_cast<const uint16_t*>(w.xl[cur]);
+      a.al = xl;
       a.sa = z.x;
       a.lda = z.cp;
       a.bh = w.bh;
       a.bl = w.bl;
       a.sb = z.a;
       a.ldb = z.mp;
-      launch_mm<C, kApply, true, true>("orth_apply", a, z.split, s);
+      launch_any<kApply, true, true>("orth_apply", a, z, s);
     } else {  // B X
       a.ah = w.bh;
       a.al = w.bl;
       a.sa = z.a;
       a.lda = z.mp;
       a.bh = w.xh[cur];
-      a.bl = static_cast<const uint16_t*>(w.xl[cur]);
+      a.bl = xl;
       a.sb = z.x;
       a.ldb = z.cp;
-      launch_mm<C, kApply, true, false>("orth_apply", a, z.split, s);
+      launch_any<kApply, true, false>("orth_apply", a, z, s);
     }
   }
 }
@@ -1012,16 +1167,18 @@ void run_pre(const Sizes& z, const PreArgs& a, hipStream_t s) {
 // start in [0, 1] and |a x + b x^3 + c x^5| over [0, s] bounds the next ones.
 // The fp16 buffers hold values up to 15 (kS 15 < 65504); steps that could leave
 // that range are refused.  growth: the largest factor by which a step multiplies
-// a singular value.
+// a singular value.  lo_scale: what 8-bit lo parts are multiplied by; a value x kS
+// has |lo| <= 2^-11 |x| kS = 2 |x|, and |x| is at most the largest singular value.
 struct Plan {
   float coef[kMaxSteps][3];
   float growth[kMaxSteps];
+  float lo_scale;
 };
 constexpr double kRange = 15.0;
 
 int make_plan(const float* coef, int steps, Plan& p) {
   static const float kQuintic[3] = {3.4445f, -4.7750f, 2.0315f};
-  double s = 1.0 + 1e-3;
+  double s = 1.0 + 1e-3, most = s;
   for (int i = 0; i < steps; ++i) {
     const float* c = coef ? coef + 3 * i : kQuintic;
     for (int j = 0; j < 3; ++j) {
@@ -1051,7 +1208,10 @@ int make_plan(const float* coef, int steps, Plan& p) {
     if (!(s * s <= kRange) || !(top <= kRange) || !(poly <= kRange)) return MOE_EUNSUPPORTED;
     p.growth[i] = static_cast<float>(gain > 1.0 ? gain : 1.0);
     s = top * (1.0 + 1e-2);  // rounding in the products
+    most = std::fmax(most, s);
   }
+  p.lo_scale = 256.0f;
+  while (p.lo_scale * 2.0 * most > 440.0) p.lo_scale *= 0.5f;
   return MOE_OK;
 }
 
@@ -1100,6 +1260,8 @@ int run(const void* g, int dtype, int E, int rows, int cols, int steps, const fl
   pre.nesterov = st.nesterov;
   pre.part = w.part;
   pre.cs = w.cs;
+  pre.ticket = w.ticket;
+  pre.tickets = w.tickets;
   pre.xh = w.xh[0];
   // a bf16 gradient has its 8 mantissa bits in hi (its smallest elements, below
   // 2^-26 of the norm, lose bits far below the result's accuracy)
@@ -1112,6 +1274,7 @@ int run(const void* g, int dtype, int E, int rows, int cols, int steps, const fl
   pre.chunks = z.chunks;
   pre.steps = steps;
   pre.eps = eps;
+  pre.lo_scale = plan.lo_scale;
   for (int i = 0; i < steps; ++i) pre.growth[i] = plan.growth[i];
   if (z.split) {
     if (st.mom) run_pre<float, true>(z, pre, s);
@@ -1128,10 +1291,9 @@ int run(const void* g, int dtype, int E, int rows, int cols, int steps, const fl
   a.cols = cols;
   a.keep = st.keep;
   a.gain = st.gain;
+  a.lo_scale = plan.lo_scale;
   const int kind = st.w ? kOutW : kOutO;
-  const int64_t big = cdiv(z.rp, 256) * cdiv(z.cp, 256) * E;
-  if (big >= 256) run_products<Tile<256, 128, 32, 3>>(z, w, a, plan.coef, kind, exact0, s);
-  else run_products<Tile<128, 128, 32, 4>>(z, w, a, plan.coef, kind, exact0, s);
+  run_products(z, w, a, plan.coef, kind, exact0, s);
   return launch_status();
 }
 
