@@ -943,6 +943,269 @@ void orth_mm_kernel(MmArgs p) {
 }
 
 // ---------------------------------------------------------------------------
+// Small matrices: all steps of a matrix in one workgroup, X and A in LDS.  The
+// same arithmetic as above with 32 x 32 outputs per wave and task; a chain of
+// short launches would cost more than the work (8 matrices of 64 x 128: 17
+// launches).
+// ---------------------------------------------------------------------------
+constexpr int kSmallThreads = 512, kSmallWaves = kSmallThreads / 64;
+constexpr int kSmallTasks = 5;                 // 32 x 32 outputs of X per wave at most
+constexpr int kSmallLds = 160 * 1024;
+
+// LDS rows of any multiple of 64 elements, 16-byte chunks swizzled: free of
+// conflicts for 8 consecutive rows at one chunk and for the transposing reads.
+__device__ __forceinline__ int sm_swz(int r) { return ((r & 3) << 1) | ((r >> 2) & 1); }
+__device__ __forceinline__ int sm_at(int r, int ld, int chunk) { return r * ld + (chunk ^ sm_swz(r)) * 8; }
+
+template <bool KC>
+__device__ __forceinline__ f16x8 sm_frag(const uint16_t* t, int ld, int base, int ks, int lane) {
+  if constexpr (KC) {
+    return *reinterpret_cast<const f16x8*>(t + sm_at(base + (lane & 31), ld, ks * 2 + (lane >> 5)));
+  } else {  // as frag_tr
+    const int G = lane >> 4, L = lane & 15;
+    const int k = ks * 16 + 8 * (G >> 1) + (L >> 2);
+    const int c = base + 16 * (G & 1) + 4 * (L & 3);
+    typedef __attribute__((address_space(3))) i16x4 lds_i16x4;
+    const i16x4 a = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_i16x4*)(t + sm_at(k, ld, c >> 3) + (c & 7)));
+    const i16x4 b = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_i16x4*)(t + sm_at(k + 4, ld, c >> 3) + (c & 7)));
+    const short v[8] = {a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]};
+    f16x8 r;
+    __builtin_memcpy(&r, v, 16);
+    return r;
+  }
+}
+
+struct SmMat {
+  uint16_t *h, *l;
+  int ld;
+};
+
+// Task u of this wave: the 32 x 32 outputs at (r, c) of an M x N output, or none.
+__device__ __forceinline__ bool sm_task(int u, int wave, int M, int N, int& r, int& c) {
+  const int t = u * kSmallWaves + wave, nc = N / 32;
+  r = t / nc * 32;
+  c = (t - t / nc * nc) * 32;
+  return t < (M / 32) * nc;
+}
+
+template <bool AKC, bool BKC, bool SPLIT, int TASKS>
+__device__ __forceinline__ void sm_product(f32x16 (&acc)[TASKS], const SmMat& A, const SmMat& B, int M, int N, int K,
+                                           int wave, int lane) {
+#pragma unroll
+  for (int u = 0; u < TASKS; ++u) {
+#pragma unroll
+    for (int q = 0; q < 16; ++q) acc[u][q] = 0.f;
+    int r, c;
+    if (!sm_task(u, wave, M, N, r, c)) continue;
+#pragma unroll 4
+    for (int ks = 0; ks < K / 16; ++ks) {
+      const f16x8 a = sm_frag<AKC>(A.h, A.ld, r, ks, lane), b = sm_frag<BKC>(B.h, B.ld, c, ks, lane);
+      acc[u] = __builtin_amdgcn_mfma_f32_32x32x16_f16(b, a, acc[u], 0, 0, 0);
+      if constexpr (SPLIT) {
+        const f16x8 al = sm_frag<AKC>(A.l, A.ld, r, ks, lane), bl = sm_frag<BKC>(B.l, B.ld, c, ks, lane);
+        acc[u] = __builtin_amdgcn_mfma_f32_32x32x16_f16(bl, a, acc[u], 0, 0, 0);
+        acc[u] = __builtin_amdgcn_mfma_f32_32x32x16_f16(b, al, acc[u], 0, 0, 0);
+      }
+    }
+  }
+}
+
+// The 8-column chunks of a wave's task as (row, column, values).
+template <class F>
+__device__ __forceinline__ void sm_chunks(const f32x16& acc, int r, int c, int lane, F&& f) {
+  float v[2][8];
+  to_chunks(acc, v);
+#pragma unroll
+  for (int h = 0; h < 2; ++h) f(r + (lane & 31), c + 16 * h + 8 * (lane >> 5), v[h]);
+}
+
+__device__ __forceinline__ void sm_get(const SmMat& m, int r, int c, float* x) {  // hi + lo
+  const int at = sm_at(r, m.ld, c >> 3);
+  const f16x8 h = *reinterpret_cast<const f16x8*>(m.h + at);
+#pragma unroll
+  for (int q = 0; q < 8; ++q) x[q] = static_cast<float>(h[q]);
+}
+
+struct SmArgs {
+  PreArgs pre;
+  float coef[kMaxSteps][3];
+  void* o;
+  const void* w;   // nullptr: write the result, else the updated weight
+  float keep, gain;
+};
+
+template <class T, bool MOM, bool TALL>
+__global__ __launch_bounds__(kSmallThreads) void orth_small_kernel(SmArgs p) {
+  constexpr bool SPLIT = sizeof(T) == 4;
+  constexpr float kTheta = SPLIT ? 1.0f : 0.5f;
+  __shared__ __attribute__((aligned(16))) uint8_t lds[kSmallLds];
+  const PreArgs& a = p.pre;
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int64_t e = blockIdx.x;
+  const int rp = a.rp, cp = a.cp, mp = TALL ? cp : rp, n = rp * cp;
+  uint16_t* base = reinterpret_cast<uint16_t*>(lds);
+  const SmMat X{base, base + n, cp};
+  const SmMat A{base + 2 * n, base + 2 * n + mp * mp, mp};
+  float* da = reinterpret_cast<float*>(base + 2 * n + (SPLIT ? 2 : 1) * mp * mp);
+  float* db = da + mp;
+  double* red = reinterpret_cast<double*>(db + mp);
+
+  // norm, then the scaled pair (both passes give an element to the same thread)
+  const int64_t g0 = e * a.rows * a.cols;
+  const int cv = cp / 8;
+  double s = 0.0;
+  auto each = [&](auto&& f) {
+    for (int i = tid; i < n / 8; i += kSmallThreads) {
+      const int r = i / cv, c = i - r * cv;
+      const int k = r < a.rows ? a.cols - 8 * c : 0;
+      f(r, c, k < 0 ? 0 : (k < 8 ? k : 8), g0 + static_cast<int64_t>(r) * a.cols + 8 * c);
+    }
+  };
+  each([&](int, int, int k, int64_t o) {
+    float u[8];
+    if (k > 0) update8<T, MOM>(a, o, k, true, u);
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      if (j < k) s += static_cast<double>(u[j]) * static_cast<double>(u[j]);
+  });
+#pragma unroll
+  for (int o = 32; o >= 1; o >>= 1) s += __shfl_xor(s, o, 64);
+  if (lane == 0) red[wave] = s;
+  __syncthreads();
+  s = 0.0;
+  for (int w = 0; w < kSmallWaves; ++w) s += red[w];
+  const double norm = sqrt(s);
+  const bool ok = norm - norm == 0.0;
+  int q2 = 0;
+  if (ok && norm > 0.0) {
+    frexp(norm, &q2);
+    q2 = -q2;
+  }
+  double cd = ok && norm > 0.0 ? ldexp(1.0, -q2) / (norm + static_cast<double>(a.eps)) : 1.0;
+  each([&](int r, int c, int k, int64_t o) {
+    float u[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+    if (k > 0) update8<T, MOM>(a, o, k, false, u);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) u[j] = j < k ? (ok ? ldexpf(u[j], q2) * kS : NAN) : 0.f;
+    uint4 hi, lo;
+    split8(u, hi, lo);
+    lds_put16(X.h + sm_at(r, cp, c), hi);
+    lds_put16(X.l + sm_at(r, cp, c), lo);
+  });
+  __syncthreads();
+
+  for (int st = 0; st < a.steps; ++st) {
+    const float ci = static_cast<float>(cd);
+    cd = fmin(1.0, cd * static_cast<double>(a.growth[st]));
+    const float cn = static_cast<float>(cd);
+    const float ca = p.coef[st][0], cb = p.coef[st][1], cc = p.coef[st][2];
+    const bool last = st + 1 == a.steps;
+    // Gram
+    {
+      f32x16 acc[2];
+      sm_product<!TALL, !TALL, SPLIT, 2>(acc, X, X, mp, mp, TALL ? rp : cp, wave, lane);
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        int r0, c0;
+        if (!sm_task(u, wave, mp, mp, r0, c0)) continue;
+        sm_chunks(acc[u], r0, c0, lane, [&](int r, int c, float* v) {
+#pragma unroll
+          for (int q = 0; q < 8; ++q) {
+            v[q] *= ci * ci / kS;
+            if (c + q == r) {
+              da[r] = v[q] / kS;
+              v[q] = 0.f;
+            }
+          }
+          uint4 hi, lo;
+          split8(v, hi, lo);
+          lds_put16(A.h + sm_at(r, mp, c >> 3), hi);
+          if constexpr (SPLIT) lds_put16(A.l + sm_at(r, mp, c >> 3), lo);
+        });
+      }
+    }
+    __syncthreads();
+    // polynomial, in A's place
+    {
+      f32x16 acc[2];
+      sm_product<true, true, SPLIT, 2>(acc, A, A, mp, mp, mp, wave, lane);
+      __syncthreads();
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        int r0, c0;
+        if (!sm_task(u, wave, mp, mp, r0, c0)) continue;
+        sm_chunks(acc[u], r0, c0, lane, [&](int r, int c, float* v) {
+          float x[8];
+          const int at = sm_at(r, mp, c >> 3);
+          sm_get(A, r, c, x);
+          if constexpr (SPLIT) {
+            const f16x8 l = *reinterpret_cast<const f16x8*>(A.l + at);
+#pragma unroll
+            for (int q = 0; q < 8; ++q) x[q] += static_cast<float>(l[q]);
+          }
+          const float d = da[r];
+#pragma unroll
+          for (int q = 0; q < 8; ++q) {
+            v[q] *= cc / kS;
+            if (c + q == r) {
+              db[r] = v[q] / kS + d * (cb + cc * d);
+              v[q] = 0.f;
+            } else {
+              v[q] += x[q] * (cb + cc * (d + da[c + q]));
+            }
+          }
+          uint4 hi, lo;
+          split8(v, hi, lo);
+          lds_put16(A.h + at, hi);
+          if constexpr (SPLIT) lds_put16(A.l + at, lo);
+        });
+      }
+    }
+    __syncthreads();
+    // apply, in X's place or to the result
+    f32x16 acc[kSmallTasks];
+    if constexpr (TALL) sm_product<true, true, SPLIT, kSmallTasks>(acc, X, A, rp, cp, mp, wave, lane);
+    else sm_product<true, false, SPLIT, kSmallTasks>(acc, A, X, rp, cp, mp, wave, lane);
+    __syncthreads();
+    const float f = last ? ci / kS : ci / cn;
+#pragma unroll
+    for (int u = 0; u < kSmallTasks; ++u) {
+      int r0, c0;
+      if (!sm_task(u, wave, rp, cp, r0, c0)) continue;
+      sm_chunks(acc[u], r0, c0, lane, [&](int r, int c, float* v) {
+        float x[8];
+        const int at = sm_at(r, cp, c >> 3);
+        sm_get(X, r, c, x);
+        const f16x8 l = *reinterpret_cast<const f16x8*>(X.l + at);
+#pragma unroll
+        for (int q = 0; q < 8; ++q) {
+          const float d = TALL ? db[c + q] : db[r], y = static_cast<float>(l[q]);
+          v[q] = f * ((ca + d) * x[q] + (ca + kTheta * d) * y + v[q] / kS);
+        }
+        if (!last) {
+          uint4 hi, lo;
+          split8(v, hi, lo);
+          lds_put16(X.h + at, hi);
+          lds_put16(X.l + at, lo);
+        } else if (r < a.rows && c < a.cols) {
+          const int64_t o = g0 + static_cast<int64_t>(r) * a.cols + c;
+          const int k = a.cols - c;
+          if (p.w) {
+            float w[8];
+            ld8(static_cast<const T*>(p.w) + o, k, w);
+#pragma unroll
+            for (int q = 0; q < 8; ++q) v[q] = p.keep * w[q] - p.gain * v[q];
+          }
+          st8(static_cast<T*>(p.o) + o, k, v);
+        }
+      });
+    }
+    __syncthreads();
+  }
+}
+
+// ---------------------------------------------------------------------------
 // Host side.
 // ---------------------------------------------------------------------------
 struct Sizes {
@@ -988,11 +1251,14 @@ int64_t rect_tiles(int64_t r, int64_t c, int64_t E) {
 }
 
 // Workgroups that share the K steps of a symmetric product's tile (Small tiles):
-// enough to occupy the chip, each with at least eight of the steps of 64.
+// enough to occupy the chip, each with at least eight of the steps of 64, and
+// only where it shortens the longest chain by 16 steps or more, about 5 us, which
+// is what joining costs (4096 x 128: Gram 25 -> 12 us; at 8 steps saved 12 -> 13 us).
 int k_split(int64_t tiles, int64_t steps) {
   int64_t n = 512 / tiles;
   if (n > steps / 8) n = steps / 8;
-  return static_cast<int>(n < 1 ? 1 : (n > 16 ? 16 : n));
+  if (n > 16) n = 16;
+  return n > 1 && steps - cdiv(steps, n) >= 16 ? static_cast<int>(n) : 1;
 }
 // of the Gram (K = the longer side) or the polynomial (the shorter side); 1 where other tiles are used
 int k_split(const Sizes& z, int64_t K) {
@@ -1225,6 +1491,20 @@ int check_shape(int64_t E, int rows, int cols, int dtype) {
   return MOE_OK;
 }
 
+// Matrices that fit one workgroup: X (pairs) and A in its LDS, their 32 x 32
+// outputs within its waves' tasks.
+bool small_fits(const Sizes& z) {
+  const int64_t bytes = 4 * z.x + (z.split ? 4 : 2) * z.a + 8 * z.mp + 8 * kSmallWaves;
+  return bytes <= kSmallLds && z.x <= 1024 * kSmallWaves * kSmallTasks && z.a <= 1024 * kSmallWaves * 2;
+}
+
+template <class T, bool MOM>
+void run_small(const Sizes& z, const SmArgs& a, hipStream_t s) {
+  const dim3 grid(static_cast<unsigned>(z.E)), block(kSmallThreads);
+  if (z.tall) MOE_LAUNCH("orth_small", (orth_small_kernel<T, MOM, true>), grid, block, 0, s, a);
+  else MOE_LAUNCH("orth_small", (orth_small_kernel<T, MOM, false>), grid, block, 0, s, a);
+}
+
 struct Step {  // the Muon step's part; mom nullptr: orthogonalise only
   const float* mom;
   float* mom_out;
@@ -1276,6 +1556,19 @@ int run(const void* g, int dtype, int E, int rows, int cols, int steps, const fl
   pre.eps = eps;
   pre.lo_scale = plan.lo_scale;
   for (int i = 0; i < steps; ++i) pre.growth[i] = plan.growth[i];
+  if (small_fits(z)) {
+    SmArgs sm{};
+    sm.pre = pre;
+    for (int i = 0; i < steps; ++i)
+      for (int j = 0; j < 3; ++j) sm.coef[i][j] = plan.coef[i][j];
+    sm.o = out;
+    sm.w = st.w;
+    sm.keep = st.keep;
+    sm.gain = st.gain;
+    if (z.split) st.mom ? run_small<float, true>(z, sm, s) : run_small<float, false>(z, sm, s);
+    else st.mom ? run_small<uint16_t, true>(z, sm, s) : run_small<uint16_t, false>(z, sm, s);
+    return launch_status();
+  }
   if (z.split) {
     if (st.mom) run_pre<float, true>(z, pre, s);
     else run_pre<float, false>(z, pre, s);
