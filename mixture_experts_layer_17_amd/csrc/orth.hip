@@ -980,31 +980,50 @@ struct SmMat {
   int ld;
 };
 
-// Task u of this wave: the 32 x 32 outputs at (r, c) of an M x N output, or none.
-__device__ __forceinline__ bool sm_task(int u, int wave, int M, int N, int& r, int& c) {
-  const int t = u * kSmallWaves + wave, nc = N / 32;
-  r = t / nc * 32;
-  c = (t - t / nc * nc) * 32;
-  return t < (M / 32) * nc;
-}
+// This wave's tasks of an M x N output: 32 x 32 outputs at (r, c) each.
+template <int TASKS>
+struct SmTasks {
+  int r[TASKS], c[TASKS], n;
+  __device__ __forceinline__ void init(int M, int N, int wave) {
+    const int nc = N / 32, all = M / 32 * nc;
+    n = 0;
+#pragma unroll
+    for (int u = 0; u < TASKS; ++u) {
+      const int t = u * kSmallWaves + wave;
+      r[u] = __builtin_amdgcn_readfirstlane(t / nc * 32);
+      c[u] = __builtin_amdgcn_readfirstlane(t % nc * 32);
+      n += t < all;
+    }
+  }
+};
 
 template <bool AKC, bool BKC, bool SPLIT, int TASKS>
-__device__ __forceinline__ void sm_product(f32x16 (&acc)[TASKS], const SmMat& A, const SmMat& B, int M, int N, int K,
-                                           int wave, int lane) {
+__device__ __forceinline__ void sm_product(f32x16 (&acc)[TASKS], const SmMat& A, const SmMat& B,
+                                           const SmTasks<TASKS>& t, int K, int lane) {
 #pragma unroll
   for (int u = 0; u < TASKS; ++u) {
 #pragma unroll
     for (int q = 0; q < 16; ++q) acc[u][q] = 0.f;
-    int r, c;
-    if (!sm_task(u, wave, M, N, r, c)) continue;
-#pragma unroll 4
-    for (int ks = 0; ks < K / 16; ++ks) {
-      const f16x8 a = sm_frag<AKC>(A.h, A.ld, r, ks, lane), b = sm_frag<BKC>(B.h, B.ld, c, ks, lane);
-      acc[u] = __builtin_amdgcn_mfma_f32_32x32x16_f16(b, a, acc[u], 0, 0, 0);
-      if constexpr (SPLIT) {
-        const f16x8 al = sm_frag<AKC>(A.l, A.ld, r, ks, lane), bl = sm_frag<BKC>(B.l, B.ld, c, ks, lane);
-        acc[u] = __builtin_amdgcn_mfma_f32_32x32x16_f16(bl, a, acc[u], 0, 0, 0);
-        acc[u] = __builtin_amdgcn_mfma_f32_32x32x16_f16(b, al, acc[u], 0, 0, 0);
+    if (u >= t.n) continue;
+    const int r = t.r[u], c = t.c[u];
+    for (int k4 = 0; k4 < K / 16; k4 += 4) {  // K is a multiple of 64
+      f16x8 a[4], b[4], al[SPLIT ? 4 : 1], bl[SPLIT ? 4 : 1];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        a[i] = sm_frag<AKC>(A.h, A.ld, r, k4 + i, lane);
+        b[i] = sm_frag<BKC>(B.h, B.ld, c, k4 + i, lane);
+        if constexpr (SPLIT) {
+          al[i] = sm_frag<AKC>(A.l, A.ld, r, k4 + i, lane);
+          bl[i] = sm_frag<BKC>(B.l, B.ld, c, k4 + i, lane);
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        acc[u] = __builtin_amdgcn_mfma_f32_32x32x16_f16(b[i], a[i], acc[u], 0, 0, 0);
+        if constexpr (SPLIT) {
+          acc[u] = __builtin_amdgcn_mfma_f32_32x32x16_f16(bl[i], a[i], acc[u], 0, 0, 0);
+          acc[u] = __builtin_amdgcn_mfma_f32_32x32x16_f16(b[i], al[i], acc[u], 0, 0, 0);
+        }
       }
     }
   }
@@ -1019,11 +1038,16 @@ __device__ __forceinline__ void sm_chunks(const f32x16& acc, int r, int c, int l
   for (int h = 0; h < 2; ++h) f(r + (lane & 31), c + 16 * h + 8 * (lane >> 5), v[h]);
 }
 
-__device__ __forceinline__ void sm_get(const SmMat& m, int r, int c, float* x) {  // hi + lo
+__device__ __forceinline__ void sm_get(const SmMat& m, int r, int c, float* x) {  // the hi part
   const int at = sm_at(r, m.ld, c >> 3);
   const f16x8 h = *reinterpret_cast<const f16x8*>(m.h + at);
 #pragma unroll
   for (int q = 0; q < 8; ++q) x[q] = static_cast<float>(h[q]);
+}
+
+__device__ __forceinline__ void sm_row8(const float* d, int c, float* o) {  // c a multiple of 8
+  Elem<float>::unpack(lds_get16(d + c), o);
+  Elem<float>::unpack(lds_get16(d + c + 4), o + 4);
 }
 
 struct SmArgs {
@@ -1095,6 +1119,10 @@ __global__ __launch_bounds__(kSmallThreads) void orth_small_kernel(SmArgs p) {
   });
   __syncthreads();
 
+  SmTasks<2> ta;            // tasks of A, and of X
+  SmTasks<kSmallTasks> tx;
+  ta.init(mp, mp, wave);
+  tx.init(rp, cp, wave);
   for (int st = 0; st < a.steps; ++st) {
     const float ci = static_cast<float>(cd);
     cd = fmin(1.0, cd * static_cast<double>(a.growth[st]));
@@ -1104,20 +1132,20 @@ __global__ __launch_bounds__(kSmallThreads) void orth_small_kernel(SmArgs p) {
     // Gram
     {
       f32x16 acc[2];
-      sm_product<!TALL, !TALL, SPLIT, 2>(acc, X, X, mp, mp, TALL ? rp : cp, wave, lane);
+      sm_product<!TALL, !TALL, SPLIT, 2>(acc, X, X, ta, TALL ? rp : cp, lane);
 #pragma unroll
       for (int u = 0; u < 2; ++u) {
-        int r0, c0;
-        if (!sm_task(u, wave, mp, mp, r0, c0)) continue;
-        sm_chunks(acc[u], r0, c0, lane, [&](int r, int c, float* v) {
+        if (u >= ta.n) continue;
+        sm_chunks(acc[u], ta.r[u], ta.c[u], lane, [&](int r, int c, float* v) {
+          float t = 0.f;
 #pragma unroll
           for (int q = 0; q < 8; ++q) {
+            const bool dg = c + q == r;
             v[q] *= ci * ci / kS;
-            if (c + q == r) {
-              da[r] = v[q] / kS;
-              v[q] = 0.f;
-            }
+            t = dg ? v[q] : t;
+            v[q] = dg ? 0.f : v[q];
           }
+          if (r >= c && r < c + 8) da[r] = t / kS;
           uint4 hi, lo;
           split8(v, hi, lo);
           lds_put16(A.h + sm_at(r, mp, c >> 3), hi);
@@ -1129,13 +1157,12 @@ __global__ __launch_bounds__(kSmallThreads) void orth_small_kernel(SmArgs p) {
     // polynomial, in A's place
     {
       f32x16 acc[2];
-      sm_product<true, true, SPLIT, 2>(acc, A, A, mp, mp, mp, wave, lane);
+      sm_product<true, true, SPLIT, 2>(acc, A, A, ta, mp, lane);
       __syncthreads();
 #pragma unroll
       for (int u = 0; u < 2; ++u) {
-        int r0, c0;
-        if (!sm_task(u, wave, mp, mp, r0, c0)) continue;
-        sm_chunks(acc[u], r0, c0, lane, [&](int r, int c, float* v) {
+        if (u >= ta.n) continue;
+        sm_chunks(acc[u], ta.r[u], ta.c[u], lane, [&](int r, int c, float* v) {
           float x[8];
           const int at = sm_at(r, mp, c >> 3);
           sm_get(A, r, c, x);
@@ -1145,16 +1172,16 @@ __global__ __launch_bounds__(kSmallThreads) void orth_small_kernel(SmArgs p) {
             for (int q = 0; q < 8; ++q) x[q] += static_cast<float>(l[q]);
           }
           const float d = da[r];
+          float dc[8], t = 0.f;
+          sm_row8(da, c, dc);
 #pragma unroll
           for (int q = 0; q < 8; ++q) {
+            const bool dg = c + q == r;
             v[q] *= cc / kS;
-            if (c + q == r) {
-              db[r] = v[q] / kS + d * (cb + cc * d);
-              v[q] = 0.f;
-            } else {
-              v[q] += x[q] * (cb + cc * (d + da[c + q]));
-            }
+            t = dg ? v[q] : t;
+            v[q] = dg ? 0.f : v[q] + x[q] * (cb + cc * (d + dc[q]));
           }
+          if (r >= c && r < c + 8) db[r] = t / kS + d * (cb + cc * d);
           uint4 hi, lo;
           split8(v, hi, lo);
           lds_put16(A.h + at, hi);
@@ -1165,22 +1192,24 @@ __global__ __launch_bounds__(kSmallThreads) void orth_small_kernel(SmArgs p) {
     __syncthreads();
     // apply, in X's place or to the result
     f32x16 acc[kSmallTasks];
-    if constexpr (TALL) sm_product<true, true, SPLIT, kSmallTasks>(acc, X, A, rp, cp, mp, wave, lane);
-    else sm_product<true, false, SPLIT, kSmallTasks>(acc, A, X, rp, cp, mp, wave, lane);
+    if constexpr (TALL) sm_product<true, true, SPLIT, kSmallTasks>(acc, X, A, tx, mp, lane);
+    else sm_product<true, false, SPLIT, kSmallTasks>(acc, A, X, tx, mp, lane);
     __syncthreads();
     const float f = last ? ci / kS : ci / cn;
 #pragma unroll
     for (int u = 0; u < kSmallTasks; ++u) {
-      int r0, c0;
-      if (!sm_task(u, wave, rp, cp, r0, c0)) continue;
-      sm_chunks(acc[u], r0, c0, lane, [&](int r, int c, float* v) {
+      if (u >= tx.n) continue;
+      sm_chunks(acc[u], tx.r[u], tx.c[u], lane, [&](int r, int c, float* v) {
         float x[8];
         const int at = sm_at(r, cp, c >> 3);
         sm_get(X, r, c, x);
         const f16x8 l = *reinterpret_cast<const f16x8*>(X.l + at);
+        float dc[8];
+        if constexpr (TALL) sm_row8(db, c, dc);
+        const float dr = TALL ? 0.f : db[r];
 #pragma unroll
         for (int q = 0; q < 8; ++q) {
-          const float d = TALL ? db[c + q] : db[r], y = static_cast<float>(l[q]);
+          const float d = TALL ? dc[q] : dr, y = static_cast<float>(l[q]);
           v[q] = f * ((ca + d) * x[q] + (ca + kTheta * d) * y + v[q] / kS);
         }
         if (!last) {
