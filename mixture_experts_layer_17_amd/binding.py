@@ -106,11 +106,12 @@ def _check(status: int, what: str):
 
 
 def _p(t):
-    return None if t is None else ctypes.c_void_p(t.data_ptr())
+    return None if t is None else t.data_ptr()
 
 
 def _stream():
-    return ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)
+    # the raw handle of torch.cuda.current_stream(), without building a Stream object per call
+    return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
 
 
 def _dtype_code(t: torch.Tensor) -> int:
@@ -393,95 +394,98 @@ def mx_quantize(src, axis, seg_offsets=None, nseg=0, q=None, scales=None):
 
 # --------------------------------------------------------------------------- norm, balance loss, weight update
 
-def _arg(what, name, t, shape, dtypes, dev):
-    """A device tensor as the C ABI reads it: this shape and type, contiguous, on the current device (whose current
-    stream the call is enqueued on)."""
-    if t is None:
-        return
-    dtypes = dtypes if isinstance(dtypes, tuple) else (dtypes,)
-    if tuple(t.shape) != tuple(shape) or t.dtype not in dtypes:
-        raise MoeError(f"{what}: {name} is {t.dtype} {list(t.shape)}, expected "
-                       f"{' or '.join(str(d) for d in dtypes)} {list(shape)}")
-    if not t.is_contiguous():
-        raise MoeError(f"{what}: {name} is not contiguous")
-    if t.device != dev or dev.type != "cuda" or dev.index != torch.cuda.current_device():
-        raise MoeError(f"{what}: {name} is on {t.device}, not on the current GPU")
+def _args(what, dev, specs):
+    """Device tensors as the C ABI reads them: (name, tensor or None, shape, type) each of this shape and type,
+    contiguous, and on the current device, whose current stream the call is enqueued on."""
+    for name, t, shape, dtype in specs:
+        if t is None or (t.shape == shape and t.dtype is dtype and t.device == dev and t.is_contiguous()):
+            continue
+        if t.shape != shape or t.dtype is not dtype:
+            raise MoeError(f"{what}: {name} is {t.dtype} {list(t.shape)}, expected {dtype} {list(shape)}")
+        if not t.is_contiguous():
+            raise MoeError(f"{what}: {name} is not contiguous")
+        raise MoeError(f"{what}: {name} is on {t.device}, the others on {dev}")
+    if dev.type != "cuda" or dev.index != torch.cuda.current_device():
+        raise MoeError(f"{what}: the tensors are on {dev}, not on the current GPU")
 
 
-_STORAGE = (torch.float32, torch.bfloat16)
+def _storage(what, t, dims):
+    """The C code of t's storage type, for a tensor of `dims` dimensions."""
+    if t.dim() != dims:
+        raise MoeError(f"{what}: a tensor of {dims} dimensions is needed, not {t.dim()}")
+    return _dtype_code(t)
+
+
+_F32, _I32 = torch.float32, torch.int32
 
 
 def moe_layernorm(x, weight=None, bias=None, eps=1e-5, residual=None, out=None):
     """Layer norm of the rows of x [T, d] (of x + residual, also returned as "sum"); {"y", "mean", "rstd"[, "sum"]}."""
-    what, dev = "moe_layernorm", x.device
+    what, dev, dt = "moe_layernorm", x.device, x.dtype
+    code = _storage(what, x, 2)
     T, d = x.shape
-    _arg(what, "x", x, (T, d), _STORAGE, dev)
-    for name, t, shape in (("weight", weight, (d,)), ("bias", bias, (d,)), ("residual", residual, (T, d))):
-        _arg(what, name, t, shape, x.dtype, dev)
     if out is None:
-        out = {"y": torch.empty_like(x), "mean": torch.empty(T, dtype=torch.float32, device=dev),
-               "rstd": torch.empty(T, dtype=torch.float32, device=dev)}
+        out = {"y": torch.empty_like(x), "mean": torch.empty(T, dtype=_F32, device=dev),
+               "rstd": torch.empty(T, dtype=_F32, device=dev)}
         if residual is not None:
             out["sum"] = torch.empty_like(x)
-    for name in ("y", "sum"):
-        _arg(what, name, out.get(name), (T, d), x.dtype, dev)
-    for name in ("mean", "rstd"):
-        _arg(what, name, out.get(name), (T,), torch.float32, dev)
-    _check(lib().moe_layernorm(_p(x), _p(residual), _p(weight), _p(bias), _dtype_code(x), T, d, eps, _p(out["y"]),
-                               _p(out.get("sum")), _p(out.get("mean")), _p(out.get("rstd")), _stream()), what)
+    y, total, mean, rstd = out["y"], out.get("sum"), out.get("mean"), out.get("rstd")
+    rows, cols, per = (T, d), (d,), (T,)
+    _args(what, dev, (("x", x, rows, dt), ("weight", weight, cols, dt), ("bias", bias, cols, dt),
+                      ("residual", residual, rows, dt), ("y", y, rows, dt), ("sum", total, rows, dt),
+                      ("mean", mean, per, _F32), ("rstd", rstd, per, _F32)))
+    _check(lib().moe_layernorm(_p(x), _p(residual), _p(weight), _p(bias), code, T, d, eps, _p(y), _p(total), _p(mean),
+                               _p(rstd), _stream()), what)
     return out
 
 
 def moe_layernorm_bwd(dy, x, weight, mean, rstd, dres=None, out=None, ws=None):
     """Gradients of moe_layernorm; x: the rows that were normalised ("sum" with a residual), dres: added to dx.
     {"dx", "dw", "db"}; an out without "dw" or "db" leaves that sum out."""
-    what, dev = "moe_layernorm_bwd", x.device
+    what, dev, dt = "moe_layernorm_bwd", x.device, x.dtype
+    code = _storage(what, x, 2)
     T, d = x.shape
-    _arg(what, "x", x, (T, d), _STORAGE, dev)
-    for name, t, shape in (("dy", dy, (T, d)), ("weight", weight, (d,)), ("dres", dres, (T, d))):
-        _arg(what, name, t, shape, x.dtype, dev)
-    for name, t in (("mean", mean), ("rstd", rstd)):
-        _arg(what, name, t, (T,), torch.float32, dev)
     if out is None:
-        out = {"dx": torch.empty_like(x), "dw": torch.empty(d, dtype=x.dtype, device=dev),
-               "db": torch.empty(d, dtype=x.dtype, device=dev)}
-    _arg(what, "dx", out["dx"], (T, d), x.dtype, dev)
-    for name in ("dw", "db"):
-        _arg(what, name, out.get(name), (d,), x.dtype, dev)
-    ws = _ws(lib().moe_layernorm_bwd_workspace(T, d), dev) if ws is None else ws
-    _check(lib().moe_layernorm_bwd(_p(dy), _p(x), _p(weight), _p(mean), _p(rstd), _p(dres), _dtype_code(x), T, d,
-                                   _p(out["dx"]), _p(out.get("dw")), _p(out.get("db")), _p(ws), ws.numel(),
-                                   _stream()), what)
+        out = {"dx": torch.empty_like(x), "dw": torch.empty(d, dtype=dt, device=dev),
+               "db": torch.empty(d, dtype=dt, device=dev)}
+    dx, dw, db = out["dx"], out.get("dw"), out.get("db")
+    if ws is None:
+        ws = _ws(lib().moe_layernorm_bwd_workspace(T, d), dev)
+    rows, cols, per = (T, d), (d,), (T,)
+    _args(what, dev, (("x", x, rows, dt), ("dy", dy, rows, dt), ("weight", weight, cols, dt), ("mean", mean, per, _F32),
+                      ("rstd", rstd, per, _F32), ("dres", dres, rows, dt), ("dx", dx, rows, dt), ("dw", dw, cols, dt),
+                      ("db", db, cols, dt)))
+    _check(lib().moe_layernorm_bwd(_p(dy), _p(x), _p(weight), _p(mean), _p(rstd), _p(dres), code, T, d, _p(dx), _p(dw),
+                                   _p(db), _p(ws), ws.numel(), _stream()), what)
     return out
 
 
-def _balance_args(what, logits, k, topk_idx, seq_offsets, token_mask):
-    dev = logits.device
+def _balance_specs(logits, k, topk_idx, seq_offsets, token_mask):
+    if logits.dim() != 2:
+        raise MoeError("logits: two dimensions are needed")
     T, E = logits.shape
     S = 1 if seq_offsets is None else seq_offsets.numel() - 1
-    _arg(what, "logits", logits, (T, E), torch.float32, dev)
-    _arg(what, "topk_idx", topk_idx, (T, k), torch.int32, dev)
-    _arg(what, "seq_offsets", seq_offsets, (S + 1,), torch.int32, dev)
-    _arg(what, "token_mask", token_mask, (T,), (torch.uint8, torch.bool), dev)
-    return T, E, S, dev
+    mt = torch.bool if token_mask is not None and token_mask.dtype is torch.bool else torch.uint8
+    return T, E, S, (("logits", logits, (T, E), _F32), ("topk_idx", topk_idx, (T, k), _I32),
+                     ("seq_offsets", seq_offsets, (S + 1,), _I32), ("token_mask", token_mask, (T,), mt))
 
 
 def moe_balance_loss(logits, topk_idx, alpha, zeta, seq_offsets=None, token_mask=None, out=None, ws=None):
     """Balance and z loss of a routing: {"loss" [2], "counts" [S, E], "probs" [S, E], "lse" [T], "norm" [S + 2]}."""
-    what = "moe_balance_loss"
-    k = topk_idx.shape[1]
-    T, E, S, dev = _balance_args(what, logits, k, topk_idx, seq_offsets, token_mask)
-    f32 = dict(dtype=torch.float32, device=dev)
+    what, dev, k = "moe_balance_loss", logits.device, topk_idx.shape[1]
+    T, E, S, specs = _balance_specs(logits, k, topk_idx, seq_offsets, token_mask)
     if out is None:
-        out = {"loss": torch.empty(2, **f32), "counts": torch.empty((S, E), dtype=torch.int32, device=dev),
-               "probs": torch.empty((S, E), **f32), "lse": torch.empty(T, **f32), "norm": torch.empty(S + 2, **f32)}
-    for name, shape in (("loss", (2,)), ("probs", (S, E)), ("lse", (T,)), ("norm", (S + 2,))):
-        _arg(what, name, out[name], shape, torch.float32, dev)
-    _arg(what, "counts", out["counts"], (S, E), torch.int32, dev)
-    ws = _ws(lib().moe_balance_loss_workspace(T, E, S), dev) if ws is None else ws
+        out = {"loss": torch.empty(2, dtype=_F32, device=dev), "counts": torch.empty((S, E), dtype=_I32, device=dev),
+               "probs": torch.empty((S, E), dtype=_F32, device=dev), "lse": torch.empty(T, dtype=_F32, device=dev),
+               "norm": torch.empty(S + 2, dtype=_F32, device=dev)}
+    loss, counts, probs, lse, norm = out["loss"], out["counts"], out["probs"], out["lse"], out["norm"]
+    if ws is None:
+        ws = _ws(lib().moe_balance_loss_workspace(T, E, S), dev)
+    _args(what, dev, specs + (("loss", loss, (2,), _F32), ("counts", counts, (S, E), _I32),
+                              ("probs", probs, (S, E), _F32), ("lse", lse, (T,), _F32), ("norm", norm, (S + 2,), _F32)))
     _check(lib().moe_balance_loss(_p(logits), _p(topk_idx), T, E, k, _p(seq_offsets), S, _p(token_mask), alpha, zeta,
-                                  _p(out["loss"]), _p(out["counts"]), _p(out["probs"]), _p(out["lse"]),
-                                  _p(out["norm"]), _p(ws), ws.numel(), _stream()), what)
+                                  _p(loss), _p(counts), _p(probs), _p(lse), _p(norm), _p(ws), ws.numel(), _stream()),
+           what)
     return out
 
 
@@ -489,19 +493,17 @@ def moe_balance_loss_bwd(logits, fwd, k, alpha, zeta, dloss=None, seq_offsets=No
                          gates=None, dgates=None, out=None):
     """dlogits [T, E] of the two losses (fwd: what moe_balance_loss returned for the same arguments), plus the gates'
     gradient when gates, dgates and topk_idx are given."""
-    what = "moe_balance_loss_bwd"
-    T, E, S, dev = _balance_args(what, logits, k, topk_idx, seq_offsets, token_mask)
-    for name, shape in (("lse", (T,)), ("norm", (S + 2,))):
-        _arg(what, name, fwd[name], shape, torch.float32, dev)
-    _arg(what, "counts", fwd["counts"], (S, E), torch.int32, dev)
-    _arg(what, "dloss", dloss, (2,), torch.float32, dev)
-    _arg(what, "gates", gates, (T, k), torch.float32, dev)
-    _arg(what, "dgates", dgates, (T, k), torch.float32, dev)
-    out = torch.empty((T, E), dtype=torch.float32, device=dev) if out is None else out
-    _arg(what, "out", out, (T, E), torch.float32, dev)
-    _check(lib().moe_balance_loss_bwd(_p(logits), _p(fwd["lse"]), _p(fwd["counts"]), _p(fwd["norm"]), T, E, k,
-                                      _p(seq_offsets), S, _p(token_mask), alpha, zeta, _p(dloss), _p(topk_idx),
-                                      _p(gates), _p(dgates), _p(out), _stream()), what)
+    what, dev = "moe_balance_loss_bwd", logits.device
+    T, E, S, specs = _balance_specs(logits, k, topk_idx, seq_offsets, token_mask)
+    counts, lse, norm = fwd["counts"], fwd["lse"], fwd["norm"]
+    if out is None:
+        out = torch.empty((T, E), dtype=_F32, device=dev)
+    _args(what, dev, specs + (("counts", counts, (S, E), _I32), ("lse", lse, (T,), _F32), ("norm", norm, (S + 2,), _F32),
+                              ("dloss", dloss, (2,), _F32), ("gates", gates, (T, k), _F32),
+                              ("dgates", dgates, (T, k), _F32), ("out", out, (T, E), _F32)))
+    _check(lib().moe_balance_loss_bwd(_p(logits), _p(lse), _p(counts), _p(norm), T, E, k, _p(seq_offsets), S,
+                                      _p(token_mask), alpha, zeta, _p(dloss), _p(topk_idx), _p(gates), _p(dgates),
+                                      _p(out), _stream()), what)
     return out
 
 
@@ -524,14 +526,16 @@ def _coef(steps, coef):
 
 def moe_orthogonalize(g, steps=5, coef=None, eps=1e-7, out=None, ws=None):
     """Newton-Schulz orthogonalisation of each matrix of g [E, rows, cols]."""
-    what, dev = "moe_orthogonalize", g.device
-    E, rows, cols = g.shape
-    _arg(what, "g", g, (E, rows, cols), _STORAGE, dev)
-    out = torch.empty_like(g) if out is None else out
-    _arg(what, "out", out, (E, rows, cols), g.dtype, dev)
-    ws = _ws(moe_orthogonalize_workspace(E, rows, cols, g.dtype), dev) if ws is None else ws
-    _check(lib().moe_orthogonalize(_p(g), _dtype_code(g), E, rows, cols, steps, _coef(steps, coef), eps, _p(out),
-                                   _p(ws), ws.numel(), _stream()), what)
+    what, dev, dt = "moe_orthogonalize", g.device, g.dtype
+    code = _storage(what, g, 3)
+    E, rows, cols = shape = g.shape
+    if out is None:
+        out = torch.empty_like(g)
+    if ws is None:
+        ws = _ws(lib().moe_orthogonalize_workspace(E, rows, cols, code), dev)
+    _args(what, dev, (("g", g, shape, dt), ("out", out, shape, dt)))
+    _check(lib().moe_orthogonalize(_p(g), code, E, rows, cols, steps, _coef(steps, coef), eps, _p(out), _p(ws),
+                                   ws.numel(), _stream()), what)
     return out
 
 
@@ -539,14 +543,14 @@ def moe_muon_step(g, mom, w, lr, momentum=0.95, nesterov=True, weight_decay=0.0,
                   eps=1e-7, inplace=True, ws=None):
     """One Muon step of the weights w [E, rows, cols] with momentum mom (fp32); returns (w, mom): the tensors given,
     updated, or with inplace=False new ones."""
-    what, dev = "moe_muon_step", g.device
-    E, rows, cols = g.shape
-    _arg(what, "g", g, (E, rows, cols), _STORAGE, dev)
-    _arg(what, "w", w, (E, rows, cols), g.dtype, dev)
-    _arg(what, "mom", mom, (E, rows, cols), torch.float32, dev)
+    what, dev, dt = "moe_muon_step", g.device, g.dtype
+    code = _storage(what, g, 3)
+    E, rows, cols = shape = g.shape
+    if ws is None:
+        ws = _ws(lib().moe_orthogonalize_workspace(E, rows, cols, code), dev)
+    _args(what, dev, (("g", g, shape, dt), ("w", w, shape, dt), ("mom", mom, shape, _F32)))
     w_out, mom_out = (w, mom) if inplace else (torch.empty_like(w), torch.empty_like(mom))
-    ws = _ws(moe_orthogonalize_workspace(E, rows, cols, g.dtype), dev) if ws is None else ws
-    _check(lib().moe_muon_step(_p(g), _dtype_code(g), E, rows, cols, _p(mom), momentum, int(bool(nesterov)), steps,
+    _check(lib().moe_muon_step(_p(g), code, E, rows, cols, _p(mom), momentum, int(bool(nesterov)), steps,
                                _coef(steps, coef), eps, _p(w), lr, weight_decay, scale, _p(mom_out), _p(w_out),
                                _p(ws), ws.numel(), _stream()), what)
     return w_out, mom_out

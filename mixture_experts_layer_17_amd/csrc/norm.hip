@@ -46,11 +46,18 @@ __device__ __forceinline__ uint4 ld_vec(const T* p, int n) {
   return v;
 }
 
-template <class T>
+// NT: streaming stores, for outputs larger than the caches (see stream_out).
+template <bool NT, class T>
 __device__ __forceinline__ void st_vec(T* p, int n, const uint4& v) {
   constexpr int V = Elem<T>::kVec;
   if (n >= V) {
-    __builtin_memcpy(p, &v, 16);
+    if constexpr (NT) {
+      typedef unsigned int u32x4 __attribute__((ext_vector_type(4), aligned(2)));
+      const u32x4 w = {v.x, v.y, v.z, v.w};
+      __builtin_nontemporal_store(w, reinterpret_cast<u32x4*>(p));
+    } else {
+      __builtin_memcpy(p, &v, 16);
+    }
   } else if (n > 0) {
     T t[V];
     __builtin_memcpy(t, &v, 16);
@@ -82,7 +89,7 @@ struct BwdArgs {
 // Forward, row in registers: TPR threads per row (64, or the workgroup's 256),
 // NV vectors per thread.
 // ---------------------------------------------------------------------------
-template <class T, int NV, int TPR, bool RES>
+template <class T, int NV, int TPR, bool RES, bool NT>
 __global__ __launch_bounds__(kThreads) void layernorm_fwd_kernel(FwdArgs a) {
   constexpr int V = Elem<T>::kVec, RPB = kThreads / TPR;
   __shared__ float red[2][kThreads / 64][2];
@@ -122,7 +129,7 @@ __global__ __launch_bounds__(kThreads) void layernorm_fwd_kernel(FwdArgs a) {
 #pragma unroll
         for (int j = 0; j < V; ++j) s[i][j] += r[j];
         const uint4 sv = Elem<T>::pack(s[i]);
-        if (a.sum) st_vec(static_cast<T*>(a.sum) + t * d + (i * TPR + tl) * V, nv[i], sv);
+        if (a.sum) st_vec<NT>(static_cast<T*>(a.sum) + t * d + (i * TPR + tl) * V, nv[i], sv);
         Elem<T>::unpack(sv, s[i]);
       }
 #pragma unroll
@@ -190,7 +197,7 @@ __global__ __launch_bounds__(kThreads) void layernorm_fwd_kernel(FwdArgs a) {
 #pragma unroll
         for (int j = 0; j < V; ++j) o[j] += f[j];
       }
-      st_vec(static_cast<T*>(a.y) + t * d + (i * TPR + tl) * V, nv[i], Elem<T>::pack(o));
+      st_vec<NT>(static_cast<T*>(a.y) + t * d + (i * TPR + tl) * V, nv[i], Elem<T>::pack(o));
     }
   }
 }
@@ -215,7 +222,7 @@ __device__ __forceinline__ void block_sum(float (&v)[N], float (*red)[N]) {
 
 // Forward for rows too long for a workgroup's registers: three passes over the
 // row, the later two from the caches.
-template <class T>
+template <class T, bool NT>
 __global__ __launch_bounds__(kThreads) void layernorm_fwd_long_kernel(FwdArgs a) {
   constexpr int V = Elem<T>::kVec;
   __shared__ float red[kThreads / 64][1];
@@ -260,7 +267,7 @@ __global__ __launch_bounds__(kThreads) void layernorm_fwd_long_kernel(FwdArgs a)
     for (int c = threadIdx.x * V; c < d; c += kThreads * V) {
       float s[V], f[V];
       row(c, s);
-      if (a.sum) st_vec(static_cast<T*>(a.sum) + o0 + c, d - c, Elem<T>::pack(s));
+      if (a.sum) st_vec<NT>(static_cast<T*>(a.sum) + o0 + c, d - c, Elem<T>::pack(s));
   #pragma unroll
       for (int j = 0; j < V; ++j) s[j] = (s[j] - m) * rs;
       if (a.w) {
@@ -273,7 +280,7 @@ __global__ __launch_bounds__(kThreads) void layernorm_fwd_long_kernel(FwdArgs a)
   #pragma unroll
         for (int j = 0; j < V; ++j) s[j] += f[j];
       }
-      st_vec(static_cast<T*>(a.y) + o0 + c, d - c, Elem<T>::pack(s));
+      st_vec<NT>(static_cast<T*>(a.y) + o0 + c, d - c, Elem<T>::pack(s));
     }
   }
 }
@@ -281,11 +288,11 @@ __global__ __launch_bounds__(kThreads) void layernorm_fwd_long_kernel(FwdArgs a)
 // ---------------------------------------------------------------------------
 // Backward, row in registers; the workgroup's dw, db partials too.
 // ---------------------------------------------------------------------------
-template <class T, int NV, int TPR, bool WGRAD>
+template <class T, int NV, int TPR, bool WGRAD, bool NT>
 __global__ __launch_bounds__(kThreads) void layernorm_bwd_kernel(BwdArgs a) {
   constexpr int V = Elem<T>::kVec, RPB = kThreads / TPR;
   __shared__ float red[2][kThreads / 64][2];
-  __shared__ float comb[RPB > 1 ? TPR * V : 1];
+  __shared__ float comb[RPB][RPB > 1 && WGRAD ? TPR * NV * V : 1];
   const int d = a.d, tl = threadIdx.x % TPR;
   const T* dy = static_cast<const T*>(a.dy);
   const T* x = static_cast<const T*>(a.x);
@@ -371,7 +378,7 @@ __global__ __launch_bounds__(kThreads) void layernorm_bwd_kernel(BwdArgs a) {
 #pragma unroll
         for (int j = 0; j < V; ++j) o[j] += f[j];
       }
-      st_vec(static_cast<T*>(a.dx) + t * d + (i * TPR + tl) * V, nv[i], Elem<T>::pack(o));
+      st_vec<NT>(static_cast<T*>(a.dx) + t * d + (i * TPR + tl) * V, nv[i], Elem<T>::pack(o));
     }
   }
   if constexpr (WGRAD) {
@@ -379,21 +386,23 @@ __global__ __launch_bounds__(kThreads) void layernorm_bwd_kernel(BwdArgs a) {
     float* pb = a.part + (static_cast<int64_t>(gridDim.x) + blockIdx.x) * d;
     const int grp = threadIdx.x / TPR;
     auto flush = [&](float (&g)[NV][V], float* dst) {
+      if constexpr (RPB > 1) {  // the row groups meet in LDS and are added in order
+        __syncthreads();
 #pragma unroll
-      for (int i = 0; i < NV; ++i) {
-        if constexpr (RPB > 1) {  // add the row groups in order
-          for (int k = 0; k < RPB - 1; ++k) {
-            __syncthreads();
-            if (grp == k)
+        for (int i = 0; i < NV; ++i)
 #pragma unroll
-              for (int j = 0; j < V; ++j) comb[j * TPR + tl] = g[i][j];
-            __syncthreads();
-            if (grp == k + 1)
+          for (int j = 0; j < V; ++j) comb[grp][(i * V + j) * TPR + tl] = g[i][j];
+        __syncthreads();
+        for (int k = threadIdx.x; k < TPR * NV * V; k += kThreads) {
+          const int c = (k / TPR / V * TPR + k % TPR) * V + k / TPR % V;  // entry (i V + j) TPR + tl
+          float s = comb[0][k];
 #pragma unroll
-              for (int j = 0; j < V; ++j) g[i][j] += comb[j * TPR + tl];
-          }
+          for (int r = 1; r < RPB; ++r) s += comb[r][k];
+          if (c < d) dst[c] = s;
         }
-        if (grp == RPB - 1)
+      } else {
+#pragma unroll
+        for (int i = 0; i < NV; ++i)
 #pragma unroll
           for (int j = 0; j < V; ++j)
             if (j < nv[i]) dst[(i * TPR + tl) * V + j] = g[i][j];
@@ -405,7 +414,7 @@ __global__ __launch_bounds__(kThreads) void layernorm_bwd_kernel(BwdArgs a) {
 }
 
 // Backward of long rows: dx in two passes per row; dw, db by columns below.
-template <class T>
+template <class T, bool NT>
 __global__ __launch_bounds__(kThreads) void layernorm_bwd_long_kernel(BwdArgs a) {
   constexpr int V = Elem<T>::kVec;
   __shared__ float red[kThreads / 64][2];
@@ -447,7 +456,7 @@ __global__ __launch_bounds__(kThreads) void layernorm_bwd_long_kernel(BwdArgs a)
   #pragma unroll
         for (int j = 0; j < V; ++j) o[j] += v[j];
       }
-      st_vec(static_cast<T*>(a.dx) + o0 + c, d - c, Elem<T>::pack(o));
+      st_vec<NT>(static_cast<T*>(a.dx) + o0 + c, d - c, Elem<T>::pack(o));
     }
   }
 }
@@ -506,78 +515,81 @@ Shape shape_for(int d, int vec) {
   return {kThreads, 0};
 }
 
-constexpr int kMaxBlocks = 2048;  // forward: up to eight workgroups per compute unit, looping over rows
-constexpr int kMaxGroups = 512;   // backward: two per compute unit, each writing 2 d partial sums
+// Outputs of more than the L2s hold (8 x 4 MB) leave by streaming stores: 16384
+// rows of 4096 bf16 with a residual 103 -> 87 us (6.2 TB/s), 8192 of 2048 17.4 ->
+// 15.6 us; smaller ones stay cached for the router and the dispatch that read them.
+bool stream_out(int64_t T, int d, int bytes) { return T * d * bytes > int64_t{32} << 20; }
 
+constexpr int kMaxBlocks = 2048;  // forward: up to eight workgroups per compute unit, looping over rows
 unsigned long_grid(int64_t T) { return static_cast<unsigned>(T < kMaxBlocks ? T : kMaxBlocks); }
 
-int bwd_groups(int64_t T) {
-  return static_cast<int>(T < kMaxGroups ? (T > 0 ? T : 1) : kMaxGroups);
+// Workgroups of the backward, each writing 2 d partial sums: one per compute unit
+// where a workgroup has four rows in flight (8192 rows of 2048: 35 us against 44
+// us with two), two where it has one (16384 rows of 4096: 115 us against 120 us).
+constexpr int kMaxGroups = 512;
+int bwd_groups(int64_t T, int tpr = kThreads) {
+  const int64_t most = tpr == 64 ? kMaxGroups / 2 : kMaxGroups, n = cdiv(T > 0 ? T : 1, kThreads / tpr);
+  return static_cast<int>(n < most ? n : most);
 }
 
 size_t bwd_ws_bytes(int64_t T, int d) { return static_cast<size_t>(2) * bwd_groups(T) * d * sizeof(float); }
 
-template <class T, int NV, int TPR>
+template <class T, int NV, int TPR, bool NT>
 void launch_fwd(const FwdArgs& a, hipStream_t s) {
   const int64_t blocks = cdiv(a.T, kThreads / TPR);
   const dim3 grid(static_cast<unsigned>(blocks < kMaxBlocks ? blocks : kMaxBlocks));
-  if (a.res) MOE_LAUNCH("layernorm", (layernorm_fwd_kernel<T, NV, TPR, true>), grid, dim3(kThreads), 0, s, a);
-  else MOE_LAUNCH("layernorm", (layernorm_fwd_kernel<T, NV, TPR, false>), grid, dim3(kThreads), 0, s, a);
+  if (a.res) MOE_LAUNCH("layernorm", (layernorm_fwd_kernel<T, NV, TPR, true, NT>), grid, dim3(kThreads), 0, s, a);
+  else MOE_LAUNCH("layernorm", (layernorm_fwd_kernel<T, NV, TPR, false, NT>), grid, dim3(kThreads), 0, s, a);
 }
 
-template <class T>
+template <class T, bool NT>
 int run_fwd(const FwdArgs& a, hipStream_t s) {
   const Shape sh = shape_for(a.d, Elem<T>::kVec);
   if (sh.nv == 0) {
-    MOE_LAUNCH("layernorm", (layernorm_fwd_long_kernel<T>), dim3(long_grid(a.T)), dim3(kThreads), 0, s, a);
+    MOE_LAUNCH("layernorm", (layernorm_fwd_long_kernel<T, NT>), dim3(long_grid(a.T)), dim3(kThreads), 0, s, a);
   } else if (sh.tpr == 64) {
-    if (sh.nv == 1) launch_fwd<T, 1, 64>(a, s);
-    else if (sh.nv == 2) launch_fwd<T, 2, 64>(a, s);
-    else launch_fwd<T, 4, 64>(a, s);
+    if (sh.nv == 1) launch_fwd<T, 1, 64, NT>(a, s);
+    else if (sh.nv == 2) launch_fwd<T, 2, 64, NT>(a, s);
+    else launch_fwd<T, 4, 64, NT>(a, s);
   } else {
-    if (sh.nv == 2) launch_fwd<T, 2, 256>(a, s);
-    else launch_fwd<T, 4, 256>(a, s);
+    if (sh.nv == 2) launch_fwd<T, 2, 256, NT>(a, s);
+    else launch_fwd<T, 4, 256, NT>(a, s);
   }
   return launch_status();
 }
 
-template <class T, int NV, int TPR>
+template <class T, int NV, int TPR, bool NT>
 void launch_bwd(const BwdArgs& a, int G, hipStream_t s) {
-  if (a.part) MOE_LAUNCH("layernorm_bwd", (layernorm_bwd_kernel<T, NV, TPR, true>), dim3(G), dim3(kThreads), 0, s, a);
-  else MOE_LAUNCH("layernorm_bwd", (layernorm_bwd_kernel<T, NV, TPR, false>), dim3(G), dim3(kThreads), 0, s, a);
+  if (a.part)
+    MOE_LAUNCH("layernorm_bwd", (layernorm_bwd_kernel<T, NV, TPR, true, NT>), dim3(G), dim3(kThreads), 0, s, a);
+  else
+    MOE_LAUNCH("layernorm_bwd", (layernorm_bwd_kernel<T, NV, TPR, false, NT>), dim3(G), dim3(kThreads), 0, s, a);
 }
 
-template <class T>
+template <class T, bool NT>
 int run_bwd(const BwdArgs& a, void* dw, void* db, hipStream_t s) {
   const Shape sh = shape_for(a.d, Elem<T>::kVec);
-  int G = bwd_groups(a.T);
-  if (a.T > 0) {
-    if (sh.nv == 0) {
-      MOE_LAUNCH("layernorm_bwd", (layernorm_bwd_long_kernel<T>), dim3(long_grid(a.T)), dim3(kThreads), 0, s, a);
-      if (a.part) {
-        G = G < 64 ? G : 64;
-        MOE_LAUNCH("layernorm_wgrad", (layernorm_wgrad_long_kernel<T>),
-                   dim3(static_cast<unsigned>(cdiv(a.d, kThreads)), G), dim3(kThreads), 0, s, a);
-      }
-    } else {
-      const int64_t blocks = cdiv(a.T, kThreads / sh.tpr);
-      if (blocks < G) G = static_cast<int>(blocks);
-      if (sh.tpr == 64) {
-        if (sh.nv == 1) launch_bwd<T, 1, 64>(a, G, s);
-        else if (sh.nv == 2) launch_bwd<T, 2, 64>(a, G, s);
-        else launch_bwd<T, 4, 64>(a, G, s);
-      } else {
-        if (sh.nv == 2) launch_bwd<T, 2, 256>(a, G, s);
-        else launch_bwd<T, 4, 256>(a, G, s);
-      }
-    }
-  } else {
+  int G = bwd_groups(a.T, sh.tpr);
+  if (a.T == 0) {
     G = 0;  // no rows: the sums are zero
+  } else if (sh.nv == 0) {
+    MOE_LAUNCH("layernorm_bwd", (layernorm_bwd_long_kernel<T, NT>), dim3(long_grid(a.T)), dim3(kThreads), 0, s, a);
+    if (a.part) {
+      G = G < 64 ? G : 64;
+      MOE_LAUNCH("layernorm_wgrad", (layernorm_wgrad_long_kernel<T>),
+                 dim3(static_cast<unsigned>(cdiv(a.d, kThreads)), G), dim3(kThreads), 0, s, a);
+    }
+  } else if (sh.tpr == 64) {
+    if (sh.nv == 1) launch_bwd<T, 1, 64, NT>(a, G, s);
+    else if (sh.nv == 2) launch_bwd<T, 2, 64, NT>(a, G, s);
+    else launch_bwd<T, 4, 64, NT>(a, G, s);
+  } else {
+    if (sh.nv == 2) launch_bwd<T, 2, 256, NT>(a, G, s);
+    else launch_bwd<T, 4, 256, NT>(a, G, s);
   }
   if (a.part)
-    MOE_LAUNCH("layernorm_wgrad_sum", (layernorm_wgrad_sum_kernel<T>),
-               dim3(static_cast<unsigned>(cdiv(a.d, 16)), 2), dim3(kThreads), 0, s, a.part, G, a.d,
-               static_cast<T*>(dw), static_cast<T*>(db));
+    MOE_LAUNCH("layernorm_wgrad_sum", (layernorm_wgrad_sum_kernel<T>), dim3(static_cast<unsigned>(cdiv(a.d, 16)), 2),
+               dim3(kThreads), 0, s, a.part, G, a.d, static_cast<T*>(dw), static_cast<T*>(db));
   return launch_status();
 }
 
@@ -604,7 +616,9 @@ extern "C" int moe_layernorm(const void* x, const void* residual, const void* we
     if (!aligned16(p)) return MOE_EINVAL;
   const FwdArgs a{x, residual, weight, bias, y, sum, mean, rstd, T, d, eps};
   hipStream_t s = static_cast<hipStream_t>(stream);
-  return dtype == MOE_F32 ? run_fwd<float>(a, s) : run_fwd<uint16_t>(a, s);
+  const bool nt = stream_out(T, d, dtype == MOE_F32 ? 4 : 2);
+  if (dtype == MOE_F32) return nt ? run_fwd<float, true>(a, s) : run_fwd<float, false>(a, s);
+  return nt ? run_fwd<uint16_t, true>(a, s) : run_fwd<uint16_t, false>(a, s);
 }
 
 extern "C" size_t moe_layernorm_bwd_workspace(int64_t T, int32_t d) {
@@ -627,5 +641,7 @@ extern "C" int moe_layernorm_bwd(const void* dy, const void* x, const void* weig
   }
   const BwdArgs a{dy, x, weight, dres, mean, rstd, dx, dw || db ? static_cast<float*>(ws) : nullptr, T, d};
   hipStream_t s = static_cast<hipStream_t>(stream);
-  return dtype == MOE_F32 ? run_bwd<float>(a, dw, db, s) : run_bwd<uint16_t>(a, dw, db, s);
+  const bool nt = stream_out(T, d, dtype == MOE_F32 ? 4 : 2);
+  if (dtype == MOE_F32) return nt ? run_bwd<float, true>(a, dw, db, s) : run_bwd<float, false>(a, dw, db, s);
+  return nt ? run_bwd<uint16_t, true>(a, dw, db, s) : run_bwd<uint16_t, false>(a, dw, db, s);
 }

@@ -113,6 +113,32 @@ def test_layernorm_bwd(gpu, T, d, dtype):
         close("dx alone", only["dx"], dx, half(dtype), 1e-6 * big + 1e-5 * np.abs(dx).max())
 
 
+@pytest.mark.parametrize("T,d,dtype", [(4200, 4096, "bf16"), (9001, 2047, "bf16"), (2100, 4097, "f32"), (9000, 1024, "f32"),
+                                       (40000, 515, "bf16"), (1100, 16400, "bf16")])
+def test_layernorm_large(gpu, T, d, dtype):
+    """Sizes past the L2s (streaming stores) and many rows per workgroup, against fp64 on the GPU."""
+    gu.say(f"case layernorm large T={T} d={d} {dtype}")
+    gen = torch.Generator(device="cuda")
+    gen.manual_seed(T + d)
+    rnd = lambda *n: torch.randn(n, generator=gen, device="cuda").to(DT[dtype])
+    x, res, dy, w, b = rnd(T, d), rnd(T, d), rnd(T, d), rnd(d), rnd(d)
+    fw = B.moe_layernorm(x, w, b, residual=res)
+    bw = B.moe_layernorm_bwd(dy, fw["sum"], w, fw["mean"], fw["rstd"], dres=res)
+    torch.cuda.synchronize()
+    assert torch.equal(fw["sum"], (x.float() + res.float()).to(x.dtype))
+    s = fw["sum"].double()
+    mu = s.mean(1, keepdim=True)
+    r = 1 / torch.sqrt(((s - mu) ** 2).mean(1, keepdim=True) + 1e-5)
+    h = (s - mu) * r
+    v = dy.double() * w.double()
+    dx = r * (v - v.mean(1, keepdim=True) - h * (v * h).mean(1, keepdim=True)) + res.double()
+    rel = half(dtype)
+    for name, got, ref, slack in (("y", fw["y"], h * w.double() + b.double(), 1e-4), ("dx", bw["dx"], dx, 1e-4),
+                                  ("dw", bw["dw"], (dy.double() * h).sum(0), 1e-5 * float((dy.double() * h).abs().sum(0).max())),
+                                  ("db", bw["db"], dy.double().sum(0), 1e-5 * float(dy.double().abs().sum(0).max()))):
+        assert bool(((got.double() - ref).abs() <= rel * ref.abs() + slack).all()), name
+
+
 def test_layernorm_no_rows(gpu):
     x = torch.empty((0, 40), device="cuda")
     st = torch.empty(0, device="cuda")
