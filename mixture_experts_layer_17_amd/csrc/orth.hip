@@ -299,16 +299,20 @@ struct MmArgs {
 
 // BM x BN outputs per workgroup by 2 x 2 waves of WM x WN; K step BK; a ring of
 // kRing K steps of both operands in LDS; fragments of KG 16-deep slices (a phase)
-// in registers at a time, twice.
-template <int BM_, int BN_, int BK_, int RING_, int KG_>
+// in registers at a time, twice.  PAIRS: operands with lo parts, which come into
+// the same step, so that the four tiles of a step serve its three products.
+template <int BM_, int BN_, int BK_, int RING_, int KG_, bool PAIRS_>
 struct Tile {
   static constexpr int BM = BM_, BN = BN_, BK = BK_, kRing = RING_, KG = KG_;
+  static constexpr bool kPairs = PAIRS_;
   static constexpr int kPhases = BK / 16 / KG;
   static constexpr int WM = BM / 2, WN = BN / 2, TM = WM / 32, TN = WN / 32;
-  static constexpr int kA = BM * BK, kSlot = (BM + BN) * BK;  // elements: the A tile, then the B tile
-  static constexpr int kLoads = kSlot / 512 / 4;              // LDS-DMA instructions per wave and step
+  static constexpr int kA = BM * BK, kHi = (BM + BN) * BK;  // elements: the A tile, then the B tile (then lo likewise)
+  static constexpr int kSlot = kHi * (PAIRS_ ? 2 : 1);
+  static constexpr int kLoads = kSlot / 512 / 4;            // LDS-DMA instructions per wave and step
   static constexpr int kLds = kRing * kSlot;
-  static_assert(kA % 2048 == 0 && kSlot % 2048 == 0, "whole LDS-DMA instructions per wave");
+  static constexpr int kWavesPerSimd = kLds * 2 > 80 * 1024 ? 1 : 2;  // workgroups per compute unit the LDS allows, at most 2
+  static_assert(kA % 2048 == 0 && kHi % 2048 == 0, "whole LDS-DMA instructions per wave");
 };
 
 // 16-byte chunk swizzles against bank conflicts.  K-contiguous tiles (BK
@@ -810,9 +814,10 @@ __device__ __forceinline__ bool join_k(f32x16 (&acc)[C::TM][C::TN], const MmArgs
 }
 
 // FINAL: apply's last step, which writes the result instead of the next X.
-template <class C, int KIND, bool AKC, bool BKC, bool SPLIT, bool FINAL>
-__global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2)))
+template <class C, int KIND, bool AKC, bool BKC, bool FINAL>
+__global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(C::kWavesPerSimd)))
 void orth_mm_kernel(MmArgs p) {
+  constexpr bool SPLIT = C::kPairs;
   __shared__ __attribute__((aligned(16))) uint16_t lds[C::kLds];
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -841,18 +846,19 @@ void orth_mm_kernel(MmArgs p) {
   A.init(p.ah + e * p.sa, SPLIT ? p.al + e * p.sa : nullptr, p.lda, m0, p.M, p.K, wave, lane);
   B.init(p.bh + e * p.sb, SPLIT ? p.bl + e * p.sb : nullptr, p.ldb, n0, p.N, p.K, wave, lane);
   const int nk1 = (p.K + C::BK - 1) / C::BK;
-  const int nk_all = SPLIT ? 3 * nk1 : nk1;  // hi hi, hi lo, lo hi
-  const int k_lo = kKSplit ? static_cast<int>(static_cast<int64_t>(nk_all) * ks_i / ks_n) : 0;
-  const int nk = (kKSplit ? static_cast<int>(static_cast<int64_t>(nk_all) * (ks_i + 1) / ks_n) : nk_all) - k_lo;
+  const int k_lo = kKSplit ? static_cast<int>(static_cast<int64_t>(nk1) * ks_i / ks_n) : 0;
+  const int nk = (kKSplit ? static_cast<int>(static_cast<int64_t>(nk1) * (ks_i + 1) / ks_n) : nk1) - k_lo;
   int head = 0;  // K step (from k_lo) to load next, and its ring slot
   int head_slot = 0;
   auto issue = [&]() {
     uint16_t* dst = lds + head_slot * C::kSlot;
-    const int at = k_lo + head;
-    const int part = SPLIT ? (at >= nk1) + (at >= 2 * nk1) : 0;
-    const int k = at - part * nk1;
-    A.issue(SPLIT && part == 2, k * A.kstep, dst, wave);
-    B.issue(SPLIT && part == 1, k * B.kstep, dst + C::kA, wave);
+    const int k = k_lo + head;
+    A.issue(false, k * A.kstep, dst, wave);
+    B.issue(false, k * B.kstep, dst + C::kA, wave);
+    if constexpr (SPLIT) {
+      A.issue(true, k * A.kstep, dst + C::kHi, wave);
+      B.issue(true, k * B.kstep, dst + C::kHi + C::kA, wave);
+    }
     ++head;
     head_slot = head_slot + 1 == C::kRing ? 0 : head_slot + 1;
   };
@@ -869,24 +875,38 @@ void orth_mm_kernel(MmArgs p) {
   // it run.  Before a step's last phase all its fragments are in registers:
   // there the waves meet, the next step's loads are known to have landed, and the
   // step's own ring slot is free for the loads of step kt + kRing.
+  constexpr int kLoG = SPLIT ? C::KG : 1;
   f16x8 fa[2][C::KG][C::TM], fb[2][C::KG][C::TN];
+  f16x8 la[2][kLoG][C::TM], lb[2][kLoG][C::TN];
   auto read = [&](int slot, int ph, int buf) {
     const uint16_t* as = lds + slot * C::kSlot;
 #pragma unroll
-    for (int g = 0; g < C::KG; ++g)
+    for (int g = 0; g < C::KG; ++g) {
       read_frags<C, AKC, BKC>(as, as + C::kA, wm, wn, ph * C::KG + g, lane, fa[buf][g], fb[buf][g]);
+      if constexpr (SPLIT)
+        read_frags<C, AKC, BKC>(as + C::kHi, as + C::kHi + C::kA, wm, wn, ph * C::KG + g, lane, la[buf][g],
+                                lb[buf][g]);
+    }
   };
   // a wave whose outputs lie above the diagonal only helps with the loads
   const bool idle = KIND != kApply && (m0 + wm * C::WM) / C::BN < (n0 + wn * C::WN) / C::BN;
   auto mma = [&](int buf) {
     if (KIND != kApply && idle) return;
-#pragma unroll
-    for (int g = 0; g < C::KG; ++g)
+    auto product = [&](const f16x8 (&x)[C::TM], const f16x8 (&y)[C::TN]) {
 #pragma unroll
       for (int i = 0; i < C::TM; ++i)
 #pragma unroll
         for (int j = 0; j < C::TN; ++j)
-          acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(fb[buf][g][j], fa[buf][g][i], acc[i][j], 0, 0, 0);
+          acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(y[j], x[i], acc[i][j], 0, 0, 0);
+    };
+#pragma unroll
+    for (int g = 0; g < C::KG; ++g) {
+      product(fa[buf][g], fb[buf][g]);
+      if constexpr (SPLIT) {
+        product(fa[buf][g], lb[buf][g]);
+        product(la[buf][g], fb[buf][g]);
+      }
+    }
   };
   for (int s = 0; s < C::kRing && s < nk; ++s) issue();
   if (nk >= C::kRing) wait_vm<(C::kRing - 1) * C::kLoads>();
@@ -1264,9 +1284,12 @@ Sizes sizes_of(int E, int rows, int cols, bool split) {
 // 256 x 128, two to a unit, once they fill the chip (8 of 1024 x 2048, 512 tiles:
 // apply 51 us against 54 and 72); 128 x 128 between (one of 2048 x 2048, 256
 // tiles: apply 33 us against 45 with 256 x 128 and 42 with 64 x 64).
-using Big = Tile<256, 128, 32, 3, 1>;
-using Mid = Tile<128, 128, 64, 2, 2>;
-using Small = Tile<64, 64, 64, 3, 2>;
+using Big = Tile<256, 128, 32, 3, 1, false>;
+using Mid = Tile<128, 128, 64, 2, 2, false>;
+using Small = Tile<64, 64, 64, 3, 2, false>;
+using BigPairs = Tile<256, 128, 32, 3, 1, true>;
+using MidPairs = Tile<128, 128, 32, 2, 1, true>;
+using SmallPairs = Tile<64, 64, 32, 3, 1, true>;
 
 // Tiles of a symmetric m x m output, and of an r x c one, in E matrices.
 template <class C>
@@ -1292,7 +1315,7 @@ int k_split(int64_t tiles, int64_t steps) {
 // of the Gram (K = the longer side) or the polynomial (the shorter side); 1 where other tiles are used
 int k_split(const Sizes& z, int64_t K) {
   const int64_t tiles = sym_tiles<Small>(z.mp, z.E);
-  return tiles > 256 ? 1 : k_split(tiles, cdiv(K, Small::BK) * (z.split ? 3 : 1));
+  return tiles > 256 ? 1 : k_split(tiles, cdiv(K, 64) * (z.split ? 2 : 1));
 }
 
 struct Ws {
@@ -1339,17 +1362,15 @@ size_t ws_layout(const Sizes& z, char* base, Ws* w) {
 }
 
 template <class C, int KIND, bool AKC, bool BKC>
-void launch_mm(const char* name, const MmArgs& a, bool split, hipStream_t s) {
+void launch_mm(const char* name, const MmArgs& a, hipStream_t s) {
   const dim3 grid(xcd_grid(a.tiles * a.ks));
-  const bool last = KIND == kApply && a.out != kOutX;
-  auto go = [&](auto sp, auto fin) {
-    MOE_LAUNCH(name, (orth_mm_kernel<C, KIND, AKC, BKC, decltype(sp)::value, decltype(fin)::value>), grid, dim3(256),
-               0, s, a);
-  };
-  constexpr std::integral_constant<bool, KIND == kApply> fin{};
-  constexpr std::false_type no{};
-  if (split) last ? go(std::true_type{}, fin) : go(std::true_type{}, no);
-  else last ? go(std::false_type{}, fin) : go(std::false_type{}, no);
+  if constexpr (KIND == kApply) {
+    if (a.out != kOutX) {
+      MOE_LAUNCH(name, (orth_mm_kernel<C, KIND, AKC, BKC, true>), grid, dim3(256), 0, s, a);
+      return;
+    }
+  }
+  MOE_LAUNCH(name, (orth_mm_kernel<C, KIND, AKC, BKC, false>), grid, dim3(256), 0, s, a);
 }
 
 template <int KIND, bool AKC, bool BKC>
@@ -1365,12 +1386,15 @@ void launch_any(const char* name, MmArgs& a, const Sizes& z, hipStream_t s) {
     }
     a.tiles = static_cast<int64_t>(a.tm) * a.tn * z.E;
     a.ks = C::BM == 64 && !(KIND == kApply) ? k_split(z, a.K) : 1;
-    launch_mm<C, KIND, AKC, BKC>(name, a, z.split, s);
+    launch_mm<C, KIND, AKC, BKC>(name, a, s);
   };
   const bool ap = KIND == kApply;
-  if ((ap ? rect_tiles<Small>(a.M, a.N, z.E) : sym_tiles<Small>(a.M, z.E)) <= 768) go(Small{});
-  else if ((ap ? rect_tiles<Big>(a.M, a.N, z.E) : sym_tiles<Big>(a.M, z.E)) >= 480) go(Big{});
-  else go(Mid{});
+  if ((ap ? rect_tiles<Small>(a.M, a.N, z.E) : sym_tiles<Small>(a.M, z.E)) <= 768)
+    z.split ? go(SmallPairs{}) : go(Small{});
+  else if ((ap ? rect_tiles<Big>(a.M, a.N, z.E) : sym_tiles<Big>(a.M, z.E)) >= 480)
+    z.split ? go(BigPairs{}) : go(Big{});
+  else
+    z.split ? go(MidPairs{}) : go(Mid{});
 }
 
 void run_products(const Sizes& z, const Ws& w, MmArgs a, const float (*coef)[3], int out, bool exact0,
