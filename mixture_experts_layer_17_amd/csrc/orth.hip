@@ -1283,11 +1283,12 @@ Sizes sizes_of(int E, int rows, int cols, bool split) {
 // x 1024: Gram 15 us against 26 us with 128 x 128 and 46 us with 256 x 128);
 // 256 x 128, two to a unit, once they fill the chip (8 of 1024 x 2048, 512 tiles:
 // apply 51 us against 54 and 72); 128 x 128 between (one of 2048 x 2048, 256
-// tiles: apply 33 us against 45 with 256 x 128 and 42 with 64 x 64).
+// tiles: apply 33 us against 45 with 256 x 128 and 42 with 64 x 64), and for
+// pairs, whose 256 x 128 steps leave room for one workgroup per unit only, from
+// there on (32 of 2048 x 1024: Gram 250 us against 306 us).
 using Big = Tile<256, 128, 32, 3, 1, false>;
 using Mid = Tile<128, 128, 64, 2, 2, false>;
 using Small = Tile<64, 64, 64, 3, 2, false>;
-using BigPairs = Tile<256, 128, 32, 3, 1, true>;
 using MidPairs = Tile<128, 128, 32, 2, 1, true>;
 using SmallPairs = Tile<64, 64, 32, 3, 1, true>;
 
@@ -1391,10 +1392,12 @@ void launch_any(const char* name, MmArgs& a, const Sizes& z, hipStream_t s) {
   const bool ap = KIND == kApply;
   if ((ap ? rect_tiles<Small>(a.M, a.N, z.E) : sym_tiles<Small>(a.M, z.E)) <= 768)
     z.split ? go(SmallPairs{}) : go(Small{});
+  else if (z.split)
+    go(MidPairs{});
   else if ((ap ? rect_tiles<Big>(a.M, a.N, z.E) : sym_tiles<Big>(a.M, z.E)) >= 480)
-    z.split ? go(BigPairs{}) : go(Big{});
+    go(Big{});
   else
-    z.split ? go(MidPairs{}) : go(Mid{});
+    go(Mid{});
 }
 
 void run_products(const Sizes& z, const Ws& w, MmArgs a, const float (*coef)[3], int out, bool exact0,
