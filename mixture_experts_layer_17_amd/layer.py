@@ -6,7 +6,8 @@ grouped GEMM, combine; the routing metadata never leaves the GPU, so the host
 enqueues the whole step without a single synchronisation.
 
 This module only allocates device buffers (once, up front) and calls the
-binding in order; every step runs in libmoe's kernels.
+binding in order; every step runs in libmoe's kernels, the norm before the
+layer, the balance loss and the weight update among them.
 """
 from __future__ import annotations
 
@@ -47,12 +48,24 @@ class LayerStep:
       "rows"                they write the bf16 rows and their rows layout (moe_dispatch_mx / moe_combine_bwd_mx),
                             the FFN quantises the token-axis layouts;
       "none"                plain dispatch and combine backward; the FFN quantises everything.
+    A block's training step around the layer (each off by default):
+      norm                  the layer runs on LayerNorm(x) (dev_inputs may hold "ln_w" and "ln_b" [d]), as in the
+                            residual block y = x + layer(LayerNorm(x)): the backward's dx is the norm's gradient plus
+                            dout, which reaches x along the residual stream (y itself is left to the next block's norm,
+                            whose residual argument adds it up in the same pass);
+      balance               (alpha, zeta): the router's balance and z losses (self.balance holds them with the counts),
+                            their gradient joining the gates' in one pass; seq_offsets and token_mask as in
+                            moe_balance_loss;
+      update(...)           a Muon step of the expert weights from this step's gradients.
     """
 
     def __init__(self, w: Workload, dev_inputs: dict, mx_weight_cache: bool = False,
-                 mx_weights_per_step: bool = False, mx_movement: str = "tok", keep_rows: bool = False):
+                 mx_weights_per_step: bool = False, mx_movement: str = "tok", keep_rows: bool = False,
+                 norm: bool = False, balance=None, seq_offsets=None, token_mask=None):
         self.w = w
         self.inp = dev_inputs
+        self.norm, self.balance_coef = bool(norm), balance
+        self.seq_offsets, self.token_mask = seq_offsets, token_mask
         self.mx_wcache = None
         self.mx_per_step = bool(mx_weights_per_step) and w.prec == "mxfp8"
         assert mx_movement in ("tok", "rows", "none"), mx_movement
@@ -103,6 +116,24 @@ class LayerStep:
             self.router_ws = B._ws(B.lib().moe_router_logits_bwd_workspace(T, d, E), dev)
         if (mx_weight_cache or self.mx_per_step) and w.prec == "mxfp8":
             self.build_weight_cache()
+        f32 = dict(dtype=torch.float32, device=dev)
+        self.h = x  # the layer's input rows
+        if self.norm:
+            self.ln = {"y": torch.empty_like(x), "mean": torch.empty(T, **f32), "rstd": torch.empty(T, **f32)}
+            self.h = self.ln["y"]
+            self.dh = torch.empty_like(x)
+            self.ln_grads = {"dx": self.dx}
+            for name in ("w", "b"):
+                if f"ln_{name}" in dev_inputs:
+                    self.ln_grads[f"d{name}"] = torch.empty(d, dtype=dt, device=dev)
+            self.ln_ws = B._ws(B.lib().moe_layernorm_bwd_workspace(T, d), dev)
+        if balance is not None:
+            S = 1 if seq_offsets is None else seq_offsets.numel() - 1
+            self.balance = {"loss": torch.empty(2, **f32), "counts": torch.empty((S, E), **i32),
+                            "probs": torch.empty((S, E), **f32), "lse": torch.empty(T, **f32),
+                            "norm": torch.empty(S + 2, **f32)}
+            self.balance_ws = B._ws(B.lib().moe_balance_loss_workspace(T, E, S), dev)
+        self.mom = None  # Muon momentum and workspaces, made by the first update
 
     def build_weight_cache(self):
         """Quantise the expert weights (both orientations) into the cache the forward and backward read."""
@@ -112,22 +143,27 @@ class LayerStep:
 
     # ------------------------------------------------------------------ steps
     def forward(self):
-        w, inp = self.w, self.inp
+        w, inp, x = self.w, self.inp, self.h
+        if self.norm:
+            B.moe_layernorm(inp["x"], inp.get("ln_w"), inp.get("ln_b"), out=self.ln)
         if self.linear_router:
-            B.moe_router_logits(inp["x"], inp["w_router"], out=self.logits)
+            B.moe_router_logits(x, inp["w_router"], out=self.logits)
         B.moe_route_topk(self.logits, w.k, out=self.route, ws=self.route_ws)
+        if self.balance_coef is not None:
+            B.moe_balance_loss(self.logits, self.route["topk_idx"], *self.balance_coef, seq_offsets=self.seq_offsets,
+                               token_mask=self.token_mask, out=self.balance, ws=self.balance_ws)
         if self.mx_movement == "tok":
-            B.moe_dispatch_mx_tok(inp["x"], self.route, w.k, w.E, out=self.x_perm, mx=self.x_mx, mxt=self.x_mxt)
+            B.moe_dispatch_mx_tok(x, self.route, w.k, w.E, out=self.x_perm, mx=self.x_mx, mxt=self.x_mxt)
         elif self.mx_movement == "rows":
-            B.moe_dispatch_mx(inp["x"], self.route["perm_dst"], w.k, out=self.x_perm, mx=self.x_mx)
+            B.moe_dispatch_mx(x, self.route["perm_dst"], w.k, out=self.x_perm, mx=self.x_mx)
         else:
-            B.moe_dispatch(inp["x"], self.route["perm_dst"], w.k, out=self.x_perm)
+            B.moe_dispatch(x, self.route["perm_dst"], w.k, out=self.x_perm)
         B.moe_grouped_ffn_fwd(self.x_perm, self.route["offsets"], inp["w_gate"], inp["w_up"], inp["w_down"], w.prec,
                               out=self.ffn, ws=self.ffn_ws_f, mx_wcache=self.mx_wcache, x_mx=self.x_mx, rows=w.R)
         B.moe_combine(self.ffn["y_perm"], self.route["gates"], self.route["perm_dst"], out=self.out)
         return self.out
 
-    def backward(self, dout=None):
+    def backward(self, dout=None, dloss=None):
         w, inp = self.w, self.inp
         dout = inp["dout"] if dout is None else dout
         if self.mx_movement == "tok":
@@ -143,12 +179,40 @@ class LayerStep:
                               self.route["offsets"], self.route["mx_blk_offsets"], inp["w_gate"], inp["w_up"],
                               inp["w_down"], w.prec, out=self.grads, ws=self.ffn_ws_b, mx_wcache=self.mx_wcache,
                               dy_mx=self.dy_mx, x_mxt=self.x_mxt, dy_mxt=self.dy_mxt)
-        B.moe_dispatch_bwd(self.grads["dx_perm"], self.route["perm_dst"], w.k, out=self.dx)
-        B.moe_route_topk_bwd(self.route["gates"], self.dgates, self.route["topk_idx"], w.E, out=self.dlogits)
+        dh = self.dh if self.norm else self.dx
+        B.moe_dispatch_bwd(self.grads["dx_perm"], self.route["perm_dst"], w.k, out=dh)
+        if self.balance_coef is not None:
+            B.moe_balance_loss_bwd(self.logits, self.balance, w.k, *self.balance_coef, dloss=dloss,
+                                   seq_offsets=self.seq_offsets, token_mask=self.token_mask,
+                                   topk_idx=self.route["topk_idx"], gates=self.route["gates"], dgates=self.dgates,
+                                   out=self.dlogits)
+        else:
+            B.moe_route_topk_bwd(self.route["gates"], self.dgates, self.route["topk_idx"], w.E, out=self.dlogits)
         if self.linear_router:
-            B.moe_router_logits_bwd(inp["x"], inp["w_router"], self.dlogits, self.dx, accumulate_dx=True,
+            B.moe_router_logits_bwd(self.h, inp["w_router"], self.dlogits, dh, accumulate_dx=True,
                                     dw_r=self.dw_router, ws=self.router_ws)
+        if self.norm:
+            B.moe_layernorm_bwd(dh, inp["x"], inp.get("ln_w"), self.ln["mean"], self.ln["rstd"], dres=dout,
+                                out=self.ln_grads, ws=self.ln_ws)
         return self.dx
+
+    def update(self, lr: float, momentum: float = 0.95, weight_decay: float = 0.0, nesterov: bool = True,
+               scale: float | None = None, steps: int = 5):
+        """A Muon step of the expert weights, in place, from the gradients of the last backward.  scale: what the
+        orthogonalised update is multiplied by besides lr; None: 0.2 sqrt(max(d, f)), which gives its entries a
+        root mean square of about 0.2.  A cache of quantised weights is built again."""
+        inp, E = self.inp, self.w.E
+        if self.mom is None:
+            self.mom = {n: torch.zeros(inp[n].shape, dtype=torch.float32, device=inp[n].device)
+                        for n in ("w_gate", "w_up", "w_down")}
+            need = max(B.moe_orthogonalize_workspace(E, *inp[n].shape[1:], inp[n].dtype) for n in self.mom)
+            self.muon_ws = B._ws(need, inp["w_gate"].device)
+        scale = 0.2 * max(self.w.d, self.w.f) ** 0.5 if scale is None else scale
+        for n, mom in self.mom.items():
+            B.moe_muon_step(self.grads["d" + n], mom, inp[n], lr, momentum=momentum, nesterov=nesterov,
+                            weight_decay=weight_decay, scale=scale, steps=steps, ws=self.muon_ws)
+        if self.mx_wcache is not None:
+            self.build_weight_cache()
 
     def step(self):
         if self.mx_per_step:

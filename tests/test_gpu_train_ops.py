@@ -436,3 +436,103 @@ def test_calls_are_deterministic_and_capturable(gpu):
         for key in ref:
             assert torch.equal(ref[key], out[key]), key
         all_calls()
+
+
+# ------------------------------------------------------------------- a block's training step
+
+@pytest.mark.parametrize("prec", ["f32", "bf16"])
+def test_training_step_of_a_block(gpu, prec):
+    """LayerStep with norm, balance loss and update: each stage against the oracle on the stage's own inputs, over
+    two steps (the second on updated weights)."""
+    from mixture_experts_layer_17_amd import layer as L
+    from mixture_experts_layer_17_amd import workloads as wl
+    from oracle import moe_oracle as mo
+
+    w = wl.scaled(wl.WORKLOADS[1 if prec == "f32" else 2], T=200, d=128, f=64, E=8, k=2)
+    inp = wl.make_inputs(w)
+    rng = np.random.default_rng(5)
+    dv = L.to_device(inp)
+    dt = DT[prec]
+    dv["ln_w"], lw = draw(rng, (w.d,), prec, 0.1, 1.0)
+    dv["ln_b"], lb = draw(rng, (w.d,), prec, 0.1)
+    seq = np.array([0, 60, 60, 190], np.int32)
+    mask = (rng.random(w.T) > 0.2).astype(np.uint8)
+    alpha, zeta = 0.05, 0.01
+    step = L.LayerStep(w, dv, norm=True, balance=(alpha, zeta), seq_offsets=dev(seq), token_mask=dev(mask))
+    gu.say(f"case training step {prec}")
+    mom = {n: np.zeros(dv[n].shape) for n in ("w_gate", "w_up", "w_down")}
+    tol = gu.TOL[prec]
+    for it in range(2):
+        wts = {n: h64(dv[n]) for n in mom}
+        step.step()
+        torch.cuda.synchronize()
+        x, dout = h64(dv["x"]), h64(dv["dout"])
+        y, mu, rstd = to.layernorm(x, lw, lb)
+        h = h64(step.h)
+        assert gu.rel_err(h, y) <= half(prec) + 1e-5
+        logits = gu.host(step.logits)
+        ref = mo.layer_forward_backward(h, wts["w_gate"], wts["w_up"], wts["w_down"], dout, w.k, logits=logits,
+                                        w_router=h64(dv["w_router"]))
+        np.testing.assert_array_equal(gu.host(step.route["topk_idx"]), ref["topk_idx"])
+        loss, cnt, _, _ = to.balance_loss(logits, ref["topk_idx"], alpha, zeta, seq, mask)
+        close("loss", step.balance["loss"], loss, 1e-5, 1e-12)
+        np.testing.assert_array_equal(step.balance["counts"].cpu().numpy(), cnt)
+        dl = to.balance_loss_bwd(logits, ref["topk_idx"], alpha, zeta, seq, mask, (1.0, 1.0), h64(step.route["gates"]),
+                                 h64(step.dgates))
+        assert gu.rel_err(gu.host(step.dlogits), dl) <= 1e-5
+        assert np.abs(dl - ref["dlogits"]).max() > 1e-6  # the balance gradient is there
+        dh = ref["dx"] + (dl - ref["dlogits"]) @ h64(dv["w_router"]).T
+        assert gu.rel_err(gu.host(step.dh), dh) <= tol
+        dx, dw, db, _, _ = to.layernorm_bwd(h64(step.dh), x, lw, dres=dout)
+        assert gu.rel_err(gu.host(step.dx), dx) <= tol
+        assert gu.rel_err(gu.host(step.ln_grads["dw"]), dw) <= tol and gu.rel_err(gu.host(step.ln_grads["db"]), db) <= tol
+        grads = {n: h64(step.grads["d" + n]) for n in mom}
+        step.update(lr=0.02, weight_decay=0.1)
+        torch.cuda.synchronize()
+        for n in mom:
+            old = mom[n]
+            rw, mom[n], o = to.muon_step(grads[n], old, wts[n], 0.02, weight_decay=0.1, scale=0.2 * 128 ** 0.5)
+            # 0.95 in fp32, the product and the sum: a rounding each, of terms that may cancel
+            close("mom", step.mom[n], mom[n], 0.0, 2.0 ** -22 * (np.abs(old) + np.abs(grads[n])))
+            close(n, dv[n], rw, half(prec) + 2.0 ** -22,
+                  (ORTH_TOL["f32"] if prec == "f32" else 9e-3) * np.abs(o).max() * 0.02 * 0.2 * 128 ** 0.5)
+            mom[n] = h64(step.mom[n])
+
+
+def test_update_rebuilds_the_mx_weight_cache(gpu):
+    from mixture_experts_layer_17_amd import layer as L
+    from mixture_experts_layer_17_amd import workloads as wl
+
+    w = wl.scaled(wl.WORKLOADS[5], T=256, d=256, f=128, E=8)
+    step = L.LayerStep(w, L.to_device(wl.make_inputs(w)), mx_weight_cache=True)
+    gu.say("case update with an MX weight cache")
+    step.step()
+    before = step.mx_wcache.clone()
+    step.update(lr=0.1)
+    fresh = B.moe_mx_weight_cache_build(*(step.inp[n] for n in ("w_gate", "w_up", "w_down")))
+    torch.cuda.synchronize()
+    assert torch.equal(step.mx_wcache, fresh) and not torch.equal(before, fresh)
+
+
+def test_refused_tensors(gpu):
+    """What the binding refuses before any launch."""
+    x = torch.randn((8, 32), device="cuda")
+    lg, idx = torch.randn((8, 4), device="cuda"), torch.zeros((8, 2), dtype=torch.int32, device="cuda")
+    g = torch.randn((2, 8, 16), device="cuda")
+    bad = [lambda: B.moe_layernorm(x.double()), lambda: B.moe_layernorm(x.T), lambda: B.moe_layernorm(x[:, ::2]),
+           lambda: B.moe_layernorm(x, torch.randn(31, device="cuda")), lambda: B.moe_layernorm(x, x[0].bfloat16()),
+           lambda: B.moe_layernorm(x, residual=x[:4]), lambda: B.moe_layernorm(x.cpu()), lambda: B.moe_layernorm(x[0]),
+           lambda: B.moe_layernorm(x, x[0].cpu()),
+           lambda: B.moe_layernorm_bwd(x, x, None, x[:, 0], x[:, 0]),
+           lambda: B.moe_balance_loss(lg, idx.long(), 0.1, 0.1), lambda: B.moe_balance_loss(lg.half(), idx, 0.1, 0.1),
+           lambda: B.moe_balance_loss(lg, idx, 0.1, 0.1, token_mask=torch.ones(8, device="cuda")),
+           lambda: B.moe_balance_loss(lg, idx, float("nan"), 0.1),
+           lambda: B.moe_orthogonalize(g.half()), lambda: B.moe_orthogonalize(g.transpose(1, 2)),
+           lambda: B.moe_orthogonalize(g, steps=0), lambda: B.moe_orthogonalize(g, ws=torch.empty(16, dtype=torch.uint8, device="cuda")),
+           lambda: B.moe_orthogonalize(g, coef=(20.0, 0.0, 0.0)),
+           lambda: B.moe_muon_step(g, g.bfloat16(), g, 0.1), lambda: B.moe_muon_step(g, g, g.bfloat16(), 0.1),
+           lambda: B.moe_muon_step(g, g, g, float("inf"))]
+    for i, call in enumerate(bad):
+        with pytest.raises(B.MoeError):
+            call()
+            raise AssertionError(f"call {i} was not refused")
