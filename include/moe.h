@@ -173,7 +173,7 @@ int moe_route_stats(const int32_t* counts, int32_t E, int32_t* stats, void* stre
  * added for every token in the same pass, so that call is not needed.
  * dloss [2] fp32 on the device: upstream gradients of the two losses (NULL: 1).
  * Errors as for moe_route_topk; MOE_EINVAL also for a non-finite alpha or zeta,
- * S < 1, and S > 1 without seq_offsets.  T = 0 is allowed (losses 0). */
+ * S < 1, and S > 1 without seq_offsets, MOE_EUNSUPPORTED for T >= 2^29.  T = 0 is allowed (losses 0). */
 size_t moe_balance_loss_workspace(int64_t T, int32_t E, int64_t S);
 int moe_balance_loss(const float* logits, const int32_t* topk_idx, int64_t T, int32_t E, int32_t k,
                      const int32_t* seq_offsets, int64_t S, const uint8_t* token_mask, float alpha, float zeta,
@@ -198,7 +198,8 @@ int moe_balance_loss_bwd(const float* logits, const float* lse, const int32_t* c
  * weight, bias, residual, dres, dw, db may be NULL (weight 1, bias 0, none);
  * weight, bias, dw, db [d] in `dtype`.  dres [T, d] is a gradient that reaches
  * s by another way (the residual stream's).  Statistics and sums are fp32.
- * T = 0 is allowed: dw and db become zero.  The workspace is needed for dw and
+ * A constant row with eps = 0 gives NaN.  T = 0 is allowed: dw and db become
+ * zero.  The workspace is needed for dw and
  * db only.  MOE_EINVAL for d < 1 and for an eps that is negative or not finite,
  * MOE_EUNSUPPORTED for d > 2^20. */
 int moe_layernorm(const void* x, const void* residual, const void* weight, const void* bias, int dtype, int64_t T,

@@ -461,8 +461,8 @@ def moe_layernorm_bwd(dy, x, weight, mean, rstd, dres=None, out=None, ws=None):
 
 
 def _balance_specs(logits, k, topk_idx, seq_offsets, token_mask):
-    if logits.dim() != 2:
-        raise MoeError("logits: two dimensions are needed")
+    if logits.dim() != 2 or (seq_offsets is not None and seq_offsets.dim() != 1):
+        raise MoeError("logits of two dimensions and seq_offsets of one are needed")
     T, E = logits.shape
     S = 1 if seq_offsets is None else seq_offsets.numel() - 1
     mt = torch.bool if token_mask is not None and token_mask.dtype is torch.bool else torch.uint8
@@ -472,7 +472,7 @@ def _balance_specs(logits, k, topk_idx, seq_offsets, token_mask):
 
 def moe_balance_loss(logits, topk_idx, alpha, zeta, seq_offsets=None, token_mask=None, out=None, ws=None):
     """Balance and z loss of a routing: {"loss" [2], "counts" [S, E], "probs" [S, E], "lse" [T], "norm" [S + 2]}."""
-    what, dev, k = "moe_balance_loss", logits.device, topk_idx.shape[1]
+    what, dev, k = "moe_balance_loss", logits.device, topk_idx.shape[-1] if topk_idx.dim() else 0
     T, E, S, specs = _balance_specs(logits, k, topk_idx, seq_offsets, token_mask)
     if out is None:
         out = {"loss": torch.empty(2, dtype=_F32, device=dev), "counts": torch.empty((S, E), dtype=_I32, device=dev),

@@ -74,17 +74,44 @@ __device__ __forceinline__ int64_t seq_at(const int32_t* seq, int64_t s, int64_t
   return v < 0 ? 0 : (v > T ? T : v);
 }
 
-// The sequence that holds token t0 (or begins next after it): the number of
-// sequences that end at or before t0.  All threads of the workgroup call it.
-__device__ __forceinline__ int64_t first_seq(const int32_t* seq, int64_t S, int64_t T, int64_t t0, int* cnt) {
+// The sequence that holds token t (or begins next after it): the number of
+// sequences that end at or before t, found 256 probes at a time.  All threads of
+// the workgroup call it.
+__device__ __forceinline__ int64_t first_seq(const int32_t* seq, int64_t S, int64_t T, int64_t t, int* cnt) {
   if (!seq) return 0;
-  if (threadIdx.x == 0) *cnt = 0;
-  __syncthreads();
-  int my = 0;
-  for (int64_t j = threadIdx.x; j < S; j += kThreads) my += seq_at(seq, j + 1, S, T) <= t0;
-  if (my) atomicAdd(cnt, my);
-  __syncthreads();
-  return *cnt;
+  int64_t lo = 0, n = S;  // the answer is in [lo, lo + n]
+  while (n > 0) {
+    const int64_t step = (n + kThreads - 1) / kThreads, last = (threadIdx.x + 1) * step;  // thread's piece ends there
+    if (threadIdx.x == 0) *cnt = 0;
+    __syncthreads();
+    if (last <= n && seq_at(seq, lo + last, S, T) <= t) atomicAdd(cnt, 1);
+    __syncthreads();
+    const int64_t whole = *cnt * step;
+    __syncthreads();
+    lo += whole;
+    if (step == 1) break;
+    n = n - whole < step ? n - whole : step;
+  }
+  return lo;
+}
+
+// Walk over the sequences' pieces within tokens [t0, t1): f(s, lo, hi) for each
+// that is not empty.  Runs of empty sequences are skipped by another search.
+template <class F>
+__device__ __forceinline__ void each_piece(const int32_t* seq, int64_t S, int64_t T, int64_t t0, int64_t t1, int* cnt,
+                                           F&& f) {
+  for (int64_t s = first_seq(seq, S, T, t0, cnt); s < S;) {
+    const int64_t from = seq_at(seq, s, S, T), to = seq_at(seq, s + 1, S, T);
+    if (from >= t1) break;
+    const int64_t lo = from < t0 ? t0 : from, hi = to > t1 ? t1 : to;
+    if (lo < hi) {
+      f(s, lo, hi);
+      ++s;
+    } else {
+      const int64_t next = first_seq(seq, S, T, lo, cnt);
+      s = next > s ? next : s + 1;
+    }
+  }
 }
 
 __device__ __forceinline__ int wave_sum_i(int v) {
@@ -181,7 +208,6 @@ __global__ __launch_bounds__(kThreads) void balance_partial_kernel(FwdArgs a) {
     const bool in = r < kTok && t0 + r < t1;
     ld_logits(a.logits, t0 + r, E, e0, in, p[q]);
   }
-  const int64_t s_first = first_seq(a.seq, a.S, a.T, t0, &s_cnt);
 #pragma unroll
   for (int q = 0; q < NP; ++q) {
     const int r = q * kPass + wave * RW + lane / LPT;
@@ -194,12 +220,7 @@ __global__ __launch_bounds__(kThreads) void balance_partial_kernel(FwdArgs a) {
     if (l == 0 && r < kTok) s_on[r] = on;
     if (l == 0 && in) a.lse[t0 + r] = 0.f;
   }
-  for (int64_t s = s_first; s < a.S; ++s) {
-    int64_t lo = seq_at(a.seq, s, a.S, a.T), hi = seq_at(a.seq, s + 1, a.S, a.T);
-    if (lo >= t1) break;
-    lo = lo < t0 ? t0 : lo;
-    hi = hi > t1 ? t1 : hi;
-    if (lo >= hi) continue;
+  each_piece(a.seq, a.S, a.T, t0, t1, &s_cnt, [&](int64_t s, int64_t lo, int64_t hi) {
     for (int e = tid; e < E; e += kThreads) s_hist[e] = 0;
     __syncthreads();
     float ps[4] = {0.f, 0.f, 0.f, 0.f}, z = 0.f;
@@ -256,7 +277,7 @@ __global__ __launch_bounds__(kThreads) void balance_partial_kernel(FwdArgs a) {
       a.ws.n[slot] = nn;
     }
     __syncthreads();
-  }
+  });
 }
 
 // Workgroup (x, y): experts [16 x, 16 x + 16) of sequences y, y + gridDim.y, ...
@@ -394,7 +415,6 @@ __global__ __launch_bounds__(kThreads) void balance_bwd_kernel(BwdArgs a) {
     on[q] = r < kTok && t0 + r < t1;
     ld_logits(a.logits, t0 + r, E, e0, on[q], p[q]);
   }
-  const int64_t s_first = first_seq(a.seq, a.S, a.T, t0, &s_cnt);
   const float live = a.norm[0], ntot = a.norm[1];
   const float g0 = a.dloss ? a.dloss[0] : 1.f, g1 = a.dloss ? a.dloss[1] : 1.f;
   const float zs = ntot > 0.f ? g1 * 2.0f * a.zeta / ntot : 0.f;
@@ -423,12 +443,9 @@ __global__ __launch_bounds__(kThreads) void balance_bwd_kernel(BwdArgs a) {
       }
     }
   }
-  for (int64_t s = s_first; s < a.S; ++s) {
-    const int64_t lo = seq_at(a.seq, s, a.S, a.T), hi = seq_at(a.seq, s + 1, a.S, a.T);
-    if (lo >= t1) break;
-    if (lo >= hi) continue;
+  each_piece(a.seq, a.S, a.T, t0, t1, &s_cnt, [&](int64_t s, int64_t lo, int64_t hi) {
     const float n = a.norm[2 + s];
-    if (!(n > 0.f)) continue;
+    if (!(n > 0.f)) return;
     const float f = g0 * a.alpha * static_cast<float>(E) / (static_cast<float>(a.k) * n * n * live);
     float c[4];
 #pragma unroll
@@ -445,7 +462,7 @@ __global__ __launch_bounds__(kThreads) void balance_bwd_kernel(BwdArgs a) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) dl[q][i] += p[q][i] * (c[i] - dot + zc[q]);
     }
-  }
+  });
 #pragma unroll
   for (int q = 0; q < NP; ++q) {
     if (!on[q]) continue;
@@ -473,8 +490,8 @@ void by_lanes(int E, F&& f) {
 }
 
 int check_sizes(int64_t T, int E, int k, int64_t S) {
-  if (E > kMaxE || k > kMaxK) return MOE_EUNSUPPORTED;
-  if (T < 0 || T >= (int64_t{1} << 31) || E < 1 || k < 1 || k > E || T * k >= (int64_t{1} << 31)) return MOE_EINVAL;
+  if (E > kMaxE || k > kMaxK || T >= (int64_t{1} << 29)) return MOE_EUNSUPPORTED;  // 2^32 threads per launch
+  if (T < 0 || E < 1 || k < 1 || k > E || T * k >= (int64_t{1} << 31)) return MOE_EINVAL;
   if (S < 1 || S >= (int64_t{1} << 31)) return MOE_EINVAL;
   return MOE_OK;
 }

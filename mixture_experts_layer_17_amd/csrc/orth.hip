@@ -1308,6 +1308,7 @@ int64_t rect_tiles(int64_t r, int64_t c, int64_t E) {
 // only where it shortens the longest chain by 16 steps or more, about 5 us, which
 // is what joining costs (4096 x 128: Gram 25 -> 12 us; at 8 steps saved 12 -> 13 us).
 int k_split(int64_t tiles, int64_t steps) {
+  if (tiles < 1) return 1;
   int64_t n = 512 / tiles;
   if (n > steps / 8) n = steps / 8;
   if (n > 16) n = 16;

@@ -212,6 +212,16 @@ def test_balance_loss(gpu, T, E, k, S, masked):
         check_balance(*routing_case(T, E, k, S, T + E, masked, zipf, pad=T // 5 if S else 0), gates=gates)
 
 
+@pytest.mark.parametrize("T,S,empty", [(300, 700, 0), (4000, 3500, 1500), (65, 2000, 1900), (2000, 70000, 69000)])
+def test_balance_loss_many_sequences(gpu, T, S, empty):
+    """More sequences than one probe of the search holds, long runs of empty ones among them."""
+    gu.say(f"case balance T={T} S={S} empty={empty}")
+    lg, idx, _, mask, rng = routing_case(T, 8, 2, 0, S, True)
+    cut = np.sort(np.concatenate([rng.integers(0, T + 1, S - 1 - empty), np.full(empty, T // 3)]))
+    seq = np.concatenate([[min(2, cut[0])], cut, [T]]).astype(np.int32)
+    check_balance(lg, idx, seq, mask, rng)
+
+
 def test_balance_loss_large(gpu):
     gu.say("case balance T=16384 E=128 S=1 and 24")
     for S in (0, 24):

@@ -65,6 +65,7 @@ def test_balance_validation(L):
     assert fwd(a=float("nan")) == fwd(z=float("inf")) == EINVAL
     need = L.moe_balance_loss_workspace(10, 8, 3)
     assert need > 0 and fwd(n=need - 1) == EWS
+    assert fwd(T=1 << 29) == EUNSUP and L.moe_balance_loss_workspace(1 << 29, 8, 3) == 0
     assert L.moe_balance_loss_workspace(10, 300, 3) == 0 and L.moe_balance_loss_workspace(10, 8, 0) == 0
 
     def bwd(lg=FAKE, lse=FAKE, c=FAKE, norm=FAKE, T=10, E=8, k=2, seq=FAKE, S=3, mask=None, a=0.1, z=0.1, up=None,
@@ -97,6 +98,9 @@ def test_orthogonalize_validation(L):
     assert need > 0 and orth(n=need - 1) == EWS
     assert L.moe_orthogonalize_workspace(2, 64, 96, 0) > need  # fp32 keeps pairs
     assert L.moe_orthogonalize_workspace(2, 0, 96, 1) == 0
+    for rows, cols in ((1, 1), (4096, 1536), (5000, 64)):
+        for dt in (0, 1):
+            assert L.moe_orthogonalize_workspace(0, rows, cols, dt) >= 0  # no matrices: answers, too
 
     def muon(g=FAKE, mom=FAKE, b=0.9, w=FAKE, lr=0.1, wd=0.0, sc=1.0, mo=FAKE, wo=FAKE, ws=FAKE, n=BIG, E=2):
         return L.moe_muon_step(g, 1, E, 64, 96, mom, b, 1, 5, None, 1e-7, w, lr, wd, sc, mo, wo, ws, n, None)
