@@ -297,22 +297,25 @@ struct MmArgs {
   int32_t* ticket;                    // [tile], zero before and after a launch
 };
 
-// BM x BN outputs per workgroup by 2 x 2 waves of WM x WN; K step BK; a ring of
+// BM x BN outputs per workgroup by 2 x NW waves of WM x WN; K step BK; a ring of
 // kRing K steps of both operands in LDS; fragments of KG 16-deep slices (a phase)
 // in registers at a time, twice.  PAIRS: operands with lo parts, which come into
 // the same step, so that the four tiles of a step serve its three products.
-template <int BM_, int BN_, int BK_, int RING_, int KG_, bool PAIRS_>
+template <int BM_, int BN_, int BK_, int RING_, int KG_, bool PAIRS_, int NW_ = 2>
 struct Tile {
+  static constexpr int kNW = NW_, kWaves = 2 * NW_, kThreads = 64 * kWaves;
   static constexpr int BM = BM_, BN = BN_, BK = BK_, kRing = RING_, KG = KG_;
   static constexpr bool kPairs = PAIRS_;
   static constexpr int kPhases = BK / 16 / KG;
-  static constexpr int WM = BM / 2, WN = BN / 2, TM = WM / 32, TN = WN / 32;
+  static constexpr int WM = BM / 2, WN = BN / NW_, TM = WM / 32, TN = WN / 32;
   static constexpr int kA = BM * BK, kHi = (BM + BN) * BK;  // elements: the A tile, then the B tile (then lo likewise)
   static constexpr int kSlot = kHi * (PAIRS_ ? 2 : 1);
-  static constexpr int kLoads = kSlot / 512 / 4;            // LDS-DMA instructions per wave and step
+  static constexpr int kLoads = kSlot / 512 / kWaves;       // LDS-DMA instructions per wave and step
   static constexpr int kLds = kRing * kSlot;
-  static constexpr int kWavesPerSimd = kLds * 2 > 80 * 1024 ? 1 : 2;  // workgroups per compute unit the LDS allows, at most 2
-  static_assert(kA % 2048 == 0 && kHi % 2048 == 0, "whole LDS-DMA instructions per wave");
+  // symmetric outputs go by squares of this size, each within whole waves' outputs
+  static constexpr int kSq = WM >= 128 ? 128 : BN;
+  static constexpr int kWavesPerSimd = kLds * 2 > 80 * 1024 ? kWaves / 4 : 2;  // workgroups per compute unit the LDS allows, at most 2
+  static_assert(kA % (512 * kWaves) == 0 && kHi % (512 * kWaves) == 0, "whole LDS-DMA instructions per wave");
 };
 
 // 16-byte chunk swizzles against bank conflicts.  K-contiguous tiles (BK
@@ -350,9 +353,9 @@ __device__ __forceinline__ f16x8 frag_tr(const uint16_t* t, int base, int ks, in
 }
 
 // One operand of a tile: W rows (KC: stored with K contiguous) or columns.
-template <int W, int BK, bool KC>
+template <int W, int BK, bool KC, int WAVES>
 struct Operand {
-  static constexpr int kLoads = W * BK / 512 / 4;  // LDS-DMA instructions per wave and step
+  static constexpr int kLoads = W * BK / 512 / WAVES;  // LDS-DMA instructions per wave and step
   __amdgpu_buffer_rsrc_t hi, lo;
   int voff, vstep, kstep;  // this lane's byte offset, per load, and per K step
 
@@ -366,9 +369,9 @@ struct Operand {
       lo = rsrc(l ? l + o : h + o, bytes);
       constexpr int CPR = BK / 8, RPI = 64 / CPR;
       const int row = wave * RPI + lane / CPR;
-      // rows advance by 4 RPI per load: a multiple of the swizzle's period
+      // rows advance by WAVES RPI per load: a multiple of the swizzle's period
       voff = (row * ld + ((lane % CPR) ^ kc_swz<BK>(row)) * 8) * 2;
-      vstep = 4 * RPI * ld * 2;
+      vstep = WAVES * RPI * ld * 2;
       kstep = BK * 2;
     } else {
       const int64_t bytes = (static_cast<int64_t>(K) * ld - mn0) * 2;
@@ -377,7 +380,7 @@ struct Operand {
       constexpr int CPR = W / 8, KPI = 64 / CPR;
       const int k = wave * KPI + lane / CPR;
       voff = (k * ld + ((lane % CPR) ^ mc_swz<W>(k)) * 8) * 2;
-      vstep = 4 * KPI * ld * 2;
+      vstep = WAVES * KPI * ld * 2;
       kstep = BK * ld * 2;
     }
   }
@@ -385,7 +388,7 @@ struct Operand {
   __device__ __forceinline__ void issue(bool low, int soff, uint16_t* dst, int wave) const {
 #pragma unroll
     for (int u = 0; u < kLoads; ++u)
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(low ? lo : hi, (lds_void*)(dst + (wave + 4 * u) * 512), 16,
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(low ? lo : hi, (lds_void*)(dst + (wave + WAVES * u) * 512), 16,
                                                voff + u * vstep, soff, 0, 0);
   }
   // MFMA fragment: 32 rows (or columns) from `base`, k-slice ks of 16.
@@ -407,9 +410,9 @@ template <class C, bool AKC, bool BKC>
 __device__ __forceinline__ void read_frags(const uint16_t* __restrict__ as, const uint16_t* __restrict__ bs, int wm,
                                            int wn, int ks, int lane, f16x8 (&fa)[C::TM], f16x8 (&fb)[C::TN]) {
 #pragma unroll
-  for (int i = 0; i < C::TM; ++i) fa[i] = Operand<C::BM, C::BK, AKC>::frag(as, wm * C::WM + i * 32, ks, lane);
+  for (int i = 0; i < C::TM; ++i) fa[i] = Operand<C::BM, C::BK, AKC, C::kWaves>::frag(as, wm * C::WM + i * 32, ks, lane);
 #pragma unroll
-  for (int j = 0; j < C::TN; ++j) fb[j] = Operand<C::BN, C::BK, BKC>::frag(bs, wn * C::WN + j * 32, ks, lane);
+  for (int j = 0; j < C::TN; ++j) fb[j] = Operand<C::BN, C::BK, BKC, C::kWaves>::frag(bs, wn * C::WN + j * 32, ks, lane);
 }
 
 // Tile i of those that meet the lower triangle, in row order: row r of tiles
@@ -631,7 +634,7 @@ __device__ __forceinline__ void epilogue(const f32x16 (&acc)[C::TM][C::TN], cons
   constexpr int CPR8 = WN / 16, RPI8 = 64 / CPR8, kPieces8 = 32 / RPI8;  // the same for an 8-bit lo part
   constexpr int kStage = kPieces + (HASLO ? (kLo8 ? kPieces8 : kPieces) : 0);
   static_assert(WN == 64 || WN == 32, "row piece layouts");
-  static_assert(4 * 4 * kPart <= C::kLds, "two buffers of hi and lo per wave");
+  static_assert(C::kWaves * 4 * kPart <= C::kLds, "two buffers of hi and lo per wave");
   const int rl = lane & 31, g = lane >> 5;
   const int mw = m0 + wm * C::WM, nw = n0 + wn * WN;  // this wave's outputs
   const int64_t ob = e * p.so;
@@ -665,11 +668,11 @@ __device__ __forceinline__ void epilogue(const f32x16 (&acc)[C::TM][C::TN], cons
         dma16(rlo, b + kPart + u * 512, (32 * i + r) * p.ldo + ((lane % CPR8) ^ lo8_swz<WN>(r)) * 16);
       }
   };
-  // symmetric outputs, in squares of BN = WM: above the diagonal there is nothing
-  // to do, squares on it are computed whole, those below are written twice
-  const bool below = KIND != kApply && mw / C::BN > nw / C::BN;
+  // symmetric outputs, by squares: above the diagonal there is nothing to do,
+  // squares on it are computed whole, those below are written twice
+  const bool below = KIND != kApply && mw / C::kSq > nw / C::kSq;
   __syncthreads();  // the ring is no longer read
-  if (KIND != kApply && mw / C::BN < nw / C::BN) return;
+  if (KIND != kApply && mw / C::kSq < nw / C::kSq) return;
   if constexpr (KIND != kGram) {
     stage(0);
     if constexpr (C::TM > 1) stage(1);
@@ -815,13 +818,13 @@ __device__ __forceinline__ bool join_k(f32x16 (&acc)[C::TM][C::TN], const MmArgs
 
 // FINAL: apply's last step, which writes the result instead of the next X.
 template <class C, int KIND, bool AKC, bool BKC, bool FINAL>
-__global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(C::kWavesPerSimd)))
+__global__ __launch_bounds__(C::kThreads) __attribute__((amdgpu_waves_per_eu(C::kWavesPerSimd)))
 void orth_mm_kernel(MmArgs p) {
   constexpr bool SPLIT = C::kPairs;
   __shared__ __attribute__((aligned(16))) uint16_t lds[C::kLds];
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int wm = wave >> 1, wn = wave & 1;
+  const int wm = wave / C::kNW, wn = wave % C::kNW;
   // consecutive tiles of a matrix on one XCD (workgroups go to the 8 XCDs in turn)
   constexpr bool kKSplit = C::BM == 64 && KIND != kApply;
   const int ks_n = kKSplit ? p.ks : 1;
@@ -841,8 +844,8 @@ void orth_mm_kernel(MmArgs p) {
   }
   const int m0 = __builtin_amdgcn_readfirstlane(r * C::BM), n0 = __builtin_amdgcn_readfirstlane(c * C::BN);
 
-  Operand<C::BM, C::BK, AKC> A;
-  Operand<C::BN, C::BK, BKC> B;
+  Operand<C::BM, C::BK, AKC, C::kWaves> A;
+  Operand<C::BN, C::BK, BKC, C::kWaves> B;
   A.init(p.ah + e * p.sa, SPLIT ? p.al + e * p.sa : nullptr, p.lda, m0, p.M, p.K, wave, lane);
   B.init(p.bh + e * p.sb, SPLIT ? p.bl + e * p.sb : nullptr, p.ldb, n0, p.N, p.K, wave, lane);
   const int nk1 = (p.K + C::BK - 1) / C::BK;
@@ -889,7 +892,7 @@ void orth_mm_kernel(MmArgs p) {
     }
   };
   // a wave whose outputs lie above the diagonal only helps with the loads
-  const bool idle = KIND != kApply && (m0 + wm * C::WM) / C::BN < (n0 + wn * C::WN) / C::BN;
+  const bool idle = KIND != kApply && (m0 + wm * C::WM) / C::kSq < (n0 + wn * C::WN) / C::kSq;
   auto mma = [&](int buf) {
     if (KIND != kApply && idle) return;
     auto product = [&](const f16x8 (&x)[C::TM], const f16x8 (&y)[C::TN]) {
@@ -1280,17 +1283,25 @@ Sizes sizes_of(int E, int rows, int cols, bool split) {
 
 // Tile sizes, chosen per product by how many tiles there are for the 256 compute
 // units.  64 x 64 while they all fit at once, three to a unit (one matrix of 2048
-// x 1024: Gram 15 us against 26 us with 128 x 128 and 46 us with 256 x 128);
-// 256 x 128, two to a unit, once they fill the chip (8 of 1024 x 2048, 512 tiles:
-// apply 51 us against 54 and 72); 128 x 128 between (one of 2048 x 2048, 256
-// tiles: apply 33 us against 45 with 256 x 128 and 42 with 64 x 64), and for
-// pairs, whose 256 x 128 steps leave room for one workgroup per unit only, from
-// there on (32 of 2048 x 1024: Gram 250 us against 306 us).
-using Big = Tile<256, 128, 32, 3, 1, false>;
+// x 1024: Gram 15 us against 26 us with 128 x 128 and 46 us with 256 x 128).
+// 256 x 256 (eight waves, one workgroup per unit) where they fill the chip in
+// whole rounds, to four fifths at least: 128 of 4096 x 1536, 12288 tiles, apply
+// 2.80 ms against 3.08 ms with 256 x 128, two per unit, and 3.23 ms with 128 x 128;
+// 32 of 2048 x 1024 fp32, 1024 tiles, apply 405 us against 490 us, but Gram, 320
+// tiles in two rounds, 296 us against 253 us.  128 x 128, two to a unit, else
+// (one of 2048 x 2048, 256 tiles: apply 33 us against 42 us with 64 x 64).
+using Big = Tile<256, 256, 64, 2, 2, false, 4>;
 using Mid = Tile<128, 128, 64, 2, 2, false>;
 using Small = Tile<64, 64, 64, 3, 2, false>;
+using BigPairs = Tile<256, 256, 32, 2, 1, true, 4>;
 using MidPairs = Tile<128, 128, 32, 2, 1, true>;
 using SmallPairs = Tile<64, 64, 32, 3, 1, true>;
+
+// From how many 256 x 256 tiles on, and in how well filled rounds of 256, they are
+// used (bf16 at 256 tiles: 55 us against 53; pairs: 102 us against 109).
+bool use_big(int64_t tiles, bool pairs) {
+  return tiles >= (pairs ? 250 : 480) && tiles * 5 >= cdiv(tiles, 256) * 256 * 4;
+}
 
 // Tiles of a symmetric m x m output, and of an r x c one, in E matrices.
 template <class C>
@@ -1368,11 +1379,11 @@ void launch_mm(const char* name, const MmArgs& a, hipStream_t s) {
   const dim3 grid(xcd_grid(a.tiles * a.ks));
   if constexpr (KIND == kApply) {
     if (a.out != kOutX) {
-      MOE_LAUNCH(name, (orth_mm_kernel<C, KIND, AKC, BKC, true>), grid, dim3(256), 0, s, a);
+      MOE_LAUNCH(name, (orth_mm_kernel<C, KIND, AKC, BKC, true>), grid, dim3(C::kThreads), 0, s, a);
       return;
     }
   }
-  MOE_LAUNCH(name, (orth_mm_kernel<C, KIND, AKC, BKC, false>), grid, dim3(256), 0, s, a);
+  MOE_LAUNCH(name, (orth_mm_kernel<C, KIND, AKC, BKC, false>), grid, dim3(C::kThreads), 0, s, a);
 }
 
 template <int KIND, bool AKC, bool BKC>
@@ -1393,12 +1404,10 @@ void launch_any(const char* name, MmArgs& a, const Sizes& z, hipStream_t s) {
   const bool ap = KIND == kApply;
   if ((ap ? rect_tiles<Small>(a.M, a.N, z.E) : sym_tiles<Small>(a.M, z.E)) <= 768)
     z.split ? go(SmallPairs{}) : go(Small{});
-  else if (z.split)
-    go(MidPairs{});
-  else if ((ap ? rect_tiles<Big>(a.M, a.N, z.E) : sym_tiles<Big>(a.M, z.E)) >= 480)
-    go(Big{});
+  else if (use_big(ap ? rect_tiles<Big>(a.M, a.N, z.E) : sym_tiles<Big>(a.M, z.E), z.split))
+    z.split ? go(BigPairs{}) : go(Big{});
   else
-    go(Mid{});
+    z.split ? go(MidPairs{}) : go(Mid{});
 }
 
 void run_products(const Sizes& z, const Ws& w, MmArgs a, const float (*coef)[3], int out, bool exact0,

@@ -338,6 +338,28 @@ def test_orthogonalize_many(gpu, E, rows, cols):
             assert err <= ORTH_TOL[dtype], (e, err)
 
 
+@pytest.mark.parametrize("E,rows,cols,dtype", [(170, 300, 520, "bf16"), (170, 520, 300, "bf16"), (84, 300, 520, "f32"),
+                                               (84, 520, 300, "f32"), (500, 250, 256, "bf16"), (9, 1000, 1300, "f32")])
+def test_orthogonalize_fills_the_chip(gpu, E, rows, cols, dtype):
+    """Whole rounds of the largest tiles, with partial tiles and mirrored ones, every matrix against fp64 on the GPU."""
+    gu.say(f"case orthogonalize E={E} {rows}x{cols} {dtype}")
+    gen = torch.Generator(device="cuda")
+    gen.manual_seed(E + rows)
+    g = torch.randn((E, rows, cols), generator=gen, device="cuda").mul_(1e-3).to(DT[dtype])
+    out = B.moe_orthogonalize(g)
+    torch.cuda.synchronize()
+    a, b, c = to.QUINTIC
+    x = (g if rows <= cols else g.transpose(1, 2)).double().contiguous()
+    x = x / (x.square().sum((1, 2), keepdim=True).sqrt() + 1e-7)
+    for _ in range(5):
+        m = torch.bmm(x, x.transpose(1, 2).contiguous())
+        x = a * x + torch.bmm(b * m + c * torch.bmm(m, m), x)
+    x = x if rows <= cols else x.transpose(1, 2)
+    err = ((out.double() - x).abs().amax((1, 2)) / x.abs().amax((1, 2))).max()
+    gu.say(f"  error {float(err):.2e}")
+    assert float(err) <= ORTH_TOL[dtype]
+
+
 def test_orthogonalize_steps_and_coefficients(gpu):
     rng = np.random.default_rng(3)
     g = gradients(rng, 2, 96, 160, "noise")
