@@ -271,7 +271,7 @@ struct MmArgs {
   int lda, ldb, K;
   int M, N;                           // padded output rows and columns
   int tm, tn;                         // output tiles (symmetric kinds: tn = 1, tm = all lower tiles)
-  int64_t tiles;                      // tm * tn * E
+  unsigned tiles;                     // tm * tn * E
   // epilogue
   const uint16_t* eh;                 // A (poly) or X (apply) at the output's place
   const void* el;                     // and its lo part; apply without split operands: 8 bits, or none (zero)
@@ -826,15 +826,16 @@ void orth_mm_kernel(MmArgs p) {
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int wm = wave / C::kNW, wn = wave % C::kNW;
   // consecutive tiles of a matrix on one XCD (workgroups go to the 8 XCDs in turn)
+  // (32-bit arithmetic: 64-bit divisions here took a microsecond of each launch)
   constexpr bool kKSplit = C::BM == 64 && KIND != kApply;
-  const int ks_n = kKSplit ? p.ks : 1;
-  const int64_t wid = xcd_tile(blockIdx.x, p.tiles * ks_n);
-  if (wid < 0) return;
-  const int64_t lid = kKSplit ? wid / ks_n : wid;
+  const unsigned ks_n = kKSplit ? p.ks : 1, total = p.tiles * ks_n;
+  const unsigned wid = blockIdx.x % kNumXcd * ((total + kNumXcd - 1) / kNumXcd) + blockIdx.x / kNumXcd;
+  if (blockIdx.x / kNumXcd >= (total + kNumXcd - 1) / kNumXcd || wid >= total) return;
+  const unsigned lid = kKSplit ? wid / ks_n : wid;
   const int ks_i = kKSplit ? static_cast<int>(wid - lid * ks_n) : 0;
-  const int per = p.tm * p.tn;
-  const int64_t e = lid / per;
-  const int t = static_cast<int>(lid - e * per);
+  const unsigned per = p.tm * p.tn, el = lid / per;
+  const int64_t e = el;
+  const int t = static_cast<int>(lid - el * per);
   int r, c;
   if constexpr (KIND == kApply) {  // the shorter side inside
     if (p.tm <= p.tn) { c = t / p.tm; r = t - c * p.tm; }
@@ -849,8 +850,8 @@ void orth_mm_kernel(MmArgs p) {
   A.init(p.ah + e * p.sa, SPLIT ? p.al + e * p.sa : nullptr, p.lda, m0, p.M, p.K, wave, lane);
   B.init(p.bh + e * p.sb, SPLIT ? p.bl + e * p.sb : nullptr, p.ldb, n0, p.N, p.K, wave, lane);
   const int nk1 = (p.K + C::BK - 1) / C::BK;
-  const int k_lo = kKSplit ? static_cast<int>(static_cast<int64_t>(nk1) * ks_i / ks_n) : 0;
-  const int nk = (kKSplit ? static_cast<int>(static_cast<int64_t>(nk1) * (ks_i + 1) / ks_n) : nk1) - k_lo;
+  const int k_lo = kKSplit ? static_cast<int>(static_cast<unsigned>(nk1 * ks_i) / ks_n) : 0;
+  const int nk = (kKSplit ? static_cast<int>(static_cast<unsigned>(nk1 * (ks_i + 1)) / ks_n) : nk1) - k_lo;
   int head = 0;  // K step (from k_lo) to load next, and its ring slot
   int head_slot = 0;
   auto issue = [&]() {
@@ -1376,7 +1377,7 @@ size_t ws_layout(const Sizes& z, char* base, Ws* w) {
 
 template <class C, int KIND, bool AKC, bool BKC>
 void launch_mm(const char* name, const MmArgs& a, hipStream_t s) {
-  const dim3 grid(xcd_grid(a.tiles * a.ks));
+  const dim3 grid(xcd_grid(static_cast<int64_t>(a.tiles) * a.ks));
   if constexpr (KIND == kApply) {
     if (a.out != kOutX) {
       MOE_LAUNCH(name, (orth_mm_kernel<C, KIND, AKC, BKC, true>), grid, dim3(C::kThreads), 0, s, a);
@@ -1397,7 +1398,7 @@ void launch_any(const char* name, MmArgs& a, const Sizes& z, hipStream_t s) {
       a.tm = static_cast<int>(sym_tiles<C>(a.M, 1));
       a.tn = 1;
     }
-    a.tiles = static_cast<int64_t>(a.tm) * a.tn * z.E;
+    a.tiles = static_cast<unsigned>(static_cast<int64_t>(a.tm) * a.tn * z.E);
     a.ks = C::BM == 64 && !(KIND == kApply) ? k_split(z, a.K) : 1;
     launch_mm<C, KIND, AKC, BKC>(name, a, s);
   };
