@@ -306,7 +306,7 @@ struct Tile {
   static constexpr int kNW = NW_, kWaves = 2 * NW_, kThreads = 64 * kWaves;
   static constexpr int BM = BM_, BN = BN_, BK = BK_, kRing = RING_, KG = KG_;
   static constexpr bool kPairs = PAIRS_;
-  static constexpr int kPhases = BK / 16 / KG;
+  static constexpr int kPhases = BK / 16 / KG;  // per step
   static constexpr int WM = BM / 2, WN = BN / NW_, TM = WM / 32, TN = WN / 32;
   static constexpr int kA = BM * BK, kHi = (BM + BN) * BK;  // elements: the A tile, then the B tile (then lo likewise)
   static constexpr int kSlot = kHi * (PAIRS_ ? 2 : 1);
@@ -626,145 +626,159 @@ __device__ __forceinline__ void epi_diagonal(const f32x16& acc, uint16_t* hi, ui
   }
 }
 
+// stage() brings a block's inputs, run() does the rest; init() loads the
+// coefficients.  Where a tile is one block (WM = 32), the kernel calls the first
+// two before the K loop ends, so that their latencies pass behind it.
 template <class C, int KIND, bool SPLIT, bool BYROW, bool FINAL, bool HASLO>
-__device__ __forceinline__ void epilogue(const f32x16 (&acc)[C::TM][C::TN], const MmArgs& p, uint16_t* lds, int64_t e,
-                                         int m0, int n0, int wm, int wn, int wave, int lane) {
-  constexpr int WN = C::WN, kPart = 32 * WN, CPR = WN / 8, RPI = 64 / CPR, kPieces = 32 / RPI;
-  constexpr bool kLo8 = KIND == kApply && !SPLIT;
-  constexpr int CPR8 = WN / 16, RPI8 = 64 / CPR8, kPieces8 = 32 / RPI8;  // the same for an 8-bit lo part
-  constexpr int kStage = kPieces + (HASLO ? (kLo8 ? kPieces8 : kPieces) : 0);
+struct Epilogue {
+  static constexpr int WN = C::WN, kPart = 32 * WN, CPR = WN / 8, RPI = 64 / CPR, kPieces = 32 / RPI;
+  static constexpr bool kLo8 = KIND == kApply && !SPLIT;
+  static constexpr int CPR8 = WN / 16, RPI8 = 64 / CPR8, kPieces8 = 32 / RPI8;  // the same for an 8-bit lo part
+  static constexpr int kStage = kPieces + (HASLO ? (kLo8 ? kPieces8 : kPieces) : 0);
+  static constexpr int kBuffers = C::TM > 1 ? 2 : 1;
   static_assert(WN == 64 || WN == 32, "row piece layouts");
-  static_assert(C::kWaves * 4 * kPart <= C::kLds, "two buffers of hi and lo per wave");
-  const int rl = lane & 31, g = lane >> 5;
-  const int mw = m0 + wm * C::WM, nw = n0 + wn * WN;  // this wave's outputs
-  const int64_t ob = e * p.so;
-  uint16_t* mine = lds + wave * 4 * kPart;
-  Coef<C, KIND, SPLIT, BYROW> k;
-  k.init(p, e, mw, nw, lane);
+  static_assert(C::kWaves * kBuffers * 2 * kPart <= (C::TM > 1 ? C::kLds : C::kSlot), "buffers of hi and lo per wave");
 
-  const int64_t eo = ob + static_cast<int64_t>(mw) * p.ldo + nw;
-  const int64_t left = mw < p.M && nw < p.N ? (static_cast<int64_t>(p.M - mw) * p.ldo - nw) * 2 : 0;
+  const MmArgs& p;
+  const int64_t e;
+  const int mw, nw, lane;  // this wave's outputs begin at row mw, column nw
+  const int64_t ob, eo;
+  Coef<C, KIND, SPLIT, BYROW> k;
   __amdgpu_buffer_rsrc_t rh, rlo;
-  if constexpr (KIND != kGram) rh = rsrc(p.eh + eo, left);
-  if constexpr (HASLO)
-    rlo = kLo8 ? rsrc(static_cast<const uint8_t*>(p.el) + eo, left / 2)
-               : rsrc(static_cast<const uint16_t*>(p.el) + eo, left);
-  // row pieces: piece u of a block is rows [u RPI, (u + 1) RPI), 16 bytes per lane; the
-  // swizzle's column term repeats every 16 rows
-  const int pr = lane / CPR, pr8 = lane / CPR8;
-  auto piece_col = [&](int u) { return ((lane % CPR) ^ ep_swz<WN>(u * RPI + pr)) * 8; };
-  auto stage = [&](int i) {
+  uint16_t* mine;          // this wave's buffers
+
+  __device__ __forceinline__ Epilogue(const MmArgs& p_, int64_t e_, int mw_, int nw_, int lane_)
+      : p(p_), e(e_), mw(mw_), nw(nw_), lane(lane_), ob(e_ * p_.so),
+        eo(e_ * p_.so + static_cast<int64_t>(mw_) * p_.ldo + nw_), mine(nullptr) {}
+
+  __device__ __forceinline__ void init() {
+    k.init(p, e, mw, nw, lane);
+    const int64_t left = mw < p.M && nw < p.N ? (static_cast<int64_t>(p.M - mw) * p.ldo - nw) * 2 : 0;
+    if constexpr (KIND != kGram) rh = rsrc(p.eh + eo, left);
+    if constexpr (HASLO)
+      rlo = kLo8 ? rsrc(static_cast<const uint8_t*>(p.el) + eo, left / 2)
+                 : rsrc(static_cast<const uint16_t*>(p.el) + eo, left);
+  }
+  __device__ __forceinline__ void place(uint16_t* lds, int wave) { mine = lds + wave * kBuffers * 2 * kPart; }
+  // row pieces: piece u of a block is rows [u RPI, (u + 1) RPI), 16 bytes per lane
+  __device__ __forceinline__ int piece_col(int u) const {
+    return ((lane % CPR) ^ ep_swz<WN>(u * RPI + lane / CPR)) * 8;
+  }
+  __device__ __forceinline__ void stage(int i) const {
+    if constexpr (KIND == kGram) return;
     uint16_t* b = mine + (i & 1) * 2 * kPart;
 #pragma unroll
     for (int u = 0; u < kPieces; ++u) {
-      const int voff = ((32 * i + u * RPI + pr) * p.ldo + piece_col(u)) * 2;
+      const int voff = ((32 * i + u * RPI + lane / CPR) * p.ldo + piece_col(u)) * 2;
       dma16(rh, b + u * 512, voff);
       if constexpr (HASLO && !kLo8) dma16(rlo, b + kPart + u * 512, voff);
     }
     if constexpr (HASLO && kLo8)
 #pragma unroll
       for (int u = 0; u < kPieces8; ++u) {
-        const int r = u * RPI8 + pr8;
+        const int r = u * RPI8 + lane / CPR8;
         dma16(rlo, b + kPart + u * 512, (32 * i + r) * p.ldo + ((lane % CPR8) ^ lo8_swz<WN>(r)) * 16);
       }
-  };
-  // symmetric outputs, by squares: above the diagonal there is nothing to do,
-  // squares on it are computed whole, those below are written twice
-  const bool below = KIND != kApply && mw / C::kSq > nw / C::kSq;
-  __syncthreads();  // the ring is no longer read
-  if (KIND != kApply && mw / C::kSq < nw / C::kSq) return;
-  if constexpr (KIND != kGram) {
-    stage(0);
+  }
+
+  // staged: the first block is on its way already
+  __device__ __forceinline__ void run(const f32x16 (&acc)[C::TM][C::TN], int m0, int n0, bool staged) const {
+    const int rl = lane & 31, g = lane >> 5, pr = lane / CPR, pr8 = lane / CPR8;
+    // symmetric outputs, by squares: above the diagonal there is nothing to do,
+    // squares on it are computed whole, those below are written twice
+    const bool below = KIND != kApply && mw / C::kSq > nw / C::kSq;
+    if (KIND != kApply && mw / C::kSq < nw / C::kSq) return;
+    if (!staged) stage(0);
     if constexpr (C::TM > 1) stage(1);
-  }
 #pragma unroll
-  for (int i = 0; i < C::TM; ++i) {
-    uint16_t* hi = mine + (i & 1) * 2 * kPart;
-    uint16_t* lo = hi + kPart;
-    if constexpr (KIND != kGram) {  // block i has landed; block i + 1 may be in flight
-      if (i + 1 < C::TM) wait_vm<kStage>();
-      else wait_vm<0>();
-    }
-    epi_block<C, KIND, SPLIT, BYROW, FINAL, HASLO>(acc[i], hi, lo, k, i, lane);
-    if constexpr (KIND != kApply) {
-      const int row = mw + 32 * i + rl;
+    for (int i = 0; i < C::TM; ++i) {
+      uint16_t* hi = mine + (i & 1) * 2 * kPart;
+      uint16_t* lo = hi + kPart;
+      if constexpr (KIND != kGram) {  // block i has landed; block i + 1 may be in flight
+        if (i + 1 < C::TM) wait_vm<kStage>();
+        else wait_vm<0>();
+      }
+      epi_block<C, KIND, SPLIT, BYROW, FINAL, HASLO>(acc[i], hi, lo, k, i, lane);
+      if constexpr (KIND != kApply) {
+        const int row = mw + 32 * i + rl;
 #pragma unroll
-      for (int j = 0; j < C::TN; ++j)
-        if (mw + 32 * i == nw + 32 * j) {
-          wave_lds_fence();
-          epi_diagonal<C, KIND, SPLIT>(acc[i][j], hi, lo, k, i, j, p.dout + e * p.sd + row, row < p.M, lane);
-        }
-    }
-    wave_lds_fence();
-    if constexpr (FINAL) {
-      using T = typename std::conditional<SPLIT, float, uint16_t>::type;
+        for (int j = 0; j < C::TN; ++j)
+          if (mw + 32 * i == nw + 32 * j) {
+            wave_lds_fence();
+            epi_diagonal<C, KIND, SPLIT>(acc[i][j], hi, lo, k, i, j, p.dout + e * p.sd + row, row < p.M, lane);
+          }
+      }
+      wave_lds_fence();
+      if constexpr (FINAL) {
+        using T = typename std::conditional<SPLIT, float, uint16_t>::type;
 #pragma unroll 1
-      for (int u = 0; u < kPieces; ++u) {
-        float o[8];
-        Elem<float>::unpack(lds_get16(hi + u * 512 + lane * 8), o);
-        Elem<float>::unpack(lds_get16(lo + u * 512 + lane * 8), o + 4);
-        const int orow = mw + 32 * i + u * RPI + pr, col = nw + piece_col(u);
-        if (orow < p.rows && col < p.cols) {
-          const int64_t off = (e * p.rows + orow) * p.cols + col;
-          const int n = p.cols - col;
-          if (p.out == kOutW) {
-            float w[8];
-            ld8(static_cast<const T*>(p.w) + off, n, w);
+        for (int u = 0; u < kPieces; ++u) {
+          float o[8];
+          Elem<float>::unpack(lds_get16(hi + u * 512 + lane * 8), o);
+          Elem<float>::unpack(lds_get16(lo + u * 512 + lane * 8), o + 4);
+          const int orow = mw + 32 * i + u * RPI + pr, col = nw + piece_col(u);
+          if (orow < p.rows && col < p.cols) {
+            const int64_t off = (e * p.rows + orow) * p.cols + col;
+            const int n = p.cols - col;
+            if (p.out == kOutW) {
+              float w[8];
+              ld8(static_cast<const T*>(p.w) + off, n, w);
 #pragma unroll
-            for (int q = 0; q < 8; ++q) o[q] = p.keep * w[q] - p.gain * o[q];
-          }
-          st8(static_cast<T*>(p.o) + off, n, o);
-        }
-      }
-    } else {
-#pragma unroll
-      for (int u = 0; u < kPieces; ++u) {
-        const int orow = 32 * i + u * RPI + pr, col = piece_col(u);
-        const uint4 vh = lds_get16(hi + u * 512 + lane * 8);
-        uint4 vl;
-        if constexpr (SPLIT) vl = lds_get16(lo + u * 512 + lane * 8);
-        if (mw + orow < p.M && nw + col < p.N) {
-          const int64_t off = eo + orow * p.ldo + col;
-          *reinterpret_cast<uint4*>(p.oh + off) = vh;
-          if constexpr (SPLIT) *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.ol) + off) = vl;
-        }
-      }
-      if (kLo8 && p.ol)
-#pragma unroll
-        for (int u = 0; u < kPieces8; ++u) {
-          const int r = u * RPI8 + pr8, orow = 32 * i + r, col = ((lane % CPR8) ^ lo8_swz<WN>(r)) * 16;
-          const uint4 vl = lds_get16(lo + u * 512 + lane * 8);
-          if (mw + orow < p.M && nw + col < p.N)
-            *reinterpret_cast<uint4*>(static_cast<uint8_t*>(p.ol) + eo + orow * p.ldo + col) = vl;
-        }
-    }
-    if constexpr (KIND != kApply) {
-      if (below) {  // the mirror image: 8 of the block's rows at one column per lane
-        auto swz = [](int r) { return ep_swz<WN>(r); };
-        const int64_t mo = ob + static_cast<int64_t>(nw + rl) * p.ldo + mw + 8 * g;
-#pragma unroll
-        for (int t = 0; t < WN / 32 * 2; ++t) {
-          const int cb = (t >> 1) * 32, ks = t & 1;
-          const f16x8 vh = frag_tr<WN>(hi, cb, ks, lane, swz);
-          f16x8 vl;
-          if constexpr (SPLIT) vl = frag_tr<WN>(lo, cb, ks, lane, swz);
-          if (nw + cb + rl < p.N && mw + 32 * i + ks * 16 + 8 * g < p.M) {
-            const int64_t off = mo + cb * p.ldo + 32 * i + ks * 16;
-            *reinterpret_cast<uint4*>(p.oh + off) = __builtin_bit_cast(uint4, vh);
-            if constexpr (SPLIT)
-              *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.ol) + off) = __builtin_bit_cast(uint4, vl);
+              for (int q = 0; q < 8; ++q) o[q] = p.keep * w[q] - p.gain * o[q];
+            }
+            st8(static_cast<T*>(p.o) + off, n, o);
           }
         }
+      } else {
+#pragma unroll
+        for (int u = 0; u < kPieces; ++u) {
+          const int orow = 32 * i + u * RPI + pr, col = piece_col(u);
+          const uint4 vh = lds_get16(hi + u * 512 + lane * 8);
+          uint4 vl;
+          if constexpr (SPLIT) vl = lds_get16(lo + u * 512 + lane * 8);
+          if (mw + orow < p.M && nw + col < p.N) {
+            const int64_t off = eo + orow * p.ldo + col;
+            *reinterpret_cast<uint4*>(p.oh + off) = vh;
+            if constexpr (SPLIT) *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.ol) + off) = vl;
+          }
+        }
+        if (kLo8 && p.ol)
+#pragma unroll
+          for (int u = 0; u < kPieces8; ++u) {
+            const int r = u * RPI8 + pr8, orow = 32 * i + r, col = ((lane % CPR8) ^ lo8_swz<WN>(r)) * 16;
+            const uint4 vl = lds_get16(lo + u * 512 + lane * 8);
+            if (mw + orow < p.M && nw + col < p.N)
+              *reinterpret_cast<uint4*>(static_cast<uint8_t*>(p.ol) + eo + orow * p.ldo + col) = vl;
+          }
       }
+      if constexpr (KIND != kApply) {
+        if (below) {  // the mirror image: 8 of the block's rows at one column per lane
+          auto swz = [](int r) { return ep_swz<WN>(r); };
+          const int64_t mo = ob + static_cast<int64_t>(nw + rl) * p.ldo + mw + 8 * g;
+#pragma unroll
+          for (int t = 0; t < WN / 32 * 2; ++t) {
+            const int cb = (t >> 1) * 32, ks = t & 1;
+            const f16x8 vh = frag_tr<WN>(hi, cb, ks, lane, swz);
+            f16x8 vl;
+            if constexpr (SPLIT) vl = frag_tr<WN>(lo, cb, ks, lane, swz);
+            if (nw + cb + rl < p.N && mw + 32 * i + ks * 16 + 8 * g < p.M) {
+              const int64_t off = mo + cb * p.ldo + 32 * i + ks * 16;
+              *reinterpret_cast<uint4*>(p.oh + off) = __builtin_bit_cast(uint4, vh);
+              if constexpr (SPLIT)
+                *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.ol) + off) = __builtin_bit_cast(uint4, vl);
+            }
+          }
+        }
+      }
+      wave_lds_fence();
+      if constexpr (KIND != kGram)
+        if (i + 2 < C::TM) {
+          __builtin_amdgcn_s_waitcnt(0xC07F);  // lgkmcnt(0): the buffer has been read out
+          stage(i + 2);
+        }
     }
-    wave_lds_fence();
-    if constexpr (KIND != kGram)
-      if (i + 2 < C::TM) {
-        __builtin_amdgcn_s_waitcnt(0xC07F);  // lgkmcnt(0): the buffer has been read out
-        stage(i + 2);
-      }
   }
-}
+};
 
 // Joins the workgroups that share a tile's K: each writes its accumulators to
 // the workspace, and the last to arrive adds them all, in order, whichever it
@@ -816,8 +830,11 @@ __device__ __forceinline__ bool join_k(f32x16 (&acc)[C::TM][C::TN], const MmArgs
   return true;
 }
 
-// FINAL: apply's last step, which writes the result instead of the next X.
-template <class C, int KIND, bool AKC, bool BKC, bool FINAL>
+// MODE of apply: the next X from one without a lo part, from one with it, or the
+// last step's result.
+enum { kX0 = 0, kX = 1, kLast = 2 };
+
+template <class C, int KIND, bool AKC, bool BKC, int MODE>
 __global__ __launch_bounds__(C::kThreads) __attribute__((amdgpu_waves_per_eu(C::kWavesPerSimd)))
 void orth_mm_kernel(MmArgs p) {
   constexpr bool SPLIT = C::kPairs;
@@ -825,8 +842,8 @@ void orth_mm_kernel(MmArgs p) {
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int wm = wave / C::kNW, wn = wave % C::kNW;
-  // consecutive tiles of a matrix on one XCD (workgroups go to the 8 XCDs in turn)
-  // (32-bit arithmetic: 64-bit divisions here took a microsecond of each launch)
+  // consecutive tiles of a matrix on one XCD (workgroups go to the 8 XCDs in
+  // turn); 32-bit arithmetic, as 64-bit divisions took half a microsecond of each launch
   constexpr bool kKSplit = C::BM == 64 && KIND != kApply;
   const unsigned ks_n = kKSplit ? p.ks : 1, total = p.tiles * ks_n;
   const unsigned wid = blockIdx.x % kNumXcd * ((total + kNumXcd - 1) / kNumXcd) + blockIdx.x / kNumXcd;
@@ -849,6 +866,11 @@ void orth_mm_kernel(MmArgs p) {
   Operand<C::BN, C::BK, BKC, C::kWaves> B;
   A.init(p.ah + e * p.sa, SPLIT ? p.al + e * p.sa : nullptr, p.lda, m0, p.M, p.K, wave, lane);
   B.init(p.bh + e * p.sb, SPLIT ? p.bl + e * p.sb : nullptr, p.ldb, n0, p.N, p.K, wave, lane);
+  constexpr bool kHasLo = KIND == kGram ? false : SPLIT || (KIND == kApply && MODE == kX);
+  Epilogue<C, KIND, SPLIT, KIND != kApply || !BKC, MODE == kLast, kHasLo> epi(p, e, m0 + wm * C::WM, n0 + wn * C::WN,
+                                                                              lane);
+  const bool early = C::TM == 1 && ks_n == 1;
+  if (early) epi.init();
   const int nk1 = (p.K + C::BK - 1) / C::BK;
   const int k_lo = kKSplit ? static_cast<int>(static_cast<unsigned>(nk1 * ks_i) / ks_n) : 0;
   const int nk = (kKSplit ? static_cast<int>(static_cast<unsigned>(nk1 * (ks_i + 1)) / ks_n) : nk1) - k_lo;
@@ -918,52 +940,43 @@ void orth_mm_kernel(MmArgs p) {
   lds_barrier();
   read(0, 0, 0);
   int slot = 0;
-  // the step's end: wait for step kt + 1, refill the slot, read on
-  auto advance = [&](int kt, int buf) {
-    const int next = slot + 1 == C::kRing ? 0 : slot + 1;
-    if (kt + 1 < nk) {
-      const int ahead = nk - 2 - kt;  // steps whose loads may stay outstanding
-      if (ahead >= C::kRing - 2) wait_vm<(C::kRing - 2) * C::kLoads>();
-      else if (C::kRing > 3 && ahead == 1) wait_vm<C::kLoads>();
-      else wait_vm<0>();
-      lds_barrier();
-      if (head < nk) issue();
-      read(next, 0, buf);
-    }
-    slot = next;
-  };
-  static_assert(C::kRing >= 2 && C::kRing <= 4, "ring waits");
-  if constexpr (C::kPhases == 1) {
-    for (int kt = 0; kt < nk; kt += 2) {
-      advance(kt, 1);
-      mma(0);
-      if (kt + 1 < nk) {
-        advance(kt + 1, 0);
-        mma(1);
-      }
-    }
-  } else {
-    static_assert(C::kPhases % 2 == 0, "phase buffers alternate");
-    for (int kt = 0; kt < nk; ++kt) {
+  static_assert(C::kRing == 2 || C::kRing == 3, "ring waits");
+  static_assert(C::kPhases % 2 == 0, "phase buffers alternate");
+  for (int kt = 0; kt + 1 < nk; ++kt) {
 #pragma unroll
-      for (int ph = 0; ph < C::kPhases; ++ph) {
-        if (ph + 1 < C::kPhases) read(slot, ph + 1, (ph + 1) & 1);
-        else advance(kt, 0);
-        mma(ph & 1);
-      }
+    for (int ph = 0; ph + 1 < C::kPhases; ++ph) {
+      read(slot, ph + 1, (ph + 1) & 1);
+      mma(ph & 1);
     }
+    // the loads of one more step may stay outstanding, if there are any
+    if (C::kRing == 3 && kt + 2 < nk) wait_vm<C::kLoads>();
+    else wait_vm<0>();
+    lds_barrier();
+    if (head < nk) issue();
+    slot = slot + 1 == C::kRing ? 0 : slot + 1;
+    read(slot, 0, 0);
+    mma((C::kPhases - 1) & 1);
+  }
+  // the last step; no other slot is read any more, so the epilogue's first inputs
+  // can go into the next one
+  if (early) {
+    epi.place(lds + (slot + 1 == C::kRing ? 0 : slot + 1) * C::kSlot, wave);
+    epi.stage(0);
+  }
+#pragma unroll
+  for (int ph = 0; ph < C::kPhases; ++ph) {
+    if (ph + 1 < C::kPhases) read(slot, ph + 1, (ph + 1) & 1);
+    mma(ph & 1);
   }
   if constexpr (kKSplit) {
     if (ks_n > 1 && !join_k<C>(acc, p, lid, ks_i, lds, tid)) return;
   }
-  if constexpr (KIND != kApply)
-    epilogue<C, KIND, SPLIT, true, false, KIND == kPoly && SPLIT>(acc, p, lds, e, m0, n0, wm, wn, wave, lane);
-  else if constexpr (SPLIT || FINAL)
-    epilogue<C, KIND, SPLIT, !BKC, FINAL, SPLIT>(acc, p, lds, e, m0, n0, wm, wn, wave, lane);
-  else if (p.el)
-    epilogue<C, KIND, SPLIT, !BKC, FINAL, true>(acc, p, lds, e, m0, n0, wm, wn, wave, lane);
-  else
-    epilogue<C, KIND, SPLIT, !BKC, FINAL, false>(acc, p, lds, e, m0, n0, wm, wn, wave, lane);
+  if (!early) {
+    epi.init();
+    __syncthreads();  // the ring is no longer read
+    epi.place(lds, wave);
+  }
+  epi.run(acc, m0, n0, early);
 }
 
 // ---------------------------------------------------------------------------
@@ -1378,13 +1391,15 @@ size_t ws_layout(const Sizes& z, char* base, Ws* w) {
 template <class C, int KIND, bool AKC, bool BKC>
 void launch_mm(const char* name, const MmArgs& a, hipStream_t s) {
   const dim3 grid(xcd_grid(static_cast<int64_t>(a.tiles) * a.ks));
+  auto go = [&](auto mode) {
+    MOE_LAUNCH(name, (orth_mm_kernel<C, KIND, AKC, BKC, decltype(mode)::value>), grid, dim3(C::kThreads), 0, s, a);
+  };
   if constexpr (KIND == kApply) {
-    if (a.out != kOutX) {
-      MOE_LAUNCH(name, (orth_mm_kernel<C, KIND, AKC, BKC, true>), grid, dim3(C::kThreads), 0, s, a);
-      return;
-    }
+    if (a.out != kOutX) return go(std::integral_constant<int, kLast>{});
+    if constexpr (!C::kPairs)
+      if (!a.el) return go(std::integral_constant<int, kX0>{});
   }
-  MOE_LAUNCH(name, (orth_mm_kernel<C, KIND, AKC, BKC, false>), grid, dim3(C::kThreads), 0, s, a);
+  go(std::integral_constant<int, kX>{});
 }
 
 template <int KIND, bool AKC, bool BKC>
