@@ -114,6 +114,11 @@ __device__ __forceinline__ void each_piece(const int32_t* seq, int64_t S, int64_
   }
 }
 
+__device__ __forceinline__ double wave_sum_d(double v) {
+#pragma unroll
+  for (int o = 32; o >= 1; o >>= 1) v += __shfl_xor(v, o, 64);
+  return v;
+}
 __device__ __forceinline__ int wave_sum_i(int v) {
 #pragma unroll
   for (int o = 32; o >= 1; o >>= 1) v += __shfl_xor(v, o, 64);
@@ -285,7 +290,7 @@ __global__ __launch_bounds__(kThreads) void balance_partial_kernel(FwdArgs a) {
 // is does not matter to the result.
 __global__ __launch_bounds__(kSumThreads) void balance_sum_kernel(FwdArgs a) {
   constexpr int G = kSumThreads / kCols, W = kSumThreads / 64;
-  __shared__ float s_p[G][kCols + 1], s_f[W];
+  __shared__ double s_p[G][kCols + 1], s_f[W];
   __shared__ int s_c[G][kCols + 1], s_i[W], s_last;
   const int tid = threadIdx.x, cl = tid % kCols, g = tid / kCols, E = a.E;
   const int e = blockIdx.x * kCols + cl;
@@ -295,20 +300,20 @@ __global__ __launch_bounds__(kSumThreads) void balance_sum_kernel(FwdArgs a) {
   for (int64_t s = blockIdx.y; s < a.S; s += gridDim.y) {
     const int64_t lo = seq_at(a.seq, s, a.S, a.T), hi = seq_at(a.seq, s + 1, a.S, a.T);
     const int64_t f = lo < hi ? lo / kTok + s : 0, end = lo < hi ? (hi - 1) / kTok + s + 1 : 0;
-    float p = 0.f, z = 0.f;
+    double p = 0.0, z = 0.0;
     int c = 0, n = 0;
     if (e < E)
 #pragma unroll 4
       for (int64_t i = f + g; i < end; i += G) {
-        p += a.ws.p[i * E + e];
+        p += static_cast<double>(a.ws.p[i * E + e]);
         c += a.ws.c[i * E + e];
       }
     for (int64_t i = f + tid; i < end; i += kSumThreads) {
       n += a.ws.n[i];
-      z += a.ws.z[i];
+      z += static_cast<double>(a.ws.z[i]);
     }
     n = wave_sum_i(n);
-    z = wave_sum(z);
+    z = wave_sum_d(z);
     s_p[g][cl] = p;
     s_c[g][cl] = c;
     if ((tid & 63) == 0) {
@@ -317,7 +322,7 @@ __global__ __launch_bounds__(kSumThreads) void balance_sum_kernel(FwdArgs a) {
     }
     __syncthreads();
     n = 0;
-    z = 0.f;
+    z = 0.0;
 #pragma unroll
     for (int w = 0; w < W; ++w) {
       n += s_i[w];
@@ -329,20 +334,20 @@ __global__ __launch_bounds__(kSumThreads) void balance_sum_kernel(FwdArgs a) {
         p += s_p[k][cl];
         c += s_c[k][cl];
       }
-      const float inv = n > 0 ? 1.0f / static_cast<float>(n) : 0.f;
+      const double inv = n > 0 ? 1.0 / n : 0.0;
       float term = 0.f;
       if (e < E) {
         p *= inv;
-        a.probs[s * E + e] = p;
+        a.probs[s * E + e] = static_cast<float>(p);
         a.counts[s * E + e] = c;
-        term = static_cast<float>(c) * p * inv;
+        term = static_cast<float>(c * p * inv);
       }
 #pragma unroll
       for (int o = kCols / 2; o >= 1; o >>= 1) term += __shfl_xor(term, o, 64);
       if (cl == 0) st(a.ws.bal + s * gridDim.x + blockIdx.x, term);
       if (cl == 0 && blockIdx.x == 0) {
         st(a.norm + 2 + s, static_cast<float>(n));
-        st(a.ws.zs + s, z);
+        st(a.ws.zs + s, static_cast<float>(z));
       }
     }
     __syncthreads();
@@ -355,29 +360,29 @@ __global__ __launch_bounds__(kSumThreads) void balance_sum_kernel(FwdArgs a) {
   __syncthreads();
   if (!s_last) return;
   auto ld = [](const float* p) { return __hip_atomic_load(p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT); };
-  float v[4] = {0.f, 0.f, 0.f, 0.f};  // sum of terms, of lse^2, live sequences, tokens
+  double v[4] = {0.0, 0.0, 0.0, 0.0};  // sum of terms, of lse^2, live sequences, tokens
   const int64_t terms = a.S * gridDim.x;
   for (int64_t i = tid; i < terms; i += kSumThreads) v[0] += ld(a.ws.bal + i);
   for (int64_t s = tid; s < a.S; s += kSumThreads) {
     const float n = ld(a.norm + 2 + s);
     v[1] += ld(a.ws.zs + s);
-    v[2] += n > 0.f ? 1.f : 0.f;
+    v[2] += n > 0.f ? 1.0 : 0.0;
     v[3] += n;
   }
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    v[i] = wave_sum(v[i]);
+    v[i] = wave_sum_d(v[i]);
     __syncthreads();
     if ((tid & 63) == 0) s_f[tid >> 6] = v[i];
     __syncthreads();
-    v[i] = 0.f;
+    v[i] = 0.0;
     for (int w = 0; w < W; ++w) v[i] += s_f[w];
   }
   if (tid == 0) {
-    a.loss[0] = v[2] > 0.f ? a.alpha * static_cast<float>(E) / (static_cast<float>(a.k) * v[2]) * v[0] : 0.f;
-    a.loss[1] = v[3] > 0.f && a.zeta != 0.f ? a.zeta / v[3] * v[1] : 0.f;
-    a.norm[0] = v[2];
-    a.norm[1] = v[3];
+    a.loss[0] = v[2] > 0.0 ? static_cast<float>(a.alpha * E / (a.k * v[2]) * v[0]) : 0.f;
+    a.loss[1] = v[3] > 0.0 && a.zeta != 0.f ? static_cast<float>(a.zeta / v[3] * v[1]) : 0.f;
+    a.norm[0] = static_cast<float>(v[2]);
+    a.norm[1] = static_cast<float>(v[3]);
   }
 }
 

@@ -420,6 +420,79 @@ def test_muon_step(gpu, E, rows, cols, dtype):
         assert torch.equal(dw, w2) and torch.equal(dm, m2)
 
 
+# ------------------------------------------------------------------- offsets past 32 bits
+
+def plain_orth_f32(m):
+    """The iteration in fp32 with library products (one matrix)."""
+    a, b, c = to.QUINTIC
+    x = m.float()
+    x = x.T.contiguous() if x.shape[0] > x.shape[1] else x
+    x = x / (x.double().norm().float() + 1e-7)
+    for _ in range(5):
+        q = x @ x.T.contiguous()
+        x = a * x + (b * q + c * (q @ q)) @ x
+    return x.T if m.shape[0] > m.shape[1] else x
+
+
+def test_orthogonalize_large(gpu):
+    """One large odd matrix, and a stack whose elements pass 2^31 (its last matrix checked)."""
+    gen = torch.Generator(device="cuda")
+    gen.manual_seed(1)
+    for E, rows, cols in ((1, 20001, 6001), (1, 3001, 20010), (34, 8192, 8192)):
+        gu.say(f"case orthogonalize large E={E} {rows}x{cols}")
+        g = torch.randn((E, rows, cols), generator=gen, device="cuda", dtype=torch.bfloat16)
+        out = B.moe_orthogonalize(g)
+        torch.cuda.synchronize()
+        for e in {0, E - 1}:
+            ref = plain_orth_f32(g[e])
+            assert float((out[e].float() - ref).abs().max() / ref.abs().max()) <= ORTH_TOL["bf16"]
+        del g, out
+        torch.cuda.empty_cache()
+
+
+def test_layernorm_offsets_past_32_bits(gpu):
+    T, d = 270001, 8190
+    gu.say(f"case layernorm T={T} d={d}")
+    gen = torch.Generator(device="cuda")
+    gen.manual_seed(2)
+    x = torch.randn((T, d), generator=gen, device="cuda", dtype=torch.bfloat16)
+    w = torch.randn(d, generator=gen, device="cuda").bfloat16()
+    fw = B.moe_layernorm(x, w, w)
+    bw = B.moe_layernorm_bwd(x, x, w, fw["mean"], fw["rstd"])
+    torch.cuda.synchronize()
+    rows = torch.tensor([0, 1, 131000, T - 2, T - 1], device="cuda")
+    s, y = h64(x[rows]), to.layernorm(h64(x[rows]), h64(w), h64(w))[0]
+    close("y", fw["y"][rows], y, half("bf16"), 1e-4)
+    close("dx", bw["dx"][rows], to.layernorm_bwd(s, s, h64(w))[0], half("bf16"), 1e-4)
+    db = sum(c.double().sum(0) for c in x.split(20000))
+    ab = sum(c.double().abs().sum(0) for c in x.split(20000))
+    assert bool(((bw["db"].double() - db).abs() <= half("bf16") * db.abs() + 1e-5 * ab).all())
+    torch.cuda.empty_cache()
+
+
+def test_balance_offsets_past_32_bits(gpu):
+    T, E, k = 8_500_000, 256, 2
+    gu.say(f"case balance T={T} E={E}")
+    gen = torch.Generator(device="cuda")
+    gen.manual_seed(3)
+    lg = torch.randn((T, E), generator=gen, device="cuda")
+    idx = torch.stack([torch.arange(T, device="cuda") % E, (torch.arange(T, device="cuda") + 1) % E], 1).int()
+    seq = torch.tensor([0, 1000, T - 7, T], dtype=torch.int32, device="cuda")
+    got = B.moe_balance_loss(lg, idx, 1.0, 1.0, seq_offsets=seq)
+    dl = B.moe_balance_loss_bwd(lg, got, k, 1.0, 1.0, seq_offsets=seq)
+    torch.cuda.synchronize()
+    assert int(got["counts"].sum()) == T * k and int(got["counts"][2].sum()) == 7 * k
+    tail = slice(T - 7, T)
+    p = torch.softmax(lg[tail].double(), 1)
+    lse = torch.logsumexp(lg[tail].double(), 1)
+    close("lse", got["lse"][tail], h64(lse), 1e-6, 1e-6)
+    close("probs", got["probs"][2], h64(p.mean(0)), 1e-5, 1e-8)
+    a = E * got["counts"][2].double() / (k * 49 * 3)
+    ref = p * (a - (p * a).sum(1, keepdim=True) + 2 / T * lse[:, None])
+    close("dlogits", dl[tail], h64(ref), 1e-5, 1e-5 * float(ref.abs().max()))
+    torch.cuda.empty_cache()
+
+
 # ------------------------------------------------------------------- how the calls are used
 
 def test_calls_are_deterministic_and_capturable(gpu):
