@@ -164,7 +164,8 @@ int moe_route_stats(const int32_t* counts, int32_t E, int32_t* stats, void* stre
  * token of -inf only chooses nothing).  A counted token with a NaN or +inf logit
  * makes the losses NaN; what masked tokens hold does not matter.
  * topk_idx [T, k] from moe_route_topk; logits [T, E] fp32; counts [S, E] int32;
- * probs [S, E], lse, loss [2] fp32.  Sums are fp32 in a fixed order.
+ * probs [S, E], lse, loss [2] fp32.  Sums are
+ * fp32 over at most 32 tokens and fp64 beyond, in a fixed order.
  * The backward writes
  *   dlogits[t,e] = p_e (a_e - sum_j a_j p_j) + dloss[1] 2 zeta / N lse_t p_e,
  *   a_e = dloss[0] alpha E counts[s,e] / (k n_s^2 S')       (no gradient through counts)
@@ -400,13 +401,14 @@ int mx_quantize(const void* src, int src_dtype, int64_t batch, int64_t rows, int
  * overlap.  coef: HOST array [steps][3] of a, b, c, read before the call returns;
  * NULL: 3.4445, -4.7750, 2.0315 in every step.
  * Accuracy: fp32 sums; products on matrix cores, with operands of 22 mantissa bits
- * for MOE_F32, and for MOE_BF16 of 11 bits with the iterate itself kept to 22.  A
+ * for MOE_F32, and for MOE_BF16 of 11 bits with the iterate itself kept to 15.  A
  * zero matrix gives zeros; a non-finite element makes its own matrix NaN only.
  * Limits: rows, cols <= 32768 with rows x cols (rounded up to 64) < 2^30,
  * E <= 65535, 1 <= steps <= 16, and coefficients whose polynomial keeps singular
  * values and its own terms within 15 over all steps (fp16 operands), else
- * MOE_EUNSUPPORTED; MOE_EINVAL for non-finite scalars and negative eps.  E = 0 is a
- * no-op.  One workspace size serves both calls. */
+ * MOE_EUNSUPPORTED; MOE_EINVAL for non-finite scalars (lr scale and lr weight_decay
+ * among them) and negative eps.  E = 0 is a no-op.  One workspace size serves both
+ * calls. */
 size_t moe_orthogonalize_workspace(int32_t E, int32_t rows, int32_t cols, int dtype);
 int moe_orthogonalize(const void* g, int dtype, int32_t E, int32_t rows, int32_t cols, int32_t steps,
                       const float* coef, float eps, void* out, void* ws, size_t ws_bytes, void* stream);

@@ -145,7 +145,7 @@ struct PreArgs {
   float beta;
   int nesterov;
   double* part;       // [E][chunks] sums of squares
-  float* cs;          // [E][steps + 1]
+  float* cs;          // [E][2][steps]: c_i, then c_i / c_{i+1}
   uint16_t* xh;       // [E][rp][cp]
   void* xl;           // lo: fp16 for fp32 gradients, else 8 bits; nullptr: not needed
   int32_t* ticket;    // zeroed here
@@ -219,11 +219,12 @@ __global__ __launch_bounds__(kNormThreads) void orth_scale_kernel(PreArgs a) {
   }
   if (blockIdx.x == 0 && threadIdx.x == 0) {
     double c = ok && norm > 0.0 ? ldexp(1.0, -q) / (norm + static_cast<double>(a.eps)) : 1.0;
-    float* cs = a.cs + e * (a.steps + 1);
-    cs[0] = static_cast<float>(c);
+    float* cs = a.cs + e * 2 * a.steps;
     for (int i = 0; i < a.steps; ++i) {  // X may grow by growth[i]; c >= 1 becomes 1
-      c = fmin(1.0, c * static_cast<double>(a.growth[i]));
-      cs[i + 1] = static_cast<float>(c);
+      const double next = fmin(1.0, c * static_cast<double>(a.growth[i]));
+      cs[i] = static_cast<float>(c);
+      cs[a.steps + i] = static_cast<float>(c / next);  // also where c itself is below fp32's range
+      c = next;
     }
   }
   if (blockIdx.x == 0)
@@ -491,14 +492,14 @@ struct Coef {
   float a, b, c, v, f, lo_scale, lo_inv;
 
   __device__ __forceinline__ void init(const MmArgs& p, int64_t e, int mw, int nw, int lane) {
-    const float* cs = p.cs + e * (p.steps + 1) + p.step;
+    const float* cs = p.cs + e * 2 * p.steps + p.step;
     const int rl = lane & 31, g = lane >> 5;
     a = p.ca;
     b = p.cb;
     c = p.cc;
     lo_scale = p.lo_scale;
     lo_inv = SPLIT ? 1.0f : 1.0f / p.lo_scale;
-    f = KIND != kApply ? 1.0f : p.out == kOutX ? cs[0] / cs[1] : cs[0] / kS;
+    f = KIND != kApply ? 1.0f : p.out == kOutX ? cs[p.steps] : cs[0] / kS;
     v = KIND == kGram ? cs[0] * cs[0] / kS : (KIND == kPoly ? p.cc : f) / kS;
     if constexpr (KIND != kGram) {
       const float* d = p.din + e * p.sd;
@@ -1162,8 +1163,9 @@ __global__ __launch_bounds__(kSmallThreads) void orth_small_kernel(SmArgs p) {
   tx.init(rp, cp, wave);
   for (int st = 0; st < a.steps; ++st) {
     const float ci = static_cast<float>(cd);
-    cd = fmin(1.0, cd * static_cast<double>(a.growth[st]));
-    const float cn = static_cast<float>(cd);
+    const double next = fmin(1.0, cd * static_cast<double>(a.growth[st]));
+    const float ratio = static_cast<float>(cd / next);
+    cd = next;
     const float ca = p.coef[st][0], cb = p.coef[st][1], cc = p.coef[st][2];
     const bool last = st + 1 == a.steps;
     // Gram
@@ -1232,7 +1234,7 @@ __global__ __launch_bounds__(kSmallThreads) void orth_small_kernel(SmArgs p) {
     if constexpr (TALL) sm_product<true, true, SPLIT, kSmallTasks>(acc, X, A, tx, mp, lane);
     else sm_product<true, false, SPLIT, kSmallTasks>(acc, A, X, tx, mp, lane);
     __syncthreads();
-    const float f = last ? ci / kS : ci / cn;
+    const float f = last ? ci / kS : ratio;
 #pragma unroll
     for (int u = 0; u < kSmallTasks; ++u) {
       if (u >= tx.n) continue;
@@ -1367,7 +1369,7 @@ size_t ws_layout(const Sizes& z, char* base, Ws* w) {
   };
   Ws t;
   t.part = reinterpret_cast<double*>(take(static_cast<size_t>(z.E) * z.chunks * 8));
-  t.cs = reinterpret_cast<float*>(take(static_cast<size_t>(z.E) * (kMaxSteps + 1) * 4));
+  t.cs = reinterpret_cast<float*>(take(static_cast<size_t>(z.E) * 2 * kMaxSteps * 4));
   t.da = reinterpret_cast<float*>(take(static_cast<size_t>(z.E) * z.mp * 4));
   t.db = reinterpret_cast<float*>(take(static_cast<size_t>(z.E) * z.mp * 4));
   const int64_t tiles = sym_tiles<Small>(z.mp, z.E);
@@ -1696,5 +1698,6 @@ extern "C" int moe_muon_step(const void* g, int dtype, int32_t E, int32_t rows, 
   if (!finite(momentum) || !finite(lr) || !finite(weight_decay) || !finite(scale)) return MOE_EINVAL;
   if (E != 0 && (!mom || !mom_out || !w)) return MOE_EINVAL;
   const Step st{mom, mom_out, momentum, nesterov != 0, w, 1.0f - lr * weight_decay, lr * scale};
+  if (!finite(st.keep) || !finite(st.gain)) return MOE_EINVAL;
   return run(g, dtype, E, rows, cols, steps, coef, eps, st, w_out, ws, ws_bytes, static_cast<hipStream_t>(stream));
 }

@@ -398,6 +398,27 @@ def test_orthogonalize_special_matrices(gpu, dtype):
 
 
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("rows,cols", [(40, 72), (130, 300)])
+def test_orthogonalize_eps_far_above_the_norm(gpu, rows, cols, dtype):
+    """X = U / (|U| + eps) near and below the smallest fp32 number: small results, not NaN."""
+    g = gradients(np.random.default_rng(9), 4, rows, cols, "noise")
+    g /= np.sqrt((g ** 2).sum((1, 2), keepdims=True))
+    g[1] *= 1e-25
+    g[2] *= 1e-32
+    g[3] *= 1e-37
+    t = torch.from_numpy(g.astype(np.float32)).to(DT[dtype])
+    gu.say(f"case orthogonalize eps {rows}x{cols} {dtype}")
+    for eps in (1.0, 1e8, 1e30):
+        out = h64(B.moe_orthogonalize(t.cuda(), eps=eps))
+        ref = to.orthogonalize(t.double().numpy(), eps=np.float64(np.float32(eps)))
+        for e in range(4):
+            # besides the usual error, the last factor times 2^12 elements' units is below fp32's normal
+            # numbers for results under 2^-114: half a unit 2^-149 of it, and the result's own, in bf16 2^-134
+            err = np.abs(out[e] - ref[e]).max()
+            assert err <= ORTH_TOL[dtype] * np.abs(ref[e]).max() + 2.0 ** -133, (eps, e, err, np.abs(ref[e]).max())
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
 @pytest.mark.parametrize("E,rows,cols", [(1, 1, 3), (3, 70, 33), (2, 33, 70), (2, 128, 260)])
 def test_muon_step(gpu, E, rows, cols, dtype):
     rng = np.random.default_rng(rows * 3 + cols)

@@ -112,6 +112,14 @@ def test_orthogonalize_validation(L):
     assert muon(n=need - 1) == EWS and muon(E=0, g=None) == 0
 
 
+def test_muon_refuses_products_of_its_scalars_that_overflow(L):
+    def muon(lr=0.1, wd=0.0, sc=1.0):
+        return L.moe_muon_step(FAKE, 1, 2, 64, 96, FAKE, 0.9, 1, 5, None, 1e-7, FAKE, lr, wd, sc, FAKE, FAKE, FAKE, BIG,
+                               None)
+
+    assert muon(lr=1e30, sc=1e30) == muon(lr=1e30, wd=1e30) == EINVAL
+
+
 def test_oracle_layernorm_gradient_against_differences():
     rng = np.random.default_rng(0)
     x, dy, w, b = rng.standard_normal((3, 11)), rng.standard_normal((3, 11)), rng.standard_normal(11), rng.standard_normal(11)
