@@ -404,8 +404,10 @@ struct BwdArgs {
 };
 
 // The same walk over pieces as the forward; the softmax comes back as
-// exp(l - lse) from the saved lse, so a token needs one reduction.  A token of
-// -inf only has lse 0 saved and gets zeros from the exponentials.  A workgroup
+// exp(l - lse) from the saved lse, divided by its sum: for logits far from zero
+// the rounding of lse (half an ulp, all of log E at the type's lowest value)
+// would be the relative error of every p.  A token of -inf only has lse 0 saved
+// and gets zeros from the exponentials.  A workgroup
 // takes the tokens that its lanes hold at once: with more, one after the other,
 // their loads waited for each other (16384 x 128: 13.1 us at 32 tokens, 10.5 at
 // the 8 of this kernel).  Launches past kBwdGroups workgroups go round.
@@ -445,16 +447,19 @@ __global__ __launch_bounds__(kThreads) void balance_bwd_kernel(BwdArgs a) {
       const float n = a.norm[2 + s];
       if (!(n > 0.f)) return;
       const float f = g0 * a.alpha * static_cast<float>(E) / (static_cast<float>(a.k) * n * n * live);
-      float c[4], dot = 0.f;
+      float c[4], dot = 0.f, sum = 0.f;
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         c[i] = e0 + i < E ? f * static_cast<float>(a.counts[s * E + e0 + i]) : 0.f;
         dot += c[i] * p[i];
+        sum += p[i];
       }
       dot = Row<LPT>::sum(dot);
+      sum = Row<LPT>::sum(sum);
+      const float inv = sum == 0.f ? 0.f : 1.0f / sum;
       if (on && t >= lo && t < hi)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) dl[i] += p[i] * (c[i] - dot + zc);
+        for (int i = 0; i < 4; ++i) dl[i] += p[i] * inv * (c[i] - dot * inv + zc);
     });
     if (!on) continue;
     float* o = a.dlogits + t * E + e0;

@@ -89,7 +89,8 @@ def balance_loss_bwd(logits, idx, alpha, zeta, seq=None, mask=None, dloss=(1.0, 
     for s, r in enumerate(rows):
         if len(r) == 0:
             continue
-        p = np.exp(lg[r] - lse[r][:, None])
+        p = np.exp(lg[r] - lg[r].max(1, keepdims=True))  # not from lse, whose rounding loses log E at the lowest logits
+        p /= p.sum(1, keepdims=True)
         a = dloss[0] * alpha * E * cnt[s] / (k * len(r) ** 2 * live)
         dl[r] = p * (a - (p * a).sum(1, keepdims=True)) + dloss[1] * 2 * zeta / n_all * lse[r][:, None] * p
     if gates is not None:

@@ -252,6 +252,23 @@ def test_balance_loss_rows_that_do_not_count(gpu):
     assert bool(torch.isnan(bad["loss"]).all()) or seq[0] > 0
 
 
+def test_balance_loss_logits_far_from_zero(gpu):
+    """Softmax and gradient do not depend on a common shift, however coarse the shifted lse is."""
+    gu.say("case balance shifted logits, uniform rows of the lowest value")
+    lg, idx, seq, mask, rng = routing_case(300, 24, 3, 4, 13, True)
+    lg[::3] += 1e4
+    lg[1::3] -= 1e6
+    check_balance(lg, idx, seq, mask, rng)
+    lg[:] = np.finfo(np.float32).min
+    got, dl = check_balance(lg, idx, None, None, rng, zeta=0.0, gates=False)
+    # p = 1 / E in every row, so each row's gradient p (a_e - avg a) adds up to zero.  In units of u = 2^-24 and
+    # relative to the largest a: a_e has 4 roundings, the average 7 more (products, five levels of sums, its division
+    # by the sum of p), the difference and its products 4; 24 entries of p = 1 / 24 add up to at most 19 u of it
+    n, k = idx.shape
+    top = 0.7 * 0.02 * 24 * h64(got["counts"]).max() / (k * float(n) ** 2)
+    assert (np.abs(h64(dl).sum(1)) <= 19 * 2.0 ** -24 * top).all() and dl.any()
+
+
 def test_balance_loss_no_tokens(gpu):
     lg = torch.empty((0, 8), device="cuda")
     idx = torch.empty((0, 2), dtype=torch.int32, device="cuda")
