@@ -32,7 +32,7 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kWaves = kThreads / 64;
 constexpr int kTok = 32;      // tokens per workgroup of the forward
-constexpr int64_t kBwdGroups = 1 << 16;
+constexpr int64_t kGridX = 1 << 16;  // workgroups of the backward beyond these go along y
 constexpr int kCols = 16;     // experts per workgroup of the second launch
 constexpr int kSumThreads = 512;
 
@@ -410,66 +410,66 @@ struct BwdArgs {
 // and gets zeros from the exponentials.  A workgroup
 // takes the tokens that its lanes hold at once: with more, one after the other,
 // their loads waited for each other (16384 x 128: 13.1 us at 32 tokens, 10.5 at
-// the 8 of this kernel).  Launches past kBwdGroups workgroups go round.
+// the 8 of this kernel; 12.8 with a loop over the grid around it).
 template <int LPT>
 __global__ __launch_bounds__(kThreads) void balance_bwd_kernel(BwdArgs a) {
   constexpr int kPass = kThreads / LPT;
   __shared__ int s_cnt;
   const int l = threadIdx.x % LPT, e0 = 4 * l, E = a.E;
-  for (int64_t t0 = static_cast<int64_t>(blockIdx.x) * kPass; t0 < a.T; t0 += static_cast<int64_t>(gridDim.x) * kPass) {
-    const int64_t t1 = t0 + kPass < a.T ? t0 + kPass : a.T;
-    const int64_t t = t0 + threadIdx.x / LPT;
-    const bool on = t < t1;
-    float p[4], dl[4] = {0.f, 0.f, 0.f, 0.f}, zc = 0.f;
-    ld_logits(a.logits, t, E, e0, on, p);
-    const float live = a.norm[0], ntot = a.norm[1];
-    const float g0 = a.dloss ? a.dloss[0] : 1.f, g1 = a.dloss ? a.dloss[1] : 1.f;
-    const float zs = ntot > 0.f ? g1 * 2.0f * a.zeta / ntot : 0.f;
-    if (on) {
-      const float lse = a.lse[t];
-      const bool use = !a.mask || a.mask[t];
-      zc = use ? zs * lse : 0.f;
+  const int64_t t0 = (static_cast<int64_t>(blockIdx.y) * gridDim.x + blockIdx.x) * kPass;
+  if (t0 >= a.T) return;
+  const int64_t t1 = t0 + kPass < a.T ? t0 + kPass : a.T;
+  const int64_t t = t0 + threadIdx.x / LPT;
+  const bool on = t < t1;
+  float p[4], dl[4] = {0.f, 0.f, 0.f, 0.f}, zc = 0.f;
+  ld_logits(a.logits, t, E, e0, on, p);
+  const float live = a.norm[0], ntot = a.norm[1];
+  const float g0 = a.dloss ? a.dloss[0] : 1.f, g1 = a.dloss ? a.dloss[1] : 1.f;
+  const float zs = ntot > 0.f ? g1 * 2.0f * a.zeta / ntot : 0.f;
+  if (on) {
+    const float lse = a.lse[t];
+    const bool use = !a.mask || a.mask[t];
+    zc = use ? zs * lse : 0.f;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) p[i] = use && e0 + i < E ? expf(p[i] - lse) : 0.f;
-      if (a.gates) {
-        const int64_t o = t * a.k;
-        float dot = 0.f;
-        for (int j = 0; j < a.k; ++j) dot += a.gates[o + j] * a.dgates[o + j];
-        for (int j = 0; j < a.k; ++j) {
-          const int c = a.idx[o + j] - e0;
-          const float v = a.gates[o + j] * (a.dgates[o + j] - dot);
+    for (int i = 0; i < 4; ++i) p[i] = use && e0 + i < E ? expf(p[i] - lse) : 0.f;
+    if (a.gates) {
+      const int64_t o = t * a.k;
+      float dot = 0.f;
+      for (int j = 0; j < a.k; ++j) dot += a.gates[o + j] * a.dgates[o + j];
+      for (int j = 0; j < a.k; ++j) {
+        const int c = a.idx[o + j] - e0;
+        const float v = a.gates[o + j] * (a.dgates[o + j] - dot);
 #pragma unroll
-          for (int i = 0; i < 4; ++i) dl[i] += c == i ? v : 0.f;
-        }
+        for (int i = 0; i < 4; ++i) dl[i] += c == i ? v : 0.f;
       }
     }
-    each_piece(a.seq, a.S, a.T, t0, t1, &s_cnt, [&](int64_t s, int64_t lo, int64_t hi) {
-      const float n = a.norm[2 + s];
-      if (!(n > 0.f)) return;
-      const float f = g0 * a.alpha * static_cast<float>(E) / (static_cast<float>(a.k) * n * n * live);
-      float c[4], dot = 0.f, sum = 0.f;
+  }
+  each_piece(a.seq, a.S, a.T, t0, t1, &s_cnt, [&](int64_t s, int64_t lo, int64_t hi) {
+    const float n = a.norm[2 + s];
+    if (!(n > 0.f)) return;
+    const float f = g0 * a.alpha * static_cast<float>(E) / (static_cast<float>(a.k) * n * n * live);
+    float c[4], dot = 0.f, sum = 0.f;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        c[i] = e0 + i < E ? f * static_cast<float>(a.counts[s * E + e0 + i]) : 0.f;
-        dot += c[i] * p[i];
-        sum += p[i];
-      }
-      dot = Row<LPT>::sum(dot);
-      sum = Row<LPT>::sum(sum);
-      const float inv = sum == 0.f ? 0.f : 1.0f / sum;
-      if (on && t >= lo && t < hi)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) dl[i] += p[i] * inv * (c[i] - dot * inv + zc);
-    });
-    if (!on) continue;
-    float* o = a.dlogits + t * E + e0;
-    if ((E & 3) == 0) {
-      if (e0 < E) *reinterpret_cast<float4*>(o) = make_float4(dl[0], dl[1], dl[2], dl[3]);
-    } else {
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-        if (e0 + i < E) o[i] = dl[i];
+    for (int i = 0; i < 4; ++i) {
+      c[i] = e0 + i < E ? f * static_cast<float>(a.counts[s * E + e0 + i]) : 0.f;
+      dot += c[i] * p[i];
+      sum += p[i];
     }
+    dot = Row<LPT>::sum(dot);
+    sum = Row<LPT>::sum(sum);
+    const float inv = sum == 0.f ? 0.f : 1.0f / sum;
+    if (on && t >= lo && t < hi)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) dl[i] += p[i] * inv * (c[i] - dot * inv + zc);
+  });
+  if (!on) return;
+  float* o = a.dlogits + t * E + e0;
+  if ((E & 3) == 0) {
+    if (e0 < E) *reinterpret_cast<float4*>(o) = make_float4(dl[0], dl[1], dl[2], dl[3]);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (e0 + i < E) o[i] = dl[i];
   }
 }
 
@@ -552,9 +552,10 @@ extern "C" int moe_balance_loss_bwd(const float* logits, const float* lse, const
   const BwdArgs a{logits, lse, counts, norm, seq_offsets, token_mask, dloss, topk_idx, gates, dgates, dlogits,
                   T, S, E, k, alpha, zeta};
   by_lanes(E, [&](auto lpt) {
+    const int64_t groups = cdiv(T * decltype(lpt)::value, kThreads), x = std::min(groups, kGridX);
     MOE_LAUNCH("balance_bwd", (balance_bwd_kernel<decltype(lpt)::value>),
-               dim3(static_cast<unsigned>(std::min(cdiv(T * decltype(lpt)::value, kThreads), kBwdGroups))),
-               dim3(kThreads), 0, static_cast<hipStream_t>(stream), a);
+               dim3(static_cast<unsigned>(x), static_cast<unsigned>(cdiv(groups, x))), dim3(kThreads), 0,
+               static_cast<hipStream_t>(stream), a);
   });
   return launch_status();
 }
