@@ -459,6 +459,15 @@ __device__ __forceinline__ uint2* lo8_at(uint16_t* lo, int r, int q) {
                                   (q & 1) * 8);
 }
 
+// Transposed pieces of a block (restrict-qualified as in read_frags).
+template <int WN, bool SPLIT>
+__device__ __forceinline__ void mirror_frags(const uint16_t* __restrict__ hi, const uint16_t* __restrict__ lo, int cb,
+                                             int ks, int lane, f16x8& vh, f16x8& vl) {
+  auto swz = [](int r) { return ep_swz<WN>(r); };
+  vh = frag_tr<WN>(hi, cb, ks, lane, swz);
+  if constexpr (SPLIT) vl = frag_tr<WN>(lo, cb, ks, lane, swz);
+}
+
 // Barrier of the K loop: LDS accesses are ordered across it, the LDS-DMA loads in
 // flight are left alone (a full fence may wait for all of them).
 __device__ __forceinline__ void lds_barrier() {
@@ -491,16 +500,16 @@ struct Coef {
   float dc[kCols ? C::TN : 1][2][8];              // at its columns
   float a, b, c, v, f, lo_scale, lo_inv;
 
-  __device__ __forceinline__ void init(const MmArgs& p, int64_t e, int mw, int nw, int lane) {
-    const float* cs = p.cs + e * 2 * p.steps + p.step;
+  // cs: c_i, ratio: c_i / c_{i+1}
+  __device__ __forceinline__ void init(const MmArgs& p, int64_t e, float cs, float ratio, int mw, int nw, int lane) {
     const int rl = lane & 31, g = lane >> 5;
     a = p.ca;
     b = p.cb;
     c = p.cc;
     lo_scale = p.lo_scale;
     lo_inv = SPLIT ? 1.0f : 1.0f / p.lo_scale;
-    f = KIND != kApply ? 1.0f : p.out == kOutX ? cs[p.steps] : cs[0] / kS;
-    v = KIND == kGram ? cs[0] * cs[0] / kS : (KIND == kPoly ? p.cc : f) / kS;
+    f = KIND != kApply ? 1.0f : p.out == kOutX ? ratio : cs / kS;
+    v = KIND == kGram ? cs * cs / kS : (KIND == kPoly ? p.cc : f) / kS;
     if constexpr (KIND != kGram) {
       const float* d = p.din + e * p.sd;
 #pragma unroll
@@ -627,18 +636,33 @@ __device__ __forceinline__ void epi_diagonal(const f32x16& acc, uint16_t* hi, ui
   }
 }
 
-// stage() brings a block's inputs, run() does the rest; init() loads the
-// coefficients.  Where a tile is one block (WM = 32), the kernel calls the first
-// two before the K loop ends, so that their latencies pass behind it.
+// NT: streaming stores.
+template <bool NT>
+__device__ __forceinline__ void st16(void* p, const uint4& v) {
+  if constexpr (NT) {
+    typedef unsigned int u32x4 __attribute__((ext_vector_type(4)));
+    const u32x4 t = {v.x, v.y, v.z, v.w};
+    __builtin_nontemporal_store(t, static_cast<u32x4*>(p));
+  } else {
+    *static_cast<uint4*>(p) = v;
+  }
+}
+
+// stage() brings a block's inputs, run() does the rest; coefs() loads the
+// coefficients.  The kernel stages the first block (and where a tile is one block,
+// WM = 32, calls coefs() too) before the K loop ends, so that the latency passes
+// behind it.
 template <class C, int KIND, bool SPLIT, bool BYROW, bool FINAL, bool HASLO>
 struct Epilogue {
   static constexpr int WN = C::WN, kPart = 32 * WN, CPR = WN / 8, RPI = 64 / CPR, kPieces = 32 / RPI;
   static constexpr bool kLo8 = KIND == kApply && !SPLIT;
   static constexpr int CPR8 = WN / 16, RPI8 = 64 / CPR8, kPieces8 = 32 / RPI8;  // the same for an 8-bit lo part
   static constexpr int kStage = kPieces + (HASLO ? (kLo8 ? kPieces8 : kPieces) : 0);
-  static constexpr int kBuffers = C::TM > 1 ? 2 : 1;
+  // 256 x 256 tiles are used where the outputs are far larger than the L2s: by
+  // streaming stores 128 of 2048 x 1024 took 6.62 ms, not 6.74
+  static constexpr bool NT = C::BM == 256;
   static_assert(WN == 64 || WN == 32, "row piece layouts");
-  static_assert(C::kWaves * kBuffers * 2 * kPart <= (C::TM > 1 ? C::kLds : C::kSlot), "buffers of hi and lo per wave");
+  static_assert(C::kWaves * 2 * kPart <= C::kSlot && (C::TM == 1 || C::kRing == 2), "a buffer per wave in each ring slot");
 
   const MmArgs& p;
   const int64_t e;
@@ -646,28 +670,29 @@ struct Epilogue {
   const int64_t ob, eo;
   Coef<C, KIND, SPLIT, BYROW> k;
   __amdgpu_buffer_rsrc_t rh, rlo;
-  uint16_t* mine;          // this wave's buffers
+  uint16_t* buf[2];        // this wave's buffers, of even and odd blocks
 
   __device__ __forceinline__ Epilogue(const MmArgs& p_, int64_t e_, int mw_, int nw_, int lane_)
       : p(p_), e(e_), mw(mw_), nw(nw_), lane(lane_), ob(e_ * p_.so),
-        eo(e_ * p_.so + static_cast<int64_t>(mw_) * p_.ldo + nw_), mine(nullptr) {}
-
-  __device__ __forceinline__ void init() {
-    k.init(p, e, mw, nw, lane);
+        eo(e_ * p_.so + static_cast<int64_t>(mw_) * p_.ldo + nw_) {
     const int64_t left = mw < p.M && nw < p.N ? (static_cast<int64_t>(p.M - mw) * p.ldo - nw) * 2 : 0;
     if constexpr (KIND != kGram) rh = rsrc(p.eh + eo, left);
     if constexpr (HASLO)
       rlo = kLo8 ? rsrc(static_cast<const uint8_t*>(p.el) + eo, left / 2)
                  : rsrc(static_cast<const uint16_t*>(p.el) + eo, left);
   }
-  __device__ __forceinline__ void place(uint16_t* lds, int wave) { mine = lds + wave * kBuffers * 2 * kPart; }
+  __device__ __forceinline__ void coefs(float cs, float ratio) { k.init(p, e, cs, ratio, mw, nw, lane); }
+  __device__ __forceinline__ void place(uint16_t* even, uint16_t* odd, int wave) {
+    buf[0] = even + wave * 2 * kPart;
+    buf[1] = odd + wave * 2 * kPart;
+  }
   // row pieces: piece u of a block is rows [u RPI, (u + 1) RPI), 16 bytes per lane
   __device__ __forceinline__ int piece_col(int u) const {
     return ((lane % CPR) ^ ep_swz<WN>(u * RPI + lane / CPR)) * 8;
   }
   __device__ __forceinline__ void stage(int i) const {
     if constexpr (KIND == kGram) return;
-    uint16_t* b = mine + (i & 1) * 2 * kPart;
+    uint16_t* b = buf[i & 1];
 #pragma unroll
     for (int u = 0; u < kPieces; ++u) {
       const int voff = ((32 * i + u * RPI + lane / CPR) * p.ldo + piece_col(u)) * 2;
@@ -682,23 +707,43 @@ struct Epilogue {
       }
   }
 
-  // staged: the first block is on its way already
-  __device__ __forceinline__ void run(const f32x16 (&acc)[C::TM][C::TN], int m0, int n0, bool staged) const {
+  // Waits until block i's inputs have landed, but neither for those of block i + 1
+  // nor for the outputs of block i - 1, which were issued after them (vector memory
+  // operations complete in order).  On the matrix's edge some of those stores may
+  // not have been issued: there the wait covers them.
+  static constexpr int kStores = kPieces * (SPLIT && !FINAL ? 2 : 1);                    // per block, at least
+  static constexpr int kMirror = KIND == kApply ? 0 : WN / 32 * 2 * (SPLIT ? 2 : 1);  // and below the diagonal
+  __device__ __forceinline__ void wait_block(int i, bool full, bool below) const {
+    const bool more = i + 1 < C::TM;
+    if (i == 0 || !full) {
+      if (more) wait_vm<kStage>();
+      else wait_vm<0>();
+    } else if (kLo8 && !FINAL && p.ol) {
+      if (more) wait_vm<kStage + kStores + kPieces8>();
+      else wait_vm<kStores + kPieces8>();
+    } else if (below) {
+      if (more) wait_vm<kStage + kStores + kMirror>();
+      else wait_vm<kStores + kMirror>();
+    } else {
+      if (more) wait_vm<kStage + kStores>();
+      else wait_vm<kStores>();
+    }
+  }
+
+  // staged: the first block is on its way (and the second, if there is one)
+  __device__ __forceinline__ void run(const f32x16 (&acc)[C::TM][C::TN], bool staged) const {
     const int rl = lane & 31, g = lane >> 5, pr = lane / CPR, pr8 = lane / CPR8;
     // symmetric outputs, by squares: above the diagonal there is nothing to do,
     // squares on it are computed whole, those below are written twice
     const bool below = KIND != kApply && mw / C::kSq > nw / C::kSq;
     if (KIND != kApply && mw / C::kSq < nw / C::kSq) return;
+    const bool full = FINAL ? mw + C::WM <= p.rows && nw + WN <= p.cols : mw + C::WM <= p.M && nw + WN <= p.N;
     if (!staged) stage(0);
-    if constexpr (C::TM > 1) stage(1);
 #pragma unroll
     for (int i = 0; i < C::TM; ++i) {
-      uint16_t* hi = mine + (i & 1) * 2 * kPart;
+      uint16_t* hi = buf[i & 1];
       uint16_t* lo = hi + kPart;
-      if constexpr (KIND != kGram) {  // block i has landed; block i + 1 may be in flight
-        if (i + 1 < C::TM) wait_vm<kStage>();
-        else wait_vm<0>();
-      }
+      if constexpr (KIND != kGram) wait_block(i, full, below);
       epi_block<C, KIND, SPLIT, BYROW, FINAL, HASLO>(acc[i], hi, lo, k, i, lane);
       if constexpr (KIND != kApply) {
         const int row = mw + 32 * i + rl;
@@ -739,8 +784,8 @@ struct Epilogue {
           if constexpr (SPLIT) vl = lds_get16(lo + u * 512 + lane * 8);
           if (mw + orow < p.M && nw + col < p.N) {
             const int64_t off = eo + orow * p.ldo + col;
-            *reinterpret_cast<uint4*>(p.oh + off) = vh;
-            if constexpr (SPLIT) *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.ol) + off) = vl;
+            st16<NT>(p.oh + off, vh);
+            if constexpr (SPLIT) st16<NT>(static_cast<uint16_t*>(p.ol) + off, vl);
           }
         }
         if (kLo8 && p.ol)
@@ -749,19 +794,17 @@ struct Epilogue {
             const int r = u * RPI8 + pr8, orow = 32 * i + r, col = ((lane % CPR8) ^ lo8_swz<WN>(r)) * 16;
             const uint4 vl = lds_get16(lo + u * 512 + lane * 8);
             if (mw + orow < p.M && nw + col < p.N)
-              *reinterpret_cast<uint4*>(static_cast<uint8_t*>(p.ol) + eo + orow * p.ldo + col) = vl;
+              st16<NT>(static_cast<uint8_t*>(p.ol) + eo + orow * p.ldo + col, vl);
           }
       }
       if constexpr (KIND != kApply) {
         if (below) {  // the mirror image: 8 of the block's rows at one column per lane
-          auto swz = [](int r) { return ep_swz<WN>(r); };
           const int64_t mo = ob + static_cast<int64_t>(nw + rl) * p.ldo + mw + 8 * g;
 #pragma unroll
           for (int t = 0; t < WN / 32 * 2; ++t) {
             const int cb = (t >> 1) * 32, ks = t & 1;
-            const f16x8 vh = frag_tr<WN>(hi, cb, ks, lane, swz);
-            f16x8 vl;
-            if constexpr (SPLIT) vl = frag_tr<WN>(lo, cb, ks, lane, swz);
+            f16x8 vh, vl;
+            mirror_frags<WN, SPLIT>(hi, lo, cb, ks, lane, vh, vl);
             if (nw + cb + rl < p.N && mw + 32 * i + ks * 16 + 8 * g < p.M) {
               const int64_t off = mo + cb * p.ldo + 32 * i + ks * 16;
               *reinterpret_cast<uint4*>(p.oh + off) = __builtin_bit_cast(uint4, vh);
@@ -870,8 +913,9 @@ void orth_mm_kernel(MmArgs p) {
   constexpr bool kHasLo = KIND == kGram ? false : SPLIT || (KIND == kApply && MODE == kX);
   Epilogue<C, KIND, SPLIT, KIND != kApply || !BKC, MODE == kLast, kHasLo> epi(p, e, m0 + wm * C::WM, n0 + wn * C::WN,
                                                                               lane);
-  const bool early = C::TM == 1 && ks_n == 1;
-  if (early) epi.init();
+  const float cs = p.cs[e * 2 * p.steps + p.step], ratio = p.cs[e * 2 * p.steps + p.steps + p.step];
+  const bool early = ks_n == 1;
+  if (C::TM == 1 && early) epi.coefs(cs, ratio);
   const int nk1 = (p.K + C::BK - 1) / C::BK;
   const int k_lo = kKSplit ? static_cast<int>(static_cast<unsigned>(nk1 * ks_i) / ks_n) : 0;
   const int nk = (kKSplit ? static_cast<int>(static_cast<unsigned>(nk1 * (ks_i + 1)) / ks_n) : nk1) - k_lo;
@@ -961,7 +1005,7 @@ void orth_mm_kernel(MmArgs p) {
   // the last step; no other slot is read any more, so the epilogue's first inputs
   // can go into the next one
   if (early) {
-    epi.place(lds + (slot + 1 == C::kRing ? 0 : slot + 1) * C::kSlot, wave);
+    epi.place(lds + (slot + 1 == C::kRing ? 0 : slot + 1) * C::kSlot, lds + slot * C::kSlot, wave);
     epi.stage(0);
   }
 #pragma unroll
@@ -972,12 +1016,15 @@ void orth_mm_kernel(MmArgs p) {
   if constexpr (kKSplit) {
     if (ks_n > 1 && !join_k<C>(acc, p, lid, ks_i, lds, tid)) return;
   }
-  if (!early) {
-    epi.init();
-    __syncthreads();  // the ring is no longer read
-    epi.place(lds, wave);
+  if constexpr (C::TM > 1) {
+    epi.coefs(cs, ratio);
+    lds_barrier();  // the last step's slot is no longer read
+    epi.stage(1);
+  } else if (!early) {  // after join_k, whose barriers came after the last reads of the ring
+    epi.coefs(cs, ratio);
+    epi.place(lds, lds, wave);
   }
-  epi.run(acc, m0, n0, early);
+  epi.run(acc, early);
 }
 
 // ---------------------------------------------------------------------------
