@@ -434,7 +434,7 @@ __device__ __forceinline__ void tri_tile(int i, int& r, int& c) {
 // pieces; the results go back into the same places and leave as whole row
 // pieces too, and for the symmetric outputs once more transposed.  (Straight
 // from registers, where a lane holds 16 bytes of its row at a time, the apply
-// launch of 128 matrices of 4096 x 1536 took 4.07 ms.)
+// launch of 128 matrices of 4096 x 1536 took 4.07 ms and not 3.08, with 256 x 128 tiles.)
 // ---------------------------------------------------------------------------
 
 // Chunk swizzle of a block's rows: free of conflicts for 16 consecutive rows at
@@ -1346,13 +1346,9 @@ Sizes sizes_of(int E, int rows, int cols, bool split) {
 
 // Tile sizes, chosen per product by how many tiles there are for the 256 compute
 // units.  64 x 64 while they all fit at once, three to a unit (one matrix of 2048
-// x 1024: Gram 15 us against 26 us with 128 x 128 and 46 us with 256 x 128).
-// 256 x 256 (eight waves, one workgroup per unit) where they fill the chip in
-// whole rounds, to four fifths at least: 128 of 4096 x 1536, 12288 tiles, apply
-// 2.80 ms against 3.08 ms with 256 x 128, two per unit, and 3.23 ms with 128 x 128;
-// 32 of 2048 x 1024 fp32, 1024 tiles, apply 405 us against 490 us, but Gram, 320
-// tiles in two rounds, 296 us against 253 us.  128 x 128, two to a unit, else
-// (one of 2048 x 2048, 256 tiles: apply 33 us against 42 us with 64 x 64).
+// x 1024: Gram 14 us against 26 us with 128 x 128; past that, one of 2048 x 2048,
+// apply 41 us against 32 us).  Else 256 x 256 (eight waves, one workgroup per unit)
+// or 128 x 128 (two per unit), see use_big.
 using Big = Tile<256, 256, 64, 2, 2, false, 4>;
 using Mid = Tile<128, 128, 64, 2, 2, false>;
 using Small = Tile<64, 64, 64, 3, 2, false>;
@@ -1360,11 +1356,16 @@ using BigPairs = Tile<256, 256, 32, 2, 1, true, 4>;
 using MidPairs = Tile<128, 128, 32, 2, 1, true>;
 using SmallPairs = Tile<64, 64, 32, 3, 1, true>;
 
-// From how many 256 x 256 tiles on, and in how well filled rounds of 256, they are
-// used (bf16 at 256 tiles: 55 us against 53; pairs: 102 us against 109).
-bool use_big(int64_t tiles, bool pairs) {
-  return tiles >= (pairs ? 250 : 480) && tiles * 5 >= cdiv(tiles, 256) * 256 * 4;
-}
+// 256 x 256 tiles do the work of four 128 x 128 ones from half the LDS and L2
+// traffic, in rounds of 256 against 512.  A round takes 1.7 times as long, its last
+// partial one about as long as a full one, so the shorter sum of rounds is taken.
+// Over 42 products of 19 sizes it was off by 5% at most in bf16 and 11% in fp32 (two
+// of 1.1 rounds).  Measured, 256 x 256 against 128 x 128: apply of 128 of 4096 x
+// 1536 (48 rounds against 96) 2.71 ms against 3.23; one of 4096 x 4096 (1 against 2)
+// 134 us against 160, fp32 332 against 407; 8 of 1024 x 2048 (1 against 2) 46.5
+// against 49; two of 2048 x 2048 (1 against 1) 59 against 45; 40 of 512 x 1024 (2
+// against 3) 54 against 42.
+bool use_big(int64_t big, int64_t mid) { return 17 * cdiv(big, 256) <= 10 * cdiv(mid, 512); }
 
 // Tiles of a symmetric m x m output, and of an r x c one, in E matrices.
 template <class C>
@@ -1469,7 +1470,8 @@ void launch_any(const char* name, MmArgs& a, const Sizes& z, hipStream_t s) {
   const bool ap = KIND == kApply;
   if ((ap ? rect_tiles<Small>(a.M, a.N, z.E) : sym_tiles<Small>(a.M, z.E)) <= 768)
     z.split ? go(SmallPairs{}) : go(Small{});
-  else if (use_big(ap ? rect_tiles<Big>(a.M, a.N, z.E) : sym_tiles<Big>(a.M, z.E), z.split))
+  else if (ap ? use_big(rect_tiles<Big>(a.M, a.N, z.E), rect_tiles<Mid>(a.M, a.N, z.E))
+              : use_big(sym_tiles<Big>(a.M, z.E), sym_tiles<Mid>(a.M, z.E)))
     z.split ? go(BigPairs{}) : go(Big{});
   else
     z.split ? go(MidPairs{}) : go(Mid{});

@@ -377,6 +377,13 @@ def test_orthogonalize_fills_the_chip(gpu, E, rows, cols, dtype):
     assert float(err) <= ORTH_TOL[dtype]
 
 
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("E,rows,cols", [(10, 1400, 1700), (10, 1700, 1400), (1, 2900, 2890), (30, 700, 2000)])
+def test_orthogonalize_one_round_of_the_largest_tiles(gpu, E, rows, cols, dtype):
+    """Few of the largest tiles, chosen because twice as many rounds of smaller ones would be needed."""
+    test_orthogonalize_fills_the_chip(gpu, E, rows, cols, dtype)
+
+
 def test_orthogonalize_steps_and_coefficients(gpu):
     rng = np.random.default_rng(3)
     g = gradients(rng, 2, 96, 160, "noise")
