@@ -1359,7 +1359,7 @@ using SmallPairs = Tile<64, 64, 32, 3, 1, true>;
 // 256 x 256 tiles do the work of four 128 x 128 ones from half the LDS and L2
 // traffic, in rounds of 256 against 512.  A round takes 1.7 times as long, its last
 // partial one about as long as a full one, so the shorter sum of rounds is taken.
-// Over 42 products of 19 sizes it was off by 5% at most in bf16 and 11% in fp32 (two
+// Over 49 products of 19 sizes it was off by 3% at most in bf16 and 11% in fp32 (two
 // of 1.1 rounds).  Measured, 256 x 256 against 128 x 128: apply of 128 of 4096 x
 // 1536 (48 rounds against 96) 2.71 ms against 3.23; one of 4096 x 4096 (1 against 2)
 // 134 us against 160, fp32 332 against 407; 8 of 1024 x 2048 (1 against 2) 46.5
