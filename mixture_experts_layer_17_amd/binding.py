@@ -396,7 +396,8 @@ def mx_quantize(src, axis, seg_offsets=None, nseg=0, q=None, scales=None):
 
 def _args(what, dev, specs):
     """Device tensors as the C ABI reads them: (name, tensor or None, shape, type) each of this shape and type,
-    contiguous, and on the current device, whose current stream the call is enqueued on."""
+    contiguous, and on the current device, whose current stream the call is enqueued on.  Only what the caller gave
+    need be listed: a check costs about as much as allocating a tensor (0.7 us)."""
     for name, t, shape, dtype in specs:
         if t is None or (t.shape == shape and t.dtype is dtype and t.device == dev and t.is_contiguous()):
             continue
@@ -407,6 +408,10 @@ def _args(what, dev, specs):
         raise MoeError(f"{what}: {name} is on {t.device}, the others on {dev}")
     if dev.type != "cuda" or dev.index != torch.cuda.current_device():
         raise MoeError(f"{what}: the tensors are on {dev}, not on the current GPU")
+
+
+def _ws_spec(ws):
+    return () if ws is None else (("ws", ws, (ws.numel(),), torch.uint8),)
 
 
 def _storage(what, t, dims):
@@ -424,16 +429,19 @@ def moe_layernorm(x, weight=None, bias=None, eps=1e-5, residual=None, out=None):
     what, dev, dt = "moe_layernorm", x.device, x.dtype
     code = _storage(what, x, 2)
     T, d = x.shape
+    rows, cols, per = (T, d), (d,), (T,)
+    specs = (("x", x, rows, dt), ("weight", weight, cols, dt), ("bias", bias, cols, dt),
+             ("residual", residual, rows, dt))
     if out is None:
         out = {"y": torch.empty_like(x), "mean": torch.empty(T, dtype=_F32, device=dev),
                "rstd": torch.empty(T, dtype=_F32, device=dev)}
         if residual is not None:
             out["sum"] = torch.empty_like(x)
+    else:
+        specs += (("y", out["y"], rows, dt), ("sum", out.get("sum"), rows, dt), ("mean", out.get("mean"), per, _F32),
+                  ("rstd", out.get("rstd"), per, _F32))
     y, total, mean, rstd = out["y"], out.get("sum"), out.get("mean"), out.get("rstd")
-    rows, cols, per = (T, d), (d,), (T,)
-    _args(what, dev, (("x", x, rows, dt), ("weight", weight, cols, dt), ("bias", bias, cols, dt),
-                      ("residual", residual, rows, dt), ("y", y, rows, dt), ("sum", total, rows, dt),
-                      ("mean", mean, per, _F32), ("rstd", rstd, per, _F32)))
+    _args(what, dev, specs)
     _check(lib().moe_layernorm(_p(x), _p(residual), _p(weight), _p(bias), code, T, d, eps, _p(y), _p(total), _p(mean),
                                _p(rstd), _stream()), what)
     return out
@@ -445,16 +453,18 @@ def moe_layernorm_bwd(dy, x, weight, mean, rstd, dres=None, out=None, ws=None):
     what, dev, dt = "moe_layernorm_bwd", x.device, x.dtype
     code = _storage(what, x, 2)
     T, d = x.shape
+    rows, cols, per = (T, d), (d,), (T,)
+    specs = (("x", x, rows, dt), ("dy", dy, rows, dt), ("weight", weight, cols, dt), ("mean", mean, per, _F32),
+             ("rstd", rstd, per, _F32), ("dres", dres, rows, dt)) + _ws_spec(ws)
     if out is None:
         out = {"dx": torch.empty_like(x), "dw": torch.empty(d, dtype=dt, device=dev),
                "db": torch.empty(d, dtype=dt, device=dev)}
+    else:
+        specs += (("dx", out["dx"], rows, dt), ("dw", out.get("dw"), cols, dt), ("db", out.get("db"), cols, dt))
     dx, dw, db = out["dx"], out.get("dw"), out.get("db")
+    _args(what, dev, specs)
     if ws is None:
         ws = _ws(lib().moe_layernorm_bwd_workspace(T, d), dev)
-    rows, cols, per = (T, d), (d,), (T,)
-    _args(what, dev, (("x", x, rows, dt), ("dy", dy, rows, dt), ("weight", weight, cols, dt), ("mean", mean, per, _F32),
-                      ("rstd", rstd, per, _F32), ("dres", dres, rows, dt), ("dx", dx, rows, dt), ("dw", dw, cols, dt),
-                      ("db", db, cols, dt)))
     _check(lib().moe_layernorm_bwd(_p(dy), _p(x), _p(weight), _p(mean), _p(rstd), _p(dres), code, T, d, _p(dx), _p(dw),
                                    _p(db), _p(ws), ws.numel(), _stream()), what)
     return out
@@ -474,15 +484,19 @@ def moe_balance_loss(logits, topk_idx, alpha, zeta, seq_offsets=None, token_mask
     """Balance and z loss of a routing: {"loss" [2], "counts" [S, E], "probs" [S, E], "lse" [T], "norm" [S + 2]}."""
     what, dev, k = "moe_balance_loss", logits.device, topk_idx.shape[-1] if topk_idx.dim() else 0
     T, E, S, specs = _balance_specs(logits, k, topk_idx, seq_offsets, token_mask)
+    specs += _ws_spec(ws)
     if out is None:
         out = {"loss": torch.empty(2, dtype=_F32, device=dev), "counts": torch.empty((S, E), dtype=_I32, device=dev),
                "probs": torch.empty((S, E), dtype=_F32, device=dev), "lse": torch.empty(T, dtype=_F32, device=dev),
                "norm": torch.empty(S + 2, dtype=_F32, device=dev)}
+    else:
+        specs += (("loss", out["loss"], (2,), _F32), ("counts", out["counts"], (S, E), _I32),
+                  ("probs", out["probs"], (S, E), _F32), ("lse", out["lse"], (T,), _F32),
+                  ("norm", out["norm"], (S + 2,), _F32))
     loss, counts, probs, lse, norm = out["loss"], out["counts"], out["probs"], out["lse"], out["norm"]
+    _args(what, dev, specs)
     if ws is None:
         ws = _ws(lib().moe_balance_loss_workspace(T, E, S), dev)
-    _args(what, dev, specs + (("loss", loss, (2,), _F32), ("counts", counts, (S, E), _I32),
-                              ("probs", probs, (S, E), _F32), ("lse", lse, (T,), _F32), ("norm", norm, (S + 2,), _F32)))
     _check(lib().moe_balance_loss(_p(logits), _p(topk_idx), T, E, k, _p(seq_offsets), S, _p(token_mask), alpha, zeta,
                                   _p(loss), _p(counts), _p(probs), _p(lse), _p(norm), _p(ws), ws.numel(), _stream()),
            what)
@@ -496,11 +510,11 @@ def moe_balance_loss_bwd(logits, fwd, k, alpha, zeta, dloss=None, seq_offsets=No
     what, dev = "moe_balance_loss_bwd", logits.device
     T, E, S, specs = _balance_specs(logits, k, topk_idx, seq_offsets, token_mask)
     counts, lse, norm = fwd["counts"], fwd["lse"], fwd["norm"]
-    if out is None:
-        out = torch.empty((T, E), dtype=_F32, device=dev)
     _args(what, dev, specs + (("counts", counts, (S, E), _I32), ("lse", lse, (T,), _F32), ("norm", norm, (S + 2,), _F32),
                               ("dloss", dloss, (2,), _F32), ("gates", gates, (T, k), _F32),
                               ("dgates", dgates, (T, k), _F32), ("out", out, (T, E), _F32)))
+    if out is None:
+        out = torch.empty((T, E), dtype=_F32, device=dev)
     _check(lib().moe_balance_loss_bwd(_p(logits), _p(lse), _p(counts), _p(norm), T, E, k, _p(seq_offsets), S,
                                       _p(token_mask), alpha, zeta, _p(dloss), _p(topk_idx), _p(gates), _p(dgates),
                                       _p(out), _stream()), what)
@@ -529,11 +543,11 @@ def moe_orthogonalize(g, steps=5, coef=None, eps=1e-7, out=None, ws=None):
     what, dev, dt = "moe_orthogonalize", g.device, g.dtype
     code = _storage(what, g, 3)
     E, rows, cols = shape = g.shape
+    _args(what, dev, (("g", g, shape, dt), ("out", out, shape, dt)) + _ws_spec(ws))
     if out is None:
         out = torch.empty_like(g)
     if ws is None:
         ws = _ws(lib().moe_orthogonalize_workspace(E, rows, cols, code), dev)
-    _args(what, dev, (("g", g, shape, dt), ("out", out, shape, dt)))
     _check(lib().moe_orthogonalize(_p(g), code, E, rows, cols, steps, _coef(steps, coef), eps, _p(out), _p(ws),
                                    ws.numel(), _stream()), what)
     return out
@@ -546,9 +560,9 @@ def moe_muon_step(g, mom, w, lr, momentum=0.95, nesterov=True, weight_decay=0.0,
     what, dev, dt = "moe_muon_step", g.device, g.dtype
     code = _storage(what, g, 3)
     E, rows, cols = shape = g.shape
+    _args(what, dev, (("g", g, shape, dt), ("w", w, shape, dt), ("mom", mom, shape, _F32)) + _ws_spec(ws))
     if ws is None:
         ws = _ws(lib().moe_orthogonalize_workspace(E, rows, cols, code), dev)
-    _args(what, dev, (("g", g, shape, dt), ("w", w, shape, dt), ("mom", mom, shape, _F32)))
     w_out, mom_out = (w, mom) if inplace else (torch.empty_like(w), torch.empty_like(mom))
     _check(lib().moe_muon_step(_p(g), code, E, rows, cols, _p(mom), momentum, int(bool(nesterov)), steps,
                                _coef(steps, coef), eps, _p(w), lr, weight_decay, scale, _p(mom_out), _p(w_out),

@@ -686,3 +686,27 @@ def test_refused_tensors(gpu):
         with pytest.raises(B.MoeError):
             call()
             raise AssertionError(f"call {i} was not refused")
+
+
+def test_refused_workspaces_and_outputs(gpu):
+    """A workspace or an output that the kernels could not write, before any launch."""
+    x = torch.randn((8, 32), device="cuda")
+    per = torch.zeros(8, device="cuda")
+    lg, idx = torch.randn((8, 4), device="cuda"), torch.zeros((8, 2), dtype=torch.int32, device="cuda")
+    g = torch.randn((2, 8, 16), device="cuda")
+    fwd = B.moe_balance_loss(lg, idx, 0.1, 0.1)
+    big = 1 << 20
+    host, wide = torch.empty(big, dtype=torch.uint8), torch.empty(big, device="cuda")
+    strided = torch.empty(2 * big, dtype=torch.uint8, device="cuda")[::2]
+    for ws in (host, wide, strided):
+        for call in (lambda: B.moe_layernorm_bwd(x, x, None, per, per, ws=ws),
+                     lambda: B.moe_balance_loss(lg, idx, 0.1, 0.1, ws=ws), lambda: B.moe_orthogonalize(g, ws=ws),
+                     lambda: B.moe_muon_step(g, g.clone(), g.clone(), 0.1, ws=ws)):
+            with pytest.raises(B.MoeError):
+                call()
+    for call in (lambda: B.moe_layernorm(x, out={"y": x.cpu()}), lambda: B.moe_layernorm(x, out={"y": x, "mean": per[:4]}),
+                 lambda: B.moe_layernorm_bwd(x, x, None, per, per, out={"dx": x, "dw": x}),
+                 lambda: B.moe_balance_loss(lg, idx, 0.1, 0.1, out={**fwd, "lse": per.cpu()}),
+                 lambda: B.moe_balance_loss_bwd(lg, fwd, 2, 0.1, 0.1, out=lg.T), lambda: B.moe_orthogonalize(g, out=g[:1])):
+        with pytest.raises(B.MoeError):
+            call()
