@@ -1355,6 +1355,10 @@ using Small = Tile<64, 64, 64, 3, 2, false>;
 using BigPairs = Tile<256, 256, 32, 2, 1, true, 4>;
 using MidPairs = Tile<128, 128, 32, 2, 1, true>;
 using SmallPairs = Tile<64, 64, 32, 3, 1, true>;
+// where both operands are stored with K contiguous: K steps of 64 read whole
+// 128-byte lines (one of 2900 x 2000: polynomial 62.5 -> 53.6 us; 4 of 1000 x 500:
+// apply 16.6 -> 14.3 us; the others lost, 8 of 1001 x 777: Gram 30 -> 33 us)
+using SmallPairsK = Tile<64, 64, 64, 2, 2, true>;
 
 // 256 x 256 tiles do the work of four 128 x 128 ones from half the LDS and L2
 // traffic, in rounds of 256 against 512.  A round takes 1.7 times as long, its last
@@ -1469,7 +1473,7 @@ void launch_any(const char* name, MmArgs& a, const Sizes& z, hipStream_t s) {
   };
   const bool ap = KIND == kApply;
   if ((ap ? rect_tiles<Small>(a.M, a.N, z.E) : sym_tiles<Small>(a.M, z.E)) <= 768)
-    z.split ? go(SmallPairs{}) : go(Small{});
+    z.split ? go(typename std::conditional<AKC && BKC, SmallPairsK, SmallPairs>::type{}) : go(Small{});
   else if (ap ? use_big(rect_tiles<Big>(a.M, a.N, z.E), rect_tiles<Mid>(a.M, a.N, z.E))
               : use_big(sym_tiles<Big>(a.M, z.E), sym_tiles<Mid>(a.M, z.E)))
     z.split ? go(BigPairs{}) : go(Big{});
