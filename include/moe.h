@@ -199,10 +199,10 @@ int moe_balance_loss_bwd(const float* logits, const float* lse, const int32_t* c
  * weight, bias, residual, dres, dw, db may be NULL (weight 1, bias 0, none);
  * weight, bias, dw, db [d] in `dtype`.  dres [T, d] is a gradient that reaches
  * s by another way (the residual stream's).  Statistics and sums are fp32.
- * A constant row with eps = 0 gives NaN.  T = 0 is allowed: dw and db become
- * zero.  The workspace is needed for dw and
- * db only.  MOE_EINVAL for d < 1 and for an eps that is negative or not finite,
- * MOE_EUNSUPPORTED for d > 2^20. */
+ * A constant row with eps = 0 gives NaN.  In place: y or sum may be x or residual,
+ * dx may be dy, x or dres; no other overlap.  T = 0 is allowed: dw and db become
+ * zero.  The workspace is needed for dw and db only.  MOE_EINVAL for d < 1 and for
+ * an eps that is negative or not finite, MOE_EUNSUPPORTED for d > 2^20. */
 int moe_layernorm(const void* x, const void* residual, const void* weight, const void* bias, int dtype, int64_t T,
                   int32_t d, float eps, void* y, void* sum, float* mean, float* rstd, void* stream);
 size_t moe_layernorm_bwd_workspace(int64_t T, int32_t d);

@@ -573,12 +573,12 @@ int run_bwd(const BwdArgs& a, void* dw, void* db, hipStream_t s) {
   if (a.T == 0) {
     G = 0;  // no rows: the sums are zero
   } else if (sh.nv == 0) {
-    MOE_LAUNCH("layernorm_bwd", (layernorm_bwd_long_kernel<T, NT>), dim3(long_grid(a.T)), dim3(kThreads), 0, s, a);
-    if (a.part) {
+    if (a.part) {  // first: dx may take the place of dy or x
       G = G < 64 ? G : 64;
       MOE_LAUNCH("layernorm_wgrad", (layernorm_wgrad_long_kernel<T>),
                  dim3(static_cast<unsigned>(cdiv(a.d, kThreads)), G), dim3(kThreads), 0, s, a);
     }
+    MOE_LAUNCH("layernorm_bwd", (layernorm_bwd_long_kernel<T, NT>), dim3(long_grid(a.T)), dim3(kThreads), 0, s, a);
   } else if (sh.tpr == 64) {
     if (sh.nv == 1) launch_bwd<T, 1, 64, NT>(a, G, s);
     else if (sh.nv == 2) launch_bwd<T, 2, 64, NT>(a, G, s);

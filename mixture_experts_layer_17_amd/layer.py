@@ -200,9 +200,12 @@ class LayerStep:
                scale: float | None = None, steps: int = 5):
         """A Muon step of the expert weights, in place, from the gradients of the last backward.  scale: what the
         orthogonalised update is multiplied by besides lr; None: 0.2 sqrt(max(d, f)), which gives its entries a
-        root mean square of about 0.2.  A cache of quantised weights is built again."""
+        root mean square of about 0.2.  A cache of quantised weights is built again.  The first call makes the momentum
+        (zero) and the workspace; in a graph capture it is refused, since every replay would clear the momentum."""
         inp, E = self.inp, self.w.E
         if self.mom is None:
+            if torch.cuda.is_current_stream_capturing():
+                raise B.MoeError("update: the first call cannot be captured")
             self.mom = {n: torch.zeros(inp[n].shape, dtype=torch.float32, device=inp[n].device)
                         for n in ("w_gate", "w_up", "w_down")}
             need = max(B.moe_orthogonalize_workspace(E, *inp[n].shape[1:], inp[n].dtype) for n in self.mom)

@@ -139,6 +139,31 @@ def test_layernorm_large(gpu, T, d, dtype):
         assert bool(((got.double() - ref).abs() <= rel * ref.abs() + slack).all()), name
 
 
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("T,d", [(300, 777), (130, 2049), (9, 8192), (70, 20001)])
+def test_layernorm_in_place(gpu, T, d, dtype):
+    """Outputs in their inputs' places give the bits of separate ones."""
+    rng = np.random.default_rng(T + d)
+    x, res, dy, dres = (draw(rng, (T, d), dtype, 1.0)[0] for _ in range(4))
+    w, b = draw(rng, (d,), dtype)[0], draw(rng, (d,), dtype)[0]
+    gu.say(f"case layernorm in place {T}x{d} {dtype}")
+    f = B.moe_layernorm(x, w, b, residual=res)
+    for y_in, s_in in ((0, 1), (1, 0)):
+        t = [x.clone(), res.clone()]
+        out = {"y": t[y_in], "sum": t[s_in], "mean": torch.empty(T, device="cuda"), "rstd": torch.empty(T, device="cuda")}
+        B.moe_layernorm(t[0], w, b, residual=t[1], out=out)
+        assert all(torch.equal(out[k], f[k]) for k in f), (y_in, s_in)
+    y = x.clone()
+    alone = B.moe_layernorm(x, w, b)["y"]
+    assert torch.equal(B.moe_layernorm(y, w, b, out={"y": y})["y"], alone)
+    g = B.moe_layernorm_bwd(dy, f["sum"], w, f["mean"], f["rstd"], dres=dres)
+    for at in range(3):
+        t = [dy.clone(), f["sum"].clone(), dres.clone()]
+        out = {"dx": t[at], "dw": torch.empty_like(w), "db": torch.empty_like(w)}
+        B.moe_layernorm_bwd(t[0], t[1], w, f["mean"], f["rstd"], dres=t[2], out=out)
+        assert all(torch.equal(out[k], g[k]) for k in g), at
+
+
 def test_layernorm_no_rows(gpu):
     x = torch.empty((0, 40), device="cuda")
     st = torch.empty(0, device="cuda")
@@ -662,6 +687,47 @@ def test_update_rebuilds_the_mx_weight_cache(gpu):
     fresh = B.moe_mx_weight_cache_build(*(step.inp[n] for n in ("w_gate", "w_up", "w_down")))
     torch.cuda.synchronize()
     assert torch.equal(step.mx_wcache, fresh) and not torch.equal(before, fresh)
+
+
+@pytest.mark.parametrize("workload,kw", [(2, {}), (5, dict(mx_weight_cache=True))])
+def test_captured_training_step(gpu, workload, kw):
+    """Forward, backward and update as one captured graph: every replay gives the bits of an eager twin's step."""
+    from mixture_experts_layer_17_amd import layer as L
+    from mixture_experts_layer_17_amd import workloads as wl
+
+    w = wl.scaled(wl.WORKLOADS[workload], T=256, d=256, f=128, E=8)
+    seq = dev(np.array([0, 100, 256], np.int32))
+
+    def make():
+        dv = L.to_device(wl.make_inputs(w))
+        dv["ln_w"] = torch.ones(w.d, dtype=dv["x"].dtype, device="cuda")
+        return L.LayerStep(w, dv, norm=True, balance=(0.05, 0.01), seq_offsets=seq, **kw)
+
+    eager, twin = make(), make()
+    gu.say(f"case captured step {w.prec}")
+    side = torch.cuda.Stream()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=side):
+        twin.forward()
+        with pytest.raises(B.MoeError):
+            twin.update(lr=0.05)           # its momentum would be cleared by every replay
+    for s in (eager, twin):
+        s.step()
+        s.update(lr=0.05)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=side):
+        twin.step()
+        twin.update(lr=0.05)
+    for it in range(4):
+        eager.step()
+        eager.update(lr=0.05)
+        graph.replay()
+        torch.cuda.synchronize()
+        for n in ("w_gate", "w_up", "w_down"):
+            assert torch.equal(eager.inp[n], twin.inp[n]) and torch.equal(eager.mom[n], twin.mom[n]), (it, n)
+        assert torch.equal(eager.dx, twin.dx) and torch.equal(eager.balance["loss"], twin.balance["loss"]), it
+        assert bool(torch.isfinite(eager.dx.float()).all())
 
 
 def test_refused_tensors(gpu):
