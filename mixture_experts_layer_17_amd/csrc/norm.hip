@@ -515,10 +515,11 @@ Shape shape_for(int d, int vec) {
   return {kThreads, 0};
 }
 
-// Outputs of more than the L2s hold (8 x 4 MB) leave by streaming stores: 16384
-// rows of 4096 bf16 with a residual 103 -> 87 us (6.2 TB/s), 8192 of 2048 17.4 ->
-// 15.6 us; smaller ones stay cached for the router and the dispatch that read them.
-bool stream_out(int64_t T, int d, int bytes) { return T * d * bytes > int64_t{32} << 20; }
+// Outputs that fill the L2s (8 x 4 MB) leave by streaming stores: 16384 rows of
+// 4096 bf16 with a residual 103 -> 87 us (6.2 TB/s), 8192 of 2048 16.9 -> 15.7 us,
+// their backward 32.1 -> 30.5 us; smaller ones stay cached for the router and the
+// dispatch that read them.
+bool stream_out(int64_t T, int d, int bytes) { return T * d * bytes >= int64_t{32} << 20; }
 
 constexpr int kMaxBlocks = 2048;  // forward: up to eight workgroups per compute unit, looping over rows
 unsigned long_grid(int64_t T) { return static_cast<unsigned>(T < kMaxBlocks ? T : kMaxBlocks); }
