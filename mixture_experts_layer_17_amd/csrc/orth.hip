@@ -736,7 +736,10 @@ struct Epilogue {
     // symmetric outputs, by squares: above the diagonal there is nothing to do,
     // squares on it are computed whole, those below are written twice
     const bool below = KIND != kApply && mw / C::kSq > nw / C::kSq;
-    if (KIND != kApply && mw / C::kSq < nw / C::kSq) return;
+    if (KIND != kApply && mw / C::kSq < nw / C::kSq) {
+      wait_vm<0>();  // no load into LDS outlives its wave
+      return;
+    }
     const bool full = FINAL ? mw + C::WM <= p.rows && nw + WN <= p.cols : mw + C::WM <= p.M && nw + WN <= p.N;
     if (!staged) stage(0);
 #pragma unroll
