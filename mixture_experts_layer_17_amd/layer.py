@@ -35,10 +35,12 @@ class LayerStep:
 
     MXFP8 expert weights, three ways:
       default               the forward and the backward quantise the layouts they use (no cache);
-      mx_weights_per_step   every step first quantises the weights into both layouts from one read
-                            (moe_mx_weight_cache_build), and its forward and backward use them: the weights
-                            change once per optimiser step, so this is the whole per-step conversion;
-      mx_weight_cache       quantised once here and reused by every step (valid while the weights do not change).
+      mx_weights_per_step   every step's forward first quantises the weights into both layouts from one read
+                            (moe_mx_weight_cache_build), and it and the backward use them: the weights
+                            change once per optimiser step, so this is the whole per-step conversion, also
+                            with update(), which leaves it to the next forward;
+      mx_weight_cache       quantised once here and reused by every step (valid while the weights do not change:
+                            update() quantises them again).
     MXFP8 activations (mx_movement), bit-identical results every way:
       "tok" (default)       the dispatch and the combine backward write X and dY straight into both MX layouts the
                             FFN uses, rows (along d) and token-axis (along each expert's tokens, for the weight
@@ -144,6 +146,8 @@ class LayerStep:
     # ------------------------------------------------------------------ steps
     def forward(self):
         w, inp, x = self.w, self.inp, self.h
+        if self.mx_per_step:
+            self.build_weight_cache()
         if self.norm:
             B.moe_layernorm(inp["x"], inp.get("ln_w"), inp.get("ln_b"), out=self.ln)
         if self.linear_router:
@@ -200,8 +204,9 @@ class LayerStep:
                scale: float | None = None, steps: int = 5):
         """A Muon step of the expert weights, in place, from the gradients of the last backward.  scale: what the
         orthogonalised update is multiplied by besides lr; None: 0.2 sqrt(max(d, f)), which gives its entries a
-        root mean square of about 0.2.  A cache of quantised weights is built again.  The first call makes the momentum
-        (zero) and the workspace; in a graph capture it is refused, since every replay would clear the momentum."""
+        root mean square of about 0.2.  With mx_weight_cache the cache is built again; with mx_weights_per_step the
+        next forward does that.  The first call makes the momentum (zero) and the workspace; in a graph capture it is
+        refused, since every replay would clear the momentum."""
         inp, E = self.inp, self.w.E
         if self.mom is None:
             if torch.cuda.is_current_stream_capturing():
@@ -214,11 +219,9 @@ class LayerStep:
         for n, mom in self.mom.items():
             B.moe_muon_step(self.grads["d" + n], mom, inp[n], lr, momentum=momentum, nesterov=nesterov,
                             weight_decay=weight_decay, scale=scale, steps=steps, ws=self.muon_ws)
-        if self.mx_wcache is not None:
+        if self.mx_wcache is not None and not self.mx_per_step:
             self.build_weight_cache()
 
     def step(self):
-        if self.mx_per_step:
-            self.build_weight_cache()
         self.forward()
         self.backward()

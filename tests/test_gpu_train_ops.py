@@ -776,3 +776,50 @@ def test_refused_workspaces_and_outputs(gpu):
                  lambda: B.moe_balance_loss_bwd(lg, fwd, 2, 0.1, 0.1, out=lg.T), lambda: B.moe_orthogonalize(g, out=g[:1])):
         with pytest.raises(B.MoeError):
             call()
+
+
+@pytest.mark.parametrize("whole", [True, False])
+def test_update_with_weights_quantised_per_step(gpu, monkeypatch, whole):
+    """mx_weights_per_step and update(): one conversion per step, of the updated weights, whether the step is called
+    whole or as forward and backward, or replayed; the bits of a twin that quantises its own layouts."""
+    from mixture_experts_layer_17_amd import layer as L
+    from mixture_experts_layer_17_amd import workloads as wl
+
+    w = wl.scaled(wl.WORKLOADS[5], T=256, d=256, f=128, E=8)
+    built = []
+    build = B.moe_mx_weight_cache_build
+
+    def counted(*a, **kw):
+        built.append(1)
+        return build(*a, **kw)
+
+    def once(s):
+        if whole:
+            s.step()
+        else:
+            s.forward()
+            s.backward()
+        s.update(lr=0.1)
+
+    twin = L.LayerStep(w, L.to_device(wl.make_inputs(w)))
+    step = L.LayerStep(w, L.to_device(wl.make_inputs(w)), mx_weights_per_step=True)
+    replayed = L.LayerStep(w, L.to_device(wl.make_inputs(w)), mx_weights_per_step=True)
+    monkeypatch.setattr(B, "moe_mx_weight_cache_build", counted)
+    gu.say(f"case update with weights quantised per step, whole={whole}")
+    once(replayed)
+    graph = torch.cuda.CUDAGraph()
+    built.clear()
+    with torch.cuda.graph(graph, stream=torch.cuda.Stream()):
+        once(replayed)
+    assert len(built) == 1
+    for it in range(4):
+        once(twin)
+        built.clear()
+        once(step)
+        assert len(built) == 1
+        if it:
+            graph.replay()
+        torch.cuda.synchronize()
+        for s in (step, replayed):
+            assert torch.equal(s.out, twin.out) and torch.equal(s.dx, twin.dx), it
+            assert all(torch.equal(s.inp[n], twin.inp[n]) for n in ("w_gate", "w_up", "w_down")), it
