@@ -448,13 +448,14 @@ __global__ __launch_bounds__(kThreads) void balance_bwd_kernel(BwdArgs a) {
     const float n = a.norm[2 + s];
     if (!(n > 0.f)) return;
     const float f = g0 * a.alpha * static_cast<float>(E) / (static_cast<float>(a.k) * n * n * live);
-    const float even = static_cast<float>(a.k) * n / static_cast<float>(E);
+    const int even = static_cast<int>(static_cast<float>(a.k) * n / static_cast<float>(E));  // at most n: k <= E
     float c[4], dot = 0.f, sum = 0.f;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      // less the average count, which a_e - sum_j a_j p_j does not see: the
-      // difference of the large terms would lose what near-even counts differ by
-      c[i] = e0 + i < E ? f * (static_cast<float>(a.counts[s * E + e0 + i]) - even) : 0.f;
+      // less about the average count, as a_e - sum_j a_j p_j does not see a common
+      // number: the difference of the large terms would lose what near-even counts
+      // differ by, and so would a count past 2^24 itself in fp32
+      c[i] = e0 + i < E ? f * static_cast<float>(a.counts[s * E + e0 + i] - even) : 0.f;
       dot += c[i] * p[i];
       sum += p[i];
     }

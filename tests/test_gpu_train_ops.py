@@ -823,3 +823,29 @@ def test_update_with_weights_quantised_per_step(gpu, monkeypatch, whole):
         for s in (step, replayed):
             assert torch.equal(s.out, twin.out) and torch.equal(s.dx, twin.dx), it
             assert all(torch.equal(s.inp[n], twin.inp[n]) for n in ("w_gate", "w_up", "w_down")), it
+
+
+# ------------------------------------------------------------------- loads past 2^24 rows, tokens that do not count
+
+@pytest.mark.parametrize("E", [2, 3])
+def test_balance_gradient_of_near_even_loads_past_24_bits(gpu, E):
+    """Counts that fp32 cannot hold and that differ by a few: the gradient is proportional to those differences."""
+    T = (1 << 26) + 5
+    gu.say(f"case balance near-even T={T} E={E}")
+    gen = torch.Generator(device="cuda")
+    gen.manual_seed(E)
+    lg = torch.randn((T, E), generator=gen, device="cuda")
+    cnt = np.array([T // E + 3, T // E - 2, 0][:E])
+    cnt[-1] = T - cnt[:-1].sum()
+    idx = torch.repeat_interleave(torch.arange(E, device="cuda", dtype=torch.int32), dev(cnt)).view(T, 1)
+    fw = B.moe_balance_loss(lg, idx, 1.0, 0.0)
+    dl = B.moe_balance_loss_bwd(lg, fw, 1, 1.0, 0.0)
+    torch.cuda.synchronize()
+    np.testing.assert_array_equal(fw["counts"][0].cpu().numpy(), cnt)
+    rows = torch.cat([torch.arange(4096, device="cuda"), torch.arange(T - 4096, T, device="cuda")])
+    p = torch.softmax(lg[rows].double(), 1)
+    f = E / float(T) ** 2
+    a = f * dev(cnt - T // E).double()  # less a common number, which the difference does not see
+    ref = p * (a - (p * a).sum(1, keepdim=True))
+    # 4 roundings in f, 3 in p, 8 in the average, 3 behind it, of terms of at most 5 f
+    close("dlogits", dl[rows], h64(ref), 0.0, 18 * 2.0 ** -24 * 5 * f)
