@@ -169,7 +169,7 @@ int moe_route_stats(const int32_t* counts, int32_t E, int32_t* stats, void* stre
  * The backward writes
  *   dlogits[t,e] = p_e (a_e - sum_j a_j p_j) + dloss[1] 2 zeta / N lse_t p_e,
  *   a_e = dloss[0] alpha E counts[s,e] / (k n_s^2 S')       (no gradient through counts)
- * and zero for tokens that do not count; with gates and dgates (both or
+ * and zero for tokens that do not count, whatever dloss holds; with gates and dgates (both or
  * neither; then topk_idx too) the gates' gradient of moe_route_topk_bwd is
  * added for every token in the same pass, so that call is not needed.
  * dloss [2] fp32 on the device: upstream gradients of the two losses (NULL: 1).

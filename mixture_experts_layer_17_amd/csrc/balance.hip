@@ -461,8 +461,10 @@ __global__ __launch_bounds__(kThreads) void balance_bwd_kernel(BwdArgs a) {
     }
     dot = Row<LPT>::sum(dot);
     sum = Row<LPT>::sum(sum);
-    const float inv = sum == 0.f ? 0.f : 1.0f / sum;
-    if (on && t >= lo && t < hi)
+    const float inv = 1.0f / sum;
+    // a token that does not count has the sum 0 (one that does over E^-2, however coarse its lse);
+    // 0 times an infinite upstream gradient would not be 0
+    if (on && t >= lo && t < hi && sum != 0.f)
 #pragma unroll
       for (int i = 0; i < 4; ++i) dl[i] += p[i] * inv * (c[i] - dot * inv + zc);
   });

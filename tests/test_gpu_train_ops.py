@@ -849,3 +849,17 @@ def test_balance_gradient_of_near_even_loads_past_24_bits(gpu, E):
     ref = p * (a - (p * a).sum(1, keepdim=True))
     # 4 roundings in f, 3 in p, 8 in the average, 3 behind it, of terms of at most 5 f
     close("dlogits", dl[rows], h64(ref), 0.0, 18 * 2.0 ** -24 * 5 * f)
+
+
+def test_balance_tokens_that_do_not_count_get_zero_for_any_upstream(gpu):
+    lg, idx, seq, mask, rng = routing_case(200, 24, 3, 6, 3, True, pad=20)
+    mask[7] = 1
+    lg[7] = -np.inf
+    gu.say("case balance infinite upstream gradients")
+    fw = B.moe_balance_loss(dev(lg), dev(idx), 0.1, 0.1, seq_offsets=dev(seq), token_mask=dev(mask))
+    off = mask == 0
+    off[7], off[180:] = True, True
+    for up in ((np.inf, 1.0), (1.0, np.inf), (np.nan, np.nan)):
+        dl = B.moe_balance_loss_bwd(dev(lg), fw, 3, 0.1, 0.1, dloss=dev(np.array(up, np.float32)), seq_offsets=dev(seq),
+                                    token_mask=dev(mask))
+        assert not dl[dev(off)].any(), up
