@@ -174,7 +174,7 @@ int moe_route_stats(const int32_t* counts, int32_t E, int32_t* stats, void* stre
  * added for every token in the same pass, so that call is not needed.
  * dloss [2] fp32 on the device: upstream gradients of the two losses (NULL: 1).
  * Errors as for moe_route_topk; MOE_EINVAL also for a non-finite alpha or zeta,
- * S < 1, and S > 1 without seq_offsets, MOE_EUNSUPPORTED for T >= 2^29.  T = 0 is allowed (losses 0). */
+ * S < 1, and S > 1 without seq_offsets, MOE_EUNSUPPORTED for T > 2^29 - 32.  T = 0 is allowed (losses 0). */
 size_t moe_balance_loss_workspace(int64_t T, int32_t E, int64_t S);
 int moe_balance_loss(const float* logits, const int32_t* topk_idx, int64_t T, int32_t E, int32_t k,
                      const int32_t* seq_offsets, int64_t S, const uint8_t* token_mask, float alpha, float zeta,

@@ -491,7 +491,9 @@ void by_lanes(int E, F&& f) {
 }
 
 int check_sizes(int64_t T, int E, int k, int64_t S) {
-  if (E > kMaxE || k > kMaxK || T >= (int64_t{1} << 29)) return MOE_EUNSUPPORTED;  // 2^32 threads per launch
+  // a launch has fewer than 2^32 threads along x: the forward's, of kThreads for every kTok tokens begun
+  constexpr int64_t kMaxT = ((int64_t{1} << 32) / kThreads - 1) * kTok;
+  if (E > kMaxE || k > kMaxK || T > kMaxT) return MOE_EUNSUPPORTED;
   if (T < 0 || E < 1 || k < 1 || k > E || T * k >= (int64_t{1} << 31)) return MOE_EINVAL;
   if (S < 1 || S >= (int64_t{1} << 31)) return MOE_EINVAL;
   return MOE_OK;

@@ -863,3 +863,24 @@ def test_balance_tokens_that_do_not_count_get_zero_for_any_upstream(gpu):
         dl = B.moe_balance_loss_bwd(dev(lg), fw, 3, 0.1, 0.1, dloss=dev(np.array(up, np.float32)), seq_offsets=dev(seq),
                                     token_mask=dev(mask))
         assert not dl[dev(off)].any(), up
+
+
+def test_balance_most_tokens(gpu):
+    """The largest T that is not refused: each launch still has fewer than 2^32 threads."""
+    T = (1 << 29) - 32
+    gu.say(f"case balance T={T} E=1")
+    lg = torch.full((T, 1), 0.5, device="cuda")
+    idx = torch.zeros((T, 1), dtype=torch.int32, device="cuda")
+    fw = B.moe_balance_loss(lg, idx, 0.25, 2.0)
+    dl = B.moe_balance_loss_bwd(lg, fw, 1, 0.25, 2.0)
+    torch.cuda.synchronize()
+    assert fw["loss"].tolist() == [0.25, 0.5] and int(fw["counts"]) == T and float(fw["probs"]) == 1.0
+    assert bool((fw["lse"] == 0.5).all())
+    close("dlogits", dl[-100:], np.full((100, 1), 2.0 / T), 8 * 2.0 ** -24, 0.0)  # 2 zeta / N lse; p and its sum are 1
+    assert bool((dl == dl[-1, 0]).all())
+    del lg, idx, fw, dl
+    torch.cuda.empty_cache()
+    with pytest.raises(B.MoeError, match="unsupported"):
+        B.moe_balance_loss(torch.empty((T + 1, 1), device="cuda"), torch.empty((T + 1, 1), dtype=torch.int32, device="cuda"),
+                           0.25, 2.0)
+    torch.cuda.empty_cache()

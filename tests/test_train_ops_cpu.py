@@ -164,3 +164,13 @@ def test_oracle_orthogonalize_flattens_singular_values():
         assert np.all(np.abs(s - 1) < 0.2)              # the cubic iteration converges to 1 from below
         q = np.linalg.svd(to.orthogonalize(m), compute_uv=False)
         assert np.all((q > 0.3) & (q < 1.3))            # the quintic keeps them in a band
+
+
+def test_balance_refuses_more_tokens_than_a_launch_has_threads_for(L):
+    # 256 threads for every 32 tokens begun, below 2^32
+    most = (1 << 29) - 32
+    for T in (most + 1, (1 << 29) - 1):
+        assert L.moe_balance_loss_workspace(T, 1, 1) == 0
+        assert L.moe_balance_loss(FAKE, FAKE, T, 1, 1, None, 1, None, 0.1, 0.1, FAKE, FAKE, FAKE, FAKE, FAKE, FAKE, BIG,
+                                  None) == EUNSUP
+    assert L.moe_balance_loss_workspace(most, 1, 1) > 0
