@@ -174,3 +174,29 @@ def test_balance_refuses_more_tokens_than_a_launch_has_threads_for(L):
         assert L.moe_balance_loss(FAKE, FAKE, T, 1, 1, None, 1, None, 0.1, 0.1, FAKE, FAKE, FAKE, FAKE, FAKE, FAKE, BIG,
                                   None) == EUNSUP
     assert L.moe_balance_loss_workspace(most, 1, 1) > 0
+
+
+def test_balance_refusals_one_by_one(L):
+    def fwd(T=10, E=8, k=2, S=3):
+        return L.moe_balance_loss(FAKE, FAKE, T, E, k, FAKE, S, None, 0.1, 0.1, FAKE, FAKE, FAKE, FAKE, FAKE, FAKE, BIG,
+                                  None)
+
+    def bwd(T=10, E=8, k=2, S=3):
+        return L.moe_balance_loss_bwd(FAKE, FAKE, FAKE, FAKE, T, E, k, FAKE, S, None, 0.1, 0.1, None, FAKE, FAKE, FAKE,
+                                      FAKE, None)
+
+    for call in (fwd, bwd):
+        assert call(S=0) == EINVAL
+        assert call(S=-1) == EINVAL
+        assert call(T=-1) == EINVAL
+        assert call(k=0) == EINVAL
+        assert call(k=5, E=4) == EINVAL
+        assert call(k=9) == EUNSUP
+        assert call(k=9, E=16) == EUNSUP
+        assert call(E=257) == EUNSUP
+
+
+def test_orthogonalize_workspace_of_no_matrices(L):
+    for rows, cols in ((1, 1), (4096, 1536), (5000, 64)):
+        for dt in (0, 1):
+            assert L.moe_orthogonalize_workspace(0, rows, cols, dt) < L.moe_orthogonalize_workspace(1, rows, cols, dt)
