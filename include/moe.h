@@ -401,7 +401,9 @@ int mx_quantize(const void* src, int src_dtype, int64_t batch, int64_t rows, int
  * overlap.  coef: HOST array [steps][3] of a, b, c, read before the call returns;
  * NULL: 3.4445, -4.7750, 2.0315 in every step.
  * Accuracy: fp32 sums; products on matrix cores, with operands of 22 mantissa bits
- * for MOE_F32, and for MOE_BF16 of 11 bits with the iterate itself kept to 15.  A
+ * for MOE_F32, and of 11 for MOE_BF16, where the a X term takes X with 15 (matrices
+ * of one workgroup: 22) in all steps but the last.  With the default coefficients
+ * that is 0.08 to 0.15% (rms) beside the 0.17% of the result's rounding to bf16.  A
  * zero matrix gives zeros; a non-finite element makes its own matrix NaN only.
  * Limits: rows, cols <= 32768 with rows x cols (rounded up to 64) < 2^30,
  * E <= 65535, 1 <= steps <= 16, and coefficients whose polynomial keeps singular

@@ -16,10 +16,11 @@
 // rounding noise outside the matrix's own range (a gradient's rank is at most
 // its token count).  So X is held as an fp16 pair hi + lo.  bf16 gradients: the
 // products use hi only (their error stays inside X's range, where it does not
-// grow), the a X term uses both.  The diagonals of A and B, which outweigh the
-// other entries, are kept apart in fp32 and applied in the epilogues.  Against
-// fp64 the result is off by 0.06-0.11% (rms; without the split diagonals up to
-// 0.17%), less than its rounding to bf16 (0.17%).  fp32 gradients
+// grow), the a X term uses both, but in the last step.  The diagonals of A and B,
+// which outweigh the other entries, are kept apart in fp32 and applied in the
+// epilogues.  Against fp64 the result is off by 0.08-0.15% (rms, before its
+// rounding; rank 1 to full rank, 64 to 8200 rows), less than its rounding to bf16
+// (0.17%).  fp32 gradients
 // need the products too at fp32 accuracy: X, A and B are pairs and every
 // product is hi hi + hi lo + lo hi (22 bits; lo lo is below fp32's last bit).
 //
@@ -489,12 +490,14 @@ __device__ __forceinline__ void wave_lds_fence() {
 //   poly   o = (b + c (D_r + D_c)) (x + y) + kv v            (A A = O O + (D_r + D_c) O off the diagonal)
 //   apply  o = f ((a + D) x + (a + theta D) y + kv v)
 // (D: the diagonal in fp32; O: A without it.)  In apply the diagonal acts on
-// what the product saw of X: for pairs on all of it.  For hi-only products half
-// of lo measured best over full-rank and rank-deficient matrices (the product
-// leaves out B lo, which the diagonal's lo completes in part).
+// what the product saw of X: on x + y for pairs (theta 1), on x for hi-only
+// products (theta 0).  With the diagonal on y too and O not, hi-only products
+// would treat a rounding in B's range and outside it alike, far off for both where
+// the rank is low: theta 1/2 is off by 0.06-0.08% (rms, without the output's
+// rounding) for full rank but 0.18% for rank 42 of 128; 0 by 0.08-0.12% for all.
 template <class C, int KIND, bool SPLIT, bool BYROW>
 struct Coef {
-  static constexpr float kTheta = SPLIT ? 1.0f : 0.5f;
+  static constexpr float kTheta = SPLIT ? 1.0f : 0.0f;
   static constexpr bool kCols = KIND == kPoly || (KIND == kApply && !BYROW);
   float dr[C::TM];                                // at this lane's rows
   float dc[kCols ? C::TN : 1][2][8];              // at its columns
@@ -1151,7 +1154,7 @@ struct SmArgs {
 template <class T, bool MOM, bool TALL, int AT, int XT>
 __global__ __launch_bounds__(kSmallThreads) void orth_small_kernel(SmArgs p) {
   constexpr bool SPLIT = sizeof(T) == 4;
-  constexpr float kTheta = SPLIT ? 1.0f : 0.5f;
+  constexpr float kTheta = SPLIT ? 1.0f : 0.0f;  // as in Coef
   __shared__ __attribute__((aligned(16))) uint8_t lds[kSmallLds];
   const PreArgs& a = p.pre;
   const int tid = threadIdx.x, lane = tid & 63;
@@ -1301,7 +1304,7 @@ __global__ __launch_bounds__(kSmallThreads) void orth_small_kernel(SmArgs p) {
 #pragma unroll
         for (int q = 0; q < 8; ++q) {
           const float d = TALL ? dc[q] : dr, y = static_cast<float>(l[q]);
-          v[q] = f * ((ca + d) * x[q] + (ca + kTheta * d) * y + v[q] / kS);
+          v[q] = f * ((ca + d) * x[q] + (SPLIT || !last ? ca + kTheta * d : 0.f) * y + v[q] / kS);
         }
         if (!last) {
           uint4 hi, lo;
@@ -1529,8 +1532,11 @@ void run_products(const Sizes& z, const Ws& w, MmArgs a, const float (*coef)[3],
     a.M = z.rp;
     a.N = z.cp;
     a.eh = w.xh[cur];
-    // without split operands the last step does without X's lo part (noise in it
-    // is multiplied by a once more only), and the first of a bf16 gradient has none
+    // without split operands the last step does without X's lo part, and the first
+    // of a bf16 gradient has none.  Singular values are near 1 by then, where the
+    // polynomial makes of a small change c between -1.6 c and c: that is nearer to
+    // none than to the a c of the other steps (128 x 160 of full rank 0.12% off, with
+    // it 0.14%; rank 1 to 8 0.09-0.12% against 0.05-0.10%, from the noise elsewhere)
     a.el = !z.split && (i + 1 == a.steps || (i == 0 && exact0)) ? nullptr : w.xl[cur];
     a.din = w.db;
     a.oh = w.xh[nxt];

@@ -281,3 +281,21 @@ def test_layernorm_f32_by_its_roundings(gpu, T, d):
     e1 = 86 * U * (v * h).abs().mean(1, keepdim=True)
     bound = r * (6 * U * v.abs() + e0 + 4 * U * c0.abs() + h.abs() * (e1 + 8 * U * c1.abs())) + 2 * U * (dres.double().abs() + dx.abs())
     assert bool(((bw["dx"].double() - dx).abs() <= bound).all())
+
+
+# ------------------------------------------------------------------- bf16 against its own rounding
+
+@pytest.mark.parametrize("E,rows,cols", [(2, 130, 2100), (1, 4096, 128), (4, 128, 1024), (5, 129, 8200), (32, 512, 1101),
+                                         (8, 64, 128), (8, 100, 65), (3, 700, 260)])
+def test_orthogonalize_bf16_is_nearer_than_its_rounding(gpu, E, rows, cols):
+    """From rank one to full rank the iteration itself is off by less than the rounding of its result to bf16, so
+    both together (they are independent) by less than sqrt(2) of that rounding."""
+    m = min(rows, cols)
+    for rank in (1, max(1, m // 16), m // 8, m // 3, m // 2, None):
+        g = stack(rows + 3 * cols, E, rows, cols, rank, "bf16")
+        ref = orth64(g)
+        own = norm_err(ref.bfloat16(), ref)
+        gu.say(f"case bf16 E={E} {rows}x{cols} rank={rank}")
+        err = norm_err(B.moe_orthogonalize(g), ref)
+        gu.say(f"  error {err:.2e}, rounding {own:.2e}")
+        assert err <= 2 ** 0.5 * own
