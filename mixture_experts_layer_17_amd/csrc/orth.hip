@@ -317,6 +317,7 @@ struct Tile {
   // symmetric outputs go by squares of this size, each within whole waves' outputs
   static constexpr int kSq = WM >= 128 ? 128 : BN;
   static constexpr int kWavesPerSimd = kLds * 2 > 80 * 1024 ? kWaves / 4 : 2;  // workgroups per compute unit the LDS allows, at most 2
+  static_assert(BM == BN, "square tiles: symmetric outputs go by their lower triangle");
   static_assert(kA % (512 * kWaves) == 0 && kHi % (512 * kWaves) == 0, "whole LDS-DMA instructions per wave");
 };
 
@@ -417,14 +418,12 @@ __device__ __forceinline__ void read_frags(const uint16_t* __restrict__ as, cons
   for (int j = 0; j < C::TN; ++j) fb[j] = Operand<C::BN, C::BK, BKC, C::kWaves>::frag(bs, wn * C::WN + j * 32, ks, lane);
 }
 
-// Tile i of those that meet the lower triangle, in row order: row r of tiles
-// BM = R BN high has R (r + 1) of them.
-template <int R>
+// Tile i of those of the lower triangle, in row order.
 __device__ __forceinline__ void tri_tile(int i, int& r, int& c) {
-  r = static_cast<int>((__builtin_sqrtf(8.0f / R * static_cast<float>(i) + 1.0f) - 1.0f) * 0.5f);
-  while (R * (r * (r + 1) / 2) > i) --r;
-  while (R * ((r + 1) * (r + 2) / 2) <= i) ++r;
-  c = i - R * (r * (r + 1) / 2);
+  r = static_cast<int>((__builtin_sqrtf(8.0f * static_cast<float>(i) + 1.0f) - 1.0f) * 0.5f);
+  while (r * (r + 1) / 2 > i) --r;
+  while ((r + 1) * (r + 2) / 2 <= i) ++r;
+  c = i - r * (r + 1) / 2;
 }
 
 // ---------------------------------------------------------------------------
@@ -908,7 +907,7 @@ void orth_mm_kernel(MmArgs p) {
     if (p.tm <= p.tn) { c = t / p.tm; r = t - c * p.tm; }
     else { r = t / p.tn; c = t - r * p.tn; }
   } else {
-    tri_tile<C::BM / C::BN>(t, r, c);
+    tri_tile(t, r, c);
   }
   const int m0 = __builtin_amdgcn_readfirstlane(r * C::BM), n0 = __builtin_amdgcn_readfirstlane(c * C::BN);
 
@@ -1383,7 +1382,7 @@ bool use_big(int64_t big, int64_t mid) { return 17 * cdiv(big, 256) <= 10 * cdiv
 template <class C>
 int64_t sym_tiles(int64_t m, int64_t E) {
   const int64_t n = cdiv(m, C::BM);
-  return C::BM / C::BN * (n * (n + 1) / 2) * E;
+  return n * (n + 1) / 2 * E;
 }
 template <class C>
 int64_t rect_tiles(int64_t r, int64_t c, int64_t E) {
