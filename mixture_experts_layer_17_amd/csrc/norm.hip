@@ -515,10 +515,14 @@ Shape shape_for(int d, int vec) {
   return {kThreads, 0};
 }
 
-// Outputs that fill the L2s (8 x 4 MB) leave by streaming stores: 16384 rows of
-// 4096 bf16 with a residual 103 -> 87 us (6.2 TB/s), 8192 of 2048 16.9 -> 15.7 us,
-// their backward 32.1 -> 30.5 us; smaller ones stay cached for the router and the
-// dispatch that read them.
+// Outputs that fill the L2s (8 x 4 MB) leave by streaming stores; smaller ones stay
+// cached for the router and the dispatch that read them.  For the kernel alone the
+// streaming stores are the faster ones from 8 MB on (rows of 2048 bf16 with a
+// residual: 8 MB 11.9 -> 9.3 us, 24 MB 21.9 -> 19.6, 32 MB 26.4 -> 24.5, 128 MB
+// 104 -> 86, 6.2 TB/s; their backward at 32 MB 30.6 -> 29.8), but a reader that
+// follows loses by them: norm and a 32-expert router together 308 -> 311 us at 16 MB,
+// 355 -> 368 at 31, 357 -> 373 at 32, 1010 -> 1031 at 128.  A training step of eight
+// experts is the same with either at 32 and at 64 MB (1563 and 1565, 2921 and 2920 us).
 bool stream_out(int64_t T, int d, int bytes) { return T * d * bytes >= int64_t{32} << 20; }
 
 constexpr int kMaxBlocks = 2048;  // forward: up to eight workgroups per compute unit, looping over rows

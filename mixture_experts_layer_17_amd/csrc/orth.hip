@@ -1352,7 +1352,7 @@ Sizes sizes_of(int E, int rows, int cols, bool split) {
 }
 
 // Tile sizes, chosen per product by how many tiles there are for the 256 compute
-// units.  64 x 64 while they all fit at once, three to a unit (one matrix of 2048
+// units.  64 x 64 up to 768 of them, three to a unit by their LDS (one matrix of 2048
 // x 1024: Gram 14 us against 26 us with 128 x 128; past that, one of 2048 x 2048,
 // apply 41 us against 32 us).  Else 256 x 256 (eight waves, one workgroup per unit)
 // or 128 x 128 (two per unit), see use_big.
@@ -1364,7 +1364,12 @@ using MidPairs = Tile<128, 128, 32, 2, 1, true>;
 using SmallPairs = Tile<64, 64, 32, 3, 1, true>;
 // where both operands are stored with K contiguous: K steps of 64 read whole
 // 128-byte lines (one of 2900 x 2000: polynomial 62.5 -> 53.6 us; 4 of 1000 x 500:
-// apply 16.6 -> 14.3 us; the others lost, 8 of 1001 x 777: Gram 30 -> 33 us)
+// apply 16.6 -> 14.3 us; the others lost, 8 of 1001 x 777: Gram 30 -> 33 us).  Two
+// of these fit a unit, so that past 512 tiles a second round begins, and they are
+// the fastest there too: over 14 sizes of 528 to 756 tiles the whole call took 0.87
+// to 1.02 of the time with SmallPairs and 0.95 to 1.02 of that with MidPairs (8 of
+// 777 x 1001, 728 tiles: Gram 29.2 us against 31.8 and 30.7, polynomial 25.5
+// against 28.2 and 29.2).
 using SmallPairsK = Tile<64, 64, 64, 2, 2, true>;
 
 // 256 x 256 tiles do the work of four 128 x 128 ones from half the LDS and L2
@@ -1639,7 +1644,10 @@ int check_shape(int64_t E, int rows, int cols, int dtype) {
 }
 
 // Matrices that fit one workgroup: X (pairs) and A in its LDS, their 32 x 32
-// outputs within its waves' tasks.
+// outputs within its waves' tasks.  Whatever their number: 1 to 4096 of 32 x 64 to 128
+// x 192 took 0.21 to 0.86 of the time of the tiled launches (one of 128 x 128 fp32 63
+// us against 76, 1024 of 64 x 192 fp32 143 against 418), also in fp32 past 8192
+// elements, where the kernel spills 28 registers.
 bool small_fits(const Sizes& z) {
   const int64_t bytes = 4 * z.x + (z.split ? 4 : 2) * z.a + 8 * z.mp + 8 * kSmallWaves;
   return bytes <= kSmallLds && z.x <= 1024 * kSmallWaves * kSmallX && z.a <= 1024 * kSmallWaves * kSmallA;
