@@ -1366,8 +1366,8 @@ using SmallPairs = Tile<64, 64, 32, 3, 1, true>;
 // 128-byte lines (one of 2900 x 2000: polynomial 62.5 -> 53.6 us; 4 of 1000 x 500:
 // apply 16.6 -> 14.3 us; the others lost, 8 of 1001 x 777: Gram 30 -> 33 us).  Two
 // of these fit a unit, so that past 512 tiles a second round begins, and they are
-// the fastest there too: over 14 sizes of 528 to 756 tiles the whole call took 0.87
-// to 1.02 of the time with SmallPairs and 0.95 to 1.02 of that with MidPairs (8 of
+// the fastest there too: over 14 sizes of 528 to 756 tiles the whole call took 0.86
+// to 1.02 of the time with SmallPairs and 0.94 to 1.02 of that with MidPairs (8 of
 // 777 x 1001, 728 tiles: Gram 29.2 us against 31.8 and 30.7, polynomial 25.5
 // against 28.2 and 29.2).
 using SmallPairsK = Tile<64, 64, 64, 2, 2, true>;
