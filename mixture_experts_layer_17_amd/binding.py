@@ -530,9 +530,11 @@ def moe_orthogonalize_workspace(E, rows, cols, dtype):
 
 def _coef(steps, coef):
     """Per-step (a, b, c): one triple for all steps, a list of `steps` triples, or None."""
+    if not 1 <= steps <= 16:
+        raise MoeError(f"steps: 1 to 16, not {steps}")
     if coef is None:
         return None
-    rows = [coef] * steps if not hasattr(coef[0], "__len__") else list(coef)
+    rows = list(coef) if len(coef) == 0 or hasattr(coef[0], "__len__") else [coef] * steps
     if len(rows) != steps or any(len(r) != 3 for r in rows):
         raise MoeError(f"coef: expected three coefficients, or {steps} triples")
     return (ctypes.c_float * (3 * steps))(*[float(v) for r in rows for v in r])

@@ -200,3 +200,16 @@ def test_orthogonalize_workspace_of_no_matrices(L):
     for rows, cols in ((1, 1), (4096, 1536), (5000, 64)):
         for dt in (0, 1):
             assert L.moe_orthogonalize_workspace(0, rows, cols, dt) < L.moe_orthogonalize_workspace(1, rows, cols, dt)
+
+
+def test_coefficients_that_no_step_has(L):
+    """Refused as the binding refuses, and so are numbers of steps that no call takes, or that 32 bits would cut."""
+    for coef in ([], [()], [(1.0, 0.0)], [(1.0, 0.0, 0.0)] * 2, (1.0, 0.0)):
+        with pytest.raises(B.MoeError):
+            B._coef(3, coef)
+    for steps in (0, -1, 17, (1 << 32) + 5):
+        for coef in (None, (1.0, 0.0, 0.0)):
+            with pytest.raises(B.MoeError):
+                B._coef(steps, coef)
+    assert list(B._coef(2, (1.0, 2.0, 3.0))) == [1.0, 2.0, 3.0] * 2
+    assert list(B._coef(1, [(1.0, 2.0, 3.0)])) == [1.0, 2.0, 3.0]
