@@ -418,7 +418,14 @@ def _storage(what, t, dims):
     """The C code of t's storage type, for a tensor of `dims` dimensions."""
     if t.dim() != dims:
         raise MoeError(f"{what}: a tensor of {dims} dimensions is needed, not {t.dim()}")
+    _sizes(what, t)
     return _dtype_code(t)
+
+
+def _sizes(what, t):
+    """The C ABI takes most sizes in 32 bits: a larger one would be cut."""
+    if max(t.shape) >> 31:
+        raise MoeError(f"{what}: {list(t.shape)} has a size of 2^31 or more")
 
 
 _F32, _I32 = torch.float32, torch.int32
@@ -473,6 +480,7 @@ def moe_layernorm_bwd(dy, x, weight, mean, rstd, dres=None, out=None, ws=None):
 def _balance_specs(logits, k, topk_idx, seq_offsets, token_mask):
     if logits.dim() != 2 or (seq_offsets is not None and seq_offsets.dim() != 1):
         raise MoeError("logits of two dimensions and seq_offsets of one are needed")
+    _sizes("logits", logits)
     T, E = logits.shape
     S = 1 if seq_offsets is None else seq_offsets.numel() - 1
     mt = torch.bool if token_mask is not None and token_mask.dtype is torch.bool else torch.uint8

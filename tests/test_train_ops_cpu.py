@@ -213,3 +213,18 @@ def test_coefficients_that_no_step_has(L):
                 B._coef(steps, coef)
     assert list(B._coef(2, (1.0, 2.0, 3.0))) == [1.0, 2.0, 3.0] * 2
     assert list(B._coef(1, [(1.0, 2.0, 3.0)])) == [1.0, 2.0, 3.0]
+
+
+def test_sizes_past_32_bits_are_refused():
+    """A size that the C ABI's 32 bits would cut to one it takes (no memory behind these tensors)."""
+    import torch
+
+    long = (1 << 32) + 64
+    empty = lambda *shape: torch.empty(shape, device="meta", dtype=torch.float32)
+    for t in (empty(1, long), empty(long, 1), empty(1, long, 1), empty(1, 1, long), empty(long, 1, 1)):
+        with pytest.raises(B.MoeError, match="2\\^31"):
+            B._storage("call", t, t.dim())
+    for shape in ((1, long), (long, 1)):
+        with pytest.raises(B.MoeError, match="2\\^31"):
+            B._balance_specs(empty(*shape), 1, torch.empty((shape[0], 1), device="meta", dtype=torch.int32), None, None)
+    assert B._storage("call", empty(0, 8), 2) == B.MOE_F32
