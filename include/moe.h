@@ -155,7 +155,7 @@ int moe_route_stats(const int32_t* counts, int32_t E, int32_t* stats, void* stre
  *   loss[0] = alpha / S' sum_s E sum_e counts[s,e] / (k n_s) probs[s,e]
  *   loss[1] = zeta / N sum_t lse_t^2                         (both 0 if N = 0)
  *   lse [T]: 0 for a token that does not count
- *   norm [S + 2] fp32: S', N, then n_s, kept for the backward
+ *   norm [S + 2] fp32: S', N, then n_s (rounded past 2^24), kept for the backward
  * seq_offsets [S+1] int32 (device, non-decreasing, within [0, T]): sequence s
  * holds tokens [seq_offsets[s], seq_offsets[s+1]); empty sequences are allowed,
  * and tokens before the first or behind the last one do not count.  NULL (then

@@ -1367,7 +1367,7 @@ using SmallPairs = Tile<64, 64, 32, 3, 1, true>;
 // apply 16.6 -> 14.3 us; the others lost, 8 of 1001 x 777: Gram 30 -> 33 us).  Two
 // of these fit a unit, so that past 512 tiles a second round begins, and they are
 // the fastest there too: over 14 sizes of 528 to 756 tiles the whole call took 0.86
-// to 1.02 of the time with SmallPairs and 0.94 to 1.02 of that with MidPairs (8 of
+// to 1.02 of the time with SmallPairs and 0.93 to 1.02 of that with MidPairs (8 of
 // 777 x 1001, 728 tiles: Gram 29.2 us against 31.8 and 30.7, polynomial 25.5
 // against 28.2 and 29.2).
 using SmallPairsK = Tile<64, 64, 64, 2, 2, true>;
@@ -1538,9 +1538,9 @@ void run_products(const Sizes& z, const Ws& w, MmArgs a, const float (*coef)[3],
     a.eh = w.xh[cur];
     // without split operands the last step does without X's lo part, and the first
     // of a bf16 gradient has none.  Singular values are near 1 by then, where the
-    // polynomial makes of a small change c between -1.6 c and c: that is nearer to
-    // none than to the a c of the other steps (128 x 160 of full rank 0.12% off, with
-    // it 0.14%; rank 1 to 8 0.09-0.12% against 0.05-0.10%, from the noise elsewhere)
+    // polynomial makes of a small change c between -1.6 c and 1.7 c, which is nearer to
+    // none than to the a c of the other steps (64 x 128 of full rank 0.13% off, with it
+    // 0.15%; but rank 1, whose noise is elsewhere, 0.09% against 0.04%)
     a.el = !z.split && (i + 1 == a.steps || (i == 0 && exact0)) ? nullptr : w.xl[cur];
     a.din = w.db;
     a.oh = w.xh[nxt];
