@@ -266,7 +266,7 @@ def _own(st):
     if op == "linear_bwd":
         return B.moe_linear_bwd(st["dy"], st["x"], st["w"], z=st.get("z"), act=c["act"], in_z=st.get("in_z"),
                                 in_act=c["in_act"], dres=st.get("dres"), ws=st["ws"])
-    w, state = B.moe_adamw_step(st["plan"], LR, STEP, betas=BETAS, eps=EPS, seed=st["seed"], gscale=st["gscale"])
+    w, state = B.moe_adamw_step(st["plan"], LR, STEP, betas=BETAS, eps=EPS, seed=st["seed"], grad_scale=st["gscale"])
     out = {"w": w}
     if c["bits"] == 8:
         out.update(B.moe_adamw_state_values(state))
