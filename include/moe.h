@@ -138,6 +138,47 @@ int moe_route_topk_noalloc(const float* logits, int64_t T, int32_t E, int32_t k,
 int moe_route_topk_bwd(const float* gates, const float* dgates, const int32_t* topk_idx, int64_t T,
                        int32_t E, int32_t k, float* dlogits, void* stream);
 
+/* Routing by scores (no page gives these formulas; they are the usual ones of
+ * layers with many small experts).  A token's scores over the E experts:
+ *   MOE_SOFTMAX  s = softmax(logits), MOE_SIGMOID  s = 1 / (1 + exp(-logits))
+ * It chooses by c = s + bias (bias [E] fp32, NULL: 0).  `groups` groups of E / groups
+ * consecutive experts: a group's worth is the sum of its `group_best` (1 or 2) best
+ * choices, and the top_groups worthiest stay in (ties: the lower group).  The k best
+ * choices among them, in falling order (ties: the lower index), are topk_idx, and
+ *   gates = scale s, or with renorm != 0  scale s / (sum of the k chosen s)
+ * (0 where that sum is 0).  The order is that of c in 64 bits, so it does not hang on
+ * rounding; gates are rounded once to fp32.  A token of -inf only has scores 0 under
+ * softmax; a NaN or +inf logit makes its whole row's scores NaN there; a NaN choice
+ * ranks below every number, -inf included, NaNs among themselves by index.
+ * counts, offsets, perm_src, perm_dst, mx_blk_offsets (NULL allowed): as
+ * moe_route_topk writes them, for the calls that take its metadata.
+ * MOE_EINVAL for groups that do not divide E, top_groups outside 1..groups, fewer than
+ * k experts in top_groups groups, group_best above a group's size, a scale that is not
+ * finite, a null or unaligned pointer; MOE_EUNSUPPORTED for more than 64 groups.
+ * T = 0 is allowed (counts and offsets become zero). */
+typedef enum { MOE_SOFTMAX = 0, MOE_SIGMOID = 1 } moe_score;
+size_t moe_route_scored_workspace(int64_t T, int32_t E, int32_t k);
+int moe_route_scored(const float* logits, const float* bias, int64_t T, int32_t E, int32_t k, int score,
+                     int32_t groups, int32_t top_groups, int32_t group_best, int renorm, float scale,
+                     int32_t* topk_idx, float* gates, int32_t* counts, int32_t* offsets, int32_t* perm_src,
+                     int32_t* perm_dst, int32_t* mx_blk_offsets, void* ws, size_t ws_bytes, void* stream);
+
+/* Backward of moe_route_scored's gates: the gradient of the logits for dgates [T, k]
+ * (the choice itself, the groups and the bias have none).  topk_idx [T, k]: distinct
+ * experts per token, as moe_route_scored wrote them for these logits.  Experts that
+ * were not chosen get zero, but under softmax without renorm, where every score
+ * depends on all logits.  dlogits [T, E] is overwritten, or with accumulate != 0
+ * added to (so it joins the gradient of moe_balance_loss_bwd). */
+int moe_route_scored_bwd(const float* logits, const int32_t* topk_idx, const float* dgates, int64_t T, int32_t E,
+                         int32_t k, int score, int renorm, float scale, int accumulate, float* dlogits, void* stream);
+
+/* Update of the balancing bias from the load of a step: with n[e] the sum over s of
+ * counts[s,e] (counts [S, E]: moe_route_scored's with S = 1, or moe_balance_loss's,
+ * which leave padded tokens out) bias_out[e] = bias[e] + rate sign(mean(n) - n[e]).
+ * bias_out may be bias. */
+int moe_route_bias_update(const int32_t* counts, int64_t S, int32_t E, float rate, const float* bias, float* bias_out,
+                          void* stream);
+
 /* Load statistics of a routing ("Scaling to the trillion-parameter range":
  * a balance metric alone can be gamed, so the observable load is exported).
  * counts [E] int32 (from moe_route_topk), 1 <= E <= 256; stats [4] int32 on
@@ -418,6 +459,76 @@ int moe_muon_step(const void* g, int dtype, int32_t E, int32_t rows, int32_t col
                   int nesterov, int32_t steps, const float* coef, float eps, const void* w, float lr,
                   float weight_decay, float scale, float* mom_out, void* w_out, void* ws, size_t ws_bytes,
                   void* stream);
+
+/* ---------------------------------------------------------------------------
+ * Dense product with bias, activation and residual (a shared expert beside the
+ * routed ones; no page defines it).  In `dtype` (MOE_F32 or MOE_BF16), fp32 sums,
+ * each output rounded once:
+ *   forward:  z = x w + bias, y = act(z) + residual
+ *   backward: dz = dy act'(z), dx = (dz w^T) in_act'(in_z) + dres, dw = x^T dz,
+ *             db = sum of dz over the rows
+ * x, dx, in_z, dres [M, K]; w, dw [K, N]; y, dy, z, residual [M, N]; bias, db [N]; any
+ * sizes (K, N up to 2^20).  bias, residual, z (forward: not kept) and dres may be NULL, and so
+ * may any of dx, dw, db (not computed).  The backward takes z as the forward kept it;
+ * with act MOE_ACT_NONE it needs none.  in_z, in_act: the pre-activation and activation
+ * that x came from, so that dx is the gradient of that in_z; MOE_ACT_NONE: dx is that of x.
+ * MOE_ACT_GELU is z Phi(z) with the error function; relu'(0) = 0.  For MOE_BF16 the products
+ * take dz rounded to bf16 (db does not).  y may be residual; dx may be dres or in_z; no
+ * other overlap.  M = 0 is allowed (dw and db become zero).  MOE_EUNSUPPORTED for K or N
+ * past 2^20 and for more than 2^35 elements (rounded up to 8 columns). */
+typedef enum { MOE_ACT_NONE = 0, MOE_ACT_RELU = 1, MOE_ACT_SILU = 2, MOE_ACT_GELU = 3 } moe_act;
+size_t moe_linear_workspace(int dtype, int64_t M, int32_t K, int32_t N, int is_bwd);
+int moe_linear(const void* x, const void* w, const void* bias, const void* residual, int dtype, int64_t M, int32_t K,
+               int32_t N, int act, void* y, void* z, void* ws, size_t ws_bytes, void* stream);
+int moe_linear_bwd(const void* dy, const void* x, const void* w, const void* z, int dtype, int64_t M, int32_t K,
+                   int32_t N, int act, const void* in_z, int in_act, const void* dres, void* dx, void* dw, void* db,
+                   void* ws, size_t ws_bytes, void* stream);
+
+/* ---------------------------------------------------------------------------
+ * AdamW step of a list of tensors (no page gives an optimiser formula; AdamW as
+ * published).  With g times *grad_scale (device, NULL: 1) and t the step:
+ *   m' = beta1 m + (1 - beta1) g,  v' = beta2 v + (1 - beta2) g^2
+ *   w' = (1 - r weight_decay) w - r m' / (1 - beta1^t) / (sqrt(v' / (1 - beta2^t)) + eps)
+ * with r = lr lr_scale, in fp32.  `tensors` is a HOST array, read before the call returns;
+ * w, g, w_out of a tensor in `dtype` (MOE_F32 or MOE_BF16), w_out may be w.
+ * The states of all tensors lie in one buffer each, a tensor's at elements
+ * [offset, offset + n) with offset a multiple of 32, rising over the list without overlap;
+ * what follows up to the next multiple of 32 belongs to it and stays zero.
+ *   bits 32: m, v fp32 [state_len]
+ *   bits 8:  m and the root of v as E4M3 codes [state_len] with one byte b per 32 values
+ *            ([state_len / 32], it stands for 2^(b - 127); 255: a value was not finite, the
+ *            block reads as NaN).  The power of two is the least that keeps the block's
+ *            largest value within 448.  A value between two codes takes the upper one if
+ *            its place between them and a random number in (0, 1) sum to 1 or more: the number
+ *            is (r + 1/2) / 2^16 with r the high (m) or low (root of v) half of
+ *            hash(i 0x9E3779B9 + hash(hash(seed + j 0x9E3779B9) + t 0x9E3779B9)) for
+ *            element i of tensor j, all modulo 2^32.  A root above 0 is at least the least code.
+ * master (MOE_BF16 only, NULL: none): fp32 weights [state_len]; the step is theirs, and
+ * w_out their rounding (w is not read).  All *_out buffers may be their inputs; no other
+ * overlap, and no tensor twice.
+ * step_dev (NULL: `step` counts): t on the device, at least 1, for captured graphs.
+ * MOE_EINVAL for betas outside [0, 1), a negative eps, scalars that are not finite (products
+ * of lr, lr_scale and weight_decay among them), step < 1, n < 0 (0 is skipped), bad offsets, a
+ * null or unaligned pointer, a master with MOE_F32; MOE_EUNSUPPORTED for 2^37 elements or more
+ * in a tensor.  A launch takes 60 tensors. */
+typedef struct {
+  const void* w;
+  const void* g;
+  void* w_out;
+  int64_t n;
+  int64_t offset;
+  float weight_decay;
+  float lr_scale;
+} moe_adamw_tensor;
+int moe_adamw_step(const moe_adamw_tensor* tensors, int32_t count, int dtype, int bits, int64_t state_len,
+                   const void* m, const void* v, const uint8_t* m_scale, const uint8_t* v_scale, const float* master,
+                   double lr, double beta1, double beta2, double eps, int64_t step, const int64_t* step_dev,
+                   const float* grad_scale, uint32_t seed, void* m_out, void* v_out, uint8_t* m_scale_out,
+                   uint8_t* v_scale_out, float* master_out, void* stream);
+
+/* The values of an 8-bit state (codes [state_len], scale [state_len / 32]) in bf16, which
+ * holds them exactly (scales below 2^-124 apart). */
+int moe_adamw_state_values(const uint8_t* codes, const uint8_t* scale, int64_t state_len, void* values, void* stream);
 
 /* ---------------------------------------------------------------------------
  * Diagnostics: per-kernel timing for benchmarks and profiling (no page

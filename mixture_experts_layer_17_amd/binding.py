@@ -22,7 +22,7 @@ MOE_F32, MOE_BF16, MOE_MXFP8 = 0, 1, 2
 _PREC = {"f32": MOE_F32, "bf16": MOE_BF16, "mxfp8": MOE_MXFP8}
 
 _c_void_p, _i64, _i32, _sz, _int = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int32, ctypes.c_size_t, ctypes.c_int
-_f32 = ctypes.c_float
+_f32, _f64 = ctypes.c_float, ctypes.c_double
 
 _SIGS = {
     "moe_abi_version": (_int, []),
@@ -69,6 +69,18 @@ _SIGS = {
                                  _c_void_p]),
     "moe_muon_step": (_int, [_c_void_p, _int, _i32, _i32, _i32, _c_void_p, _f32, _int, _i32, _c_void_p, _f32,
                              _c_void_p, _f32, _f32, _f32, _c_void_p, _c_void_p, _c_void_p, _sz, _c_void_p]),
+    "moe_route_scored_workspace": (_sz, [_i64, _i32, _i32]),
+    "moe_route_scored": (_int, [_c_void_p, _c_void_p, _i64, _i32, _i32, _int, _i32, _i32, _i32, _int, _f32]
+                         + [_c_void_p] * 8 + [_sz, _c_void_p]),
+    "moe_route_scored_bwd": (_int, [_c_void_p] * 3 + [_i64, _i32, _i32, _int, _int, _f32, _int, _c_void_p, _c_void_p]),
+    "moe_route_bias_update": (_int, [_c_void_p, _i64, _i32, _f32, _c_void_p, _c_void_p, _c_void_p]),
+    "moe_linear_workspace": (_sz, [_int, _i64, _i32, _i32, _int]),
+    "moe_linear": (_int, [_c_void_p] * 4 + [_int, _i64, _i32, _i32, _int] + [_c_void_p] * 3 + [_sz, _c_void_p]),
+    "moe_linear_bwd": (_int, [_c_void_p] * 4 + [_int, _i64, _i32, _i32, _int, _c_void_p, _int] + [_c_void_p] * 5
+                       + [_sz, _c_void_p]),
+    "moe_adamw_step": (_int, [_c_void_p, _i32, _int, _int, _i64] + [_c_void_p] * 5 + [_f64] * 4
+                       + [_i64, _c_void_p, _c_void_p, ctypes.c_uint32] + [_c_void_p] * 6),
+    "moe_adamw_state_values": (_int, [_c_void_p, _c_void_p, _i64, _c_void_p, _c_void_p]),
     "moe_timing_enable": (_int, [_int]),
     "moe_timing_report": (_int, [ctypes.c_char_p, _sz]),
 }
@@ -578,6 +590,265 @@ def moe_muon_step(g, mom, w, lr, momentum=0.95, nesterov=True, weight_decay=0.0,
                                _coef(steps, coef), eps, _p(w), lr, weight_decay, scale, _p(mom_out), _p(w_out),
                                _p(ws), ws.numel(), _stream()), what)
     return w_out, mom_out
+
+
+# --------------------------------------------------------------------------- routing by scores
+
+_SCORE = {"softmax": 0, "sigmoid": 1}
+_ACT = {"none": 0, "relu": 1, "silu": 2, "gelu": 3}
+
+
+def _named(what, kind, table, name):
+    if name not in table:
+        raise MoeError(f"{what}: {kind} {name!r}, expected one of {sorted(table)}")
+    return table[name]
+
+
+def _route_sizes(what, logits, k):
+    if logits.dim() != 2:
+        raise MoeError(f"{what}: logits of two dimensions are needed, not {logits.dim()}")
+    _sizes(what, logits)
+    T, E = logits.shape
+    if not 1 <= k <= E:
+        raise MoeError(f"{what}: k = {k} of {E} experts")
+    return T, E
+
+
+def _route_out(T, E, k, dev):
+    i32 = dict(dtype=_I32, device=dev)
+    return {"topk_idx": torch.empty((T, k), **i32), "gates": torch.empty((T, k), dtype=_F32, device=dev),
+            "counts": torch.empty(E, **i32), "offsets": torch.empty(E + 1, **i32), "perm_src": torch.empty(T * k, **i32),
+            "perm_dst": torch.empty(T * k, **i32), "mx_blk_offsets": torch.empty(E + 1, **i32)}
+
+
+def moe_route_scored(logits, k, score="softmax", bias=None, groups=1, top_groups=1, group_best=1, renorm=True, scale=1.0,
+                     out=None, ws=None):
+    """Routing by softmax or sigmoid scores, a bias and groups of experts; returns what moe_route_topk returns."""
+    what, dev = "moe_route_scored", logits.device
+    code = _named(what, "score", _SCORE, score)
+    T, E = _route_sizes(what, logits, k)
+    specs = (("logits", logits, (T, E), _F32), ("bias", bias, (E,), _F32)) + _ws_spec(ws)
+    if out is not None:
+        specs += (("topk_idx", out["topk_idx"], (T, k), _I32), ("gates", out["gates"], (T, k), _F32),
+                  ("counts", out["counts"], (E,), _I32), ("offsets", out["offsets"], (E + 1,), _I32),
+                  ("perm_src", out["perm_src"], (T * k,), _I32), ("perm_dst", out["perm_dst"], (T * k,), _I32),
+                  ("mx_blk_offsets", out.get("mx_blk_offsets"), (E + 1,), _I32))
+    _args(what, dev, specs)
+    if out is None:
+        out = _route_out(T, E, k, dev)
+    if ws is None:
+        ws = _ws(lib().moe_route_scored_workspace(T, E, k), dev)
+    _check(lib().moe_route_scored(_p(logits), _p(bias), T, E, k, code, groups, top_groups, group_best, int(bool(renorm)),
+                                  scale, _p(out["topk_idx"]), _p(out["gates"]), _p(out["counts"]), _p(out["offsets"]),
+                                  _p(out["perm_src"]), _p(out["perm_dst"]), _p(out.get("mx_blk_offsets")), _p(ws),
+                                  ws.numel(), _stream()), what)
+    return out
+
+
+def moe_route_scored_bwd(logits, topk_idx, dgates, score="softmax", renorm=True, scale=1.0, out=None, accumulate=False):
+    """dlogits [T, E] of moe_route_scored's gates; with accumulate added to `out`."""
+    what, dev, k = "moe_route_scored_bwd", logits.device, topk_idx.shape[-1] if topk_idx.dim() else 0
+    code = _named(what, "score", _SCORE, score)
+    T, E = _route_sizes(what, logits, k)
+    if accumulate and out is None:
+        raise MoeError(f"{what}: accumulate needs out")
+    _args(what, dev, (("logits", logits, (T, E), _F32), ("topk_idx", topk_idx, (T, k), _I32),
+                      ("dgates", dgates, (T, k), _F32), ("out", out, (T, E), _F32)))
+    if out is None:
+        out = torch.empty((T, E), dtype=_F32, device=dev)
+    _check(lib().moe_route_scored_bwd(_p(logits), _p(topk_idx), _p(dgates), T, E, k, code, int(bool(renorm)), scale,
+                                      int(bool(accumulate)), _p(out), _stream()), what)
+    return out
+
+
+def moe_route_bias_update(counts, bias, rate, inplace=True):
+    """bias [E] moved by rate towards the experts below the mean of counts [E] or [S, E]; returns it (or a new one)."""
+    what, dev = "moe_route_bias_update", bias.device
+    if bias.dim() != 1 or counts.dim() not in (1, 2):
+        raise MoeError(f"{what}: bias [E] and counts [E] or [S, E] are needed")
+    E, S = bias.shape[0], 1 if counts.dim() == 1 else counts.shape[0]
+    _args(what, dev, (("counts", counts, (E,) if counts.dim() == 1 else (S, E), _I32), ("bias", bias, (E,), _F32)))
+    out = bias if inplace else torch.empty_like(bias)
+    _check(lib().moe_route_bias_update(_p(counts), S, E, rate, _p(bias), _p(out), _stream()), what)
+    return out
+
+
+# --------------------------------------------------------------------------- dense product
+
+def _linear_sizes(what, x, w):
+    code = _storage(what, x, 2)
+    if w.dim() != 2:
+        raise MoeError(f"{what}: w of two dimensions is needed, not {w.dim()}")
+    _sizes(what, w)
+    return code, x.shape[0], x.shape[1], w.shape[1]
+
+
+def moe_linear_workspace(x, w, bwd=False):
+    """A workspace for moe_linear (or its backward) of these tensors' sizes."""
+    code, M, K, N = _linear_sizes("moe_linear_workspace", x, w)
+    n = lib().moe_linear_workspace(code, M, K, N, int(bool(bwd)))
+    if n == 0:
+        raise MoeError(f"moe_linear_workspace: {M} x {K} x {N} is not supported")
+    return _ws(n, x.device)
+
+
+def moe_linear(x, w, bias=None, act="none", residual=None, save=False, out=None, ws=None):
+    """{"y"[, "z"]}: y = act(x w + bias) + residual; z (with save, or in out) is what act was applied to."""
+    what, dev, dt = "moe_linear", x.device, x.dtype
+    acode = _named(what, "act", _ACT, act)
+    code, M, K, N = _linear_sizes(what, x, w)
+    specs = (("x", x, (M, K), dt), ("w", w, (K, N), dt), ("bias", bias, (N,), dt),
+             ("residual", residual, (M, N), dt)) + _ws_spec(ws)
+    if out is not None:
+        specs += (("y", out["y"], (M, N), dt), ("z", out.get("z"), (M, N), dt))
+    _args(what, dev, specs)
+    if out is None:
+        out = {name: torch.empty((M, N), dtype=dt, device=dev) for name in (("y", "z") if save else ("y",))}
+    if ws is None:
+        ws = moe_linear_workspace(x, w)
+    _check(lib().moe_linear(_p(x), _p(w), _p(bias), _p(residual), code, M, K, N, acode, _p(out["y"]), _p(out.get("z")),
+                            _p(ws), ws.numel(), _stream()), what)
+    return out
+
+
+def moe_linear_bwd(dy, x, w, z=None, act="none", in_z=None, in_act="none", dres=None, out=None, ws=None):
+    """Gradients {"dx", "dw", "db"} of moe_linear; an out without one of them leaves it out.  With in_act, dx is the
+    gradient of in_z, where x = in_act(in_z); dres is added to dx."""
+    what, dev, dt = "moe_linear_bwd", x.device, x.dtype
+    acode, icode = _named(what, "act", _ACT, act), _named(what, "in_act", _ACT, in_act)
+    code, M, K, N = _linear_sizes(what, x, w)
+    specs = (("dy", dy, (M, N), dt), ("x", x, (M, K), dt), ("w", w, (K, N), dt), ("z", z, (M, N), dt),
+             ("in_z", in_z, (M, K), dt), ("dres", dres, (M, K), dt)) + _ws_spec(ws)
+    if out is not None:
+        specs += (("dx", out.get("dx"), (M, K), dt), ("dw", out.get("dw"), (K, N), dt), ("db", out.get("db"), (N,), dt))
+    _args(what, dev, specs)
+    if out is None:
+        out = {"dx": torch.empty((M, K), dtype=dt, device=dev), "dw": torch.empty((K, N), dtype=dt, device=dev),
+               "db": torch.empty(N, dtype=dt, device=dev)}
+    if ws is None:
+        ws = moe_linear_workspace(x, w, bwd=True)
+    _check(lib().moe_linear_bwd(_p(dy), _p(x), _p(w), _p(z), code, M, K, N, acode, _p(in_z), icode, _p(dres),
+                                _p(out.get("dx")), _p(out.get("dw")), _p(out.get("db")), _p(ws), ws.numel(), _stream()),
+           what)
+    return out
+
+
+# --------------------------------------------------------------------------- AdamW
+
+class _AdamwTensor(ctypes.Structure):
+    _fields_ = [("w", _c_void_p), ("g", _c_void_p), ("w_out", _c_void_p), ("n", _i64), ("offset", _i64),
+                ("weight_decay", _f32), ("lr_scale", _f32)]
+
+
+def _adamw_offsets(params):
+    off = [0]
+    for t in params:
+        off.append(off[-1] + -(-t.numel() // 32) * 32)
+    return off
+
+
+def moe_adamw_state(params, bits=32, master=False):
+    """Zero states for a list of tensors, tensor i at [offsets[i], offsets[i] + its size) of each flat buffer:
+    {"bits", "offsets", "m", "v"[, "m_scale", "v_scale"][, "master"]}.  bits 8: codes (m, and the root of v) and their
+    scales; master: fp32 copies of bf16 weights."""
+    if bits not in (32, 8) or not params:
+        raise MoeError(f"moe_adamw_state: bits 32 or 8 and a tensor are needed, not {bits} and {len(params)}")
+    off, dev = _adamw_offsets(params), params[0].device
+    state = {"bits": bits, "offsets": off[:-1]}
+    for name in ("m", "v"):
+        state[name] = torch.zeros(off[-1], dtype=_F32 if bits == 32 else torch.uint8, device=dev)
+        if bits == 8:
+            state[name + "_scale"] = torch.zeros(off[-1] // 32, dtype=torch.uint8, device=dev)
+    if master:
+        state["master"] = torch.zeros(off[-1], dtype=_F32, device=dev)
+        for t, o in zip(params, off):
+            state["master"][o:o + t.numel()] = t.detach().reshape(-1)
+    return state
+
+
+class AdamwPlan:
+    """What moe_adamw_step needs of a list of tensors, checked and laid out once (moe_adamw_plan).  It holds the tensors
+    and their addresses; a step refuses tensors that have been given other memory since."""
+
+    def __init__(self, dtype, bits, length, table, params, grads, w_out, state, state_out):
+        self.dtype, self.bits, self.length, self.table = dtype, bits, length, table
+        self.params, self.grads, self.w_out, self.state, self.state_out = params, grads, w_out, state, state_out
+        names = ("m", "v", "m_scale", "v_scale", "master")
+        self.device = params[0].device
+        self.tensors = ([*params, *grads, *w_out] + [state[n] for n in names if n in state]
+                        + [state_out[n] for n in names if n in state_out])
+        self.at = [t.data_ptr() for t in self.tensors]
+        self.ins, self.outs = [_p(state.get(n)) for n in names], [_p(state_out.get(n)) for n in names]
+
+
+def moe_adamw_plan(params, grads, state, weight_decay=0.0, lr_scale=1.0, out=None):
+    """A plan for steps of params (of one type, fp32 or bf16) from grads (of the same shapes) with state
+    (moe_adamw_state).  weight_decay, lr_scale: numbers, or one per tensor.  out: (tensors, state) that take the results;
+    None: in place."""
+    what = "moe_adamw_plan"
+    params, grads = list(params), list(grads)
+    if not params or len(grads) != len(params):
+        raise MoeError(f"{what}: {len(params)} tensors and {len(grads)} gradients")
+    w_out, state_out = (params, state) if out is None else (list(out[0]), out[1])
+    if len(w_out) != len(params):
+        raise MoeError(f"{what}: {len(params)} tensors and {len(w_out)} outputs")
+    n, dev, dt = len(params), params[0].device, params[0].dtype
+    code = _dtype_code(params[0])
+    per = {"weight_decay": weight_decay, "lr_scale": lr_scale}
+    for name, v in per.items():
+        per[name] = list(v) if hasattr(v, "__len__") else [v] * n
+        if len(per[name]) != n:
+            raise MoeError(f"{what}: {len(per[name])} values of {name} for {n} tensors")
+    off = _adamw_offsets(params)
+    bits = state["bits"]
+    kind = _F32 if bits == 32 else torch.uint8
+    specs = []
+    for i, (w, g, o) in enumerate(zip(params, grads, w_out)):
+        specs += [(f"tensor {i}", w, w.shape, dt), (f"gradient {i}", g, w.shape, dt), (f"output {i}", o, w.shape, dt)]
+    for st in (state, state_out):
+        if st["bits"] != bits or st["offsets"] != off[:-1] or ("master" in st) != ("master" in state):
+            raise MoeError(f"{what}: a state of other tensors")
+        specs += [(name, st[name], (off[-1],), kind) for name in ("m", "v")]
+        if bits == 8:
+            specs += [(name, st[name], (off[-1] // 32,), torch.uint8) for name in ("m_scale", "v_scale")]
+        specs += [("master", st.get("master"), (off[-1],), _F32)]
+    if "master" in state and dt is _F32:
+        raise MoeError(f"{what}: a master for fp32 tensors")
+    _args(what, dev, specs)
+    written = sorted((t.data_ptr(), t.data_ptr() + t.numel() * t.element_size()) for t in w_out if t.numel())
+    if any(a[1] > b[0] for a, b in zip(written, written[1:])):
+        raise MoeError(f"{what}: outputs overlap (a tensor twice)")
+    table = (_AdamwTensor * n)(*[_AdamwTensor(_p(w), _p(g), _p(o), w.numel(), at, wd, ls) for w, g, o, at, wd, ls in
+                                 zip(params, grads, w_out, off, per["weight_decay"], per["lr_scale"])])
+    return AdamwPlan(code, bits, off[-1], table, params, grads, w_out, state, state_out)
+
+
+def moe_adamw_step(plan, lr, step=1, betas=(0.9, 0.999), eps=1e-8, seed=0, grad_scale=None, step_dev=None):
+    """One AdamW step (step counts from 1; step_dev: an int64 tensor [1] on the device in its place); returns the
+    updated (tensors, state)."""
+    what = "moe_adamw_step"
+    if [t.data_ptr() for t in plan.tensors] != plan.at:
+        raise MoeError(f"{what}: a tensor of the plan has other memory now")
+    _args(what, plan.device, (("grad_scale", grad_scale, (1,), _F32), ("step_dev", step_dev, (1,), torch.int64)))
+    m, v, ms, vs, master = plan.ins
+    mo, vo, mso, vso, mastero = plan.outs
+    _check(lib().moe_adamw_step(plan.table, len(plan.params), plan.dtype, plan.bits, plan.length, m, v, ms, vs, master,
+                                lr, *betas, eps, step, _p(step_dev), _p(grad_scale), seed & 0xFFFFFFFF, mo, vo, mso, vso,
+                                mastero, _stream()), what)
+    return plan.w_out, plan.state_out
+
+
+def moe_adamw_state_values(state):
+    """The values of an 8-bit state in bf16: {"m", "root"} (the root of v), flat as the state is."""
+    what, dev, n = "moe_adamw_state_values", state["m"].device, state["m"].numel()
+    if state["bits"] != 8:
+        raise MoeError(f"{what}: a state of 8 bits is needed")
+    _args(what, dev, tuple((k, state[k], (n,), torch.uint8) for k in ("m", "v"))
+          + tuple((k, state[k], (n // 32,), torch.uint8) for k in ("m_scale", "v_scale")))
+    out = {"m": torch.empty(n, dtype=torch.bfloat16, device=dev), "root": torch.empty(n, dtype=torch.bfloat16, device=dev)}
+    for q, name in (("m", "m"), ("v", "root")):
+        _check(lib().moe_adamw_state_values(_p(state[q]), _p(state[q + "_scale"]), n, _p(out[name]), _stream()), what)
+    return out
 
 
 # --------------------------------------------------------------------------- diagnostics

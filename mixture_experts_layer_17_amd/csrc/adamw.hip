@@ -1,0 +1,391 @@
+// AdamW step of a list of tensors in few launches, and the values of 8-bit states.
+//
+// Per element, in fp32:  m' = b1 m + (1 - b1) g,  v' = b2 v + (1 - b2) g^2,
+//   w' = (1 - lr decay) w - lr / (1 - b1^t) m' / (sqrt(v') / sqrt(1 - b2^t) + eps)
+// One pass: every operand read once and written once, which is what bounds it.
+//
+// The tensors' addresses and sizes travel in the kernel's arguments (kMaxList a
+// launch), so nothing is copied to the device and a captured graph keeps them.
+// A workgroup takes kUnit elements of one tensor, found by a search over the
+// tensors' first units in scalar registers.
+//
+// States in 8 bits: m and the root of v as E4M3 codes with one power of two per
+// 32 values (a lane holds 8, four lanes a block).  The root has half the range
+// of v.  A state moves by a fraction of a step of such a code (v by 1 - b2, a
+// thousandth), so rounding to nearest would leave it where it is; it is rounded
+// up with the chance that the part cut off gives, from a hash of the seed, the
+// step, the tensor and the element, which keeps its expectation and makes the
+// step repeatable.  A root above zero is not stored as zero: the next step
+// would divide by little more than eps.
+#include <cmath>
+
+#include "common.hpp"
+
+namespace moe {
+namespace {
+
+constexpr int kMaxList = 60;    // tensors per launch: the arguments stay below 4 KB
+constexpr int kThreads = 256;
+constexpr int kPer = 8;         // elements per lane and turn: 16 bytes of bf16
+constexpr int kTurns = 4;
+constexpr int kUnit = kThreads * kPer * kTurns;
+constexpr int64_t kMaxUnits = int64_t{1} << 24;  // a launch holds fewer than 2^32 threads
+
+struct ListEntry {
+  const void* w;
+  const void* g;
+  void* w_out;
+  int64_t n;
+  int64_t offset;  // of its states, in elements
+  double lr;
+  float keep;      // 1 - lr weight_decay
+  uint32_t seed;
+};
+
+struct AdamArgs {
+  ListEntry list[kMaxList];
+  int32_t first[kMaxList + 1];  // the first unit of each tensor
+  int32_t count;
+  const void* m;
+  const void* v;
+  const uint8_t* m_scale;
+  const uint8_t* v_scale;
+  const float* master;
+  void* m_out;
+  void* v_out;
+  uint8_t* m_scale_out;
+  uint8_t* v_scale_out;
+  float* master_out;
+  double beta1, beta2;
+  float eps;
+  int64_t step;
+  const int64_t* step_dev;
+  const float* gscale;
+};
+static_assert(sizeof(AdamArgs) <= 4096, "kernel arguments");
+
+// A hash of 32 bits: two rounds of xor-shift and odd multiplication.
+__host__ __device__ __forceinline__ uint32_t mix(uint32_t h) {
+  h ^= h >> 16;
+  h *= 0x7FEB352Du;
+  h ^= h >> 15;
+  h *= 0x846CA68Bu;
+  return h ^ (h >> 16);
+}
+constexpr uint32_t kGolden = 0x9E3779B9u;
+
+// b^t by squaring, t >= 0.
+__host__ __device__ __forceinline__ double int_pow(double b, int64_t t) {
+  double r = 1.0;
+  for (; t > 0; t >>= 1) {
+    if (t & 1) r *= b;
+    b *= b;
+  }
+  return r;
+}
+
+__device__ __forceinline__ float scale_of(uint32_t byte) {
+  return __uint_as_float(byte == 255 ? 0x7FC00000u : (byte == 0 ? 0x00400000u : byte << 23));
+}
+
+// Eight E4M3 codes times their block's power of two.
+__device__ __forceinline__ void decode8(uint2 q, uint32_t byte, float (&x)[kPer]) {
+  typedef float f2 __attribute__((ext_vector_type(2)));
+  const float s = scale_of(byte);
+  const f2 a = __builtin_amdgcn_cvt_pk_f32_fp8(static_cast<int>(q.x), false), b = __builtin_amdgcn_cvt_pk_f32_fp8(static_cast<int>(q.x), true);
+  const f2 c = __builtin_amdgcn_cvt_pk_f32_fp8(static_cast<int>(q.y), false), d = __builtin_amdgcn_cvt_pk_f32_fp8(static_cast<int>(q.y), true);
+  x[0] = a[0] * s; x[1] = a[1] * s; x[2] = b[0] * s; x[3] = b[1] * s;
+  x[4] = c[0] * s; x[5] = c[1] * s; x[6] = d[0] * s; x[7] = d[1] * s;
+}
+
+// The E4M3 code of y in [0, 448] with the random number (r + 1/2) / 2^16, by 64 bits.
+__device__ __forceinline__ uint32_t code64(double y, uint32_t r) {
+  uint32_t c;
+  if (y < 0x1p-6) {
+    c = static_cast<uint32_t>(y * 512.0 + (r + 0.5) * 0x1p-16);
+  } else {
+    const uint64_t b = static_cast<uint64_t>(__double_as_longlong(y)) + (static_cast<uint64_t>(16 * r + 8) << 29);
+    c = static_cast<uint32_t>(b >> 49) - (1016u << 3);
+  }
+  return c < 126u ? c : 126u;
+}
+
+// The codes of a lane's eight values under their block's scale, which comes out
+// as its byte: the power of two that puts the block's largest value into
+// (224, 448], so that it is never cut.  Scaled by a further 2^-120 a value has
+// its code in the float's top bits, subnormal codes as subnormal floats, and the
+// random number is added below them.  Blocks with an infinity or a NaN get the
+// byte 255, which reads as NaN.  ROOT: values above zero get a code above zero.
+//
+// Values within 4 units of fp32 (kNear) of where the code or the scale changes
+// are decided by exact(j), the j-th value in 64 bits: 8 in 2^20 are, and the codes
+// are those of the formula, whatever the order of its operations.
+constexpr uint32_t kNear = 4;
+template <bool ROOT, class F>
+__device__ __forceinline__ uint2 encode8(const float (&x)[kPer], const uint32_t (&h)[kPer], uint32_t& byte, F&& exact) {
+  auto quad_max = [](uint32_t v) {
+    v = max(v, static_cast<uint32_t>(__builtin_amdgcn_mov_dpp(static_cast<int>(v), 0xB1, 0xF, 0xF, true)));  // lane ^ 1
+    return max(v, static_cast<uint32_t>(__builtin_amdgcn_mov_dpp(static_cast<int>(v), 0x4E, 0xF, 0xF, true)));  // lane ^ 2
+  };
+  uint32_t top = 0;
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) top = max(top, __float_as_uint(x[i]) & 0x7FFFFFFFu);
+  top = quad_max(top);
+  const bool finite = top < 0x7F800000u;
+  uint32_t above = (top & 0x7FFFFFu) > 0x600000u ? 1u : 0u;  // 1.75 times a power of two
+  if (finite && ((top + kNear - 0x600000u) & 0x7FFFFFu) < 2 * kNear) {
+    const double edge = static_cast<double>(__uint_as_float((top & 0x7F800000u) | 0x600000u));
+    above = 0;
+    for (int i = 0; i < kPer; ++i) {
+      const uint32_t b = __float_as_uint(x[i]) & 0x7FFFFFFFu;
+      if (b + 2 * kNear > top && fabs(exact(i)) > edge) above = 1;
+    }
+    above = quad_max(above);
+  }
+  const int e = static_cast<int>(top >> 23) - 8 + static_cast<int>(above);
+  byte = finite ? (e > 0 ? e : 0) : 255;
+  const float inv = __uint_as_float((254u - (finite ? byte : 0u)) << 23);
+  uint32_t code[kPer], near = 0;
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) {
+    const float y = fabsf(x[i]) * inv * 0x1p-120f;
+    const uint32_t r = ROOT ? (h[i] << 4 & 0xFFFF0u) : (h[i] >> 12 & 0xFFFF0u);
+    const uint32_t t = __float_as_uint(y) + r + 8u;
+    near |= ((t + kNear) & 0xFFFFFu) < 2 * kNear ? 1u << i : 0u;
+    code[i] = t >> 20 < 126u ? t >> 20 : 126u;
+  }
+  if (near && finite) {
+#pragma unroll
+    for (int i = 0; i < kPer; ++i)
+      if (near >> i & 1) code[i] = code64(fabs(exact(i)) * static_cast<double>(inv), ROOT ? h[i] & 0xFFFFu : h[i] >> 16);
+  }
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) {
+    if (ROOT) code[i] = code[i] == 0 && x[i] > 0.f ? 1u : code[i];
+    else code[i] |= __float_as_uint(x[i]) >> 24 & 0x80u;
+    code[i] = finite ? code[i] : 0u;
+  }
+  return make_uint2(code[0] | code[1] << 8 | code[2] << 16 | code[3] << 24,
+                    code[4] | code[5] << 8 | code[6] << 16 | code[7] << 24);
+}
+
+__device__ __forceinline__ float decode1(const void* q, const uint8_t* scale, int64_t i) {
+  return __builtin_amdgcn_cvt_f32_fp8(static_cast<const uint8_t*>(q)[i], 0) * scale_of(scale[i >> 5]);
+}
+
+template <class T>
+__device__ __forceinline__ void load8(const T* p, int64_t i, int valid, float (&x)[kPer]) {
+  if (valid == kPer) {
+#pragma unroll
+    for (int u = 0; u < kPer; u += Elem<T>::kVec) Elem<T>::unpack(*reinterpret_cast<const uint4*>(p + i + u), x + u);
+  } else {
+#pragma unroll
+    for (int u = 0; u < kPer; ++u) x[u] = u < valid ? Elem<T>::load1(p, i + u) : 0.f;
+  }
+}
+template <class T>
+__device__ __forceinline__ void store8(T* p, int64_t i, int valid, const float (&x)[kPer]) {
+  if (valid == kPer) {
+#pragma unroll
+    for (int u = 0; u < kPer; u += Elem<T>::kVec) *reinterpret_cast<uint4*>(p + i + u) = Elem<T>::pack(x + u);
+  } else {
+#pragma unroll
+    for (int u = 0; u < kPer; ++u)
+      if (u < valid) Elem<T>::store1(p, i + u, x[u]);
+  }
+}
+
+// T: weights and gradients (float, or uint16_t for bf16).  States are whole
+// blocks of 32: what lies behind a tensor's end in its last block is zero.
+template <class T, bool EIGHT, bool MASTER>
+__global__ __launch_bounds__(kThreads) void adamw_kernel(AdamArgs p) {
+  const int b = blockIdx.x;
+  int lo = 0, hi = p.count;  // first[lo] <= b < first[hi]
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (p.first[mid] <= b) lo = mid;
+    else hi = mid;
+  }
+  const ListEntry& t = p.list[lo];
+  const int64_t n = t.n, base = static_cast<int64_t>(b - p.first[lo]) * kUnit;
+  const int64_t step = p.step_dev ? *p.step_dev : p.step;
+  const float b1 = static_cast<float>(p.beta1), b2 = static_cast<float>(p.beta2);
+  const float a1 = static_cast<float>(1.0 - p.beta1), a2 = static_cast<float>(1.0 - p.beta2);
+  const float b1_low = static_cast<float>(p.beta1 - b1), a1_low = static_cast<float>(1.0 - p.beta1 - a1);
+  const float rate = static_cast<float>(t.lr / (1.0 - int_pow(p.beta1, step)));
+  const float root2 = static_cast<float>(1.0 / sqrt(1.0 - int_pow(p.beta2, step)));
+  const float gs = p.gscale ? *p.gscale : 1.0f;
+  const uint32_t key = mix(mix(t.seed) + kGolden * static_cast<uint32_t>(step));
+
+  for (int u = 0; u < kTurns; ++u) {
+    const int64_t i = base + (u * kThreads + static_cast<int>(threadIdx.x)) * kPer;
+    if (i >= ((n + 31) & ~int64_t{31})) break;
+    const int valid = n - i >= kPer ? kPer : (n > i ? static_cast<int>(n - i) : 0);
+    const int64_t o = t.offset + i;
+    float w[kPer], g[kPer], m[kPer], v[kPer];
+    if constexpr (MASTER) load8(p.master, o, kPer, w);
+    else load8(static_cast<const T*>(t.w), i, valid, w);
+    load8(static_cast<const T*>(t.g), i, valid, g);
+    if constexpr (EIGHT) {
+      decode8(*reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(p.m) + o), p.m_scale[o >> 5], m);
+      decode8(*reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(p.v) + o), p.v_scale[o >> 5], v);
+    } else {
+      load8(static_cast<const float*>(p.m), o, kPer, m);
+      load8(static_cast<const float*>(p.v), o, kPer, v);
+    }
+#pragma unroll
+    for (int j = 0; j < kPer; ++j) {
+      const float gg = g[j] * gs;
+      if constexpr (EIGHT) {
+        // m's terms can cancel; their roundings (and those of the constants) are added up beside them, so that the sum
+        // is within a unit of the formula's and the code that it gets can be told
+        const float t = a1 * gg;
+        float low = fmaf(a1, gg, -t);
+        low = fmaf(a1, fmaf(g[j], gs, -gg), low);
+        low = fmaf(a1_low, gg, low);
+        low = fmaf(b1_low, m[j], low);
+        m[j] = fmaf(b1, m[j], t) + low;
+        v[j] *= v[j];
+      } else {
+        m[j] = b1 * m[j] + a1 * gg;
+      }
+      v[j] = b2 * v[j] + a2 * gg * gg;
+      const float root = sqrtf(v[j]);
+      if (EIGHT) v[j] = root;
+      w[j] = t.keep * w[j] - rate * (m[j] / (root * root2 + p.eps));
+    }
+    // behind the tensor's end (its gradient reads as zero) states and master stay what they are made of: zero
+    if (valid < kPer) {
+#pragma unroll
+      for (int j = 0; j < kPer; ++j)
+        if (j >= valid) m[j] = v[j] = w[j] = 0.f;
+    }
+    store8(static_cast<T*>(t.w_out), i, valid, w);
+    if constexpr (MASTER) store8(p.master_out, o, kPer, w);
+    if constexpr (EIGHT) {
+      uint32_t h[kPer], bm, bv;
+#pragma unroll
+      for (int j = 0; j < kPer; ++j) h[j] = mix((static_cast<uint32_t>(i) + j) * kGolden + key);
+      // one value again in 64 bits, from what is still in memory (outputs may be in its place, stored below)
+      auto grad = [&](int j) { return j < valid ? static_cast<double>(Elem<T>::load1(t.g, i + j)) * gs : 0.0; };
+      const uint2 qm = encode8<false>(m, h, bm, [&](int j) {
+        return p.beta1 * decode1(p.m, p.m_scale, o + j) + (1.0 - p.beta1) * grad(j);
+      });
+      const uint2 qv = encode8<true>(v, h, bv, [&](int j) {
+        const double root = decode1(p.v, p.v_scale, o + j), gg = grad(j);
+        return sqrt(p.beta2 * root * root + (1.0 - p.beta2) * gg * gg);
+      });
+      *reinterpret_cast<uint2*>(static_cast<uint8_t*>(p.m_out) + o) = qm;
+      *reinterpret_cast<uint2*>(static_cast<uint8_t*>(p.v_out) + o) = qv;
+      if ((threadIdx.x & 3) == 0) {
+        p.m_scale_out[o >> 5] = static_cast<uint8_t>(bm);
+        p.v_scale_out[o >> 5] = static_cast<uint8_t>(bv);
+      }
+    } else {
+      store8(static_cast<float*>(p.m_out), o, kPer, m);
+      store8(static_cast<float*>(p.v_out), o, kPer, v);
+    }
+  }
+}
+
+// The values of 8-bit states in bf16, which holds them exactly (four bits times a power of two).
+__global__ __launch_bounds__(kThreads) void state_values_kernel(const uint8_t* __restrict__ q,
+                                                                const uint8_t* __restrict__ scale, int64_t n,
+                                                                uint16_t* __restrict__ out) {
+  const int64_t i = (static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x) * kPer;
+  if (i >= n) return;
+  float x[kPer];
+  decode8(*reinterpret_cast<const uint2*>(q + i), scale[i >> 5], x);
+  *reinterpret_cast<uint4*>(out + i) = Elem<uint16_t>::pack(x);
+}
+
+int64_t pad32(int64_t n) { return (n + 31) & ~int64_t{31}; }
+
+}  // namespace
+}  // namespace moe
+
+using namespace moe;
+
+extern "C" int moe_adamw_step(const moe_adamw_tensor* tensors, int32_t count, int dtype, int bits, int64_t state_len,
+                              const void* m, const void* v, const uint8_t* m_scale, const uint8_t* v_scale,
+                              const float* master, double lr, double beta1, double beta2, double eps, int64_t step,
+                              const int64_t* step_dev, const float* grad_scale, uint32_t seed, void* m_out, void* v_out,
+                              uint8_t* m_scale_out, uint8_t* v_scale_out, float* master_out, void* stream) {
+  if (count < 0 || (dtype != MOE_F32 && dtype != MOE_BF16) || (bits != 32 && bits != 8) || state_len < 0) return MOE_EINVAL;
+  if (!(beta1 >= 0.0 && beta1 < 1.0) || !(beta2 >= 0.0 && beta2 < 1.0) || !(eps >= 0.0) || !std::isfinite(eps) ||
+      !std::isfinite(lr) || (!step_dev && step < 1))
+    return MOE_EINVAL;
+  if (!std::isfinite(static_cast<float>(eps)) || !std::isfinite(static_cast<float>(lr))) return MOE_EINVAL;
+  if (dtype == MOE_F32 && (master || master_out)) return MOE_EINVAL;
+  if (!master != !master_out) return MOE_EINVAL;
+  if (count == 0) return MOE_OK;
+  if (!tensors || !m || !v || !m_out || !v_out) return MOE_EINVAL;
+  if (bits == 8 && (!m_scale || !v_scale || !m_scale_out || !v_scale_out)) return MOE_EINVAL;
+  for (const void* q : {m, v, static_cast<const void*>(m_scale), static_cast<const void*>(v_scale),
+                        static_cast<const void*>(master), static_cast<const void*>(step_dev),
+                        static_cast<const void*>(grad_scale), static_cast<const void*>(m_out),
+                        static_cast<const void*>(v_out), static_cast<const void*>(m_scale_out),
+                        static_cast<const void*>(v_scale_out), static_cast<const void*>(master_out)})
+    if (!aligned16(q)) return MOE_EINVAL;
+  int64_t end = 0;
+  for (int32_t i = 0; i < count; ++i) {
+    const moe_adamw_tensor& t = tensors[i];
+    if (t.n < 0 || t.offset < end || t.offset % 32 || t.offset > state_len || pad32(t.n) > state_len - t.offset)
+      return MOE_EINVAL;
+    if (t.n > 0 && (!t.w || !t.g || !t.w_out)) return MOE_EINVAL;
+    if (!aligned16(t.w) || !aligned16(t.g) || !aligned16(t.w_out)) return MOE_EINVAL;
+    if (!std::isfinite(t.weight_decay) || !std::isfinite(t.lr_scale) || !std::isfinite(static_cast<float>(lr * t.lr_scale)) ||
+        !std::isfinite(static_cast<float>(lr * t.lr_scale * t.weight_decay)))
+      return MOE_EINVAL;
+    if (cdiv(t.n, kUnit) >= kMaxUnits) return MOE_EUNSUPPORTED;
+    end = t.offset + pad32(t.n);
+  }
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  AdamArgs a;
+  a.m = m; a.v = v; a.m_scale = m_scale; a.v_scale = v_scale; a.master = master;
+  a.m_out = m_out; a.v_out = v_out; a.m_scale_out = m_scale_out; a.v_scale_out = v_scale_out; a.master_out = master_out;
+  a.beta1 = beta1; a.beta2 = beta2; a.eps = static_cast<float>(eps);
+  a.step = step; a.step_dev = step_dev; a.gscale = grad_scale;
+  for (int32_t i = 0; i < count;) {
+    a.count = 0;
+    int64_t units = 0;
+    for (; i < count && a.count < kMaxList; ++i) {
+      const moe_adamw_tensor& t = tensors[i];
+      const int64_t more = cdiv(t.n, kUnit);
+      if (more == 0) continue;
+      if (units + more >= kMaxUnits) break;
+      const double rate = lr * t.lr_scale;
+      a.list[a.count] = ListEntry{t.w, t.g, t.w_out, t.n, t.offset, rate,
+                                  static_cast<float>(1.0 - rate * t.weight_decay), seed + kGolden * static_cast<uint32_t>(i)};
+      a.first[a.count++] = static_cast<int32_t>(units);
+      units += more;
+    }
+    if (a.count == 0) break;
+    a.first[a.count] = static_cast<int32_t>(units);
+    const dim3 grid(static_cast<unsigned>(units)), block(kThreads);
+    if (dtype == MOE_F32) {
+      if (bits == 8) MOE_LAUNCH("adamw", (adamw_kernel<float, true, false>), grid, block, 0, s, a);
+      else MOE_LAUNCH("adamw", (adamw_kernel<float, false, false>), grid, block, 0, s, a);
+    } else if (master) {
+      if (bits == 8) MOE_LAUNCH("adamw", (adamw_kernel<uint16_t, true, true>), grid, block, 0, s, a);
+      else MOE_LAUNCH("adamw", (adamw_kernel<uint16_t, false, true>), grid, block, 0, s, a);
+    } else {
+      if (bits == 8) MOE_LAUNCH("adamw", (adamw_kernel<uint16_t, true, false>), grid, block, 0, s, a);
+      else MOE_LAUNCH("adamw", (adamw_kernel<uint16_t, false, false>), grid, block, 0, s, a);
+    }
+    const int st = launch_status();
+    if (st != MOE_OK) return st;
+  }
+  return MOE_OK;
+}
+
+extern "C" int moe_adamw_state_values(const uint8_t* codes, const uint8_t* scale, int64_t state_len, void* values,
+                                      void* stream) {
+  if (state_len < 0 || state_len % 32) return MOE_EINVAL;
+  if (state_len == 0) return MOE_OK;
+  if (!codes || !scale || !values || !aligned16(codes) || !aligned16(scale) || !aligned16(values)) return MOE_EINVAL;
+  if (cdiv(state_len, kThreads * kPer) >= kMaxUnits) return MOE_EUNSUPPORTED;
+  MOE_LAUNCH("adamw_state_values", state_values_kernel, dim3(static_cast<unsigned>(cdiv(state_len, kThreads * kPer))),
+             dim3(kThreads), 0, static_cast<hipStream_t>(stream), codes, scale, state_len, static_cast<uint16_t*>(values));
+  return launch_status();
+}

@@ -1,0 +1,713 @@
+// Dense product with bias, activation and residual in its epilogue, and its
+// backward: the shared expert beside the routed ones.
+//
+//   forward   z = x W + bias,  y = act(z) + residual
+//   backward  dz = dy act'(z)  (one pass, which also sums db by row chunks),
+//             dx = (dz W^T) in_act'(in_z) + dres,  dw = x^T dz
+//
+// bf16 runs on v_mfma_f32_32x32x16_bf16 with the tiles of the grouped expert
+// products: operands go from global memory straight into LDS rings and are read
+// from there as they lie, contiguous along the contraction or along their rows or
+// columns, so that no operand is transposed.  fp32 runs on v_mfma_f32_32x32x2_f32
+// with tiles staged through registers, for any size and alignment.
+//
+// 16-byte loads need rows of whole 16 bytes: a bf16 operand with an odd row
+// length is first copied into the workspace with padded rows (zeros behind).
+//
+// Few output tiles leave compute units idle; then the contraction is split over
+// workgroups, which write fp32 sums, and a second launch adds them in order and
+// applies the epilogue.
+#include "gemm_bf16_tile.hpp"
+
+namespace moe {
+namespace {
+using namespace gemm;
+
+constexpr int kCUs = 256;
+constexpr int64_t kMaxWidth = 1 << 20;
+
+enum { kActNone = MOE_ACT_NONE, kActRelu = MOE_ACT_RELU, kActSilu = MOE_ACT_SILU, kActGelu = MOE_ACT_GELU };
+
+__device__ __forceinline__ float act_f(float z, int act) {
+  switch (act) {
+    case kActRelu: return z > 0.f || z != z ? z : 0.f;
+    case kActSilu: return silu_f(z);
+    case kActGelu: return 0.5f * z * erfcf(-0.70710678f * z);
+    default: return z;
+  }
+}
+__device__ __forceinline__ float dact_f(float z, int act) {
+  switch (act) {
+    case kActRelu: return z > 0.f ? 1.f : 0.f;
+    case kActSilu: {
+      const float s = sigmoid_f(z);
+      return s * (1.0f + z * (1.0f - s));
+    }
+    case kActGelu: return 0.5f * erfcf(-0.70710678f * z) + z * 0.39894228f * __expf(-0.5f * z * z);
+    default: return 1.f;
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Eight consecutive columns of a row: the whole epilogue.
+// ---------------------------------------------------------------------------
+struct Epilogue {
+  const void* bias;  // [cols]
+  void* z;           // the pre-activation, kept for the backward
+  const void* in_z;  // times in_act'(in_z)
+  const void* add;   // residual or dres
+  void* out;
+  int act, in_act;
+  int64_t ld;        // of all of them: the number of columns
+};
+
+template <class T>
+__device__ __forceinline__ void read8(const void* p, int64_t i, int valid, bool vec, float (&x)[8]) {
+  const T* q = static_cast<const T*>(p) + i;
+  if (vec) {
+#pragma unroll
+    for (int u = 0; u < 8; u += Elem<T>::kVec) Elem<T>::unpack(*reinterpret_cast<const uint4*>(q + u), x + u);
+  } else {
+#pragma unroll
+    for (int u = 0; u < 8; ++u) x[u] = u < valid ? Elem<T>::load1(q, u) : 0.f;
+  }
+}
+template <class T>
+__device__ __forceinline__ void write8(void* p, int64_t i, int valid, bool vec, const float (&x)[8]) {
+  T* q = static_cast<T*>(p) + i;
+  if (vec) {
+#pragma unroll
+    for (int u = 0; u < 8; u += Elem<T>::kVec) *reinterpret_cast<uint4*>(q + u) = Elem<T>::pack(x + u);
+  } else {
+#pragma unroll
+    for (int u = 0; u < 8; ++u)
+      if (u < valid) Elem<T>::store1(q, u, x[u]);
+  }
+}
+
+template <class T>
+__device__ __forceinline__ void apply8(const Epilogue& e, int64_t row, int col, float (&v)[8]) {
+  const int valid = e.ld - col < 8 ? static_cast<int>(e.ld - col) : 8;
+  const bool vec = valid == 8 && e.ld % Elem<T>::kVec == 0;
+  const int64_t o = row * e.ld + col;
+  float u[8];
+  if (e.bias) {
+    read8<T>(e.bias, col, valid, valid == 8, u);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] += u[i];
+  }
+  if (e.z) write8<T>(e.z, o, valid, vec, v);
+  if (e.act != kActNone) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = act_f(v[i], e.act);
+  }
+  if (e.in_act != kActNone) {
+    read8<T>(e.in_z, o, valid, vec, u);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] *= dact_f(u[i], e.in_act);
+  }
+  if (e.add) {
+    read8<T>(e.add, o, valid, vec, u);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] += u[i];
+  }
+  write8<T>(e.out, o, valid, vec, v);
+}
+
+// One product: out [rows, cols] = A B over `depth`, A(row, k), B(k, col).
+struct Product {
+  const void* a;
+  const void* b;
+  int64_t lda, ldb;
+  int64_t rows;
+  int cols;
+  int64_t depth;
+  int gm, gn;        // tiles
+  int splits;        // workgroups that share a tile's contraction
+  int64_t per_split; // contraction of one of them, whole K steps
+  float* part;       // [splits][rows][part_ld] where splits > 1
+  int64_t part_ld;
+  Epilogue epi;
+};
+
+constexpr int kGroupRows = 4;  // row tiles taken together, column tile by column tile
+
+// Tile of workgroup id: XCDs take contiguous ranges, and inside a range
+// neighbours share row or column operands in one L2.
+__device__ __forceinline__ bool product_tile(const Product& p, int64_t id, int& mt, int& nt, int& split) {
+  const int64_t lid = xcd_tile(id, static_cast<int64_t>(p.gm) * p.gn * p.splits);
+  if (lid < 0) return false;
+  const int64_t tiles = static_cast<int64_t>(p.gm) * p.gn;
+  split = static_cast<int>(lid / tiles);
+  const int64_t t = lid - split * tiles;
+  const int64_t band = t / (static_cast<int64_t>(kGroupRows) * p.gn);
+  const int m0 = static_cast<int>(band) * kGroupRows;
+  const int h = p.gm - m0 < kGroupRows ? p.gm - m0 : kGroupRows;
+  const int64_t r = t - band * kGroupRows * p.gn;
+  nt = static_cast<int>(r / h);
+  mt = m0 + static_cast<int>(r - static_cast<int64_t>(nt) * h);
+  return true;
+}
+
+// The accumulators of a wave (tiles computed transposed): runs of eight columns
+// through the epilogue, or as fp32 sums where the contraction is split.
+template <class T, class C>
+__device__ __forceinline__ void finish(const Acc<C>& acc, const Product& p, int64_t row0, int col0, int split, int lane,
+                                       int wm, int wn) {
+  const int rl = lane & 31, hc = 8 * (lane >> 5);
+#pragma unroll
+  for (int i = 0; i < C::TM; ++i) {
+    const int64_t row = row0 + wm * C::WTM + i * 32 + rl;
+#pragma unroll
+    for (int j = 0; j < C::TN; ++j) {
+      float v[2][8];
+      to_chunks(acc[i][j], v);
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        const int col = col0 + wn * C::WTN + j * 32 + 16 * c + hc;
+        if (row < p.rows && col < p.cols) {
+          if (p.splits > 1) {
+            float* q = p.part + (split * p.rows + row) * p.part_ld + col;
+            *reinterpret_cast<float4*>(q) = make_float4(v[c][0], v[c][1], v[c][2], v[c][3]);
+            *reinterpret_cast<float4*>(q + 4) = make_float4(v[c][4], v[c][5], v[c][6], v[c][7]);
+          } else {
+            apply8<T>(p.epi, row, col, v[c]);
+          }
+        }
+      }
+    }
+  }
+}
+
+// ---------------------------------------------------------------------------
+// bf16
+// ---------------------------------------------------------------------------
+using Wide = Cfg<256, 256, 2, 4, 64, 2, 2, 1, true>;   // one workgroup per CU
+using Narrow = Cfg<128, 128, 2, 2, 64, 2, 2, 1, true>; // two
+
+// One K step of an operand contiguous along the contraction; rows past the
+// last one and chunks past the contraction's end read as zero.
+template <class C, int ROWS>
+__device__ __forceinline__ void load_kc(const uint16_t* base, int64_t ld, int rows, int k0, int k_end, uint16_t* dst,
+                                        int wave, int lane) {
+  constexpr int CPR = C::BK / 8, RPI = 64 / CPR, NI = ROWS / RPI;
+  static_assert(NI % C::kWaves == 0, "tile rows over the waves");
+  const __amdgpu_buffer_rsrc_t r = rsrc(base, static_cast<int64_t>(rows < ROWS ? rows : ROWS) * ld * 2);
+  const int rl = lane / CPR, ph = lane % CPR;
+#pragma unroll
+  for (int u = 0; u < NI / C::kWaves; ++u) {
+    const int i = wave + u * C::kWaves;
+    const int row = i * RPI + rl;
+    const int k = k0 + (ph ^ kc_swz<C::BK>(row)) * 8;
+    dma16(r, dst + i * 512, k < k_end ? static_cast<int>((row * ld + k) * 2) : 0x7FFFFFF0);
+  }
+}
+
+template <class C, bool AKC, bool BKC>
+__global__ __launch_bounds__(C::kThreads) __attribute__((amdgpu_waves_per_eu(C::kWavesPerSimd)))
+void linear_bf16_kernel(Product p) {
+  __shared__ __attribute__((aligned(16))) uint16_t lds[C::kLds];
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int wm = wave / C::WN, wn = wave % C::WN;
+  int mt, nt, split;
+  if (!product_tile(p, blockIdx.x, mt, nt, split)) return;
+  mt = __builtin_amdgcn_readfirstlane(mt);
+  nt = __builtin_amdgcn_readfirstlane(nt);
+  split = __builtin_amdgcn_readfirstlane(split);
+  const int64_t row0 = static_cast<int64_t>(mt) * C::BM;
+  const int col0 = nt * C::BN;
+  const int64_t k0 = split * p.per_split;
+  const int64_t len = p.depth - k0 < p.per_split ? p.depth - k0 : p.per_split;
+  const int nk = static_cast<int>((len + C::BK - 1) / C::BK);
+  const uint16_t* A = static_cast<const uint16_t*>(p.a);
+  const uint16_t* B = static_cast<const uint16_t*>(p.b);
+  const int rows = static_cast<int>(p.rows - row0 < C::BM ? p.rows - row0 : C::BM);
+  const int cols = p.cols - col0 < C::BN ? p.cols - col0 : C::BN;
+
+  auto load_a = [&](int kt) {
+    uint16_t* st = lds + (kt & 1) * C::kA;
+    if constexpr (AKC)
+      load_kc<C, C::BM>(A + row0 * p.lda, p.lda, rows, static_cast<int>(k0) + kt * C::BK, static_cast<int>(p.depth), st, wave, lane);
+    else
+      dma_mc<C, C::BM, 1>(McOp{A + k0 * p.lda, nullptr, p.lda, static_cast<int>(row0), static_cast<int>(len)}, kt * C::BK,
+                          st, wave, lane);
+  };
+  auto load_b = [&](int kt) {
+    uint16_t* st = lds + C::kBOff + (kt & 1) * C::kB;
+    if constexpr (BKC)
+      load_kc<C, C::BN>(B + col0 * p.ldb, p.ldb, cols, static_cast<int>(k0) + kt * C::BK, static_cast<int>(p.depth), st, wave, lane);
+    else
+      dma_mc<C, C::BN, 1>(McOp{B + k0 * p.ldb, nullptr, p.ldb, col0, static_cast<int>(len)}, kt * C::BK, st, wave, lane);
+  };
+
+  Acc<C> acc;
+#pragma unroll
+  for (int i = 0; i < C::TM; ++i)
+#pragma unroll
+    for (int j = 0; j < C::TN; ++j)
+#pragma unroll
+      for (int r = 0; r < 16; ++r) acc[i][j][r] = 0.f;
+  load_a(0);
+  load_b(0);
+  for (int kt = 0; kt < nk; ++kt) {
+    wait_vm<0>();
+    __syncthreads();
+    const uint16_t* As = lds + (kt & 1) * C::kA;
+    const uint16_t* Bs = lds + C::kBOff + (kt & 1) * C::kB;
+    const bool more = kt + 1 < nk;
+#pragma unroll
+    for (int ks = 0; ks < C::BK / 16; ++ks) {
+      if (more && ks == 0) load_a(kt + 1);
+      if (more && ks == 1) load_b(kt + 1);
+      bf16x8 a[C::TM], b[C::TN];
+#pragma unroll
+      for (int i = 0; i < C::TM; ++i)
+        a[i] = AKC ? frag_kc<C>(As, wm * C::WTM + i * 32, ks, lane) : frag_mc<C, C::BM>(As, wm * C::WTM + i * 32, ks, lane);
+#pragma unroll
+      for (int j = 0; j < C::TN; ++j)
+        b[j] = BKC ? frag_kc<C>(Bs, wn * C::WTN + j * 32, ks, lane) : frag_mc<C, C::BN>(Bs, wn * C::WTN + j * 32, ks, lane);
+#pragma unroll
+      for (int i = 0; i < C::TM; ++i)
+#pragma unroll
+        for (int j = 0; j < C::TN; ++j) acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(b[j], a[i], acc[i][j], 0, 0, 0);
+    }
+  }
+  finish<uint16_t, C>(acc, p, row0, col0, split, lane, wm, wn);
+}
+
+// ---------------------------------------------------------------------------
+// fp32: 128 x 128 tiles, four waves of 64 x 64, K step 16, both operands in LDS
+// with the contraction along the rows.  The next step's values are on their way
+// into registers while a step is multiplied.
+// ---------------------------------------------------------------------------
+struct Tile32 {
+  static constexpr int BM = 128, BN = 128, BK = 16, WN = 2, kThreads = 256;
+  static constexpr int WTM = 64, WTN = 64, TM = 2, TN = 2;
+  static constexpr int kLd = BM + 4;
+};
+
+// This thread's 8 values of a BK x 128 tile.  KC: element (i, k) at p[i ld + k],
+// else at p[k ld + i]; i < n and k < k_end, zero outside.
+template <bool KC>
+__device__ __forceinline__ void fetch32(const float* p, int64_t ld, int n, int64_t k0, int64_t k_end, bool vec, int tid,
+                                        float (&v)[2][4]) {
+#pragma unroll
+  for (int u = 0; u < 2; ++u) {
+    const int id = tid + u * Tile32::kThreads;
+    const int i = KC ? id >> 2 : (id & 31) * 4;
+    const int64_t k = k0 + (KC ? (id & 3) * 4 : id >> 5);
+    const float* q = KC ? p + i * ld + k : p + k * ld + i;
+    const bool whole = KC ? (i < n && k + 3 < k_end) : (i + 3 < n && k < k_end);
+    if (vec && whole) {
+      const float4 f = *reinterpret_cast<const float4*>(q);
+      v[u][0] = f.x; v[u][1] = f.y; v[u][2] = f.z; v[u][3] = f.w;
+    } else {
+#pragma unroll
+      for (int s = 0; s < 4; ++s) {
+        const bool ok = KC ? (i < n && k + s < k_end) : (i + s < n && k < k_end);
+        v[u][s] = ok ? q[s] : 0.f;
+      }
+    }
+  }
+}
+template <bool KC>
+__device__ __forceinline__ void place32(float* t, int tid, const float (&v)[2][4]) {
+#pragma unroll
+  for (int u = 0; u < 2; ++u) {
+    const int id = tid + u * Tile32::kThreads;
+    if constexpr (KC) {
+#pragma unroll
+      for (int s = 0; s < 4; ++s) t[((id & 3) * 4 + s) * Tile32::kLd + (id >> 2)] = v[u][s];
+    } else {
+      *reinterpret_cast<float4*>(t + (id >> 5) * Tile32::kLd + (id & 31) * 4) = make_float4(v[u][0], v[u][1], v[u][2], v[u][3]);
+    }
+  }
+}
+
+template <bool AKC, bool BKC>
+__global__ __launch_bounds__(Tile32::kThreads) void linear_f32_kernel(Product p) {
+  using C = Tile32;
+  __shared__ __attribute__((aligned(16))) float lds[2][2][C::BK * C::kLd];
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int wm = wave / C::WN, wn = wave % C::WN;
+  int mt, nt, split;
+  if (!product_tile(p, blockIdx.x, mt, nt, split)) return;
+  const int64_t row0 = static_cast<int64_t>(mt) * C::BM;
+  const int col0 = nt * C::BN;
+  const int64_t k0 = split * p.per_split;
+  const int64_t k_end = p.depth - k0 < p.per_split ? p.depth : k0 + p.per_split;
+  const int nk = static_cast<int>((k_end - k0 + C::BK - 1) / C::BK);
+  const float* A = static_cast<const float*>(p.a) + (AKC ? row0 * p.lda : row0);
+  const float* B = static_cast<const float*>(p.b) + (BKC ? col0 * p.ldb : col0);
+  const int rows = static_cast<int>(p.rows - row0 < C::BM ? p.rows - row0 : C::BM);
+  const int cols = p.cols - col0 < C::BN ? p.cols - col0 : C::BN;
+  const bool va = p.lda % 4 == 0, vb = p.ldb % 4 == 0;
+
+  Acc<C> acc;
+#pragma unroll
+  for (int i = 0; i < C::TM; ++i)
+#pragma unroll
+    for (int j = 0; j < C::TN; ++j)
+#pragma unroll
+      for (int r = 0; r < 16; ++r) acc[i][j][r] = 0.f;
+  float fa[2][4], fb[2][4];
+  fetch32<AKC>(A, p.lda, rows, k0, k_end, va, tid, fa);
+  fetch32<BKC>(B, p.ldb, cols, k0, k_end, vb, tid, fb);
+  for (int kt = 0; kt < nk; ++kt) {
+    float* As = lds[kt & 1][0];
+    float* Bs = lds[kt & 1][1];
+    place32<AKC>(As, tid, fa);
+    place32<BKC>(Bs, tid, fb);
+    __syncthreads();  // also: every wave is past the step before last, whose stage this was
+    if (kt + 1 < nk) {
+      fetch32<AKC>(A, p.lda, rows, k0 + (kt + 1) * C::BK, k_end, va, tid, fa);
+      fetch32<BKC>(B, p.ldb, cols, k0 + (kt + 1) * C::BK, k_end, vb, tid, fb);
+    }
+#pragma unroll
+    for (int k = 0; k < C::BK; k += 2) {
+      const int kr = (k + (lane >> 5)) * C::kLd + (lane & 31);
+      float a[C::TM], b[C::TN];
+#pragma unroll
+      for (int i = 0; i < C::TM; ++i) a[i] = As[kr + wm * C::WTM + i * 32];
+#pragma unroll
+      for (int j = 0; j < C::TN; ++j) b[j] = Bs[kr + wn * C::WTN + j * 32];
+#pragma unroll
+      for (int i = 0; i < C::TM; ++i)
+#pragma unroll
+        for (int j = 0; j < C::TN; ++j) acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x2f32(b[j], a[i], acc[i][j], 0, 0, 0);
+    }
+  }
+  finish<float, C>(acc, p, row0, col0, split, lane, wm, wn);
+}
+
+// ---------------------------------------------------------------------------
+// The sums of a split contraction, added in order, through the epilogue.
+// ---------------------------------------------------------------------------
+template <class T>
+__global__ __launch_bounds__(256) void linear_join_kernel(Product p) {
+  const int64_t per = p.part_ld / 8;
+  const int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
+  if (i >= p.rows * per) return;
+  const int64_t row = i / per;
+  const int col = static_cast<int>(i - row * per) * 8;
+  float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+  for (int s = 0; s < p.splits; ++s) {
+    const float* q = p.part + (s * p.rows + row) * p.part_ld + col;
+    const float4 a = *reinterpret_cast<const float4*>(q), b = *reinterpret_cast<const float4*>(q + 4);
+    v[0] += a.x; v[1] += a.y; v[2] += a.z; v[3] += a.w;
+    v[4] += b.x; v[5] += b.y; v[6] += b.z; v[7] += b.w;
+  }
+  apply8<T>(p.epi, row, col, v);
+}
+
+// dst [rows, ld] = src [rows, cols], zeros behind (bf16, ld a multiple of 8).
+__global__ __launch_bounds__(256) void pad_rows_kernel(const uint16_t* __restrict__ src, int64_t rows, int cols, int ld,
+                                                       uint16_t* __restrict__ dst) {
+  const int per = ld / 8;
+  const int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
+  if (i >= rows * per) return;
+  const int64_t row = i / per;
+  const int c = static_cast<int>(i - row * per) * 8;
+  uint32_t w[8];
+#pragma unroll
+  for (int u = 0; u < 8; ++u) w[u] = c + u < cols ? src[row * cols + c + u] : 0;
+  *reinterpret_cast<uint4*>(dst + row * ld + c) = make_uint4(w[0] | w[1] << 16, w[2] | w[3] << 16, w[4] | w[5] << 16, w[6] | w[7] << 16);
+}
+
+// ---------------------------------------------------------------------------
+// dz = dy act'(z) and its column sums over chunks of rows.  A workgroup takes a
+// chunk and 512 columns: 64 lanes of eight columns, four rows at a time.
+// ---------------------------------------------------------------------------
+struct DzArgs {
+  const void* dy;
+  const void* z;     // null: no activation
+  int64_t rows, chunk;
+  int cols, ld_dz;
+  int act;
+  void* dz;          // null: not written
+  float* part;       // [chunks][part_ld], null: no sums
+  int64_t part_ld;
+};
+
+template <class T>
+__global__ __launch_bounds__(256) void linear_dz_kernel(DzArgs p) {
+  __shared__ float sums[4][512];
+  const int lane = threadIdx.x & 63, phase = threadIdx.x >> 6;
+  const int col = (blockIdx.x * 64 + lane) * 8;
+  const int64_t r0 = blockIdx.y * p.chunk, r1 = r0 + p.chunk < p.rows ? r0 + p.chunk : p.rows;
+  const int valid = p.cols - col < 8 ? p.cols - col : 8;
+  const bool vec = valid == 8 && p.cols % Elem<T>::kVec == 0;
+  float acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+  if (valid > 0) {
+#pragma unroll 2
+    for (int64_t r = r0 + phase; r < r1; r += 4) {
+      float g[8], z[8];
+      read8<T>(p.dy, r * p.cols + col, valid, vec, g);
+      if (p.z) {
+        read8<T>(p.z, r * p.cols + col, valid, vec, z);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) g[i] *= dact_f(z[i], p.act);
+      }
+      // behind the last column: zeros, as the products need them (ld_dz is a multiple of 8 for bf16)
+      if (p.dz) write8<T>(p.dz, r * p.ld_dz + col, p.ld_dz - col < 8 ? p.ld_dz - col : 8, p.ld_dz % Elem<T>::kVec == 0 && p.ld_dz - col >= 8, g);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) acc[i] += g[i];
+    }
+  }
+  if (!p.part) return;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) sums[phase][lane * 8 + i] = acc[i];
+  __syncthreads();
+  for (int c = threadIdx.x; c < 512; c += 256) {
+    const int64_t at = static_cast<int64_t>(blockIdx.x) * 512 + c;
+    if (at < p.cols) p.part[blockIdx.y * p.part_ld + at] = (sums[0][c] + sums[1][c]) + (sums[2][c] + sums[3][c]);
+  }
+}
+
+// db = the chunks' sums in order: 32 columns by 8 parts of the chunks.
+template <class T>
+__global__ __launch_bounds__(256) void linear_db_kernel(const float* __restrict__ part, int64_t part_ld, int64_t chunks,
+                                                        int cols, T* __restrict__ db) {
+  __shared__ float sums[8][32];
+  const int c = threadIdx.x & 31, ph = threadIdx.x >> 5;
+  const int64_t col = static_cast<int64_t>(blockIdx.x) * 32 + c;
+  float acc = 0.f;
+  if (col < cols)
+    for (int64_t k = ph; k < chunks; k += 8) acc += part[k * part_ld + col];
+  sums[ph][c] = acc;
+  __syncthreads();
+  if (ph == 0 && col < cols) {
+    acc = 0.f;
+    for (int q = 0; q < 8; ++q) acc += sums[q][c];
+    Elem<T>::store1(db, col, acc);
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Host side
+// ---------------------------------------------------------------------------
+int64_t up8(int64_t n) { return (n + 7) & ~int64_t{7}; }
+
+struct Plan {
+  bool wide;
+  int splits;
+  int64_t per_split, part_ld;
+  size_t part_bytes;
+};
+
+// Tile size and split of a product by the estimated time: rounds of workgroups
+// over the chip times their K steps, plus the second launch of a split.
+Plan plan_product(int dtype, int64_t rows, int64_t cols, int64_t depth) {
+  Plan best{};
+  double least = 1e300;
+  const int bk = dtype == MOE_BF16 ? 64 : 16;
+  const int64_t steps = cdiv(depth, bk);
+  for (int wide = 0; wide <= (dtype == MOE_BF16 ? 1 : 0); ++wide) {
+    const int bt = wide ? 256 : 128;
+    const int64_t tiles = cdiv(rows, bt) * cdiv(cols, bt);
+    const double step_us = dtype == MOE_F32 ? 1.7 : wide ? 2.4 : 1.4;
+    const double fixed_us = wide ? 6.0 : 3.0;
+    const int64_t slots = wide ? kCUs : 2 * kCUs;
+    for (int s = 1; s <= 64; s *= 2) {
+      const int64_t per = cdiv(steps, s);
+      if (s > 1 && (per < 2 || cdiv(steps, per) <= s / 2)) break;
+      const double bytes = s > 1 ? (s + 1.0) * rows * cols * 4 : 0;
+      if (bytes > 1.0e9) break;
+      const double t = cdiv(tiles * s, slots) * (per * step_us + fixed_us) + (s > 1 ? 4.0 + bytes / 3.0e6 : 0.0);
+      if (t < least) {
+        least = t;
+        const int n = static_cast<int>(cdiv(steps, per));
+        best = Plan{wide != 0, n, per * bk, up8(cols), n > 1 ? align_up(static_cast<size_t>(n) * rows * up8(cols) * 4, 256) : 0};
+      }
+    }
+  }
+  return best;
+}
+
+template <class T, bool AKC, bool BKC>
+int launch_product(const void* a, int64_t lda, const void* b, int64_t ldb, int64_t rows, int64_t cols, int64_t depth,
+                   const Epilogue& epi, void* part, const char* name, hipStream_t s) {
+  constexpr bool bf = sizeof(T) == 2;
+  const Plan pl = plan_product(bf ? MOE_BF16 : MOE_F32, rows, cols, depth);
+  const int bt = bf && pl.wide ? 256 : 128;
+  Product p{a, b, lda, ldb, rows, static_cast<int>(cols), depth, static_cast<int>(cdiv(rows, bt)),
+            static_cast<int>(cdiv(cols, bt)), pl.splits, pl.per_split, static_cast<float*>(part), pl.part_ld, epi};
+  const dim3 grid(xcd_grid(static_cast<int64_t>(p.gm) * p.gn * p.splits));
+  if constexpr (bf) {
+    if (pl.wide) MOE_LAUNCH(name, (linear_bf16_kernel<Wide, AKC, BKC>), grid, dim3(Wide::kThreads), 0, s, p);
+    else MOE_LAUNCH(name, (linear_bf16_kernel<Narrow, AKC, BKC>), grid, dim3(Narrow::kThreads), 0, s, p);
+  } else {
+    MOE_LAUNCH(name, (linear_f32_kernel<AKC, BKC>), grid, dim3(Tile32::kThreads), 0, s, p);
+  }
+  if (p.splits > 1)
+    MOE_LAUNCH("linear_join", linear_join_kernel<T>, dim3(static_cast<unsigned>(cdiv(rows * (pl.part_ld / 8), 256))),
+               dim3(256), 0, s, p);
+  return launch_status();
+}
+
+void launch_pad(const void* src, int64_t rows, int64_t cols, void* dst, hipStream_t s) {
+  const int64_t ld = up8(cols);
+  MOE_LAUNCH("linear_pad", pad_rows_kernel, dim3(static_cast<unsigned>(cdiv(rows * (ld / 8), 256))), dim3(256), 0, s,
+             static_cast<const uint16_t*>(src), rows, static_cast<int>(cols), static_cast<int>(ld), static_cast<uint16_t*>(dst));
+}
+
+// Rows per workgroup of the dz pass: about four workgroups per compute unit.
+int64_t dz_chunk(int64_t M, int64_t N) {
+  const int64_t c = cdiv(M * cdiv(N, 512), 4 * kCUs);
+  return (c < 16 ? 16 : c + 3) & ~int64_t{3};
+}
+
+struct Buffers {
+  size_t x, w, dz, sums, part, total;
+};
+Buffers buffers(int dtype, int64_t M, int64_t K, int64_t N, bool bwd) {
+  Buffers b{};
+  b.total = 256;
+  if (M == 0) return b;
+  size_t at = 0;
+  auto take = [&](size_t n) {
+    const size_t o = at;
+    at += align_up(n, 256);
+    return o;
+  };
+  if (dtype == MOE_BF16) {
+    b.x = take(K % 8 ? static_cast<size_t>(M) * up8(K) * 2 : 0);
+    b.w = take(N % 8 ? static_cast<size_t>(K) * up8(N) * 2 : 0);
+  }
+  if (bwd) {
+    b.dz = take(dtype == MOE_BF16 ? static_cast<size_t>(M) * up8(N) * 2 : static_cast<size_t>(M) * N * 4);
+    b.sums = take(static_cast<size_t>(cdiv(M, dz_chunk(M, N))) * up8(N) * 4);
+    const size_t dx = plan_product(dtype, M, K, N).part_bytes, dw = plan_product(dtype, K, N, M).part_bytes;
+    b.part = take(dx > dw ? dx : dw);
+  } else {
+    b.part = take(plan_product(dtype, M, N, K).part_bytes);
+  }
+  if (at > b.total) b.total = at;
+  return b;
+}
+
+// 2^32 threads in one launch are too many: the widest one has a thread per eight elements.
+int linear_sizes(int dtype, int64_t M, int64_t K, int64_t N) {
+  if ((dtype != MOE_F32 && dtype != MOE_BF16) || M < 0 || K < 1 || N < 1) return MOE_EINVAL;
+  if (M >= (1ll << 31) || K > kMaxWidth || N > kMaxWidth) return MOE_EUNSUPPORTED;
+  const int64_t big = M > K ? M : K, side = K > N ? K : N;
+  if (big * up8(side) / 8 >= (1ll << 32) - 256) return MOE_EUNSUPPORTED;
+  return MOE_OK;
+}
+bool act_ok(int act) { return act >= kActNone && act <= kActGelu; }
+
+template <class T>
+int linear_fwd(const void* x, const void* w, const void* bias, const void* residual, int64_t M, int64_t K, int64_t N,
+               int act, void* y, void* z, char* ws, hipStream_t s) {
+  constexpr bool bf = sizeof(T) == 2;
+  const Buffers b = buffers(bf ? MOE_BF16 : MOE_F32, M, K, N, false);
+  int64_t lda = K, ldb = N, depth = K;
+  if (bf && K % 8) {
+    launch_pad(x, M, K, ws + b.x, s);
+    x = ws + b.x;
+    lda = up8(K);
+  }
+  if (bf && N % 8) {
+    launch_pad(w, K, N, ws + b.w, s);
+    w = ws + b.w;
+    ldb = up8(N);
+  }
+  const Epilogue e{bias, z, nullptr, residual, y, act, kActNone, N};
+  return launch_product<T, true, false>(x, lda, w, ldb, M, N, depth, e, ws + b.part, "linear_fwd", s);
+}
+
+template <class T>
+int linear_bwd(const void* dy, const void* x, const void* w, const void* z, int64_t M, int64_t K, int64_t N, int act,
+               const void* in_z, int in_act, const void* dres, void* dx, void* dw, void* db, char* ws, hipStream_t s) {
+  constexpr bool bf = sizeof(T) == 2;
+  const Buffers b = buffers(bf ? MOE_BF16 : MOE_F32, M, K, N, true);
+  const int64_t ldn = bf ? up8(N) : N;
+  const void* dz = dy;
+  const bool write = (dx || dw) && (act != kActNone || ldn != N);
+  if (write || db) {
+    const int64_t chunk = dz_chunk(M, N), chunks = cdiv(M, chunk);
+    float* sums = reinterpret_cast<float*>(ws + b.sums);
+    const DzArgs a{dy, act != kActNone ? z : nullptr, M, chunk, static_cast<int>(N), static_cast<int>(ldn), act,
+                   write ? ws + b.dz : nullptr, db ? sums : nullptr, up8(N)};
+    MOE_LAUNCH("linear_dz", linear_dz_kernel<T>, dim3(static_cast<unsigned>(cdiv(N, 512)), static_cast<unsigned>(chunks)),
+               dim3(256), 0, s, a);
+    if (db)
+      MOE_LAUNCH("linear_db", linear_db_kernel<T>, dim3(static_cast<unsigned>(cdiv(N, 32))), dim3(256), 0, s, sums, up8(N),
+                 chunks, static_cast<int>(N), static_cast<T*>(db));
+    if (write) dz = ws + b.dz;
+  }
+  if (dx) {
+    if (bf && N % 8) {
+      launch_pad(w, K, N, ws + b.w, s);
+      w = ws + b.w;
+    }
+    const Epilogue e{nullptr, nullptr, in_z, dres, dx, kActNone, in_act, K};
+    const int st = launch_product<T, true, true>(dz, ldn, w, ldn, M, K, N, e, ws + b.part, "linear_dx", s);
+    if (st != MOE_OK) return st;
+  }
+  if (dw) {
+    int64_t ldx = K;
+    if (bf && K % 8) {
+      launch_pad(x, M, K, ws + b.x, s);
+      x = ws + b.x;
+      ldx = up8(K);
+    }
+    const Epilogue e{nullptr, nullptr, nullptr, nullptr, dw, kActNone, kActNone, N};
+    return launch_product<T, false, false>(x, ldx, dz, ldn, K, N, M, e, ws + b.part, "linear_dw", s);
+  }
+  return launch_status();
+}
+
+}  // namespace
+}  // namespace moe
+
+using namespace moe;
+
+extern "C" size_t moe_linear_workspace(int dtype, int64_t M, int32_t K, int32_t N, int is_bwd) {
+  if (linear_sizes(dtype, M, K, N) != MOE_OK) return 0;
+  return buffers(dtype, M, K, N, is_bwd != 0).total;
+}
+
+extern "C" int moe_linear(const void* x, const void* w, const void* bias, const void* residual, int dtype, int64_t M,
+                          int32_t K, int32_t N, int act, void* y, void* z, void* ws, size_t ws_bytes, void* stream) {
+  const int st = linear_sizes(dtype, M, K, N);
+  if (st != MOE_OK) return st;
+  if (!act_ok(act)) return MOE_EINVAL;
+  if (M == 0) return MOE_OK;
+  if (!x || !w || !y || !ws) return MOE_EINVAL;
+  for (const void* q : {x, w, bias, residual, static_cast<const void*>(y), static_cast<const void*>(z), static_cast<const void*>(ws)})
+    if (!aligned16(q)) return MOE_EINVAL;
+  if (ws_bytes < buffers(dtype, M, K, N, false).total) return MOE_EWORKSPACE;
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  char* b = static_cast<char*>(ws);
+  return dtype == MOE_BF16 ? linear_fwd<uint16_t>(x, w, bias, residual, M, K, N, act, y, z, b, s)
+                           : linear_fwd<float>(x, w, bias, residual, M, K, N, act, y, z, b, s);
+}
+
+extern "C" int moe_linear_bwd(const void* dy, const void* x, const void* w, const void* z, int dtype, int64_t M,
+                              int32_t K, int32_t N, int act, const void* in_z, int in_act, const void* dres, void* dx,
+                              void* dw, void* db, void* ws, size_t ws_bytes, void* stream) {
+  const int st = linear_sizes(dtype, M, K, N);
+  if (st != MOE_OK) return st;
+  if (!act_ok(act) || !act_ok(in_act)) return MOE_EINVAL;
+  if (!dx && (dres || in_act != kActNone)) return MOE_EINVAL;
+  if (M > 0 && ((!dy && (dx || dw || db)) || (dx && !w) || (dw && !x) || (act != kActNone && !z) ||
+                (in_act != kActNone && !in_z) || !ws))
+    return MOE_EINVAL;
+  for (const void* q : {dy, x, w, z, in_z, dres, static_cast<const void*>(dx), static_cast<const void*>(dw),
+                        static_cast<const void*>(db), static_cast<const void*>(ws)})
+    if (!aligned16(q)) return MOE_EINVAL;
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  const size_t es = dtype == MOE_BF16 ? 2 : 4;
+  if (M == 0) {
+    if (dw) launch_zero(dw, static_cast<size_t>(K) * N * es, s);
+    if (db) launch_zero(db, static_cast<size_t>(N) * es, s);
+    return launch_status();
+  }
+  if (ws_bytes < buffers(dtype, M, K, N, true).total) return MOE_EWORKSPACE;
+  char* b = static_cast<char*>(ws);
+  return dtype == MOE_BF16 ? linear_bwd<uint16_t>(dy, x, w, z, M, K, N, act, in_z, in_act, dres, dx, dw, db, b, s)
+                           : linear_bwd<float>(dy, x, w, z, M, K, N, act, in_z, in_act, dres, dx, dw, db, b, s);
+}

@@ -1,0 +1,548 @@
+// Routing by scores, its backward, and the update of the balancing bias.
+//
+// A token's scores are s = softmax(l) over all experts or s = sigmoid(l); it
+// chooses by c = s + b (b: a bias per expert that only moves the choice).  With
+// groups, the groups whose best one or two choices sum highest stay in; then
+// the k best c inside them are taken and their s, renormalised or not, times a
+// factor, are the gates.
+//
+// Which expert is chosen must not hang on rounding, so the order is that of c in
+// 64 bits: near ties in 32 bits are common (16384 tokens of 256 experts have some
+// ten pairs within 2^-24 of each other at the border of the choice).
+//
+// Sixteen lanes take a token (one DPP row: its maxima and sums are rotations
+// inside the row), four tokens a wave, 64 tokens a workgroup, so that a 64-bit
+// mask per expert in LDS gives each chosen slot its rank among the workgroup's
+// tokens.  The counts go out as [expert][workgroup]; one wave per expert turns
+// its row into exclusive sums, and the workgroups of the last launch make the
+// experts' offsets from the totals themselves.  No step runs on one workgroup.
+#include <cmath>
+
+#include "common.hpp"
+
+namespace moe {
+namespace {
+
+constexpr int kRow = 16;          // lanes per token
+constexpr int kTok = 64;          // tokens per workgroup (bits of a mask)
+constexpr int kSelThreads = kRow * kTok;
+
+// ---------------------------------------------------------------------------
+// Reductions over the 16 lanes of a DPP row (every lane must be active): the
+// rotations by 8, 4, 2 and 1 leave the result in all lanes.
+// ---------------------------------------------------------------------------
+template <int N>
+__device__ __forceinline__ uint32_t ror(uint32_t v) {
+  return static_cast<uint32_t>(__builtin_amdgcn_mov_dpp(static_cast<int>(v), 0x120 | N, 0xF, 0xF, true));
+}
+template <int N>
+__device__ __forceinline__ float ror(float v) {
+  return __uint_as_float(ror<N>(__float_as_uint(v)));
+}
+template <int N>
+__device__ __forceinline__ uint64_t ror(uint64_t v) {
+  return static_cast<uint64_t>(ror<N>(static_cast<uint32_t>(v >> 32))) << 32 | ror<N>(static_cast<uint32_t>(v));
+}
+template <int N>
+__device__ __forceinline__ double ror(double v) {
+  return __longlong_as_double(static_cast<long long>(ror<N>(static_cast<uint64_t>(__double_as_longlong(v)))));
+}
+template <class T, class F>
+__device__ __forceinline__ T row_reduce(T v, F f) {
+  v = f(v, ror<8>(v));
+  v = f(v, ror<4>(v));
+  v = f(v, ror<2>(v));
+  return f(v, ror<1>(v));
+}
+template <class T>
+__device__ __forceinline__ T row_max(T v) {
+  return row_reduce(v, [](T a, T b) { return a > b ? a : b; });
+}
+__device__ __forceinline__ float row_fmax(float v) {
+  return row_reduce(v, [](float a, float b) { return fmaxf(a, b); });
+}
+__device__ __forceinline__ uint32_t row_min(uint32_t v) {
+  return row_reduce(v, [](uint32_t a, uint32_t b) { return a < b ? a : b; });
+}
+template <class T>
+__device__ __forceinline__ T row_sum(T v) {
+  return row_reduce(v, [](T a, T b) { return a + b; });
+}
+
+// Choices as whole numbers of the same order: 0 is out of the race, 1 a NaN (it
+// ranks below every number), and -0 is +0.
+__device__ __forceinline__ uint64_t order_key(double c) {
+  if (c != c) return 1;
+  const int64_t b = __double_as_longlong(c + 0.0);
+  return static_cast<uint64_t>(b) ^ (static_cast<uint64_t>(b >> 63) | 0x8000000000000000ull);
+}
+
+// The score of logit x under a row maximum m before it is divided by the sum: a
+// row of -inf has none, and a NaN spoils its row.
+__device__ __forceinline__ double softmax_part(float x, float m) {
+  if (m == -INFINITY) return x == x ? 0.0 : NAN;
+  return exp(static_cast<double>(x) - static_cast<double>(m));
+}
+__device__ __forceinline__ float softmax_part32(float x, float m) {
+  if (m == -INFINITY) return x == x ? 0.f : NAN;
+  return expf(x - m);
+}
+
+// LDS written by some lanes of a wave and read by others of the same wave.
+__device__ __forceinline__ void wave_sync() {
+  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+}
+
+struct ScoreArgs {
+  const float* logits;
+  const float* bias;  // may be null
+  int64_t T;
+  int E, k, sigmoid, groups, top_groups, group_best, renorm;
+  float scale;
+  int32_t* topk_idx;
+  float* gates;
+  int32_t* rank;        // [T, k] rank of the slot among its workgroup's tokens
+  int32_t* blk_counts;  // [E, workgroups]
+  int64_t nblk;
+};
+
+// The expert of a lane's c-th value: runs of four where rows are 16-byte aligned
+// and whole (VEC), else single ones.
+template <bool VEC>
+__device__ __forceinline__ int expert_of(int c, int lane) {
+  return VEC ? ((c >> 2) * kRow + lane) * 4 + (c & 3) : c * kRow + lane;
+}
+
+// Leaves in `on` (one bit per c) the values whose group stays.  `key` is the
+// token's row in LDS, the bits of its choices; their place then takes the groups'.
+template <int C, bool VEC>
+__device__ __forceinline__ void keep_groups(const ScoreArgs& p, uint64_t* key, int lane, int tok, uint32_t& on) {
+  const int size = p.E / p.groups;
+  // lanes 0, 1, .. take groups: the sums of their best, kept in registers until every lane has read the row
+  double sum[4];
+#pragma unroll
+  for (int u = 0; u < 4; ++u) {
+    const int g = u * kRow + lane;
+    double b0 = -INFINITY, b1 = -INFINITY;
+    bool nan = false;
+    if (g < p.groups) {
+      int i = (g + tok) % size;  // lanes start apart, else they would meet on one LDS bank
+      for (int n = 0; n < size; ++n) {
+        const double v = __longlong_as_double(static_cast<long long>(key[g * size + i]));
+        if (++i == size) i = 0;
+        nan |= v != v;
+        b1 = v > b0 ? b0 : (v > b1 ? v : b1);
+        b0 = v > b0 ? v : b0;
+      }
+    }
+    sum[u] = nan ? NAN : (p.group_best == 1 ? b0 : b0 + b1);
+  }
+  wave_sync();
+#pragma unroll
+  for (int u = 0; u < 4; ++u)
+    if (u * kRow + lane < p.groups) key[u * kRow + lane] = order_key(sum[u]);
+  wave_sync();
+  // a group stays when fewer than top_groups come before it
+  uint32_t stay = 0;
+#pragma unroll
+  for (int u = 0; u < 4; ++u) {
+    const int g = u * kRow + lane;
+    if (g < p.groups) {
+      const uint64_t mine = key[g];
+      int before = 0;
+      for (int h = 0; h < p.groups; ++h) before += key[h] > mine || (key[h] == mine && h < g);
+      stay |= static_cast<uint32_t>(before < p.top_groups) << u;
+    }
+  }
+  wave_sync();
+#pragma unroll
+  for (int u = 0; u < 4; ++u)
+    if (u * kRow + lane < p.groups) key[u * kRow + lane] = (stay >> u) & 1;
+  wave_sync();
+#pragma unroll
+  for (int c = 0; c < C; ++c) {
+    const int e = expert_of<VEC>(c, lane);
+    if (e < p.E && !key[e / size]) on &= ~(1u << c);
+  }
+}
+
+template <int C, bool VEC>
+__global__ __launch_bounds__(kSelThreads) void score_select_kernel(ScoreArgs p) {
+  extern __shared__ __align__(16) unsigned char smem[];
+  unsigned long long* mask = reinterpret_cast<unsigned long long*>(smem);           // [E]
+  uint64_t* rows = reinterpret_cast<uint64_t*>(smem + static_cast<size_t>(p.E) * 8);  // [kTok][E] with groups
+  const int tid = threadIdx.x, lane = tid & (kRow - 1), tok = tid / kRow;
+  const int64_t t = static_cast<int64_t>(blockIdx.x) * kTok + tok;
+  const bool live = t < p.T;
+  const float* row = p.logits + (live ? t : p.T - 1) * p.E;  // lanes without a token follow the last one
+  const int E = p.E;
+
+  float l[C];
+  if constexpr (VEC) {
+#pragma unroll
+    for (int c = 0; c < C; c += 4) {
+      const int e = expert_of<VEC>(c, lane);
+      const float4 v = e < E ? *reinterpret_cast<const float4*>(row + e) : make_float4(0.f, 0.f, 0.f, 0.f);
+      l[c] = v.x; l[c + 1] = v.y; l[c + 2] = v.z; l[c + 3] = v.w;
+    }
+  } else {
+#pragma unroll
+    for (int c = 0; c < C; ++c) {
+      const int e = expert_of<VEC>(c, lane);
+      l[c] = e < E ? row[e] : 0.f;
+    }
+  }
+  for (int e = tid; e < E; e += kSelThreads) mask[e] = 0ull;
+
+  uint32_t on = 0;
+#pragma unroll
+  for (int c = 0; c < C; ++c) on |= static_cast<uint32_t>(expert_of<VEC>(c, lane) < E) << c;
+
+  double s[C];
+  if (p.sigmoid) {
+#pragma unroll
+    for (int c = 0; c < C; ++c) s[c] = 1.0 / (1.0 + exp(-static_cast<double>(l[c])));
+  } else {
+    float m = -INFINITY;
+#pragma unroll
+    for (int c = 0; c < C; ++c) m = (on >> c) & 1 ? fmaxf(m, l[c]) : m;
+    m = row_fmax(m);
+    double sum = 0.0;
+#pragma unroll
+    for (int c = 0; c < C; ++c) {
+      s[c] = (on >> c) & 1 ? softmax_part(l[c], m) : 0.0;
+      sum += s[c];
+    }
+    sum = row_sum(sum);
+    const double inv = sum == 0.0 ? 0.0 : 1.0 / sum;
+#pragma unroll
+    for (int c = 0; c < C; ++c) s[c] *= inv;
+  }
+
+  uint64_t key[C];
+  if (p.groups > 1) {
+    uint64_t* mine = rows + static_cast<size_t>(tok) * E;
+#pragma unroll
+    for (int c = 0; c < C; ++c) {
+      const int e = expert_of<VEC>(c, lane);
+      if (e < E) mine[e] = static_cast<uint64_t>(__double_as_longlong(s[c] + (p.bias ? static_cast<double>(p.bias[e]) : 0.0)));
+    }
+    wave_sync();
+    keep_groups<C, VEC>(p, mine, lane, tok, on);
+  }
+#pragma unroll
+  for (int c = 0; c < C; ++c) {
+    const int e = expert_of<VEC>(c, lane);
+    key[c] = (on >> c) & 1 ? order_key(s[c] + (p.bias ? static_cast<double>(p.bias[e]) : 0.0)) : 0;
+  }
+
+  int my_e = 0;
+  double my_s = 0.0;
+  for (int j = 0; j < p.k; ++j) {
+    uint64_t best = 0;
+#pragma unroll
+    for (int c = 0; c < C; ++c) best = key[c] > best ? key[c] : best;
+    best = row_max(best);
+    uint32_t e_best = 0xFFFFFFFFu;
+#pragma unroll
+    for (int c = 0; c < C; ++c) {
+      const uint32_t e = expert_of<VEC>(c, lane);
+      if (key[c] == best && e < e_best) e_best = e;
+    }
+    e_best = row_min(e_best);
+    double s_best = 0.0;
+#pragma unroll
+    for (int c = 0; c < C; ++c)
+      if (static_cast<uint32_t>(expert_of<VEC>(c, lane)) == e_best) {
+        key[c] = 0;
+        s_best = s[c];
+      }
+    s_best = row_sum(s_best);  // one lane's; the others add zeros
+    if (lane == j) {
+      my_e = static_cast<int>(e_best);
+      my_s = s_best;
+    }
+  }
+  double gate = my_s;
+  if (p.renorm) {
+    // softmax: from the chosen logits alone, which the sum over all of them divides out of
+    if (!p.sigmoid) {
+      const float lj = lane < p.k ? row[my_e] : -INFINITY;
+      const float m = row_fmax(lj);  // by all lanes
+      gate = my_s != my_s ? my_s : (lane < p.k ? softmax_part(lj, m) : 0.0);
+    }
+    const double tot = row_sum(gate);
+    gate = tot == 0.0 ? 0.0 : gate / tot;
+  }
+  const bool chosen = live && lane < p.k;
+  __syncthreads();
+  if (chosen) {
+    p.topk_idx[t * p.k + lane] = my_e;
+    p.gates[t * p.k + lane] = static_cast<float>(gate * static_cast<double>(p.scale));
+    atomicOr(&mask[my_e], 1ull << tok);
+  }
+  __syncthreads();
+  if (chosen) p.rank[t * p.k + lane] = __popcll(mask[my_e] & ((1ull << tok) - 1ull));
+  for (int e = tid; e < E; e += kSelThreads) p.blk_counts[e * p.nblk + blockIdx.x] = __popcll(mask[e]);
+}
+
+// One wave per expert: its counts over the workgroups become exclusive sums in
+// place, their total its count.
+__global__ __launch_bounds__(64) void score_scan_kernel(int32_t* __restrict__ blk, int64_t nblk,
+                                                        int32_t* __restrict__ counts) {
+  const int e = blockIdx.x, lane = threadIdx.x;
+  int32_t* row = blk + static_cast<int64_t>(e) * nblk;
+  int base = 0;
+  for (int64_t b0 = 0; b0 < nblk; b0 += 64) {
+    const int64_t b = b0 + lane;
+    const int own = b < nblk ? row[b] : 0;
+    int incl = own;
+#pragma unroll
+    for (int o = 1; o < 64; o <<= 1) {
+      const int up = __shfl_up(incl, o, 64);
+      if (lane >= o) incl += up;
+    }
+    if (b < nblk) row[b] = base + incl - own;
+    base += __shfl(incl, 63, 64);
+  }
+  if (lane == 0) counts[e] = base;
+}
+
+// Every workgroup makes the experts' offsets (exclusive sums of the counts) for
+// itself; the first one writes them out.
+__global__ __launch_bounds__(256) void score_scatter_kernel(const int32_t* __restrict__ topk_idx,
+                                                            const int32_t* __restrict__ rank,
+                                                            const int32_t* __restrict__ blk_base, int64_t nblk,
+                                                            int64_t R, int k, int E,
+                                                            const int32_t* __restrict__ counts,
+                                                            int32_t* __restrict__ offsets,
+                                                            int32_t* __restrict__ mx_blk_offsets,
+                                                            int32_t* __restrict__ perm_src,
+                                                            int32_t* __restrict__ perm_dst) {
+  __shared__ int32_t first[kMaxE];
+  __shared__ int32_t part[2][4];
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int own = tid < E ? counts[tid] : 0, ownb = (own + 31) / 32;
+  int incl = own, inclb = ownb;
+#pragma unroll
+  for (int o = 1; o < 64; o <<= 1) {
+    const int up = __shfl_up(incl, o, 64), upb = __shfl_up(inclb, o, 64);
+    if (lane >= o) {
+      incl += up;
+      inclb += upb;
+    }
+  }
+  if (lane == 63) {
+    part[0][wave] = incl;
+    part[1][wave] = inclb;
+  }
+  __syncthreads();
+  for (int w = 0; w < wave; ++w) {
+    incl += part[0][w];
+    inclb += part[1][w];
+  }
+  first[tid] = incl - own;
+  if (blockIdx.x == 0 && tid < E) {
+    if (tid == 0) {
+      offsets[0] = 0;
+      if (mx_blk_offsets) mx_blk_offsets[0] = 0;
+    }
+    offsets[tid + 1] = incl;
+    if (mx_blk_offsets) mx_blk_offsets[tid + 1] = inclb;
+  }
+  __syncthreads();
+  const int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + tid;
+  if (i >= R) return;
+  const int64_t b = i / (k * kTok);
+  const int e = topk_idx[i];
+  const int row = first[e] + blk_base[e * nblk + b] + rank[i];
+  perm_dst[i] = row;
+  perm_src[row] = static_cast<int32_t>(i);
+}
+
+// ---------------------------------------------------------------------------
+// Backward.  With a = scale, S the sum of the chosen scores:
+//   renormalised    ds_j = (a dg_j - sum_i a dg_i s_i / S) / S
+//   not             ds_j = a dg_j
+//   sigmoid         dl_j = ds_j s_j (1 - s_j), zero elsewhere
+//   softmax         dl_e = s_e (ds_e - sum_j ds_j s_j), where the sum is zero
+//                   for renormalised gates: then dl is zero elsewhere too, and
+//                   s / S is the softmax over the chosen logits alone
+// So only softmax without renormalising reads whole rows.  Sixteen lanes take a
+// token, lane j its slot j; the row is put together in LDS.
+// ---------------------------------------------------------------------------
+struct ScoreBwdArgs {
+  const float* logits;
+  const int32_t* topk_idx;
+  const float* dgates;
+  int64_t T;
+  int E, k, sigmoid, renorm, accumulate;
+  float scale;
+  float* dlogits;
+};
+
+template <bool VEC>
+__global__ __launch_bounds__(256) void score_bwd_kernel(ScoreBwdArgs p) {
+  extern __shared__ __align__(16) float brow[];
+  const int tid = threadIdx.x, lane = tid & (kRow - 1), tok = tid / kRow;
+  const int64_t t = static_cast<int64_t>(blockIdx.x) * (256 / kRow) + tok;
+  const bool live = t < p.T;
+  const int64_t tt = live ? t : p.T - 1;
+  const int E = p.E, ld = VEC ? E + 4 : E;
+  const float* row = p.logits + tt * E;
+  float* out = brow + tok * ld;
+  const bool slot = lane < p.k;
+  const int e = slot ? p.topk_idx[tt * p.k + lane] : 0;
+  const float dg = slot ? p.scale * p.dgates[tt * p.k + lane] : 0.f;
+  const float l = slot ? row[e] : -INFINITY;
+  const bool full = !p.sigmoid && !p.renorm;
+
+  float m = -INFINITY, inv = 0.f;
+  if (full) {
+    float sum = 0.f;
+    for (int c = lane; c < E; c += kRow) m = fmaxf(m, row[c]);
+    m = row_fmax(m);
+    for (int c = lane; c < E; c += kRow) sum += softmax_part32(row[c], m);
+    sum = row_sum(sum);
+    inv = sum == 0.f ? 0.f : 1.0f / sum;
+  } else if (!p.sigmoid) {
+    m = row_fmax(l);
+  }
+  // the slot's score (of all experts, or of the chosen ones alone) and gradient, in 64 bits: a lane has one
+  double s = 0.0, ds = dg;
+  if (slot) s = p.sigmoid ? 1.0 / (1.0 + exp(-static_cast<double>(l))) : softmax_part(l, m) * (full ? inv : 1.0);
+  if (p.renorm) {
+    const double tot = row_sum(s), w = tot == 0.0 ? 0.0 : 1.0 / tot;
+    ds = (ds - row_sum(ds * s) * w) * w;
+  }
+  const double dl = p.sigmoid ? ds * s / (1.0 + exp(static_cast<double>(l))) : s * ds;
+  const float inner = full ? static_cast<float>(row_sum(dl)) : 0.f;
+
+  for (int c = lane; c < E; c += kRow) out[c] = full ? -softmax_part32(row[c], m) * inv * inner : 0.f;
+  wave_sync();
+  if (slot) out[e] += static_cast<float>(dl);
+  wave_sync();
+  if (!live) return;
+  float* dst = p.dlogits + t * E;
+  if constexpr (VEC) {
+    for (int c = 4 * lane; c < E; c += 4 * kRow) {
+      float4 v = *reinterpret_cast<const float4*>(out + c);
+      if (p.accumulate) {
+        const float4 a = *reinterpret_cast<const float4*>(dst + c);
+        v.x += a.x; v.y += a.y; v.z += a.z; v.w += a.w;
+      }
+      *reinterpret_cast<float4*>(dst + c) = v;
+    }
+  } else {
+    for (int c = lane; c < E; c += kRow) dst[c] = p.accumulate ? dst[c] + out[c] : out[c];
+  }
+}
+
+// bias_out[e] = bias[e] + rate sign(sum of the counts - E counts[e]): up for an
+// expert below the mean load, down for one above.  Whole numbers of 64 bits, so
+// the sign is exact.
+__global__ __launch_bounds__(256) void bias_update_kernel(const int32_t* __restrict__ counts, int64_t S, int E, float rate,
+                                                          const float* __restrict__ bias, float* __restrict__ bias_out) {
+  __shared__ long long total[4];
+  const int e = threadIdx.x;
+  long long own = 0;
+  if (e < E)
+    for (int64_t s = 0; s < S; ++s) own += counts[s * E + e];
+  long long sum = own;
+#pragma unroll
+  for (int o = 32; o >= 1; o >>= 1) sum += __shfl_xor(sum, o, 64);
+  if ((e & 63) == 0) total[e >> 6] = sum;
+  __syncthreads();
+  const long long diff = total[0] + total[1] + total[2] + total[3] - own * E;
+  if (e < E) bias_out[e] = diff == 0 ? bias[e] : bias[e] + (diff > 0 ? rate : -rate);
+}
+
+bool score_sizes_ok(int64_t T, int E, int k) {
+  return T >= 0 && E >= 1 && E <= kMaxE && k >= 1 && k <= kMaxK && k <= E && T < (1ll << 31) && T * k < (1ll << 31);
+}
+size_t score_ws_bytes(int64_t T, int E, int k) {
+  return align_up(static_cast<size_t>(T * k) * 4, 256) + align_up(static_cast<size_t>(cdiv(T, kTok) * E) * 4, 256);
+}
+
+template <int C>
+void launch_score_select(const ScoreArgs& a, hipStream_t s) {
+  const size_t lds = static_cast<size_t>(a.E) * 8 + (a.groups > 1 ? static_cast<size_t>(kTok) * a.E * 8 : 0);
+  const dim3 grid(static_cast<unsigned>(a.nblk)), block(kSelThreads);
+  if (a.E % 4 == 0) MOE_LAUNCH("score_select", (score_select_kernel<C, true>), grid, block, lds, s, a);
+  else MOE_LAUNCH("score_select", (score_select_kernel<C, false>), grid, block, lds, s, a);
+}
+
+}  // namespace
+}  // namespace moe
+
+using namespace moe;
+
+extern "C" size_t moe_route_scored_workspace(int64_t T, int32_t E, int32_t k) {
+  return score_sizes_ok(T, E, k) ? score_ws_bytes(T, E, k) : 0;
+}
+
+extern "C" int moe_route_scored(const float* logits, const float* bias, int64_t T, int32_t E, int32_t k, int score,
+                                int32_t groups, int32_t top_groups, int32_t group_best, int renorm, float scale,
+                                int32_t* topk_idx, float* gates, int32_t* counts, int32_t* offsets, int32_t* perm_src,
+                                int32_t* perm_dst, int32_t* mx_blk_offsets, void* ws, size_t ws_bytes, void* stream) {
+  if (E > kMaxE || k > kMaxK) return MOE_EUNSUPPORTED;
+  if (!score_sizes_ok(T, E, k) || (score != MOE_SOFTMAX && score != MOE_SIGMOID) || !std::isfinite(scale)) return MOE_EINVAL;
+  if (groups < 1 || groups > E || E % groups || top_groups < 1 || top_groups > groups || group_best < 1 ||
+      group_best > 2 || group_best > E / groups || static_cast<int64_t>(top_groups) * (E / groups) < k)
+    return MOE_EINVAL;
+  if (groups > 64) return MOE_EUNSUPPORTED;
+  if (!counts || !offsets || !ws) return MOE_EINVAL;
+  if (T > 0 && (!logits || !topk_idx || !gates || !perm_src || !perm_dst)) return MOE_EINVAL;
+  for (const void* q : {static_cast<const void*>(logits), static_cast<const void*>(bias),
+                        static_cast<const void*>(topk_idx), static_cast<const void*>(gates),
+                        static_cast<const void*>(counts), static_cast<const void*>(offsets),
+                        static_cast<const void*>(perm_src), static_cast<const void*>(perm_dst),
+                        static_cast<const void*>(mx_blk_offsets), static_cast<const void*>(ws)})
+    if (!aligned16(q)) return MOE_EINVAL;
+  if (ws_bytes < score_ws_bytes(T, E, k)) return MOE_EWORKSPACE;
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  const int64_t nblk = cdiv(T, kTok), R = T * k;
+  int32_t* rank = static_cast<int32_t*>(ws);
+  int32_t* blk = reinterpret_cast<int32_t*>(static_cast<char*>(ws) + align_up(static_cast<size_t>(R) * 4, 256));
+  if (T > 0) {
+    const ScoreArgs a{logits, bias, T, E, k, score == MOE_SIGMOID, top_groups == groups ? 1 : groups,  // all stay
+                      top_groups, group_best, renorm, scale, topk_idx, gates, rank, blk, nblk};
+    if (E <= 64) launch_score_select<4>(a, s);
+    else if (E <= 128) launch_score_select<8>(a, s);
+    else launch_score_select<16>(a, s);
+  }
+  MOE_LAUNCH("score_scan", score_scan_kernel, dim3(static_cast<unsigned>(E)), dim3(64), 0, s, blk, nblk, counts);
+  MOE_LAUNCH("score_scatter", score_scatter_kernel, dim3(static_cast<unsigned>(R > 0 ? cdiv(R, 256) : 1)), dim3(256), 0,
+             s, topk_idx, rank, blk, nblk, R, k, E, counts, offsets, mx_blk_offsets, perm_src, perm_dst);
+  return launch_status();
+}
+
+extern "C" int moe_route_scored_bwd(const float* logits, const int32_t* topk_idx, const float* dgates, int64_t T,
+                                    int32_t E, int32_t k, int score, int renorm, float scale, int accumulate,
+                                    float* dlogits, void* stream) {
+  if (E > kMaxE || k > kMaxK) return MOE_EUNSUPPORTED;
+  if (!score_sizes_ok(T, E, k) || (score != MOE_SOFTMAX && score != MOE_SIGMOID) || !std::isfinite(scale)) return MOE_EINVAL;
+  if (T == 0) return MOE_OK;
+  if (!logits || !topk_idx || !dgates || !dlogits) return MOE_EINVAL;
+  if (!aligned16(logits) || !aligned16(topk_idx) || !aligned16(dgates) || !aligned16(dlogits)) return MOE_EINVAL;
+  const ScoreBwdArgs a{logits, topk_idx, dgates, T, E, k, score == MOE_SIGMOID, renorm, accumulate, scale, dlogits};
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  constexpr int kTokens = 256 / kRow;
+  const dim3 grid(static_cast<unsigned>(cdiv(T, kTokens))), block(256);
+  if (E % 4 == 0)
+    MOE_LAUNCH("score_bwd", score_bwd_kernel<true>, grid, block, static_cast<size_t>(kTokens) * (E + 4) * 4, s, a);
+  else
+    MOE_LAUNCH("score_bwd", score_bwd_kernel<false>, grid, block, static_cast<size_t>(kTokens) * E * 4, s, a);
+  return launch_status();
+}
+
+extern "C" int moe_route_bias_update(const int32_t* counts, int64_t S, int32_t E, float rate, const float* bias,
+                                     float* bias_out, void* stream) {
+  if (E < 1 || E > kMaxE || S < 1 || !counts || !bias || !bias_out || !std::isfinite(rate)) return MOE_EINVAL;
+  if (!aligned16(counts) || !aligned16(bias) || !aligned16(bias_out)) return MOE_EINVAL;
+  MOE_LAUNCH("route_bias_update", bias_update_kernel, dim3(1), dim3(256), 0, static_cast<hipStream_t>(stream), counts,
+             S, E, rate, bias, bias_out);
+  return launch_status();
+}

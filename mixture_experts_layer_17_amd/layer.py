@@ -26,7 +26,7 @@ def to_device(inp: dict, device="cuda") -> dict:
         if not isinstance(val, np.ndarray):
             continue
         t = torch.from_numpy(np.ascontiguousarray(val))
-        out[key] = t.to(device=device, dtype=torch.float32 if key == "logits" else dt)
+        out[key] = t.to(device=device, dtype=torch.float32 if key in ("logits", "router_bias") else dt)
     return out
 
 
@@ -58,12 +58,22 @@ class LayerStep:
       balance               (alpha, zeta): the router's balance and z losses (self.balance holds them with the counts),
                             their gradient joining the gates' in one pass; seq_offsets and token_mask as in
                             moe_balance_loss;
-      update(...)           a Muon step of the expert weights from this step's gradients.
+      update(...)           a Muon step of the expert weights from this step's gradients;
+      update_adamw(...)     an AdamW step of the other weights (router, norm, shared expert), or of all.
+    A layer of many small experts (each off by default):
+      routing               arguments of moe_route_scored (score, groups, top_groups, group_best, renorm, scale) in place
+                            of the renormalised softmax over logits; dev_inputs may hold "router_bias" [E] (fp32), which
+                            update_router_bias(rate) moves by the step's load.  With balance, its losses are still those
+                            of the logits' softmax, and both gradients join in dlogits;
+      shared                the activation of a shared expert, out = layer(h) + act(h w1 + b1) w2 + b2, from "shared_w1"
+                            [d, fs], "shared_w2" [fs, d] and optionally "shared_b1" [fs], "shared_b2" [d] of dev_inputs:
+                            the routed output is the second product's residual, and the routed dx that of its backward.
     """
 
     def __init__(self, w: Workload, dev_inputs: dict, mx_weight_cache: bool = False,
                  mx_weights_per_step: bool = False, mx_movement: str = "tok", keep_rows: bool = False,
-                 norm: bool = False, balance=None, seq_offsets=None, token_mask=None):
+                 norm: bool = False, balance=None, seq_offsets=None, token_mask=None, routing=None,
+                 shared: str | None = None):
         self.w = w
         self.inp = dev_inputs
         self.norm, self.balance_coef = bool(norm), balance
@@ -136,6 +146,23 @@ class LayerStep:
                             "norm": torch.empty(S + 2, **f32)}
             self.balance_ws = B._ws(B.lib().moe_balance_loss_workspace(T, E, S), dev)
         self.mom = None  # Muon momentum and workspaces, made by the first update
+        self.routing, self.shared = routing, shared
+        if routing is not None:
+            self.route_ws = B._ws(B.lib().moe_route_scored_workspace(T, E, k), dev)
+        if shared is not None:
+            w1, w2 = dev_inputs["shared_w1"], dev_inputs["shared_w2"]
+            fs = w1.shape[1]
+            self.sh = {"y": torch.empty((T, fs), dtype=dt, device=dev), "z": torch.empty((T, fs), dtype=dt, device=dev)}
+            self.sh_dz = torch.empty((T, fs), dtype=dt, device=dev)
+            self.sh_grads = {"dw1": torch.empty_like(w1), "dw2": torch.empty_like(w2)}
+            for name, n in (("b1", fs), ("b2", d)):
+                if "shared_" + name in dev_inputs:
+                    self.sh_grads["d" + name] = torch.empty(n, dtype=dt, device=dev)
+            self.sh_ws = max((B.moe_linear_workspace(a, b, bwd=True) for a, b in ((self.h, w1), (self.sh["y"], w2))),
+                             key=torch.Tensor.numel)
+            self.sh_ws_f = max((B.moe_linear_workspace(a, b) for a, b in ((self.h, w1), (self.sh["y"], w2))),
+                               key=torch.Tensor.numel)
+        self.adamw = None  # AdamW states and plan, made by the first update_adamw
 
     def build_weight_cache(self):
         """Quantise the expert weights (both orientations) into the cache the forward and backward read."""
@@ -152,7 +179,11 @@ class LayerStep:
             B.moe_layernorm(inp["x"], inp.get("ln_w"), inp.get("ln_b"), out=self.ln)
         if self.linear_router:
             B.moe_router_logits(x, inp["w_router"], out=self.logits)
-        B.moe_route_topk(self.logits, w.k, out=self.route, ws=self.route_ws)
+        if self.routing is not None:
+            B.moe_route_scored(self.logits, w.k, bias=inp.get("router_bias"), out=self.route, ws=self.route_ws,
+                               **self.routing)
+        else:
+            B.moe_route_topk(self.logits, w.k, out=self.route, ws=self.route_ws)
         if self.balance_coef is not None:
             B.moe_balance_loss(self.logits, self.route["topk_idx"], *self.balance_coef, seq_offsets=self.seq_offsets,
                                token_mask=self.token_mask, out=self.balance, ws=self.balance_ws)
@@ -165,6 +196,10 @@ class LayerStep:
         B.moe_grouped_ffn_fwd(self.x_perm, self.route["offsets"], inp["w_gate"], inp["w_up"], inp["w_down"], w.prec,
                               out=self.ffn, ws=self.ffn_ws_f, mx_wcache=self.mx_wcache, x_mx=self.x_mx, rows=w.R)
         B.moe_combine(self.ffn["y_perm"], self.route["gates"], self.route["perm_dst"], out=self.out)
+        if self.shared is not None:
+            B.moe_linear(x, inp["shared_w1"], inp.get("shared_b1"), act=self.shared, out=self.sh, ws=self.sh_ws_f)
+            B.moe_linear(self.sh["y"], inp["shared_w2"], inp.get("shared_b2"), residual=self.out, out={"y": self.out},
+                         ws=self.sh_ws_f)
         return self.out
 
     def backward(self, dout=None, dloss=None):
@@ -185,16 +220,26 @@ class LayerStep:
                               dy_mx=self.dy_mx, x_mxt=self.x_mxt, dy_mxt=self.dy_mxt)
         dh = self.dh if self.norm else self.dx
         B.moe_dispatch_bwd(self.grads["dx_perm"], self.route["perm_dst"], w.k, out=dh)
+        gates = {} if self.routing is not None else dict(topk_idx=self.route["topk_idx"], gates=self.route["gates"],
+                                                         dgates=self.dgates)
         if self.balance_coef is not None:
             B.moe_balance_loss_bwd(self.logits, self.balance, w.k, *self.balance_coef, dloss=dloss,
-                                   seq_offsets=self.seq_offsets, token_mask=self.token_mask,
-                                   topk_idx=self.route["topk_idx"], gates=self.route["gates"], dgates=self.dgates,
-                                   out=self.dlogits)
-        else:
+                                   seq_offsets=self.seq_offsets, token_mask=self.token_mask, out=self.dlogits, **gates)
+        elif self.routing is None:
             B.moe_route_topk_bwd(self.route["gates"], self.dgates, self.route["topk_idx"], w.E, out=self.dlogits)
+        if self.routing is not None:
+            how = {key: self.routing[key] for key in ("score", "renorm", "scale") if key in self.routing}
+            B.moe_route_scored_bwd(self.logits, self.route["topk_idx"], self.dgates, out=self.dlogits,
+                                   accumulate=self.balance_coef is not None, **how)
         if self.linear_router:
             B.moe_router_logits_bwd(self.h, inp["w_router"], self.dlogits, dh, accumulate_dx=True,
                                     dw_r=self.dw_router, ws=self.router_ws)
+        if self.shared is not None:
+            g = self.sh_grads
+            B.moe_linear_bwd(dout, self.sh["y"], inp["shared_w2"], in_z=self.sh["z"], in_act=self.shared,
+                             out={"dx": self.sh_dz, "dw": g["dw2"], "db": g.get("db2")}, ws=self.sh_ws)
+            B.moe_linear_bwd(self.sh_dz, self.h, inp["shared_w1"], dres=dh,
+                             out={"dx": dh, "dw": g["dw1"], "db": g.get("db1")}, ws=self.sh_ws)
         if self.norm:
             B.moe_layernorm_bwd(dh, inp["x"], inp.get("ln_w"), self.ln["mean"], self.ln["rstd"], dres=dout,
                                 out=self.ln_grads, ws=self.ln_ws)
@@ -221,6 +266,45 @@ class LayerStep:
                             weight_decay=weight_decay, scale=scale, steps=steps, ws=self.muon_ws)
         if self.mx_wcache is not None and not self.mx_per_step:
             self.build_weight_cache()
+
+    def other_parameters(self):
+        """(weights, gradients) besides the experts': those of router, norm and shared expert that the layer has."""
+        inp, pairs = self.inp, []
+        if self.linear_router:
+            pairs.append((inp["w_router"], self.dw_router))
+        if self.norm:
+            pairs += [(inp["ln_" + n], self.ln_grads["d" + n]) for n in ("w", "b") if "ln_" + n in inp]
+        if self.shared is not None:
+            pairs += [(inp["shared_" + n], self.sh_grads["d" + n]) for n in ("w1", "b1", "w2", "b2") if "shared_" + n in inp]
+        return [p for p, _ in pairs], [g for _, g in pairs]
+
+    def update_adamw(self, lr: float, step: int = 1, betas=(0.9, 0.999), eps: float = 1e-8, weight_decay: float = 0.0,
+                     bits: int = 32, master: bool = False, experts: bool = False, seed: int = 0, grad_scale=None,
+                     step_dev=None):
+        """An AdamW step, in place, of the weights that update() leaves alone, or with experts of all (in place of
+        update()), from the gradients of the last backward.  weight_decay is for matrices only.  The first call decides
+        experts, bits, master and weight_decay and makes the states; in a graph capture it is refused."""
+        if self.adamw is None:
+            if torch.cuda.is_current_stream_capturing():
+                raise B.MoeError("update_adamw: the first call cannot be captured")
+            params, grads = self.other_parameters()
+            if experts:
+                params += [self.inp[n] for n in ("w_gate", "w_up", "w_down")]
+                grads += [self.grads["d" + n] for n in ("w_gate", "w_up", "w_down")]
+            state = B.moe_adamw_state(params, bits=bits, master=master)
+            plan = B.moe_adamw_plan(params, grads, state, weight_decay=[weight_decay if p.dim() > 1 else 0.0 for p in params])
+            self.adamw = {"state": state, "plan": plan, "made": (bits, master, experts, weight_decay)}
+        if self.adamw["made"] != (bits, master, experts, weight_decay):
+            raise B.MoeError(f"update_adamw: the states are those of bits, master, experts, weight_decay = {self.adamw['made']}")
+        B.moe_adamw_step(self.adamw["plan"], lr, step, betas=betas, eps=eps, seed=seed, grad_scale=grad_scale,
+                         step_dev=step_dev)
+        if experts and self.mx_wcache is not None and not self.mx_per_step:
+            self.build_weight_cache()
+
+    def update_router_bias(self, rate: float):
+        """Move the balancing bias by the load of the last forward (without padded tokens where balance counts them)."""
+        counts = self.route["counts"] if self.balance_coef is None else self.balance["counts"]
+        return B.moe_route_bias_update(counts, self.inp["router_bias"], rate)
 
     def step(self):
         self.forward()
