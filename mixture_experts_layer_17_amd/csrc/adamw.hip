@@ -113,64 +113,92 @@ __device__ __forceinline__ uint32_t code64(double y, uint32_t r) {
 // The codes of a lane's eight values under their block's scale, which comes out
 // as its byte: the power of two that puts the block's largest value into
 // (224, 448], so that it is never cut.  Scaled by a further 2^-120 a value has
-// its code in the float's top bits, subnormal codes as subnormal floats, and the
-// random number is added below them.  Blocks with an infinity or a NaN get the
-// byte 255, which reads as NaN.  ROOT: values above zero get a code above zero.
+// its code in the float's bits 20 to 26, subnormal codes as subnormal floats, and
+// the random number is added below them; four places to the left the code stands
+// in the word's last byte, m's sign bit before it.  Blocks with an infinity or a
+// NaN get the byte 255, which reads as NaN.  ROOT: values above zero get a code
+// above zero.
 //
-// Values within 4 units of fp32 (kNear) of where the code or the scale changes
-// are decided by exact(j), the j-th value in 64 bits: 8 in 2^20 are, and the codes
-// are those of the formula, whatever the order of its operations.
-constexpr uint32_t kNear = 4;
+// Values within kNear units of fp32 of where the code or the scale changes are
+// decided by exact(j), the j-th value in 64 bits: 16 in 2^20 are, and the codes
+// are those of the formula, whatever the order of its operations.  The window's
+// half is in the sum already, so the test is of its low bits alone.
+constexpr uint32_t kNear = 8;
 template <bool ROOT, class F>
 __device__ __forceinline__ uint2 encode8(const float (&x)[kPer], const uint32_t (&h)[kPer], uint32_t& byte, F&& exact) {
   auto quad_max = [](uint32_t v) {
     v = max(v, static_cast<uint32_t>(__builtin_amdgcn_mov_dpp(static_cast<int>(v), 0xB1, 0xF, 0xF, true)));  // lane ^ 1
     return max(v, static_cast<uint32_t>(__builtin_amdgcn_mov_dpp(static_cast<int>(v), 0x4E, 0xF, 0xF, true)));  // lane ^ 2
   };
+  auto size = [&](int i) { return ROOT ? __float_as_uint(x[i]) : __float_as_uint(x[i]) & 0x7FFFFFFFu; };
   uint32_t top = 0;
 #pragma unroll
-  for (int i = 0; i < kPer; ++i) top = max(top, __float_as_uint(x[i]) & 0x7FFFFFFFu);
+  for (int i = 0; i < kPer; ++i) top = max(top, size(i));
   top = quad_max(top);
   const bool finite = top < 0x7F800000u;
   uint32_t above = (top & 0x7FFFFFu) > 0x600000u ? 1u : 0u;  // 1.75 times a power of two
   if (finite && ((top + kNear - 0x600000u) & 0x7FFFFFu) < 2 * kNear) {
     const double edge = static_cast<double>(__uint_as_float((top & 0x7F800000u) | 0x600000u));
     above = 0;
-    for (int i = 0; i < kPer; ++i) {
-      const uint32_t b = __float_as_uint(x[i]) & 0x7FFFFFFFu;
-      if (b + 2 * kNear > top && fabs(exact(i)) > edge) above = 1;
-    }
+#pragma unroll
+    for (int i = 0; i < kPer; ++i)
+      if (size(i) + 2 * kNear > top && fabs(exact(i)) > edge) above = 1;
     above = quad_max(above);
   }
   const int e = static_cast<int>(top >> 23) - 8 + static_cast<int>(above);
   byte = finite ? (e > 0 ? e : 0) : 255;
   const float inv = __uint_as_float((254u - (finite ? byte : 0u)) << 23);
-  uint32_t code[kPer], near = 0;
+  uint32_t t[kPer], low = 0xFFFFFFFFu, least = 0xFFFFFFFFu;
 #pragma unroll
   for (int i = 0; i < kPer; ++i) {
     const float y = fabsf(x[i]) * inv * 0x1p-120f;
-    const uint32_t r = ROOT ? (h[i] << 4 & 0xFFFF0u) : (h[i] >> 12 & 0xFFFF0u);
-    const uint32_t t = __float_as_uint(y) + r + 8u;
-    near |= ((t + kNear) & 0xFFFFFu) < 2 * kNear ? 1u << i : 0u;
-    code[i] = t >> 20 < 126u ? t >> 20 : 126u;
+    t[i] = __float_as_uint(y) + (ROOT ? (h[i] & 0xFFFFu) << 4 : h[i] >> 16 << 4) + (8u + kNear);
+    low = min(low, t[i] & 0xFFFFFu);
+    if (ROOT) least = min(least, t[i]);
   }
-  if (near && finite) {
+  if (low < 2 * kNear && finite) {
 #pragma unroll
     for (int i = 0; i < kPer; ++i)
-      if (near >> i & 1) code[i] = code64(fabs(exact(i)) * static_cast<double>(inv), ROOT ? h[i] & 0xFFFFu : h[i] >> 16);
+      if ((t[i] & 0xFFFFFu) < 2 * kNear)
+        t[i] = code64(fabs(exact(i)) * static_cast<double>(inv), ROOT ? h[i] & 0xFFFFu : h[i] >> 16) << 20;
+    if (ROOT) least = 0;
+  }
+  if (ROOT && least < 1u << 20) {
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) t[i] = max(t[i], x[i] > 0.f ? 1u << 20 : 0u);
   }
 #pragma unroll
   for (int i = 0; i < kPer; ++i) {
-    if (ROOT) code[i] = code[i] == 0 && x[i] > 0.f ? 1u : code[i];
-    else code[i] |= __float_as_uint(x[i]) >> 24 & 0x80u;
-    code[i] = finite ? code[i] : 0u;
+    t[i] <<= 4;
+    if (!ROOT) t[i] = (t[i] & 0x7FFFFFFFu) | (__float_as_uint(x[i]) & 0x80000000u);
   }
-  return make_uint2(code[0] | code[1] << 8 | code[2] << 16 | code[3] << 24,
-                    code[4] | code[5] << 8 | code[6] << 16 | code[7] << 24);
+  auto last_bytes = [](uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+    const uint32_t ab = __builtin_amdgcn_perm(b, a, 0x0C0C0703u), cd = __builtin_amdgcn_perm(d, c, 0x07030C0Cu);
+    return ab | cd;
+  };
+  const uint2 q = make_uint2(last_bytes(t[0], t[1], t[2], t[3]), last_bytes(t[4], t[5], t[6], t[7]));
+  return make_uint2(finite ? q.x : 0u, finite ? q.y : 0u);
 }
 
 __device__ __forceinline__ float decode1(const void* q, const uint8_t* scale, int64_t i) {
   return __builtin_amdgcn_cvt_f32_fp8(static_cast<const uint8_t*>(q)[i], 0) * scale_of(scale[i >> 5]);
+}
+
+// Roots of eight values >= 0 by the hardware's instruction, within a unit; it
+// takes subnormal values for zero, so small ones go through the library's.  (The
+// reciprocal beside it is the hardware's too, within a unit: both stay below what
+// rounding the weight costs.)
+__device__ __forceinline__ void square_roots(const float (&v)[kPer], float (&r)[kPer]) {
+  uint32_t least = 0xFFFFFFFFu;
+#pragma unroll
+  for (int j = 0; j < kPer; ++j) {
+    r[j] = __builtin_amdgcn_sqrtf(v[j]);
+    least = min(least, __float_as_uint(v[j]) - 1u);  // zeros pass
+  }
+  if (least < 0x0D800000u) {  // 2^-100
+#pragma unroll
+    for (int j = 0; j < kPer; ++j) r[j] = sqrtf(v[j]);
+  }
 }
 
 template <class T>
@@ -250,9 +278,13 @@ __global__ __launch_bounds__(kThreads) void adamw_kernel(AdamArgs p) {
         m[j] = b1 * m[j] + a1 * gg;
       }
       v[j] = b2 * v[j] + a2 * gg * gg;
-      const float root = sqrtf(v[j]);
-      if (EIGHT) v[j] = root;
-      w[j] = t.keep * w[j] - rate * (m[j] / (root * root2 + p.eps));
+    }
+    float root[kPer];
+    square_roots(v, root);
+#pragma unroll
+    for (int j = 0; j < kPer; ++j) {
+      if (EIGHT) v[j] = root[j];
+      w[j] = t.keep * w[j] - rate * (m[j] * __builtin_amdgcn_rcpf(root[j] * root2 + p.eps));
     }
     // behind the tensor's end (its gradient reads as zero) states and master stay what they are made of: zero
     if (valid < kPer) {
