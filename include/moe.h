@@ -510,7 +510,7 @@ int moe_linear_bwd(const void* dy, const void* x, const void* w, const void* z, 
  * MOE_EINVAL for betas outside [0, 1), a negative eps, scalars that are not finite (products
  * of lr, lr_scale and weight_decay among them), step < 1, n < 0 (0 is skipped), bad offsets, a
  * null or unaligned pointer, a master with MOE_F32; MOE_EUNSUPPORTED for 2^37 elements or more
- * in a tensor.  A launch takes 60 tensors. */
+ * in a tensor.  A launch takes 56 tensors. */
 typedef struct {
   const void* w;
   const void* g;
@@ -526,9 +526,10 @@ int moe_adamw_step(const moe_adamw_tensor* tensors, int32_t count, int dtype, in
                    const float* grad_scale, uint32_t seed, void* m_out, void* v_out, uint8_t* m_scale_out,
                    uint8_t* v_scale_out, float* master_out, void* stream);
 
-/* The values of an 8-bit state (codes [state_len], scale [state_len / 32]) in bf16, which
- * holds them exactly (scales below 2^-124 apart). */
-int moe_adamw_state_values(const uint8_t* codes, const uint8_t* scale, int64_t state_len, void* values, void* stream);
+/* The values of 8-bit states (m and the root of v, as moe_adamw_step keeps them) in bf16 [state_len],
+ * which holds them exactly (scales below 2^-124 apart). */
+int moe_adamw_state_values(const uint8_t* m, const uint8_t* m_scale, const uint8_t* v, const uint8_t* v_scale,
+                           int64_t state_len, void* m_values, void* root_values, void* stream);
 
 /* ---------------------------------------------------------------------------
  * Diagnostics: per-kernel timing for benchmarks and profiling (no page

@@ -80,7 +80,7 @@ _SIGS = {
                        + [_sz, _c_void_p]),
     "moe_adamw_step": (_int, [_c_void_p, _i32, _int, _int, _i64] + [_c_void_p] * 5 + [_f64] * 4
                        + [_i64, _c_void_p, _c_void_p, ctypes.c_uint32] + [_c_void_p] * 6),
-    "moe_adamw_state_values": (_int, [_c_void_p, _c_void_p, _i64, _c_void_p, _c_void_p]),
+    "moe_adamw_state_values": (_int, [_c_void_p] * 4 + [_i64] + [_c_void_p] * 3),
     "moe_timing_enable": (_int, [_int]),
     "moe_timing_report": (_int, [ctypes.c_char_p, _sz]),
 }
@@ -846,8 +846,8 @@ def moe_adamw_state_values(state):
     _args(what, dev, tuple((k, state[k], (n,), torch.uint8) for k in ("m", "v"))
           + tuple((k, state[k], (n // 32,), torch.uint8) for k in ("m_scale", "v_scale")))
     out = {"m": torch.empty(n, dtype=torch.bfloat16, device=dev), "root": torch.empty(n, dtype=torch.bfloat16, device=dev)}
-    for q, name in (("m", "m"), ("v", "root")):
-        _check(lib().moe_adamw_state_values(_p(state[q]), _p(state[q + "_scale"]), n, _p(out[name]), _stream()), what)
+    _check(lib().moe_adamw_state_values(_p(state["m"]), _p(state["m_scale"]), _p(state["v"]), _p(state["v_scale"]), n,
+                                        _p(out["m"]), _p(out["root"]), _stream()), what)
     return out
 
 

@@ -6,8 +6,9 @@
 //
 // The tensors' addresses and sizes travel in the kernel's arguments (kMaxList a
 // launch), so nothing is copied to the device and a captured graph keeps them.
-// A workgroup takes kUnit elements of one tensor, found by a search over the
-// tensors' first units in scalar registers.
+// A workgroup takes a unit of one tensor, found by a search over the
+// tensors' first units in scalar registers: four turns of its 256 lanes where there
+// is work for every compute unit several times over, else one.
 //
 // States in 8 bits: m and the root of v as E4M3 codes with one power of two per
 // 32 values (a lane holds 8, four lanes a block).  The root has half the range
@@ -24,11 +25,10 @@
 namespace moe {
 namespace {
 
-constexpr int kMaxList = 60;    // tensors per launch: the arguments stay below 4 KB
+constexpr int kMaxList = 56;    // tensors per launch: the arguments stay below 4 KB
 constexpr int kThreads = 256;
 constexpr int kPer = 8;         // elements per lane and turn: 16 bytes of bf16
-constexpr int kTurns = 4;
-constexpr int kUnit = kThreads * kPer * kTurns;
+constexpr int kTurn = kThreads * kPer;  // elements of a workgroup's turn
 constexpr int64_t kMaxUnits = int64_t{1} << 24;  // a launch holds fewer than 2^32 threads
 
 struct ListEntry {
@@ -38,6 +38,7 @@ struct ListEntry {
   int64_t n;
   int64_t offset;  // of its states, in elements
   double lr;
+  float rate;      // lr / (1 - beta1^step), for a step counted on the host
   float keep;      // 1 - lr weight_decay
   uint32_t seed;
 };
@@ -46,6 +47,7 @@ struct AdamArgs {
   ListEntry list[kMaxList];
   int32_t first[kMaxList + 1];  // the first unit of each tensor
   int32_t count;
+  int32_t turns;                // of a unit
   const void* m;
   const void* v;
   const uint8_t* m_scale;
@@ -57,7 +59,7 @@ struct AdamArgs {
   uint8_t* v_scale_out;
   float* master_out;
   double beta1, beta2;
-  float eps;
+  float eps, root2;             // root2: 1 / sqrt(1 - beta2^step)
   int64_t step;
   const int64_t* step_dev;
   const float* gscale;
@@ -235,17 +237,20 @@ __global__ __launch_bounds__(kThreads) void adamw_kernel(AdamArgs p) {
     else hi = mid;
   }
   const ListEntry& t = p.list[lo];
-  const int64_t n = t.n, base = static_cast<int64_t>(b - p.first[lo]) * kUnit;
+  const int64_t n = t.n, base = static_cast<int64_t>(b - p.first[lo]) * p.turns * kTurn;
   const int64_t step = p.step_dev ? *p.step_dev : p.step;
   const float b1 = static_cast<float>(p.beta1), b2 = static_cast<float>(p.beta2);
   const float a1 = static_cast<float>(1.0 - p.beta1), a2 = static_cast<float>(1.0 - p.beta2);
   const float b1_low = static_cast<float>(p.beta1 - b1), a1_low = static_cast<float>(1.0 - p.beta1 - a1);
-  const float rate = static_cast<float>(t.lr / (1.0 - int_pow(p.beta1, step)));
-  const float root2 = static_cast<float>(1.0 / sqrt(1.0 - int_pow(p.beta2, step)));
+  float rate = t.rate, root2 = p.root2;
+  if (p.step_dev) {
+    rate = static_cast<float>(t.lr / (1.0 - int_pow(p.beta1, step)));
+    root2 = static_cast<float>(1.0 / sqrt(1.0 - int_pow(p.beta2, step)));
+  }
   const float gs = p.gscale ? *p.gscale : 1.0f;
   const uint32_t key = mix(mix(t.seed) + kGolden * static_cast<uint32_t>(step));
 
-  for (int u = 0; u < kTurns; ++u) {
+  for (int u = 0; u < p.turns; ++u) {
     const int64_t i = base + (u * kThreads + static_cast<int>(threadIdx.x)) * kPer;
     if (i >= ((n + 31) & ~int64_t{31})) break;
     const int valid = n - i >= kPer ? kPer : (n > i ? static_cast<int>(n - i) : 0);
@@ -320,15 +325,23 @@ __global__ __launch_bounds__(kThreads) void adamw_kernel(AdamArgs p) {
   }
 }
 
-// The values of 8-bit states in bf16, which holds them exactly (four bits times a power of two).
-__global__ __launch_bounds__(kThreads) void state_values_kernel(const uint8_t* __restrict__ q,
-                                                                const uint8_t* __restrict__ scale, int64_t n,
-                                                                uint16_t* __restrict__ out) {
+// The values of 8-bit states (m, and the root of v) in bf16, which holds them exactly: four bits times a power of two.
+__global__ __launch_bounds__(kThreads) void state_values_kernel(const uint8_t* __restrict__ m,
+                                                                const uint8_t* __restrict__ m_scale,
+                                                                const uint8_t* __restrict__ v,
+                                                                const uint8_t* __restrict__ v_scale, int64_t n,
+                                                                uint16_t* __restrict__ m_out,
+                                                                uint16_t* __restrict__ v_out) {
   const int64_t i = (static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x) * kPer;
   if (i >= n) return;
   float x[kPer];
-  decode8(*reinterpret_cast<const uint2*>(q + i), scale[i >> 5], x);
-  *reinterpret_cast<uint4*>(out + i) = Elem<uint16_t>::pack(x);
+  if (blockIdx.y == 0) {
+    decode8(*reinterpret_cast<const uint2*>(m + i), m_scale[i >> 5], x);
+    *reinterpret_cast<uint4*>(m_out + i) = Elem<uint16_t>::pack(x);
+  } else {
+    decode8(*reinterpret_cast<const uint2*>(v + i), v_scale[i >> 5], x);
+    *reinterpret_cast<uint4*>(v_out + i) = Elem<uint16_t>::pack(x);
+  }
 }
 
 int64_t pad32(int64_t n) { return (n + 31) & ~int64_t{31}; }
@@ -369,7 +382,7 @@ extern "C" int moe_adamw_step(const moe_adamw_tensor* tensors, int32_t count, in
     if (!std::isfinite(t.weight_decay) || !std::isfinite(t.lr_scale) || !std::isfinite(static_cast<float>(lr * t.lr_scale)) ||
         !std::isfinite(static_cast<float>(lr * t.lr_scale * t.weight_decay)))
       return MOE_EINVAL;
-    if (cdiv(t.n, kUnit) >= kMaxUnits) return MOE_EUNSUPPORTED;
+    if (cdiv(t.n, 4 * kTurn) >= kMaxUnits) return MOE_EUNSUPPORTED;
     end = t.offset + pad32(t.n);
   }
   hipStream_t s = static_cast<hipStream_t>(stream);
@@ -377,17 +390,24 @@ extern "C" int moe_adamw_step(const moe_adamw_tensor* tensors, int32_t count, in
   a.m = m; a.v = v; a.m_scale = m_scale; a.v_scale = v_scale; a.master = master;
   a.m_out = m_out; a.v_out = v_out; a.m_scale_out = m_scale_out; a.v_scale_out = v_scale_out; a.master_out = master_out;
   a.beta1 = beta1; a.beta2 = beta2; a.eps = static_cast<float>(eps);
+  const double c1 = step_dev ? 1.0 : 1.0 - int_pow(beta1, step);
+  a.root2 = step_dev ? 1.0f : static_cast<float>(1.0 / std::sqrt(1.0 - int_pow(beta2, step)));
+  // one turn a unit until four would still leave eight workgroups to a compute unit
+  int64_t all = 0;
+  for (int32_t i = 0; i < count; ++i) all += cdiv(tensors[i].n, 4 * kTurn);
+  a.turns = all >= 8 * 256 ? 4 : 1;
+  const int64_t unit = a.turns * kTurn;
   a.step = step; a.step_dev = step_dev; a.gscale = grad_scale;
   for (int32_t i = 0; i < count;) {
     a.count = 0;
     int64_t units = 0;
     for (; i < count && a.count < kMaxList; ++i) {
       const moe_adamw_tensor& t = tensors[i];
-      const int64_t more = cdiv(t.n, kUnit);
+      const int64_t more = cdiv(t.n, unit);
       if (more == 0) continue;
       if (units + more >= kMaxUnits) break;
       const double rate = lr * t.lr_scale;
-      a.list[a.count] = ListEntry{t.w, t.g, t.w_out, t.n, t.offset, rate,
+      a.list[a.count] = ListEntry{t.w, t.g, t.w_out, t.n, t.offset, rate, static_cast<float>(rate / c1),
                                   static_cast<float>(1.0 - rate * t.weight_decay), seed + kGolden * static_cast<uint32_t>(i)};
       a.first[a.count++] = static_cast<int32_t>(units);
       units += more;
@@ -411,13 +431,18 @@ extern "C" int moe_adamw_step(const moe_adamw_tensor* tensors, int32_t count, in
   return MOE_OK;
 }
 
-extern "C" int moe_adamw_state_values(const uint8_t* codes, const uint8_t* scale, int64_t state_len, void* values,
-                                      void* stream) {
+extern "C" int moe_adamw_state_values(const uint8_t* m, const uint8_t* m_scale, const uint8_t* v, const uint8_t* v_scale,
+                                      int64_t state_len, void* m_values, void* root_values, void* stream) {
   if (state_len < 0 || state_len % 32) return MOE_EINVAL;
   if (state_len == 0) return MOE_OK;
-  if (!codes || !scale || !values || !aligned16(codes) || !aligned16(scale) || !aligned16(values)) return MOE_EINVAL;
-  if (cdiv(state_len, kThreads * kPer) >= kMaxUnits) return MOE_EUNSUPPORTED;
-  MOE_LAUNCH("adamw_state_values", state_values_kernel, dim3(static_cast<unsigned>(cdiv(state_len, kThreads * kPer))),
-             dim3(kThreads), 0, static_cast<hipStream_t>(stream), codes, scale, state_len, static_cast<uint16_t*>(values));
+  if (!m || !m_scale || !v || !v_scale || !m_values || !root_values) return MOE_EINVAL;
+  for (const void* q : {static_cast<const void*>(m), static_cast<const void*>(m_scale), static_cast<const void*>(v),
+                        static_cast<const void*>(v_scale), static_cast<const void*>(m_values),
+                        static_cast<const void*>(root_values)})
+    if (!aligned16(q)) return MOE_EINVAL;
+  if (2 * cdiv(state_len, kTurn) >= kMaxUnits) return MOE_EUNSUPPORTED;
+  MOE_LAUNCH("adamw_state_values", state_values_kernel, dim3(static_cast<unsigned>(cdiv(state_len, kTurn)), 2), dim3(kThreads),
+             0, static_cast<hipStream_t>(stream), m, m_scale, v, v_scale, state_len, static_cast<uint16_t*>(m_values),
+             static_cast<uint16_t*>(root_values));
   return launch_status();
 }

@@ -106,6 +106,8 @@ struct ScoreArgs {
   int32_t* rank;        // [T, k] rank of the slot among its workgroup's tokens
   int32_t* blk_counts;  // [E, workgroups]
   int64_t nblk;
+  // for a single workgroup, which writes them itself
+  int32_t *counts, *offsets, *perm_src, *perm_dst, *mx_blk_offsets;
 };
 
 // The expert of a lane's c-th value: runs of four where rows are 16-byte aligned
@@ -113,6 +115,48 @@ struct ScoreArgs {
 template <bool VEC>
 __device__ __forceinline__ int expert_of(int c, int lane) {
   return VEC ? ((c >> 2) * kRow + lane) * 4 + (c & 3) : c * kRow + lane;
+}
+
+// Offsets of the experts, for thread tid = expert with its count: exclusive sums
+// in `first` (LDS, every thread past the call's barrier may read it); where the
+// pointers are given, counts, offsets and 32-row block offsets go out too.  By
+// the first 256 threads of a workgroup, all of whose threads call it.
+__device__ __forceinline__ void offsets_of(int own, int E, int32_t* first, int32_t* counts, int32_t* offsets,
+                                           int32_t* mx_blk_offsets) {
+  __shared__ int32_t part[2][4];
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int ownb = (own + 31) / 32;
+  int incl = own, inclb = ownb;
+#pragma unroll
+  for (int o = 1; o < 64; o <<= 1) {
+    const int up = __shfl_up(incl, o, 64), upb = __shfl_up(inclb, o, 64);
+    if (lane >= o) {
+      incl += up;
+      inclb += upb;
+    }
+  }
+  if (wave < 4 && lane == 63) {
+    part[0][wave] = incl;
+    part[1][wave] = inclb;
+  }
+  __syncthreads();
+  if (tid < kMaxE) {
+    for (int w = 0; w < wave; ++w) {
+      incl += part[0][w];
+      inclb += part[1][w];
+    }
+    first[tid] = incl - own;
+    if (offsets && tid < E) {
+      if (tid == 0) offsets[0] = 0;
+      offsets[tid + 1] = incl;
+      if (mx_blk_offsets) {
+        if (tid == 0) mx_blk_offsets[0] = 0;
+        mx_blk_offsets[tid + 1] = inclb;
+      }
+      if (counts) counts[tid] = own;
+    }
+  }
+  __syncthreads();
 }
 
 // Leaves in `on` (one bit per c) the values whose group stays.  `key` is the
@@ -168,16 +212,231 @@ __device__ __forceinline__ void keep_groups(const ScoreArgs& p, uint64_t* key, i
   }
 }
 
+// The choice of a token by 64 bits: lane j gets its j-th expert.
+template <int C, bool VEC>
+__device__ __forceinline__ int choose_exact(const ScoreArgs& p, const float (&l)[C], float m, uint32_t on, uint64_t* mine,
+                                            int lane, int tok) {
+  double s[C];
+  if (p.sigmoid) {
+#pragma unroll
+    for (int c = 0; c < C; ++c) s[c] = 1.0 / (1.0 + exp(-static_cast<double>(l[c])));
+  } else {
+    double sum = 0.0;
+#pragma unroll
+    for (int c = 0; c < C; ++c) {
+      s[c] = (on >> c) & 1 ? softmax_part(l[c], m) : 0.0;
+      sum += s[c];
+    }
+    sum = row_sum(sum);
+    const double inv = sum == 0.0 ? 0.0 : 1.0 / sum;
+#pragma unroll
+    for (int c = 0; c < C; ++c) s[c] *= inv;
+  }
+  if (p.bias) {
+#pragma unroll
+    for (int c = 0; c < C; ++c)
+      if ((on >> c) & 1) s[c] += static_cast<double>(p.bias[expert_of<VEC>(c, lane)]);
+  }
+  if (p.groups > 1) {
+    wave_sync();
+#pragma unroll
+    for (int c = 0; c < C; ++c)
+      if ((on >> c) & 1) mine[expert_of<VEC>(c, lane)] = static_cast<uint64_t>(__double_as_longlong(s[c]));
+    wave_sync();
+    keep_groups<C, VEC>(p, mine, lane, tok, on);
+  }
+  uint64_t key[C];
+#pragma unroll
+  for (int c = 0; c < C; ++c) key[c] = (on >> c) & 1 ? order_key(s[c]) : 0;
+  int my_e = 0;
+  for (int j = 0; j < p.k; ++j) {
+    uint64_t best = 0;
+#pragma unroll
+    for (int c = 0; c < C; ++c) best = key[c] > best ? key[c] : best;
+    best = row_max(best);
+    uint32_t e_best = 0xFFFFFFFFu;
+#pragma unroll
+    for (int c = 0; c < C; ++c) {
+      const uint32_t e = expert_of<VEC>(c, lane);
+      if (key[c] == best && e < e_best) e_best = e;
+    }
+    e_best = row_min(e_best);
+#pragma unroll
+    for (int c = 0; c < C; ++c)
+      if (static_cast<uint32_t>(expert_of<VEC>(c, lane)) == e_best) key[c] = 0;
+    if (lane == j) my_e = static_cast<int>(e_best);
+  }
+  return my_e;
+}
+
+// ---------------------------------------------------------------------------
+// The choice in 32 bits, and whether it is sure to be that of 64: every value
+// further below the one before it than both can be off.  A lane's values carry
+// their place c in the key's last four bits, so that a maximum brings it along,
+// which cuts the value by up to 2^-19 of itself.  Ties, NaN and infinities are
+// never sure.  Then the wave chooses again in 64 bits.
+// ---------------------------------------------------------------------------
+__device__ __forceinline__ uint32_t order_key32(float c) {
+  const uint32_t b = __float_as_uint(c);
+  return b ^ (static_cast<uint32_t>(static_cast<int32_t>(b) >> 31) | 0x80000000u);
+}
+__device__ __forceinline__ float key_value32(uint32_t k) {
+  k &= ~15u;
+  return __uint_as_float(k & 0x80000000u ? k ^ 0x80000000u : ~k);
+}
+
+// keep_groups in 32 bits; false where two groups at the border are within `edge`.
+template <int C, bool VEC>
+__device__ __forceinline__ bool keep_groups32(const ScoreArgs& p, float* val, float edge, int lane, int tok,
+                                              uint32_t& on) {
+  const int size = p.E / p.groups;
+  float sum[4];
+#pragma unroll
+  for (int u = 0; u < 4; ++u) {
+    const int g = u * kRow + lane;
+    float b0 = -INFINITY, b1 = -INFINITY;
+    if (g < p.groups) {
+      auto take = [&](float v) {
+        b1 = fmaxf(b1, fminf(b0, v));
+        b0 = fmaxf(b0, v);
+      };
+      if (VEC && size % 4 == 0) {
+        const float4* q = reinterpret_cast<const float4*>(val + g * size);
+        int i = (g + tok) % (size / 4);  // lanes start apart, else they would meet on one LDS bank
+        for (int n = 0; n < size / 4; ++n) {
+          const float4 v = q[i];
+          if (++i == size / 4) i = 0;
+          take(v.x); take(v.y); take(v.z); take(v.w);
+        }
+      } else {
+        int i = (g + tok) % size;
+        for (int n = 0; n < size; ++n) {
+          take(val[g * size + i]);
+          if (++i == size) i = 0;
+        }
+      }
+    }
+    sum[u] = p.group_best == 1 ? b0 : b0 + b1;
+  }
+  wave_sync();
+#pragma unroll
+  for (int u = 0; u < 4; ++u)
+    if (u * kRow + lane < p.groups) val[u * kRow + lane] = sum[u];
+  wave_sync();
+  uint32_t stay = 0;
+  bool sure = true;
+#pragma unroll
+  for (int u = 0; u < 4; ++u) {
+    if (u * kRow + lane < p.groups) {
+      int over = 0, near = 0;  // groups that come first for sure, and that may
+      for (int h = 0; h < p.groups; ++h) {
+        over += val[h] > sum[u] + edge;
+        near += val[h] >= sum[u] - edge;
+      }
+      stay |= static_cast<uint32_t>(over < p.top_groups) << u;
+      sure = sure && (over >= p.top_groups || near <= p.top_groups);  // near counts the group itself
+    }
+  }
+  wave_sync();
+#pragma unroll
+  for (int u = 0; u < 4; ++u)
+    if (u * kRow + lane < p.groups) val[u * kRow + lane] = (stay >> u) & 1 ? 1.f : 0.f;
+  wave_sync();
+#pragma unroll
+  for (int c = 0; c < C; ++c) {
+    const int e = expert_of<VEC>(c, lane);
+    if (e < p.E && val[e / size] == 0.f) on &= ~(1u << c);
+  }
+  return sure;
+}
+
+template <int C, bool VEC>
+__device__ __forceinline__ bool choose_fast(const ScoreArgs& p, const float (&s)[C], float most, uint32_t on, float* mine,
+                                            int lane, int tok, int& my_e) {
+  float c[C], check = 0.f;
+#pragma unroll
+  for (int i = 0; i < C; ++i) c[i] = s[i];
+  if (p.bias) {
+    if constexpr (VEC) {
+#pragma unroll
+      for (int i = 0; i < C; i += 4) {
+        const int e = expert_of<VEC>(i, lane);
+        const float4 b = e < p.E ? *reinterpret_cast<const float4*>(p.bias + e) : make_float4(0.f, 0.f, 0.f, 0.f);
+        c[i] += b.x; c[i + 1] += b.y; c[i + 2] += b.z; c[i + 3] += b.w;
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < C; ++i) {
+        const int e = expert_of<VEC>(i, lane);
+        c[i] += e < p.E ? p.bias[e] : 0.f;
+      }
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < C; ++i) check = fmaf(c[i], 0.f, check);
+  bool sure = check == 0.f;  // a NaN or an infinity makes it NaN
+  // a choice is off by tol + rel |c| at most.  Without a bias it is off relative to itself: by 2^-24 of the exponent
+  // (up to 44: smaller ones are below tol), a few units, and the key's 2^-19
+  const float tol = p.bias ? (p.sigmoid ? 0x1p-22f : 0x1p-19f * most) : 0x1p-62f * most;
+  const float rel = p.bias ? 0x1p-18f : 0x1p-17f;
+  if (p.groups > 1) {
+    if constexpr (VEC) {
+#pragma unroll
+      for (int i = 0; i < C; i += 4)
+        if ((on >> i) & 1)
+          *reinterpret_cast<float4*>(mine + expert_of<VEC>(i, lane)) = make_float4(c[i], c[i + 1], c[i + 2], c[i + 3]);
+    } else {
+#pragma unroll
+      for (int i = 0; i < C; ++i)
+        if ((on >> i) & 1) mine[expert_of<VEC>(i, lane)] = c[i];
+    }
+    wave_sync();
+    float mag = 0.f;
+#pragma unroll
+    for (int i = 0; i < C; ++i) mag = (on >> i) & 1 ? fmaxf(mag, fabsf(c[i])) : mag;
+    // two sums of two choices each, not cut yet: their terms may cancel
+    const float edge = 4.0f * tol + (p.bias ? 0x1p-20f : 0x1p-16f) * row_fmax(mag);
+    sure = keep_groups32<C, VEC>(p, mine, edge, lane, tok, on) && sure;
+  }
+  uint32_t key[C];
+#pragma unroll
+  for (int i = 0; i < C; ++i) key[i] = (on >> i) & 1 ? (order_key32(c[i]) & ~15u) | i : 0u;
+  const int row = (threadIdx.x & 63) / kRow;
+  float last = 0.f;
+  for (int j = 0; j <= p.k; ++j) {  // one more than k: the first that is left out
+    uint32_t own = 0;
+#pragma unroll
+    for (int i = 0; i < C; ++i) own = max(own, key[i]);
+    const uint32_t best = row_max(own);
+    const uint32_t owners = static_cast<uint32_t>(__ballot(own == best) >> (row * kRow)) & 0xFFFFu;
+    const float v = key_value32(best);
+    sure = sure && (j == 0 || best == 0 || last - v > 2.0f * (tol + rel * fabsf(last)));
+    last = v;
+    if (j < p.k) {
+      sure = sure && (owners & (owners - 1)) == 0;
+      const int i = best & 15, ln = __ffs(owners) - 1;
+      const int e = VEC ? ((i >> 2) * kRow + ln) * 4 + (i & 3) : i * kRow + ln;
+      if (lane == j) my_e = e;
+      if (own == best) {
+#pragma unroll
+        for (int q = 0; q < C; ++q) key[q] = key[q] == best ? 0u : key[q];
+      }
+    }
+  }
+  return sure;
+}
+
 template <int C, bool VEC>
 __global__ __launch_bounds__(kSelThreads) void score_select_kernel(ScoreArgs p) {
   extern __shared__ __align__(16) unsigned char smem[];
-  unsigned long long* mask = reinterpret_cast<unsigned long long*>(smem);           // [E]
-  uint64_t* rows = reinterpret_cast<uint64_t*>(smem + static_cast<size_t>(p.E) * 8);  // [kTok][E] with groups
+  unsigned long long* mask = reinterpret_cast<unsigned long long*>(smem);                // [E]
+  // with groups, the choices of the tokens: [kTok][E] of 8 bytes (of which the first way uses 4)
+  const int E = p.E;
+  uint64_t* rows = reinterpret_cast<uint64_t*>(smem + ((E * 8 + 15) & ~15));
   const int tid = threadIdx.x, lane = tid & (kRow - 1), tok = tid / kRow;
   const int64_t t = static_cast<int64_t>(blockIdx.x) * kTok + tok;
   const bool live = t < p.T;
-  const float* row = p.logits + (live ? t : p.T - 1) * p.E;  // lanes without a token follow the last one
-  const int E = p.E;
+  const float* row = p.logits + (live ? t : p.T - 1) * E;  // lanes without a token follow the last one
 
   float l[C];
   if constexpr (VEC) {
@@ -195,84 +454,46 @@ __global__ __launch_bounds__(kSelThreads) void score_select_kernel(ScoreArgs p) 
     }
   }
   for (int e = tid; e < E; e += kSelThreads) mask[e] = 0ull;
-
   uint32_t on = 0;
 #pragma unroll
   for (int c = 0; c < C; ++c) on |= static_cast<uint32_t>(expert_of<VEC>(c, lane) < E) << c;
 
-  double s[C];
+  // scores in 32 bits; softmax's maximum and sum serve the gates too
+  float s[C], m = 0.f, sum = 1.f, inv = 1.f;
   if (p.sigmoid) {
 #pragma unroll
-    for (int c = 0; c < C; ++c) s[c] = 1.0 / (1.0 + exp(-static_cast<double>(l[c])));
+    for (int c = 0; c < C; ++c) s[c] = sigmoid_f(l[c]);
   } else {
-    float m = -INFINITY;
+    m = -INFINITY;
 #pragma unroll
     for (int c = 0; c < C; ++c) m = (on >> c) & 1 ? fmaxf(m, l[c]) : m;
     m = row_fmax(m);
-    double sum = 0.0;
+    sum = 0.f;
 #pragma unroll
     for (int c = 0; c < C; ++c) {
-      s[c] = (on >> c) & 1 ? softmax_part(l[c], m) : 0.0;
+      s[c] = (on >> c) & 1 ? (m == -INFINITY ? softmax_part32(l[c], m) : __expf(l[c] - m)) : 0.f;
       sum += s[c];
     }
     sum = row_sum(sum);
-    const double inv = sum == 0.0 ? 0.0 : 1.0 / sum;
+    inv = sum == 0.f ? 0.f : 1.0f / sum;
 #pragma unroll
     for (int c = 0; c < C; ++c) s[c] *= inv;
   }
-
-  uint64_t key[C];
-  if (p.groups > 1) {
-    uint64_t* mine = rows + static_cast<size_t>(tok) * E;
-#pragma unroll
-    for (int c = 0; c < C; ++c) {
-      const int e = expert_of<VEC>(c, lane);
-      if (e < E) mine[e] = static_cast<uint64_t>(__double_as_longlong(s[c] + (p.bias ? static_cast<double>(p.bias[e]) : 0.0)));
-    }
-    wave_sync();
-    keep_groups<C, VEC>(p, mine, lane, tok, on);
-  }
-#pragma unroll
-  for (int c = 0; c < C; ++c) {
-    const int e = expert_of<VEC>(c, lane);
-    key[c] = (on >> c) & 1 ? order_key(s[c] + (p.bias ? static_cast<double>(p.bias[e]) : 0.0)) : 0;
-  }
-
+  uint64_t* mine = rows + static_cast<size_t>(tok) * E;
   int my_e = 0;
-  double my_s = 0.0;
-  for (int j = 0; j < p.k; ++j) {
-    uint64_t best = 0;
-#pragma unroll
-    for (int c = 0; c < C; ++c) best = key[c] > best ? key[c] : best;
-    best = row_max(best);
-    uint32_t e_best = 0xFFFFFFFFu;
-#pragma unroll
-    for (int c = 0; c < C; ++c) {
-      const uint32_t e = expert_of<VEC>(c, lane);
-      if (key[c] == best && e < e_best) e_best = e;
-    }
-    e_best = row_min(e_best);
-    double s_best = 0.0;
-#pragma unroll
-    for (int c = 0; c < C; ++c)
-      if (static_cast<uint32_t>(expert_of<VEC>(c, lane)) == e_best) {
-        key[c] = 0;
-        s_best = s[c];
-      }
-    s_best = row_sum(s_best);  // one lane's; the others add zeros
-    if (lane == j) {
-      my_e = static_cast<int>(e_best);
-      my_s = s_best;
-    }
+  const bool sure = choose_fast<C, VEC>(p, s, inv, on, reinterpret_cast<float*>(mine), lane, tok, my_e);
+  if (!__all(sure)) my_e = choose_exact<C, VEC>(p, l, m, on, mine, lane, tok);
+
+  // the gate of lane j's expert, in 64 bits
+  const float lj = lane < p.k ? row[my_e] : -INFINITY;
+  const float mj = p.renorm ? row_fmax(lj) : m;
+  double gate = 0.0;
+  if (lane < p.k) {
+    if (p.sigmoid) gate = 1.0 / (1.0 + exp(-static_cast<double>(lj)));
+    else if (!p.renorm) gate = sum == 0.f ? 0.0 : softmax_part(lj, m) / sum;
+    else gate = sum != sum ? NAN : softmax_part(lj, mj);  // from the chosen logits alone: the sum divides out
   }
-  double gate = my_s;
   if (p.renorm) {
-    // softmax: from the chosen logits alone, which the sum over all of them divides out of
-    if (!p.sigmoid) {
-      const float lj = lane < p.k ? row[my_e] : -INFINITY;
-      const float m = row_fmax(lj);  // by all lanes
-      gate = my_s != my_s ? my_s : (lane < p.k ? softmax_part(lj, m) : 0.0);
-    }
     const double tot = row_sum(gate);
     gate = tot == 0.0 ? 0.0 : gate / tot;
   }
@@ -284,8 +505,20 @@ __global__ __launch_bounds__(kSelThreads) void score_select_kernel(ScoreArgs p) 
     atomicOr(&mask[my_e], 1ull << tok);
   }
   __syncthreads();
-  if (chosen) p.rank[t * p.k + lane] = __popcll(mask[my_e] & ((1ull << tok) - 1ull));
-  for (int e = tid; e < E; e += kSelThreads) p.blk_counts[e * p.nblk + blockIdx.x] = __popcll(mask[e]);
+  const int below = chosen ? __popcll(mask[my_e] & ((1ull << tok) - 1ull)) : 0;
+  if (p.nblk > 1) {
+    if (chosen) p.rank[t * p.k + lane] = below;
+    for (int e = tid; e < E; e += kSelThreads) p.blk_counts[e * p.nblk + blockIdx.x] = __popcll(mask[e]);
+    return;
+  }
+  // a single workgroup: the metadata at once
+  __shared__ int32_t first[kMaxE];
+  offsets_of(tid < E ? __popcll(mask[tid]) : 0, E, first, p.counts, p.offsets, p.mx_blk_offsets);
+  if (chosen) {
+    const int at = first[my_e] + below;
+    p.perm_dst[t * p.k + lane] = at;
+    p.perm_src[at] = static_cast<int32_t>(t * p.k + lane);
+  }
 }
 
 // One wave per expert: its counts over the workgroups become exclusive sums in
@@ -322,37 +555,9 @@ __global__ __launch_bounds__(256) void score_scatter_kernel(const int32_t* __res
                                                             int32_t* __restrict__ perm_src,
                                                             int32_t* __restrict__ perm_dst) {
   __shared__ int32_t first[kMaxE];
-  __shared__ int32_t part[2][4];
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  const int own = tid < E ? counts[tid] : 0, ownb = (own + 31) / 32;
-  int incl = own, inclb = ownb;
-#pragma unroll
-  for (int o = 1; o < 64; o <<= 1) {
-    const int up = __shfl_up(incl, o, 64), upb = __shfl_up(inclb, o, 64);
-    if (lane >= o) {
-      incl += up;
-      inclb += upb;
-    }
-  }
-  if (lane == 63) {
-    part[0][wave] = incl;
-    part[1][wave] = inclb;
-  }
-  __syncthreads();
-  for (int w = 0; w < wave; ++w) {
-    incl += part[0][w];
-    inclb += part[1][w];
-  }
-  first[tid] = incl - own;
-  if (blockIdx.x == 0 && tid < E) {
-    if (tid == 0) {
-      offsets[0] = 0;
-      if (mx_blk_offsets) mx_blk_offsets[0] = 0;
-    }
-    offsets[tid + 1] = incl;
-    if (mx_blk_offsets) mx_blk_offsets[tid + 1] = inclb;
-  }
-  __syncthreads();
+  const int tid = threadIdx.x;
+  const bool out = blockIdx.x == 0;
+  offsets_of(tid < E ? counts[tid] : 0, E, first, nullptr, out ? offsets : nullptr, mx_blk_offsets);
   const int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + tid;
   if (i >= R) return;
   const int64_t b = i / (k * kTok);
@@ -468,7 +673,7 @@ size_t score_ws_bytes(int64_t T, int E, int k) {
 
 template <int C>
 void launch_score_select(const ScoreArgs& a, hipStream_t s) {
-  const size_t lds = static_cast<size_t>(a.E) * 8 + (a.groups > 1 ? static_cast<size_t>(kTok) * a.E * 8 : 0);
+  const size_t lds = align_up(static_cast<size_t>(a.E) * 8, 16) + (a.groups > 1 ? static_cast<size_t>(kTok) * a.E * 8 : 0);
   const dim3 grid(static_cast<unsigned>(a.nblk)), block(kSelThreads);
   if (a.E % 4 == 0) MOE_LAUNCH("score_select", (score_select_kernel<C, true>), grid, block, lds, s, a);
   else MOE_LAUNCH("score_select", (score_select_kernel<C, false>), grid, block, lds, s, a);
@@ -508,11 +713,13 @@ extern "C" int moe_route_scored(const float* logits, const float* bias, int64_t 
   int32_t* blk = reinterpret_cast<int32_t*>(static_cast<char*>(ws) + align_up(static_cast<size_t>(R) * 4, 256));
   if (T > 0) {
     const ScoreArgs a{logits, bias, T, E, k, score == MOE_SIGMOID, top_groups == groups ? 1 : groups,  // all stay
-                      top_groups, group_best, renorm, scale, topk_idx, gates, rank, blk, nblk};
+                      top_groups, group_best, renorm, scale, topk_idx, gates, rank, blk, nblk, counts, offsets, perm_src, perm_dst,
+                      mx_blk_offsets};
     if (E <= 64) launch_score_select<4>(a, s);
     else if (E <= 128) launch_score_select<8>(a, s);
     else launch_score_select<16>(a, s);
   }
+  if (nblk == 1) return launch_status();
   MOE_LAUNCH("score_scan", score_scan_kernel, dim3(static_cast<unsigned>(E)), dim3(64), 0, s, blk, nblk, counts);
   MOE_LAUNCH("score_scatter", score_scatter_kernel, dim3(static_cast<unsigned>(R > 0 ? cdiv(R, 256) : 1)), dim3(256), 0,
              s, topk_idx, rank, blk, nblk, R, k, E, counts, offsets, mx_blk_offsets, perm_src, perm_dst);

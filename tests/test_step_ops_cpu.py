@@ -140,12 +140,12 @@ def test_adamw_validation(L):
     assert step(rows=({"weight_decay": 3e38, "lr_scale": 1e30},), lr=1.0) == EINVAL
     assert step(rows=({"n": 1 << 37},), length=1 << 40) == EUNSUP
 
-    def values(q=FAKE, s=FAKE, n=64, out=FAKE):
-        return L.moe_adamw_state_values(q, s, n, out, None)
+    def values(m=FAKE, ms=FAKE, v=FAKE, vs=FAKE, n=64, mo=FAKE, vo=FAKE):
+        return L.moe_adamw_state_values(m, ms, v, vs, n, mo, vo, None)
 
-    assert values(n=0, q=None) == 0
+    assert values(n=0, m=None) == 0
     assert values(n=-32) == values(n=33) == EINVAL
-    for name in ("q", "s", "out"):
+    for name in ("m", "ms", "v", "vs", "mo", "vo"):
         assert values(**{name: None}) == values(**{name: ODD}) == EINVAL, name
     assert values(n=1 << 40) == EUNSUP
 
