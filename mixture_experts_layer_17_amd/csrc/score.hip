@@ -270,11 +270,17 @@ __device__ __forceinline__ int choose_exact(const ScoreArgs& p, const float (&l)
 }
 
 // ---------------------------------------------------------------------------
-// The choice in 32 bits, and whether it is sure to be that of 64: every value
-// further below the one before it than both can be off.  A lane's values carry
+// The choice in 32 bits, which finds the candidates, and that of 64 among them.
+// A value may be off by tol + rel |c|, so where two that follow each other are
+// nearer than both may be off, the candidates (with those that may come before the
+// k-th) are ordered by their choices in 64 bits, one a lane.  A lane's values carry
 // their place c in the key's last four bits, so that a maximum brings it along,
-// which cuts the value by up to 2^-19 of itself.  Ties, NaN and infinities are
-// never sure.  Then the wave chooses again in 64 bits.
+// which cuts the value by up to 2^-19 of itself.  Where that does not tell (NaN,
+// infinities, more than 16 candidates, groups too near at their border) the wave
+// chooses by choose_exact.  16384 x 256 sigmoid scores, bias, 8 groups: 17 us
+// without a near pair, 21 like this, 28 with choose_exact for every wave that has one (some
+// wave of every compute unit's 16 does, and the others wait for it), 34 all in
+// 64 bits.
 // ---------------------------------------------------------------------------
 __device__ __forceinline__ uint32_t order_key32(float c) {
   const uint32_t b = __float_as_uint(c);
@@ -350,9 +356,43 @@ __device__ __forceinline__ bool keep_groups32(const ScoreArgs& p, float* val, fl
   return sure;
 }
 
+// The candidates of a row's lanes (experts, -1: none) in the order of their choices in 64 bits, as choose_exact forms
+// them: each lane counts those before its own.
 template <int C, bool VEC>
-__device__ __forceinline__ bool choose_fast(const ScoreArgs& p, const float (&s)[C], float most, uint32_t on, float* mine,
-                                            int lane, int tok, int& my_e) {
+__device__ __forceinline__ int by_choice(const ScoreArgs& p, const float (&l)[C], float m, uint32_t on, int e, int lane,
+                                         const float* logits) {
+  double c = 0.0;
+  if (p.sigmoid) {
+    if (e >= 0) c = 1.0 / (1.0 + exp(-static_cast<double>(logits[e])));
+  } else {
+    double inv = 1.0;
+    if (p.bias) {
+      double sum = 0.0;
+#pragma unroll
+      for (int i = 0; i < C; ++i) sum += (on >> i) & 1 ? softmax_part(l[i], m) : 0.0;
+      sum = row_sum(sum);
+      inv = sum == 0.0 ? 0.0 : 1.0 / sum;
+    }
+    if (e >= 0) c = softmax_part(logits[e], m) * inv;
+  }
+  if (p.bias && e >= 0) c += static_cast<double>(p.bias[e]);
+  const uint64_t key = e >= 0 ? order_key(c) : 0;
+  const uint32_t at = e >= 0 ? static_cast<uint32_t>(e) : 0x10000u + lane;
+  int before = 0;
+  auto count = [&](uint64_t k, uint32_t a) { before += k > key || (k == key && a < at); };
+  count(ror<1>(key), ror<1>(at)); count(ror<2>(key), ror<2>(at)); count(ror<3>(key), ror<3>(at));
+  count(ror<4>(key), ror<4>(at)); count(ror<5>(key), ror<5>(at)); count(ror<6>(key), ror<6>(at));
+  count(ror<7>(key), ror<7>(at)); count(ror<8>(key), ror<8>(at)); count(ror<9>(key), ror<9>(at));
+  count(ror<10>(key), ror<10>(at)); count(ror<11>(key), ror<11>(at)); count(ror<12>(key), ror<12>(at));
+  count(ror<13>(key), ror<13>(at)); count(ror<14>(key), ror<14>(at)); count(ror<15>(key), ror<15>(at));
+  return __builtin_amdgcn_ds_permute((((threadIdx.x & 63) & ~(kRow - 1)) + before) * 4, e);
+}
+
+// False where the 32 bits do not tell (all lanes of the wave agree).
+template <int C, bool VEC>
+__device__ __forceinline__ bool choose_fast(const ScoreArgs& p, const float (&l)[C], const float (&s)[C], float m, float most,
+                                            uint32_t on, float* mine, int lane, int tok, const float* logits, int& my_e) {
+  const uint32_t on_all = on;
   float c[C], check = 0.f;
 #pragma unroll
   for (int i = 0; i < C; ++i) c[i] = s[i];
@@ -394,36 +434,45 @@ __device__ __forceinline__ bool choose_fast(const ScoreArgs& p, const float (&s)
     float mag = 0.f;
 #pragma unroll
     for (int i = 0; i < C; ++i) mag = (on >> i) & 1 ? fmaxf(mag, fabsf(c[i])) : mag;
-    // two sums of two choices each, not cut yet: their terms may cancel
-    const float edge = 4.0f * tol + (p.bias ? 0x1p-20f : 0x1p-16f) * row_fmax(mag);
+    // two sums of two choices each, not cut yet, whose terms may cancel: each term by its score and half a unit, each
+    // sum by a unit of at most twice the largest
+    const float edge = 4.0f * tol + (p.bias ? 0x1p-21f : 0x1p-16f) * row_fmax(mag);
     sure = keep_groups32<C, VEC>(p, mine, edge, lane, tok, on) && sure;
   }
   uint32_t key[C];
 #pragma unroll
   for (int i = 0; i < C; ++i) key[i] = (on >> i) & 1 ? (order_key32(c[i]) & ~15u) | i : 0u;
+  // lane j takes the j-th candidate: k of them, and those that 64 bits may put before the k-th
   const int row = (threadIdx.x & 63) / kRow;
-  float last = 0.f;
-  for (int j = 0; j <= p.k; ++j) {  // one more than k: the first that is left out
+  float last = 0.f, kth = 0.f;
+  bool more = true, near = false;
+  int e_mine = -1;
+  for (int j = 0; __any(more); ++j) {
     uint32_t own = 0;
 #pragma unroll
     for (int i = 0; i < C; ++i) own = max(own, key[i]);
     const uint32_t best = row_max(own);
     const uint32_t owners = static_cast<uint32_t>(__ballot(own == best) >> (row * kRow)) & 0xFFFFu;
     const float v = key_value32(best);
-    sure = sure && (j == 0 || best == 0 || last - v > 2.0f * (tol + rel * fabsf(last)));
+    const bool apart = best == 0 || last - v > 2.0f * (tol + rel * fabsf(last));
+    more = more && (j < p.k || !(best == 0 || kth - v > 2.0f * (tol + rel * fabsf(kth))));
+    sure = sure && !(more && j == kRow);  // too many of them
+    more = more && j < kRow;
+    near = near || (more && j > 0 && !apart);
     last = v;
-    if (j < p.k) {
-      sure = sure && (owners & (owners - 1)) == 0;
-      const int i = best & 15, ln = __ffs(owners) - 1;
-      const int e = VEC ? ((i >> 2) * kRow + ln) * 4 + (i & 3) : i * kRow + ln;
-      if (lane == j) my_e = e;
-      if (own == best) {
+    if (j == p.k - 1) kth = v;
+    const int i = best & 15, ln = __ffs(owners) - 1;
+    const int e = VEC ? ((i >> 2) * kRow + ln) * 4 + (i & 3) : i * kRow + ln;
+    if (more && lane == j) e_mine = e;
+    if (lane == ln) {
 #pragma unroll
-        for (int q = 0; q < C; ++q) key[q] = key[q] == best ? 0u : key[q];
-      }
+      for (int q = 0; q < C; ++q) key[q] = key[q] == best ? 0u : key[q];
     }
   }
-  return sure;
+  if (!__all(sure)) return false;
+  if (__any(near)) e_mine = by_choice<C, VEC>(p, l, m, on_all, e_mine, lane, logits);
+  my_e = e_mine < 0 ? 0 : e_mine;
+  return true;
 }
 
 template <int C, bool VEC>
@@ -481,8 +530,8 @@ __global__ __launch_bounds__(kSelThreads) void score_select_kernel(ScoreArgs p) 
   }
   uint64_t* mine = rows + static_cast<size_t>(tok) * E;
   int my_e = 0;
-  const bool sure = choose_fast<C, VEC>(p, s, inv, on, reinterpret_cast<float*>(mine), lane, tok, my_e);
-  if (!__all(sure)) my_e = choose_exact<C, VEC>(p, l, m, on, mine, lane, tok);
+  if (!choose_fast<C, VEC>(p, l, s, m, inv, on, reinterpret_cast<float*>(mine), lane, tok, row, my_e))
+    my_e = choose_exact<C, VEC>(p, l, m, on, mine, lane, tok);
 
   // the gate of lane j's expert, in 64 bits
   const float lj = lane < p.k ? row[my_e] : -INFINITY;
