@@ -149,29 +149,117 @@ __device__ __forceinline__ bool product_tile(const Product& p, int64_t id, int& 
   return true;
 }
 
+// What the epilogue reads of 32 rows of a wave's columns: all of it asked for before any of it is used, and before
+// anything is stored (outputs may lie where inputs do, so the compiler would wait for one after the other).
+template <class T, class C>
+struct EpilogueInputs {
+  static constexpr int kQuads = 8 / Elem<T>::kVec;
+  uint4 add[C::TN][2][kQuads], in_z[C::TN][2][kQuads];
+  __device__ __forceinline__ void load(const Epilogue& e, int64_t rows, int64_t row, int col) {
+#pragma unroll
+    for (int j = 0; j < C::TN; ++j)
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        const int at = col + j * 32 + 16 * c;
+        const bool ok = row < rows && at < e.ld;
+        const int64_t o = row * e.ld + at;
+#pragma unroll
+        for (int q = 0; q < kQuads; ++q) {
+          add[j][c][q] = ok && e.add ? *reinterpret_cast<const uint4*>(static_cast<const T*>(e.add) + o + q * Elem<T>::kVec)
+                                     : make_uint4(0, 0, 0, 0);
+          in_z[j][c][q] = ok && e.in_act != kActNone
+                              ? *reinterpret_cast<const uint4*>(static_cast<const T*>(e.in_z) + o + q * Elem<T>::kVec)
+                              : make_uint4(0, 0, 0, 0);
+        }
+      }
+  }
+};
+
 // The accumulators of a wave (tiles computed transposed): runs of eight columns
 // through the epilogue, or as fp32 sums where the contraction is split.
 template <class T, class C>
 __device__ __forceinline__ void finish(const Acc<C>& acc, const Product& p, int64_t row0, int col0, int split, int lane,
                                        int wm, int wn) {
   const int rl = lane & 31, hc = 8 * (lane >> 5);
+  const int64_t first = row0 + wm * C::WTM + rl;
+  const int col1 = col0 + wn * C::WTN + hc;
+  const Epilogue& e = p.epi;
+  if (p.splits == 1 && e.ld % 8 == 0) {
+    constexpr int Q = 8 / Elem<T>::kVec;
+    uint4 bias[C::TN][2][Q];
+#pragma unroll
+    for (int j = 0; j < C::TN; ++j)
+#pragma unroll
+      for (int c = 0; c < 2; ++c)
+#pragma unroll
+        for (int q = 0; q < Q; ++q) {
+          const int at = col1 + j * 32 + 16 * c;
+          bias[j][c][q] = e.bias && at < e.ld ? *reinterpret_cast<const uint4*>(static_cast<const T*>(e.bias) + at + q * Elem<T>::kVec)
+                                              : make_uint4(0, 0, 0, 0);
+        }
+    constexpr int kAhead = sizeof(T) == 2 ? 2 : 1;  // the next 32 rows' inputs are on their way, where registers allow
+    EpilogueInputs<T, C> in[kAhead];
+    if (kAhead == 2) in[0].load(e, p.rows, first, col1);
+#pragma unroll
+    for (int i = 0; i < C::TM; ++i) {
+      const int64_t row = first + i * 32;
+      if (kAhead == 1) in[0].load(e, p.rows, row, col1);
+      else if (i + 1 < C::TM) in[(i + 1) % kAhead].load(e, p.rows, row + 32, col1);
+#pragma unroll
+      for (int j = 0; j < C::TN; ++j) {
+        float v[2][8];
+        to_chunks(acc[i][j], v);
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          const int at = col1 + j * 32 + 16 * c;
+          if (row < p.rows && at < e.ld) {
+            const int64_t o = row * e.ld + at;
+            float u[8];
+#pragma unroll
+            for (int q = 0; q < Q; ++q) Elem<T>::unpack(bias[j][c][q], u + q * Elem<T>::kVec);
+#pragma unroll
+            for (int t = 0; t < 8; ++t) v[c][t] += u[t];
+            if (e.z) write8<T>(e.z, o, 8, true, v[c]);
+            if (e.act != kActNone) {
+#pragma unroll
+              for (int t = 0; t < 8; ++t) v[c][t] = act_f(v[c][t], e.act);
+            }
+            if (e.in_act != kActNone) {
+#pragma unroll
+              for (int q = 0; q < Q; ++q) Elem<T>::unpack(in[i % kAhead].in_z[j][c][q], u + q * Elem<T>::kVec);
+#pragma unroll
+              for (int t = 0; t < 8; ++t) v[c][t] *= dact_f(u[t], e.in_act);
+            }
+            if (e.add) {
+#pragma unroll
+              for (int q = 0; q < Q; ++q) Elem<T>::unpack(in[i % kAhead].add[j][c][q], u + q * Elem<T>::kVec);
+#pragma unroll
+              for (int t = 0; t < 8; ++t) v[c][t] += u[t];
+            }
+            write8<T>(e.out, o, 8, true, v[c]);
+          }
+        }
+      }
+    }
+    return;
+  }
 #pragma unroll
   for (int i = 0; i < C::TM; ++i) {
-    const int64_t row = row0 + wm * C::WTM + i * 32 + rl;
+    const int64_t row = first + i * 32;
 #pragma unroll
     for (int j = 0; j < C::TN; ++j) {
       float v[2][8];
       to_chunks(acc[i][j], v);
 #pragma unroll
       for (int c = 0; c < 2; ++c) {
-        const int col = col0 + wn * C::WTN + j * 32 + 16 * c + hc;
+        const int col = col1 + j * 32 + 16 * c;
         if (row < p.rows && col < p.cols) {
           if (p.splits > 1) {
             float* q = p.part + (split * p.rows + row) * p.part_ld + col;
             *reinterpret_cast<float4*>(q) = make_float4(v[c][0], v[c][1], v[c][2], v[c][3]);
             *reinterpret_cast<float4*>(q + 4) = make_float4(v[c][4], v[c][5], v[c][6], v[c][7]);
           } else {
-            apply8<T>(p.epi, row, col, v[c]);
+            apply8<T>(e, row, col, v[c]);
           }
         }
       }
@@ -200,6 +288,29 @@ __device__ __forceinline__ void load_kc(const uint16_t* base, int64_t ld, int ro
     const int row = i * RPI + rl;
     const int k = k0 + (ph ^ kc_swz<C::BK>(row)) * 8;
     dma16(r, dst + i * 512, k < k_end ? static_cast<int>((row * ld + k) * 2) : 0x7FFFFFF0);
+  }
+}
+
+// One K step: slice by slice fragments and products, with issue(slice) first (the next step's loads).  The stages come as
+// restricted pointers: only then does the compiler know that the loads on their way into the other stages do not touch
+// them, and does not wait for all of those before each transposing read.
+template <class C, bool AKC, bool BKC, class F>
+__device__ __forceinline__ void multiply_step(const uint16_t* __restrict__ As, const uint16_t* __restrict__ Bs, int wm, int wn,
+                                              int lane, Acc<C>& acc, F&& issue) {
+#pragma unroll
+  for (int ks = 0; ks < C::BK / 16; ++ks) {
+    issue(ks);
+    bf16x8 a[C::TM], b[C::TN];
+#pragma unroll
+    for (int i = 0; i < C::TM; ++i)
+      a[i] = AKC ? frag_kc<C>(As, wm * C::WTM + i * 32, ks, lane) : frag_mc<C, C::BM>(As, wm * C::WTM + i * 32, ks, lane);
+#pragma unroll
+    for (int j = 0; j < C::TN; ++j)
+      b[j] = BKC ? frag_kc<C>(Bs, wn * C::WTN + j * 32, ks, lane) : frag_mc<C, C::BN>(Bs, wn * C::WTN + j * 32, ks, lane);
+#pragma unroll
+    for (int i = 0; i < C::TM; ++i)
+#pragma unroll
+      for (int j = 0; j < C::TN; ++j) acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(b[j], a[i], acc[i][j], 0, 0, 0);
   }
 }
 
@@ -253,82 +364,71 @@ void linear_bf16_kernel(Product p) {
   for (int kt = 0; kt < nk; ++kt) {
     wait_vm<0>();
     __syncthreads();
-    const uint16_t* As = lds + (kt & 1) * C::kA;
-    const uint16_t* Bs = lds + C::kBOff + (kt & 1) * C::kB;
     const bool more = kt + 1 < nk;
-#pragma unroll
-    for (int ks = 0; ks < C::BK / 16; ++ks) {
+    multiply_step<C, AKC, BKC>(lds + (kt & 1) * C::kA, lds + C::kBOff + (kt & 1) * C::kB, wm, wn, lane, acc, [&](int ks) {
       if (more && ks == 0) load_a(kt + 1);
       if (more && ks == 1) load_b(kt + 1);
-      bf16x8 a[C::TM], b[C::TN];
-#pragma unroll
-      for (int i = 0; i < C::TM; ++i)
-        a[i] = AKC ? frag_kc<C>(As, wm * C::WTM + i * 32, ks, lane) : frag_mc<C, C::BM>(As, wm * C::WTM + i * 32, ks, lane);
-#pragma unroll
-      for (int j = 0; j < C::TN; ++j)
-        b[j] = BKC ? frag_kc<C>(Bs, wn * C::WTN + j * 32, ks, lane) : frag_mc<C, C::BN>(Bs, wn * C::WTN + j * 32, ks, lane);
-#pragma unroll
-      for (int i = 0; i < C::TM; ++i)
-#pragma unroll
-        for (int j = 0; j < C::TN; ++j) acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(b[j], a[i], acc[i][j], 0, 0, 0);
-    }
+    });
   }
   finish<uint16_t, C>(acc, p, row0, col0, split, lane, wm, wn);
 }
 
 // ---------------------------------------------------------------------------
-// fp32: 128 x 128 tiles, four waves of 64 x 64, K step 16, both operands in LDS
-// with the contraction along the rows.  The next step's values are on their way
-// into registers while a step is multiplied.
+// fp32: square tiles on four waves, both operands in LDS with the contraction
+// along the rows.  The next step's values are on their way into registers while
+// a step is multiplied: 64 x 64 tiles, which spread a small product over the
+// chip, take 64 of the contraction a step, so that a step outlasts its loads.
 // ---------------------------------------------------------------------------
+template <int BT, int BK_>
 struct Tile32 {
-  static constexpr int BM = 128, BN = 128, BK = 16, WN = 2, kThreads = 256;
-  static constexpr int WTM = 64, WTN = 64, TM = 2, TN = 2;
-  static constexpr int kLd = BM + 4;
+  static constexpr int BM = BT, BN = BT, BK = BK_, WN = 2, kThreads = 256;
+  static constexpr int WTM = BT / 2, WTN = BT / 2, TM = WTM / 32, TN = WTN / 32;
+  static constexpr int kN = BT * BK / 4 / kThreads;  // 16-byte vectors a thread brings per operand and step
+  // row length in LDS: rows written across (KC) start in banks of their own, whole rows on 16 bytes
+  static constexpr int ld(bool kc) { return kc ? BT + 1 : BT + 4; }
 };
+using Large32 = Tile32<128, 32>;
+using Small32 = Tile32<64, 64>;
 
-// This thread's 8 values of a BK x 128 tile.  KC: element (i, k) at p[i ld + k],
-// else at p[k ld + i]; i < n and k < k_end, zero outside.
-template <bool KC>
-__device__ __forceinline__ void fetch32(const float* p, int64_t ld, int n, int64_t k0, int64_t k_end, bool vec, int tid,
-                                        float (&v)[2][4]) {
+// This thread's values of a BK x BT tile.  KC: element (i, k) at p[i ld + k], p at the tile's first row, n rows; else at
+// p[k ld + col0 + i].  The step starts at k0 of the contraction, of which `left` are there.  Buffer loads need no more
+// than 4-byte alignment and give zero past the last row; a KC row's end is masked, and what lies past the columns of
+// the others goes into outputs that nobody stores.
+template <class C, bool KC>
+__device__ __forceinline__ void fetch32(const float* p, int64_t ld, int n, int col0, int64_t k0, int64_t left, int tid,
+                                        float (&v)[C::kN][4]) {
+  typedef unsigned int u32x4 __attribute__((ext_vector_type(4)));
+  const __amdgpu_buffer_rsrc_t r =
+      KC ? rsrc(p, (n < C::BM ? n : C::BM) * ld * 4) : rsrc(p + k0 * ld, (left < C::BK ? left : C::BK) * ld * 4);
 #pragma unroll
-  for (int u = 0; u < 2; ++u) {
-    const int id = tid + u * Tile32::kThreads;
-    const int i = KC ? id >> 2 : (id & 31) * 4;
-    const int64_t k = k0 + (KC ? (id & 3) * 4 : id >> 5);
-    const float* q = KC ? p + i * ld + k : p + k * ld + i;
-    const bool whole = KC ? (i < n && k + 3 < k_end) : (i + 3 < n && k < k_end);
-    if (vec && whole) {
-      const float4 f = *reinterpret_cast<const float4*>(q);
-      v[u][0] = f.x; v[u][1] = f.y; v[u][2] = f.z; v[u][3] = f.w;
-    } else {
+  for (int u = 0; u < C::kN; ++u) {
+    const int id = tid + u * C::kThreads;
+    const int i = KC ? id / (C::BK / 4) : id % (C::BM / 4) * 4;
+    const int k = KC ? id % (C::BK / 4) * 4 : id / (C::BM / 4);
+    const int64_t at = KC ? i * ld + k0 + k : k * ld + col0 + i;
+    const u32x4 f = __builtin_amdgcn_raw_buffer_load_b128(r, static_cast<int>(at * 4), 0, 0);
 #pragma unroll
-      for (int s = 0; s < 4; ++s) {
-        const bool ok = KC ? (i < n && k + s < k_end) : (i + s < n && k < k_end);
-        v[u][s] = ok ? q[s] : 0.f;
-      }
-    }
+    for (int s = 0; s < 4; ++s) v[u][s] = KC && k + s >= left ? 0.f : __uint_as_float(f[s]);
   }
 }
-template <bool KC>
-__device__ __forceinline__ void place32(float* t, int tid, const float (&v)[2][4]) {
+template <class C, bool KC>
+__device__ __forceinline__ void place32(float* t, int tid, const float (&v)[C::kN][4]) {
 #pragma unroll
-  for (int u = 0; u < 2; ++u) {
-    const int id = tid + u * Tile32::kThreads;
+  for (int u = 0; u < C::kN; ++u) {
+    const int id = tid + u * C::kThreads;
     if constexpr (KC) {
 #pragma unroll
-      for (int s = 0; s < 4; ++s) t[((id & 3) * 4 + s) * Tile32::kLd + (id >> 2)] = v[u][s];
+      for (int s = 0; s < 4; ++s) t[(id % (C::BK / 4) * 4 + s) * C::ld(true) + id / (C::BK / 4)] = v[u][s];
     } else {
-      *reinterpret_cast<float4*>(t + (id >> 5) * Tile32::kLd + (id & 31) * 4) = make_float4(v[u][0], v[u][1], v[u][2], v[u][3]);
+      *reinterpret_cast<float4*>(t + id / (C::BM / 4) * C::ld(false) + id % (C::BM / 4) * 4) = make_float4(v[u][0], v[u][1], v[u][2], v[u][3]);
     }
   }
 }
 
-template <bool AKC, bool BKC>
-__global__ __launch_bounds__(Tile32::kThreads) void linear_f32_kernel(Product p) {
-  using C = Tile32;
-  __shared__ __attribute__((aligned(16))) float lds[2][2][C::BK * C::kLd];
+template <class C, bool AKC, bool BKC>
+__global__ __launch_bounds__(C::kThreads) __attribute__((amdgpu_waves_per_eu(2))) void linear_f32_kernel(Product p) {
+  constexpr int lda = C::ld(AKC), ldb = C::ld(BKC);
+  __shared__ __attribute__((aligned(16))) float as[2][C::BK * lda], bs[2][C::BK * ldb];
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int wm = wave / C::WN, wn = wave % C::WN;
@@ -337,13 +437,12 @@ __global__ __launch_bounds__(Tile32::kThreads) void linear_f32_kernel(Product p)
   const int64_t row0 = static_cast<int64_t>(mt) * C::BM;
   const int col0 = nt * C::BN;
   const int64_t k0 = split * p.per_split;
-  const int64_t k_end = p.depth - k0 < p.per_split ? p.depth : k0 + p.per_split;
-  const int nk = static_cast<int>((k_end - k0 + C::BK - 1) / C::BK);
-  const float* A = static_cast<const float*>(p.a) + (AKC ? row0 * p.lda : row0);
-  const float* B = static_cast<const float*>(p.b) + (BKC ? col0 * p.ldb : col0);
+  const int64_t len = p.depth - k0 < p.per_split ? p.depth - k0 : p.per_split;
+  const int nk = static_cast<int>((len + C::BK - 1) / C::BK);
+  const float* A = static_cast<const float*>(p.a) + (AKC ? row0 * p.lda : 0);
+  const float* B = static_cast<const float*>(p.b) + (BKC ? col0 * p.ldb : 0);
   const int rows = static_cast<int>(p.rows - row0 < C::BM ? p.rows - row0 : C::BM);
   const int cols = p.cols - col0 < C::BN ? p.cols - col0 : C::BN;
-  const bool va = p.lda % 4 == 0, vb = p.ldb % 4 == 0;
 
   Acc<C> acc;
 #pragma unroll
@@ -352,27 +451,27 @@ __global__ __launch_bounds__(Tile32::kThreads) void linear_f32_kernel(Product p)
     for (int j = 0; j < C::TN; ++j)
 #pragma unroll
       for (int r = 0; r < 16; ++r) acc[i][j][r] = 0.f;
-  float fa[2][4], fb[2][4];
-  fetch32<AKC>(A, p.lda, rows, k0, k_end, va, tid, fa);
-  fetch32<BKC>(B, p.ldb, cols, k0, k_end, vb, tid, fb);
+  float fa[C::kN][4], fb[C::kN][4];
+  auto fetch = [&](int kt) {
+    const int64_t k = static_cast<int64_t>(kt) * C::BK;
+    fetch32<C, AKC>(A, p.lda, rows, static_cast<int>(row0), k0 + k, len - k, tid, fa);
+    fetch32<C, BKC>(B, p.ldb, cols, col0, k0 + k, len - k, tid, fb);
+  };
+  fetch(0);
   for (int kt = 0; kt < nk; ++kt) {
-    float* As = lds[kt & 1][0];
-    float* Bs = lds[kt & 1][1];
-    place32<AKC>(As, tid, fa);
-    place32<BKC>(Bs, tid, fb);
+    const int st = kt & 1;
+    place32<C, AKC>(as[st], tid, fa);
+    place32<C, BKC>(bs[st], tid, fb);
     __syncthreads();  // also: every wave is past the step before last, whose stage this was
-    if (kt + 1 < nk) {
-      fetch32<AKC>(A, p.lda, rows, k0 + (kt + 1) * C::BK, k_end, va, tid, fa);
-      fetch32<BKC>(B, p.ldb, cols, k0 + (kt + 1) * C::BK, k_end, vb, tid, fb);
-    }
-#pragma unroll
+    if (kt + 1 < nk) fetch(kt + 1);
+#pragma unroll 8
     for (int k = 0; k < C::BK; k += 2) {
-      const int kr = (k + (lane >> 5)) * C::kLd + (lane & 31);
+      const int kr = k + (lane >> 5);
       float a[C::TM], b[C::TN];
 #pragma unroll
-      for (int i = 0; i < C::TM; ++i) a[i] = As[kr + wm * C::WTM + i * 32];
+      for (int i = 0; i < C::TM; ++i) a[i] = as[st][kr * lda + wm * C::WTM + i * 32 + (lane & 31)];
 #pragma unroll
-      for (int j = 0; j < C::TN; ++j) b[j] = Bs[kr + wn * C::WTN + j * 32];
+      for (int j = 0; j < C::TN; ++j) b[j] = bs[st][kr * ldb + wn * C::WTN + j * 32 + (lane & 31)];
 #pragma unroll
       for (int i = 0; i < C::TM; ++i)
 #pragma unroll
@@ -393,6 +492,7 @@ __global__ __launch_bounds__(256) void linear_join_kernel(Product p) {
   const int64_t row = i / per;
   const int col = static_cast<int>(i - row * per) * 8;
   float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+#pragma unroll 8
   for (int s = 0; s < p.splits; ++s) {
     const float* q = p.part + (s * p.rows + row) * p.part_ld + col;
     const float4 a = *reinterpret_cast<const float4*>(q), b = *reinterpret_cast<const float4*>(q + 4);
@@ -466,21 +566,24 @@ __global__ __launch_bounds__(256) void linear_dz_kernel(DzArgs p) {
   }
 }
 
-// db = the chunks' sums in order: 32 columns by 8 parts of the chunks.
+// db = the chunks' sums in order: 16 columns by 16 parts of the chunks, each part's loads eight at a time.
 template <class T>
 __global__ __launch_bounds__(256) void linear_db_kernel(const float* __restrict__ part, int64_t part_ld, int64_t chunks,
                                                         int cols, T* __restrict__ db) {
-  __shared__ float sums[8][32];
-  const int c = threadIdx.x & 31, ph = threadIdx.x >> 5;
-  const int64_t col = static_cast<int64_t>(blockIdx.x) * 32 + c;
+  __shared__ float sums[16][16];
+  const int c = threadIdx.x & 15, ph = threadIdx.x >> 4;
+  const int64_t col = static_cast<int64_t>(blockIdx.x) * 16 + c;
   float acc = 0.f;
-  if (col < cols)
-    for (int64_t k = ph; k < chunks; k += 8) acc += part[k * part_ld + col];
+  if (col < cols) {
+#pragma unroll 8
+    for (int64_t k = ph; k < chunks; k += 16) acc += part[k * part_ld + col];
+  }
   sums[ph][c] = acc;
   __syncthreads();
   if (ph == 0 && col < cols) {
     acc = 0.f;
-    for (int q = 0; q < 8; ++q) acc += sums[q][c];
+#pragma unroll
+    for (int q = 0; q < 16; ++q) acc += sums[q][c];
     Elem<T>::store1(db, col, acc);
   }
 }
@@ -497,29 +600,41 @@ struct Plan {
   size_t part_bytes;
 };
 
-// Tile size and split of a product by the estimated time: rounds of workgroups
-// over the chip times their K steps, plus the second launch of a split.
+// The two tile sizes of a type: BT x BT outputs, K steps of bk, workgroups that a compute unit holds at once, and what
+// was measured (us): a K step with one workgroup on a unit and with all that fit, first loads and epilogue likewise.
+struct TileCost {
+  int bt, bk, per_cu;
+  double step1, step, fixed1, fixed;
+};
+constexpr TileCost kTiles[2][2] = {
+    {{64, 64, 2, 1.6, 2.9, 4.0, 5.0}, {128, 32, 2, 2.6, 4.6, 4.0, 6.0}},        // fp32
+    {{128, 64, 2, 0.67, 1.0, 5.0, 5.0}, {256, 64, 1, 1.2, 1.6, 5.0, 11.0}},     // bf16
+};
+
+// Tile size and split of a product by the estimated time: whole rounds of workgroups over the chip and what is left
+// behind them, plus the second launch of a split.
 Plan plan_product(int dtype, int64_t rows, int64_t cols, int64_t depth) {
   Plan best{};
   double least = 1e300;
-  const int bk = dtype == MOE_BF16 ? 64 : 16;
-  const int64_t steps = cdiv(depth, bk);
-  for (int wide = 0; wide <= (dtype == MOE_BF16 ? 1 : 0); ++wide) {
-    const int bt = wide ? 256 : 128;
-    const int64_t tiles = cdiv(rows, bt) * cdiv(cols, bt);
-    const double step_us = dtype == MOE_F32 ? 1.7 : wide ? 2.4 : 1.4;
-    const double fixed_us = wide ? 6.0 : 3.0;
-    const int64_t slots = wide ? kCUs : 2 * kCUs;
+  for (int wide = 0; wide < 2; ++wide) {
+    const TileCost& c = kTiles[dtype == MOE_BF16][wide];
+    const int64_t steps = cdiv(depth, c.bk), tiles = cdiv(rows, c.bt) * cdiv(cols, c.bt), slots = c.per_cu * kCUs;
     for (int s = 1; s <= 64; s *= 2) {
       const int64_t per = cdiv(steps, s);
       if (s > 1 && (per < 2 || cdiv(steps, per) <= s / 2)) break;
-      const double bytes = s > 1 ? (s + 1.0) * rows * cols * 4 : 0;
+      const int n = static_cast<int>(cdiv(steps, per));
+      const double bytes = n > 1 ? (n + 1.0) * rows * cols * 4 : 0;
       if (bytes > 1.0e9) break;
-      const double t = cdiv(tiles * s, slots) * (per * step_us + fixed_us) + (s > 1 ? 4.0 + bytes / 3.0e6 : 0.0);
+      const int64_t groups = tiles * n, left = groups % slots;
+      double t = groups / slots * (per * c.step + c.fixed);
+      if (left > 0) {
+        const double full = c.per_cu == 1 ? static_cast<double>(left) / kCUs : left > kCUs ? 1.0 : 0.0;
+        t += per * (c.step1 + full * (c.step - c.step1)) + c.fixed1 + full * (c.fixed - c.fixed1);
+      }
+      if (n > 1) t += 5.0 + bytes / 3.0e6;
       if (t < least) {
         least = t;
-        const int n = static_cast<int>(cdiv(steps, per));
-        best = Plan{wide != 0, n, per * bk, up8(cols), n > 1 ? align_up(static_cast<size_t>(n) * rows * up8(cols) * 4, 256) : 0};
+        best = Plan{wide != 0, n, per * c.bk, up8(cols), n > 1 ? align_up(static_cast<size_t>(n) * rows * up8(cols) * 4, 256) : 0};
       }
     }
   }
@@ -531,7 +646,7 @@ int launch_product(const void* a, int64_t lda, const void* b, int64_t ldb, int64
                    const Epilogue& epi, void* part, const char* name, hipStream_t s) {
   constexpr bool bf = sizeof(T) == 2;
   const Plan pl = plan_product(bf ? MOE_BF16 : MOE_F32, rows, cols, depth);
-  const int bt = bf && pl.wide ? 256 : 128;
+  const int bt = kTiles[bf][pl.wide].bt;
   Product p{a, b, lda, ldb, rows, static_cast<int>(cols), depth, static_cast<int>(cdiv(rows, bt)),
             static_cast<int>(cdiv(cols, bt)), pl.splits, pl.per_split, static_cast<float*>(part), pl.part_ld, epi};
   const dim3 grid(xcd_grid(static_cast<int64_t>(p.gm) * p.gn * p.splits));
@@ -539,7 +654,8 @@ int launch_product(const void* a, int64_t lda, const void* b, int64_t ldb, int64
     if (pl.wide) MOE_LAUNCH(name, (linear_bf16_kernel<Wide, AKC, BKC>), grid, dim3(Wide::kThreads), 0, s, p);
     else MOE_LAUNCH(name, (linear_bf16_kernel<Narrow, AKC, BKC>), grid, dim3(Narrow::kThreads), 0, s, p);
   } else {
-    MOE_LAUNCH(name, (linear_f32_kernel<AKC, BKC>), grid, dim3(Tile32::kThreads), 0, s, p);
+    if (pl.wide) MOE_LAUNCH(name, (linear_f32_kernel<Large32, AKC, BKC>), grid, dim3(Large32::kThreads), 0, s, p);
+    else MOE_LAUNCH(name, (linear_f32_kernel<Small32, AKC, BKC>), grid, dim3(Small32::kThreads), 0, s, p);
   }
   if (p.splits > 1)
     MOE_LAUNCH("linear_join", linear_join_kernel<T>, dim3(static_cast<unsigned>(cdiv(rows * (pl.part_ld / 8), 256))),
@@ -634,7 +750,7 @@ int linear_bwd(const void* dy, const void* x, const void* w, const void* z, int6
     MOE_LAUNCH("linear_dz", linear_dz_kernel<T>, dim3(static_cast<unsigned>(cdiv(N, 512)), static_cast<unsigned>(chunks)),
                dim3(256), 0, s, a);
     if (db)
-      MOE_LAUNCH("linear_db", linear_db_kernel<T>, dim3(static_cast<unsigned>(cdiv(N, 32))), dim3(256), 0, s, sums, up8(N),
+      MOE_LAUNCH("linear_db", linear_db_kernel<T>, dim3(static_cast<unsigned>(cdiv(N, 16))), dim3(256), 0, s, sums, up8(N),
                  chunks, static_cast<int>(N), static_cast<T*>(db));
     if (write) dz = ws + b.dz;
   }
