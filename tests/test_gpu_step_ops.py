@@ -250,7 +250,8 @@ def test_bias_update_over_sequences(gpu):
 # ------------------------------------------------------------------- dense product
 
 LINEAR = [(1, 1, 1), (1, 2048, 1024), (2, 8, 8), (3, 5, 7), (17, 64, 64), (130, 72, 200), (129, 129, 65), (257, 300, 1001),
-          (1000, 512, 256), (33, 4097, 40), (5, 40, 2051), (700, 16, 16), (256, 2048, 256), (2049, 96, 513)]
+          (1000, 512, 256), (33, 4097, 40), (5, 40, 2051), (700, 16, 16), (256, 2048, 256), (2049, 96, 513),
+          (1, 8200, 40), (2, 777, 64), (3, 8192, 36), (4, 4100, 72), (4, 33, 1000), (1, 63, 32), (3, 129, 4104)]
 ACTS = ["none", "relu", "silu", "gelu"]
 
 
