@@ -17,6 +17,7 @@
 // its row into exclusive sums, and the workgroups of the last launch make the
 // experts' offsets from the totals themselves.  No step runs on one workgroup.
 #include <cmath>
+#include <type_traits>
 
 #include "common.hpp"
 
@@ -115,6 +116,25 @@ struct ScoreArgs {
 template <bool VEC>
 __device__ __forceinline__ int expert_of(int c, int lane) {
   return VEC ? ((c >> 2) * kRow + lane) * 4 + (c & 3) : c * kRow + lane;
+}
+
+// A lane's values of a row; `none` past its end.
+template <int C, bool VEC>
+__device__ __forceinline__ void load_row(const float* row, int E, int lane, float none, float (&x)[C]) {
+  if constexpr (VEC) {
+#pragma unroll
+    for (int c = 0; c < C; c += 4) {
+      const int e = expert_of<VEC>(c, lane);
+      const float4 v = e < E ? *reinterpret_cast<const float4*>(row + e) : make_float4(none, none, none, none);
+      x[c] = v.x; x[c + 1] = v.y; x[c + 2] = v.z; x[c + 3] = v.w;
+    }
+  } else {
+#pragma unroll
+    for (int c = 0; c < C; ++c) {
+      const int e = expert_of<VEC>(c, lane);
+      x[c] = e < E ? row[e] : none;
+    }
+  }
 }
 
 // Offsets of the experts, for thread tid = expert with its count: exclusive sums
@@ -488,20 +508,7 @@ __global__ __launch_bounds__(kSelThreads) void score_select_kernel(ScoreArgs p) 
   const float* row = p.logits + (live ? t : p.T - 1) * E;  // lanes without a token follow the last one
 
   float l[C];
-  if constexpr (VEC) {
-#pragma unroll
-    for (int c = 0; c < C; c += 4) {
-      const int e = expert_of<VEC>(c, lane);
-      const float4 v = e < E ? *reinterpret_cast<const float4*>(row + e) : make_float4(0.f, 0.f, 0.f, 0.f);
-      l[c] = v.x; l[c + 1] = v.y; l[c + 2] = v.z; l[c + 3] = v.w;
-    }
-  } else {
-#pragma unroll
-    for (int c = 0; c < C; ++c) {
-      const int e = expert_of<VEC>(c, lane);
-      l[c] = e < E ? row[e] : 0.f;
-    }
-  }
+  load_row<C, VEC>(row, E, lane, 0.f, l);
   for (int e = tid; e < E; e += kSelThreads) mask[e] = 0ull;
   uint32_t on = 0;
 #pragma unroll
@@ -592,6 +599,39 @@ __global__ __launch_bounds__(64) void score_scan_kernel(int32_t* __restrict__ bl
   if (lane == 0) counts[e] = base;
 }
 
+// Scan and scatter at once, for few counts: a workgroup takes the 64 tokens of its routing block and sums the counts of
+// all blocks for itself, those before its own apart.
+__global__ __launch_bounds__(256) void score_place_kernel(const int32_t* __restrict__ topk_idx,
+                                                          const int32_t* __restrict__ rank,
+                                                          const int32_t* __restrict__ blk, int64_t nblk, int64_t R, int k,
+                                                          int E, int32_t* __restrict__ counts,
+                                                          int32_t* __restrict__ offsets,
+                                                          int32_t* __restrict__ mx_blk_offsets,
+                                                          int32_t* __restrict__ perm_src, int32_t* __restrict__ perm_dst) {
+  __shared__ int32_t first[kMaxE];
+  const int tid = threadIdx.x, mine = blockIdx.x;
+  int own = 0, before = 0;
+  if (tid < E) {
+    const int32_t* row = blk + tid * nblk;
+#pragma unroll 8
+    for (int b = 0; b < nblk; ++b) {
+      const int c = row[b];
+      own += c;
+      before += b < mine ? c : 0;
+    }
+  }
+  offsets_of(own, E, first, mine == 0 ? counts : nullptr, mine == 0 ? offsets : nullptr, mx_blk_offsets);
+  first[tid] += before;  // its own entry, which the others read after the barrier
+  __syncthreads();
+  const int64_t i0 = static_cast<int64_t>(mine) * kTok * k;
+  for (int u = tid; u < kTok * k && i0 + u < R; u += 256) {
+    const int64_t i = i0 + u;
+    const int row = first[topk_idx[i]] + rank[i];
+    perm_dst[i] = row;
+    perm_src[row] = static_cast<int32_t>(i);
+  }
+}
+
 // Every workgroup makes the experts' offsets (exclusive sums of the counts) for
 // itself; the first one writes them out.
 __global__ __launch_bounds__(256) void score_scatter_kernel(const int32_t* __restrict__ topk_idx,
@@ -637,28 +677,34 @@ struct ScoreBwdArgs {
   float* dlogits;
 };
 
-template <bool VEC>
+template <int C, bool VEC>
 __global__ __launch_bounds__(256) void score_bwd_kernel(ScoreBwdArgs p) {
   extern __shared__ __align__(16) float brow[];
   const int tid = threadIdx.x, lane = tid & (kRow - 1), tok = tid / kRow;
   const int64_t t = static_cast<int64_t>(blockIdx.x) * (256 / kRow) + tok;
   const bool live = t < p.T;
   const int64_t tt = live ? t : p.T - 1;
-  const int E = p.E, ld = VEC ? E + 4 : E;
+  const int E = p.E;
   const float* row = p.logits + tt * E;
-  float* out = brow + tok * ld;
+  float* add = brow + tok * E;  // what the slots add to their experts' gradients
   const bool slot = lane < p.k;
   const int e = slot ? p.topk_idx[tt * p.k + lane] : 0;
   const float dg = slot ? p.scale * p.dgates[tt * p.k + lane] : 0.f;
   const float l = slot ? row[e] : -INFINITY;
   const bool full = !p.sigmoid && !p.renorm;
 
-  float m = -INFINITY, inv = 0.f;
+  float x[C], m = -INFINITY, inv = 0.f;
   if (full) {
-    float sum = 0.f;
-    for (int c = lane; c < E; c += kRow) m = fmaxf(m, row[c]);
+    load_row<C, VEC>(row, E, lane, -INFINITY, x);
+#pragma unroll
+    for (int c = 0; c < C; ++c) m = fmaxf(m, x[c]);
     m = row_fmax(m);
-    for (int c = lane; c < E; c += kRow) sum += softmax_part32(row[c], m);
+    float sum = 0.f;
+#pragma unroll
+    for (int c = 0; c < C; ++c) {
+      x[c] = expert_of<VEC>(c, lane) < E ? softmax_part32(x[c], m) : 0.f;
+      sum += x[c];
+    }
     sum = row_sum(sum);
     inv = sum == 0.f ? 0.f : 1.0f / sum;
   } else if (!p.sigmoid) {
@@ -674,23 +720,33 @@ __global__ __launch_bounds__(256) void score_bwd_kernel(ScoreBwdArgs p) {
   const double dl = p.sigmoid ? ds * s / (1.0 + exp(static_cast<double>(l))) : s * ds;
   const float inner = full ? static_cast<float>(row_sum(dl)) : 0.f;
 
-  for (int c = lane; c < E; c += kRow) out[c] = full ? -softmax_part32(row[c], m) * inv * inner : 0.f;
+#pragma unroll
+  for (int c = 0; c < C; ++c)
+    if (expert_of<VEC>(c, lane) < E) add[expert_of<VEC>(c, lane)] = 0.f;
   wave_sync();
-  if (slot) out[e] += static_cast<float>(dl);
+  if (slot) add[e] = static_cast<float>(dl);
   wave_sync();
   if (!live) return;
   float* dst = p.dlogits + t * E;
-  if constexpr (VEC) {
-    for (int c = 4 * lane; c < E; c += 4 * kRow) {
-      float4 v = *reinterpret_cast<const float4*>(out + c);
+#pragma unroll
+  for (int c = 0; c < C; c += VEC ? 4 : 1) {
+    const int at = expert_of<VEC>(c, lane);
+    if (at >= E) continue;
+    if constexpr (VEC) {
+      float4 v = *reinterpret_cast<const float4*>(add + at);
+      if (full) {
+        v.x -= x[c] * inv * inner; v.y -= x[c + 1] * inv * inner; v.z -= x[c + 2] * inv * inner; v.w -= x[c + 3] * inv * inner;
+      }
       if (p.accumulate) {
-        const float4 a = *reinterpret_cast<const float4*>(dst + c);
+        const float4 a = *reinterpret_cast<const float4*>(dst + at);
         v.x += a.x; v.y += a.y; v.z += a.z; v.w += a.w;
       }
-      *reinterpret_cast<float4*>(dst + c) = v;
+      *reinterpret_cast<float4*>(dst + at) = v;
+    } else {
+      float v = add[at];
+      if (full) v -= x[c] * inv * inner;
+      dst[at] = p.accumulate ? dst[at] + v : v;
     }
-  } else {
-    for (int c = lane; c < E; c += kRow) dst[c] = p.accumulate ? dst[c] + out[c] : out[c];
   }
 }
 
@@ -769,6 +825,13 @@ extern "C" int moe_route_scored(const float* logits, const float* bias, int64_t 
     else launch_score_select<16>(a, s);
   }
   if (nblk == 1) return launch_status();
+  // few counts: every workgroup can sum them for itself, which is a launch less (5003 x 60, 79 workgroups: 23.6 -> 21.0 us
+  // a call; with 256 x 256 counts they read 64 MB)
+  if (nblk > 0 && nblk * E <= 8192) {
+    MOE_LAUNCH("score_place", score_place_kernel, dim3(static_cast<unsigned>(nblk)), dim3(256), 0, s, topk_idx, rank, blk,
+               nblk, R, k, E, counts, offsets, mx_blk_offsets, perm_src, perm_dst);
+    return launch_status();
+  }
   MOE_LAUNCH("score_scan", score_scan_kernel, dim3(static_cast<unsigned>(E)), dim3(64), 0, s, blk, nblk, counts);
   MOE_LAUNCH("score_scatter", score_scatter_kernel, dim3(static_cast<unsigned>(R > 0 ? cdiv(R, 256) : 1)), dim3(256), 0,
              s, topk_idx, rank, blk, nblk, R, k, E, counts, offsets, mx_blk_offsets, perm_src, perm_dst);
@@ -787,10 +850,15 @@ extern "C" int moe_route_scored_bwd(const float* logits, const int32_t* topk_idx
   hipStream_t s = static_cast<hipStream_t>(stream);
   constexpr int kTokens = 256 / kRow;
   const dim3 grid(static_cast<unsigned>(cdiv(T, kTokens))), block(256);
-  if (E % 4 == 0)
-    MOE_LAUNCH("score_bwd", score_bwd_kernel<true>, grid, block, static_cast<size_t>(kTokens) * (E + 4) * 4, s, a);
-  else
-    MOE_LAUNCH("score_bwd", score_bwd_kernel<false>, grid, block, static_cast<size_t>(kTokens) * E * 4, s, a);
+  const size_t lds = static_cast<size_t>(kTokens) * E * 4;
+  auto launch = [&](auto c) {
+    constexpr int C = decltype(c)::value;
+    if (E % 4 == 0) MOE_LAUNCH("score_bwd", (score_bwd_kernel<C, true>), grid, block, lds, s, a);
+    else MOE_LAUNCH("score_bwd", (score_bwd_kernel<C, false>), grid, block, lds, s, a);
+  };
+  if (E <= 64) launch(std::integral_constant<int, 4>{});
+  else if (E <= 128) launch(std::integral_constant<int, 8>{});
+  else launch(std::integral_constant<int, 16>{});
   return launch_status();
 }
 
