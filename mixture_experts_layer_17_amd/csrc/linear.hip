@@ -28,23 +28,32 @@ constexpr int64_t kMaxWidth = 1 << 20;
 
 enum { kActNone = MOE_ACT_NONE, kActRelu = MOE_ACT_RELU, kActSilu = MOE_ACT_SILU, kActGelu = MOE_ACT_GELU };
 
-__device__ __forceinline__ float act_f(float z, int act) {
-  switch (act) {
-    case kActRelu: return z > 0.f || z != z ? z : 0.f;
-    case kActSilu: return silu_f(z);
-    case kActGelu: return 0.5f * z * erfcf(-0.70710678f * z);
-    default: return z;
+// v[i] = act(v[i]), and v[i] *= act'(z[i]); one choice for all eight.
+__device__ __forceinline__ void act8(float (&v)[8], int act) {
+  if (act == kActSilu) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = silu_f(v[i]);
+  } else if (act == kActGelu) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = 0.5f * v[i] * erfcf(-0.70710678f * v[i]);
+  } else if (act == kActRelu) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = v[i] > 0.f || v[i] != v[i] ? v[i] : 0.f;
   }
 }
-__device__ __forceinline__ float dact_f(float z, int act) {
-  switch (act) {
-    case kActRelu: return z > 0.f ? 1.f : 0.f;
-    case kActSilu: {
-      const float s = sigmoid_f(z);
-      return s * (1.0f + z * (1.0f - s));
+__device__ __forceinline__ void times_dact8(float (&v)[8], const float (&z)[8], int act) {
+  if (act == kActSilu) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const float s = sigmoid_f(z[i]);
+      v[i] *= s * (1.0f + z[i] * (1.0f - s));
     }
-    case kActGelu: return 0.5f * erfcf(-0.70710678f * z) + z * 0.39894228f * __expf(-0.5f * z * z);
-    default: return 1.f;
+  } else if (act == kActGelu) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] *= 0.5f * erfcf(-0.70710678f * z[i]) + z[i] * 0.39894228f * __expf(-0.5f * z[i] * z[i]);
+  } else if (act == kActRelu) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] *= z[i] > 0.f ? 1.f : 0.f;
   }
 }
 
@@ -97,14 +106,10 @@ __device__ __forceinline__ void apply8(const Epilogue& e, int64_t row, int col, 
     for (int i = 0; i < 8; ++i) v[i] += u[i];
   }
   if (e.z) write8<T>(e.z, o, valid, vec, v);
-  if (e.act != kActNone) {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = act_f(v[i], e.act);
-  }
+  act8(v, e.act);
   if (e.in_act != kActNone) {
     read8<T>(e.in_z, o, valid, vec, u);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] *= dact_f(u[i], e.in_act);
+    times_dact8(v, u, e.in_act);
   }
   if (e.add) {
     read8<T>(e.add, o, valid, vec, u);
@@ -220,15 +225,11 @@ __device__ __forceinline__ void finish(const Acc<C>& acc, const Product& p, int6
 #pragma unroll
             for (int t = 0; t < 8; ++t) v[c][t] += u[t];
             if (e.z) write8<T>(e.z, o, 8, true, v[c]);
-            if (e.act != kActNone) {
-#pragma unroll
-              for (int t = 0; t < 8; ++t) v[c][t] = act_f(v[c][t], e.act);
-            }
+            act8(v[c], e.act);
             if (e.in_act != kActNone) {
 #pragma unroll
               for (int q = 0; q < Q; ++q) Elem<T>::unpack(in[i % kAhead].in_z[j][c][q], u + q * Elem<T>::kVec);
-#pragma unroll
-              for (int t = 0; t < 8; ++t) v[c][t] *= dact_f(u[t], e.in_act);
+              times_dact8(v[c], u, e.in_act);
             }
             if (e.add) {
 #pragma unroll
@@ -624,8 +625,7 @@ __global__ __launch_bounds__(256) void linear_dz_kernel(DzArgs p) {
       read8<T>(p.dy, r * p.cols + col, valid, vec, g);
       if (p.z) {
         read8<T>(p.z, r * p.cols + col, valid, vec, z);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) g[i] *= dact_f(z[i], p.act);
+        times_dact8(g, z, p.act);
       }
       // behind the last column: zeros, as the products need them (ld_dz is a multiple of 8 for bf16)
       if (p.dz) write8<T>(p.dz, r * p.ld_dz + col, p.ld_dz - col < 8 ? p.ld_dz - col : 8, p.ld_dz % Elem<T>::kVec == 0 && p.ld_dz - col >= 8, g);
