@@ -154,7 +154,8 @@ int moe_route_topk_bwd(const float* gates, const float* dgates, const int32_t* t
  * moe_route_topk writes them, for the calls that take its metadata.
  * MOE_EINVAL for groups that do not divide E, top_groups outside 1..groups, fewer than
  * k experts in top_groups groups, group_best above a group's size, a scale that is not
- * finite, a null or unaligned pointer; MOE_EUNSUPPORTED for more than 64 groups.
+ * finite, a null or unaligned pointer; MOE_EUNSUPPORTED for more than 64 groups and for
+ * T > 2^28 - 64 (the backward's too).
  * T = 0 is allowed (counts and offsets become zero). */
 typedef enum { MOE_SOFTMAX = 0, MOE_SIGMOID = 1 } moe_score;
 size_t moe_route_scored_workspace(int64_t T, int32_t E, int32_t k);

@@ -118,6 +118,9 @@ __device__ __forceinline__ int expert_of(int c, int lane) {
   return VEC ? ((c >> 2) * kRow + lane) * 4 + (c & 3) : c * kRow + lane;
 }
 
+// e / size for e below 256 without a division: (e + 1/2) / size is at least 1/512 away from a whole number.
+__device__ __forceinline__ int group_of(int e, float per) { return static_cast<int>((static_cast<float>(e) + 0.5f) * per); }
+
 // A lane's values of a row; `none` past its end.
 template <int C, bool VEC>
 __device__ __forceinline__ void load_row(const float* row, int E, int lane, float none, float (&x)[C]) {
@@ -225,10 +228,11 @@ __device__ __forceinline__ void keep_groups(const ScoreArgs& p, uint64_t* key, i
   for (int u = 0; u < 4; ++u)
     if (u * kRow + lane < p.groups) key[u * kRow + lane] = (stay >> u) & 1;
   wave_sync();
+  const float per = 1.0f / static_cast<float>(size);
 #pragma unroll
   for (int c = 0; c < C; ++c) {
     const int e = expert_of<VEC>(c, lane);
-    if (e < p.E && !key[e / size]) on &= ~(1u << c);
+    if (e < p.E && !key[group_of(e, per)]) on &= ~(1u << c);
   }
 }
 
@@ -368,10 +372,11 @@ __device__ __forceinline__ bool keep_groups32(const ScoreArgs& p, float* val, fl
   for (int u = 0; u < 4; ++u)
     if (u * kRow + lane < p.groups) val[u * kRow + lane] = (stay >> u) & 1 ? 1.f : 0.f;
   wave_sync();
+  const float per = 1.0f / static_cast<float>(size);
 #pragma unroll
   for (int c = 0; c < C; ++c) {
     const int e = expert_of<VEC>(c, lane);
-    if (e < p.E && val[e / size] == 0.f) on &= ~(1u << c);
+    if (e < p.E && val[group_of(e, per)] == 0.f) on &= ~(1u << c);
   }
   return sure;
 }
@@ -753,24 +758,32 @@ __global__ __launch_bounds__(256) void score_bwd_kernel(ScoreBwdArgs p) {
 // bias_out[e] = bias[e] + rate sign(sum of the counts - E counts[e]): up for an
 // expert below the mean load, down for one above.  Whole numbers of 64 bits, so
 // the sign is exact.
-__global__ __launch_bounds__(256) void bias_update_kernel(const int32_t* __restrict__ counts, int64_t S, int E, float rate,
-                                                          const float* __restrict__ bias, float* __restrict__ bias_out) {
-  __shared__ long long total[4];
-  const int e = threadIdx.x;
-  long long own = 0;
-  if (e < E)
-    for (int64_t s = 0; s < S; ++s) own += counts[s * E + e];
-  long long sum = own;
-#pragma unroll
-  for (int o = 32; o >= 1; o >>= 1) sum += __shfl_xor(sum, o, 64);
-  if ((e & 63) == 0) total[e >> 6] = sum;
+__global__ __launch_bounds__(1024) void bias_update_kernel(const int32_t* __restrict__ counts, int64_t S, int E, float rate,
+                                                           const float* __restrict__ bias, float* __restrict__ bias_out) {
+  __shared__ unsigned long long n[kMaxE], total;
+  const int tid = threadIdx.x, parts = 1024 / E, e = tid % E, part = tid / E;
+  if (tid < E) n[tid] = 0;
+  if (tid == 0) total = 0;
   __syncthreads();
-  const long long diff = total[0] + total[1] + total[2] + total[3] - own * E;
-  if (e < E) bias_out[e] = diff == 0 ? bias[e] : bias[e] + (diff > 0 ? rate : -rate);
+  if (part < parts) {
+    long long own = 0;
+#pragma unroll 4
+    for (int64_t s = part; s < S; s += parts) own += counts[s * E + e];
+    atomicAdd(&n[e], static_cast<unsigned long long>(own));  // whole numbers: in any order
+    atomicAdd(&total, static_cast<unsigned long long>(own));
+  }
+  __syncthreads();
+  if (tid < E) {
+    const long long diff = static_cast<long long>(total) - static_cast<long long>(n[tid]) * E;
+    bias_out[tid] = diff == 0 ? bias[tid] : bias[tid] + (diff > 0 ? rate : -rate);
+  }
 }
 
-bool score_sizes_ok(int64_t T, int E, int k) {
-  return T >= 0 && E >= 1 && E <= kMaxE && k >= 1 && k <= kMaxK && k <= E && T < (1ll << 31) && T * k < (1ll << 31);
+// Sixteen lanes a token: more would be 2^32 threads in a launch.
+constexpr int64_t kMaxTokens = (int64_t{1} << 28) - kTok;
+int score_sizes(int64_t T, int E, int k) {
+  if (E > kMaxE || k > kMaxK || T > kMaxTokens) return MOE_EUNSUPPORTED;
+  return T >= 0 && E >= 1 && k >= 1 && k <= E && T * k < (1ll << 31) ? MOE_OK : MOE_EINVAL;
 }
 size_t score_ws_bytes(int64_t T, int E, int k) {
   return align_up(static_cast<size_t>(T * k) * 4, 256) + align_up(static_cast<size_t>(cdiv(T, kTok) * E) * 4, 256);
@@ -790,15 +803,16 @@ void launch_score_select(const ScoreArgs& a, hipStream_t s) {
 using namespace moe;
 
 extern "C" size_t moe_route_scored_workspace(int64_t T, int32_t E, int32_t k) {
-  return score_sizes_ok(T, E, k) ? score_ws_bytes(T, E, k) : 0;
+  return score_sizes(T, E, k) == MOE_OK ? score_ws_bytes(T, E, k) : 0;
 }
 
 extern "C" int moe_route_scored(const float* logits, const float* bias, int64_t T, int32_t E, int32_t k, int score,
                                 int32_t groups, int32_t top_groups, int32_t group_best, int renorm, float scale,
                                 int32_t* topk_idx, float* gates, int32_t* counts, int32_t* offsets, int32_t* perm_src,
                                 int32_t* perm_dst, int32_t* mx_blk_offsets, void* ws, size_t ws_bytes, void* stream) {
-  if (E > kMaxE || k > kMaxK) return MOE_EUNSUPPORTED;
-  if (!score_sizes_ok(T, E, k) || (score != MOE_SOFTMAX && score != MOE_SIGMOID) || !std::isfinite(scale)) return MOE_EINVAL;
+  const int sizes = score_sizes(T, E, k);
+  if (sizes != MOE_OK) return sizes;
+  if ((score != MOE_SOFTMAX && score != MOE_SIGMOID) || !std::isfinite(scale)) return MOE_EINVAL;
   if (groups < 1 || groups > E || E % groups || top_groups < 1 || top_groups > groups || group_best < 1 ||
       group_best > 2 || group_best > E / groups || static_cast<int64_t>(top_groups) * (E / groups) < k)
     return MOE_EINVAL;
@@ -841,8 +855,9 @@ extern "C" int moe_route_scored(const float* logits, const float* bias, int64_t 
 extern "C" int moe_route_scored_bwd(const float* logits, const int32_t* topk_idx, const float* dgates, int64_t T,
                                     int32_t E, int32_t k, int score, int renorm, float scale, int accumulate,
                                     float* dlogits, void* stream) {
-  if (E > kMaxE || k > kMaxK) return MOE_EUNSUPPORTED;
-  if (!score_sizes_ok(T, E, k) || (score != MOE_SOFTMAX && score != MOE_SIGMOID) || !std::isfinite(scale)) return MOE_EINVAL;
+  const int sizes = score_sizes(T, E, k);
+  if (sizes != MOE_OK) return sizes;
+  if ((score != MOE_SOFTMAX && score != MOE_SIGMOID) || !std::isfinite(scale)) return MOE_EINVAL;
   if (T == 0) return MOE_OK;
   if (!logits || !topk_idx || !dgates || !dlogits) return MOE_EINVAL;
   if (!aligned16(logits) || !aligned16(topk_idx) || !aligned16(dgates) || !aligned16(dlogits)) return MOE_EINVAL;
@@ -866,7 +881,7 @@ extern "C" int moe_route_bias_update(const int32_t* counts, int64_t S, int32_t E
                                      float* bias_out, void* stream) {
   if (E < 1 || E > kMaxE || S < 1 || !counts || !bias || !bias_out || !std::isfinite(rate)) return MOE_EINVAL;
   if (!aligned16(counts) || !aligned16(bias) || !aligned16(bias_out)) return MOE_EINVAL;
-  MOE_LAUNCH("route_bias_update", bias_update_kernel, dim3(1), dim3(256), 0, static_cast<hipStream_t>(stream), counts,
+  MOE_LAUNCH("route_bias_update", bias_update_kernel, dim3(1), dim3(1024), 0, static_cast<hipStream_t>(stream), counts,
              S, E, rate, bias, bias_out);
   return launch_status();
 }

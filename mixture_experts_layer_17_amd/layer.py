@@ -303,6 +303,8 @@ class LayerStep:
 
     def update_router_bias(self, rate: float):
         """Move the balancing bias by the load of the last forward (without padded tokens where balance counts them)."""
+        if "router_bias" not in self.inp:
+            raise B.MoeError("update_router_bias: the inputs have no router_bias")
         counts = self.route["counts"] if self.balance_coef is None else self.balance["counts"]
         return B.moe_route_bias_update(counts, self.inp["router_bias"], rate)
 

@@ -238,7 +238,7 @@ def test_softmax_routing_matches_route_topk(gpu):
 def test_bias_update_over_sequences(gpu):
     gu.say("case bias update")
     rng = np.random.default_rng(2)
-    for S, E in ((1, 1), (7, 33), (500, 256)):
+    for S, E in ((1, 1), (7, 33), (500, 256), (20000, 5)):
         c, b = rng.integers(0, 9, (S, E)).astype(np.int32), rng.standard_normal(E).astype(np.float32)
         c[:, -1] = 0
         bt = torch.from_numpy(b).cuda()

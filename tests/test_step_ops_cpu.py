@@ -49,7 +49,8 @@ def test_route_scored_validation(L):
     need = L.moe_route_scored_workspace(10, 16, 2)
     assert need > 0 and fwd(n=need - 1) == EWS
     assert L.moe_route_scored_workspace(10, 300, 2) == L.moe_route_scored_workspace(10, 2, 3) == 0
-    assert L.moe_route_scored_workspace(1 << 31, 8, 1) == 0
+    assert L.moe_route_scored_workspace(1 << 31, 8, 1) == L.moe_route_scored_workspace(1 << 28, 8, 1) == 0
+    assert fwd(T=1 << 28) == fwd(T=1 << 40) == EUNSUP and L.moe_route_scored_workspace((1 << 28) - 64, 8, 1) > 0
 
     def bwd(lg=FAKE, idx=FAKE, dg=FAKE, T=10, E=16, k=2, score=0, renorm=1, scale=1.0, acc=0, out=FAKE):
         return L.moe_route_scored_bwd(lg, idx, dg, T, E, k, score, renorm, scale, acc, out, None)
@@ -58,7 +59,7 @@ def test_route_scored_validation(L):
         assert bwd(**{name: None}) == bwd(**{name: ODD}) == EINVAL, name
     assert bwd(T=0, lg=None, out=None) == 0
     assert bwd(T=-1) == bwd(score=7) == bwd(scale=NAN) == bwd(k=17, E=16, T=1) == EINVAL or bwd(k=17) == EUNSUP
-    assert bwd(E=300) == EUNSUP
+    assert bwd(E=300) == bwd(T=1 << 28) == EUNSUP
 
     def upd(c=FAKE, S=1, E=8, rate=0.1, b=FAKE, out=FAKE):
         return L.moe_route_bias_update(c, S, E, rate, b, out, None)
