@@ -376,20 +376,23 @@ void linear_bf16_kernel(Product p) {
 
 // ---------------------------------------------------------------------------
 // fp32: square tiles on four waves, both operands in LDS with the contraction
-// along the rows.  The next step's values are on their way into registers while
-// a step is multiplied: 64 x 64 tiles, which spread a small product over the
-// chip, take 64 of the contraction a step, so that a step outlasts its loads.
+// along the rows.  The next steps' values are on their way into registers while a
+// step is multiplied: two of the 128 x 128 tiles' (4096^3: 1177 -> 1073 us), one
+// of the 64 x 64 tiles', which spread a small product over the chip and take 64 of
+// the contraction a step, so that a step outlasts its loads (1001 x 333 x 777:
+// 17 us, 19 with two ahead).
 // ---------------------------------------------------------------------------
-template <int BT, int BK_>
+template <int BT, int BK_, int AHEAD>
 struct Tile32 {
+  static constexpr int kAhead = AHEAD;
   static constexpr int BM = BT, BN = BT, BK = BK_, WN = 2, kThreads = 256;
   static constexpr int WTM = BT / 2, WTN = BT / 2, TM = WTM / 32, TN = WTN / 32;
   static constexpr int kN = BT * BK / 4 / kThreads;  // 16-byte vectors a thread brings per operand and step
   // row length in LDS: rows written across (KC) start in banks of their own, whole rows on 16 bytes
   static constexpr int ld(bool kc) { return kc ? BT + 1 : BT + 4; }
 };
-using Large32 = Tile32<128, 32>;
-using Small32 = Tile32<64, 64>;
+using Large32 = Tile32<128, 32, 2>;
+using Small32 = Tile32<64, 64, 1>;
 
 // This thread's values of a BK x BT tile.  KC: element (i, k) at p[i ld + k], p at the tile's first row, n rows; else at
 // p[k ld + col0 + i].  The step starts at k0 of the contraction, of which `left` are there.  Buffer loads need no more
@@ -452,19 +455,21 @@ __global__ __launch_bounds__(C::kThreads) __attribute__((amdgpu_waves_per_eu(2))
     for (int j = 0; j < C::TN; ++j)
 #pragma unroll
       for (int r = 0; r < 16; ++r) acc[i][j][r] = 0.f;
-  float fa[C::kN][4], fb[C::kN][4];
-  auto fetch = [&](int kt) {
-    const int64_t k = static_cast<int64_t>(kt) * C::BK;
-    fetch32<C, AKC>(A, p.lda, rows, static_cast<int>(row0), k0 + k, len - k, tid, fa);
-    fetch32<C, BKC>(B, p.ldb, cols, col0, k0 + k, len - k, tid, fb);
+  struct Values {
+    float a[C::kN][4], b[C::kN][4];
   };
-  fetch(0);
-  for (int kt = 0; kt < nk; ++kt) {
+  // (past the last step: zeros, by the buffers' ends and the mask)
+  auto fetch = [&](int kt, Values& v) {
+    const int64_t k = static_cast<int64_t>(kt) * C::BK;
+    fetch32<C, AKC>(A, p.lda, rows, static_cast<int>(row0), k0 + k, len - k, tid, v.a);
+    fetch32<C, BKC>(B, p.ldb, cols, col0, k0 + k, len - k, tid, v.b);
+  };
+  auto step = [&](int kt, Values& v) {
     const int st = kt & 1;
-    place32<C, AKC>(as[st], tid, fa);
-    place32<C, BKC>(bs[st], tid, fb);
+    place32<C, AKC>(as[st], tid, v.a);
+    place32<C, BKC>(bs[st], tid, v.b);
     __syncthreads();  // also: every wave is past the step before last, whose stage this was
-    if (kt + 1 < nk) fetch(kt + 1);
+    fetch(kt + C::kAhead, v);
 #pragma unroll 8
     for (int k = 0; k < C::BK; k += 2) {
       const int kr = k + (lane >> 5);
@@ -478,6 +483,17 @@ __global__ __launch_bounds__(C::kThreads) __attribute__((amdgpu_waves_per_eu(2))
 #pragma unroll
         for (int j = 0; j < C::TN; ++j) acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x2f32(b[j], a[i], acc[i][j], 0, 0, 0);
     }
+  };
+  Values even, odd;
+  fetch(0, even);
+  if constexpr (C::kAhead == 2) {
+    fetch(1, odd);
+    for (int kt = 0; kt < nk; kt += 2) {
+      step(kt, even);
+      if (kt + 1 < nk) step(kt + 1, odd);
+    }
+  } else {
+    for (int kt = 0; kt < nk; ++kt) step(kt, even);
   }
   finish<float, C>(acc, p, row0, col0, split, lane, wm, wn);
 }
@@ -684,7 +700,7 @@ struct TileCost {
   double step1, step, fixed1, fixed;
 };
 constexpr TileCost kTiles[2][2] = {
-    {{64, 64, 2, 1.6, 2.9, 4.0, 5.0}, {128, 32, 2, 2.6, 4.6, 4.0, 6.0}},        // fp32
+    {{64, 64, 2, 1.6, 2.9, 4.0, 5.0}, {128, 32, 2, 2.3, 4.1, 7.0, 8.0}},        // fp32
     {{128, 64, 2, 0.67, 1.0, 5.0, 5.0}, {256, 64, 1, 1.2, 1.6, 5.0, 11.0}},     // bf16
 };
 

@@ -760,21 +760,27 @@ __global__ __launch_bounds__(256) void score_bwd_kernel(ScoreBwdArgs p) {
 // the sign is exact.
 __global__ __launch_bounds__(1024) void bias_update_kernel(const int32_t* __restrict__ counts, int64_t S, int E, float rate,
                                                            const float* __restrict__ bias, float* __restrict__ bias_out) {
-  __shared__ unsigned long long n[kMaxE], total;
+  __shared__ unsigned long long n[kMaxE];
+  __shared__ long long part_sum[4];
   const int tid = threadIdx.x, parts = 1024 / E, e = tid % E, part = tid / E;
-  if (tid < E) n[tid] = 0;
-  if (tid == 0) total = 0;
+  if (tid < kMaxE) n[tid] = 0;
   __syncthreads();
-  if (part < parts) {
+  if (part < parts && part < S) {
     long long own = 0;
 #pragma unroll 4
     for (int64_t s = part; s < S; s += parts) own += counts[s * E + e];
     atomicAdd(&n[e], static_cast<unsigned long long>(own));  // whole numbers: in any order
-    atomicAdd(&total, static_cast<unsigned long long>(own));
+  }
+  __syncthreads();
+  if (tid < kMaxE) {
+    long long sum = static_cast<long long>(n[tid]);
+#pragma unroll
+    for (int o = 32; o >= 1; o >>= 1) sum += __shfl_xor(sum, o, 64);
+    if ((tid & 63) == 0) part_sum[tid >> 6] = sum;
   }
   __syncthreads();
   if (tid < E) {
-    const long long diff = static_cast<long long>(total) - static_cast<long long>(n[tid]) * E;
+    const long long diff = part_sum[0] + part_sum[1] + part_sum[2] + part_sum[3] - static_cast<long long>(n[tid]) * E;
     bias_out[tid] = diff == 0 ? bias[tid] : bias[tid] + (diff > 0 ? rate : -rate);
   }
 }
