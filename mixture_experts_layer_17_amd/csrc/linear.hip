@@ -580,11 +580,10 @@ __global__ __launch_bounds__(256) void linear_few_kernel(Product p) {
 // ---------------------------------------------------------------------------
 template <class T>
 __global__ __launch_bounds__(256) void linear_join_kernel(Product p) {
-  const int64_t per = p.part_ld / 8;
-  const int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
+  const uint32_t per = static_cast<uint32_t>(p.part_ld / 8), i = blockIdx.x * 256u + threadIdx.x;  // fewer than 2^32
   if (i >= p.rows * per) return;
   const int64_t row = i / per;
-  const int col = static_cast<int>(i - row * per) * 8;
+  const int col = static_cast<int>(i % per) * 8;
   float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
 #pragma unroll 8
   for (int s = 0; s < p.splits; ++s) {
@@ -596,18 +595,38 @@ __global__ __launch_bounds__(256) void linear_join_kernel(Product p) {
   apply8<T>(p.epi, row, col, v);
 }
 
-// dst [rows, ld] = src [rows, cols], zeros behind (bf16, ld a multiple of 8).
+// dst [rows, ld] = src [rows, cols], zeros behind (bf16, ld a multiple of 8).  A
+// thread's eight values start anywhere on 2 bytes: they come as the five words
+// that hold them, shifted by half a word where the first is a word's upper half;
+// only at the very end, where those would pass it, one by one.
 __global__ __launch_bounds__(256) void pad_rows_kernel(const uint16_t* __restrict__ src, int64_t rows, int cols, int ld,
                                                        uint16_t* __restrict__ dst) {
-  const int per = ld / 8;
-  const int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
+  typedef uint32_t words __attribute__((ext_vector_type(4), aligned(4)));
+  const uint32_t per = ld / 8, i = blockIdx.x * 256u + threadIdx.x;  // fewer than 2^32
   if (i >= rows * per) return;
   const int64_t row = i / per;
-  const int c = static_cast<int>(i - row * per) * 8;
-  uint32_t w[8];
+  const int c = static_cast<int>(i % per) * 8;
+  const int64_t o = row * cols + c;
+  uint32_t w[4];
+  if (o + 10 <= rows * cols) {
+    const uint32_t* q = reinterpret_cast<const uint32_t*>(src) + (o >> 1);
+    const words v = *reinterpret_cast<const words*>(q);
+    const uint32_t f[5] = {v[0], v[1], v[2], v[3], q[4]};
 #pragma unroll
-  for (int u = 0; u < 8; ++u) w[u] = c + u < cols ? src[row * cols + c + u] : 0;
-  *reinterpret_cast<uint4*>(dst + row * ld + c) = make_uint4(w[0] | w[1] << 16, w[2] | w[3] << 16, w[4] | w[5] << 16, w[6] | w[7] << 16);
+    for (int u = 0; u < 4; ++u) w[u] = o & 1 ? f[u] >> 16 | f[u + 1] << 16 : f[u];
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      if (c + 2 * u >= cols) w[u] = 0;
+      else if (c + 2 * u + 1 >= cols) w[u] &= 0xFFFFu;
+    }
+  } else {
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      w[u] = c + 2 * u < cols ? src[o + 2 * u] : 0;
+      if (c + 2 * u + 1 < cols) w[u] |= static_cast<uint32_t>(src[o + 2 * u + 1]) << 16;
+    }
+  }
+  *reinterpret_cast<uint4*>(dst + row * ld + c) = make_uint4(w[0], w[1], w[2], w[3]);
 }
 
 // ---------------------------------------------------------------------------
