@@ -2,7 +2,11 @@
 //
 // Per element, in fp32:  m' = b1 m + (1 - b1) g,  v' = b2 v + (1 - b2) g^2,
 //   w' = (1 - lr decay) w - lr / (1 - b1^t) m' / (sqrt(v') / sqrt(1 - b2^t) + eps)
-// One pass: every operand read once and written once, which is what bounds it.
+// One pass: every operand read once and written once, which is what bounds it:
+// 50 M bf16 values with fp32 weights and states take 268 us (5.6 TB/s; a large copy
+// reaches 5.2).  268 M bf16 values with 8-bit states take 555 to 600 us (4.5 to 4.9
+// TB/s): there the hash, two codes and the root, some 70 vector operations a value,
+// take about as long as the bytes.
 //
 // The tensors' addresses and sizes travel in the kernel's arguments (kMaxList a
 // launch), so nothing is copied to the device and a captured graph keeps them.
