@@ -166,7 +166,8 @@ int moe_route_scored(const float* logits, const float* bias, int64_t T, int32_t 
 
 /* Backward of moe_route_scored's gates: the gradient of the logits for dgates [T, k]
  * (the choice itself, the groups and the bias have none).  topk_idx [T, k]: distinct
- * experts per token, as moe_route_scored wrote them for these logits.  Experts that
+ * experts per token, as moe_route_scored wrote them for these logits; a slot whose
+ * index is outside 0..E-1 (a caller's mark of padding) takes no part.  Experts that
  * were not chosen get zero, but under softmax without renorm, where every score
  * depends on all logits.  dlogits [T, E] is overwritten, or with accumulate != 0
  * added to (so it joins the gradient of moe_balance_loss_bwd). */

@@ -694,8 +694,8 @@ __global__ __launch_bounds__(256) void score_bwd_kernel(ScoreBwdArgs p) {
   const int E = p.E;
   const float* row = p.logits + tt * E;
   float* add = brow + tok * E;  // what the slots add to their experts' gradients
-  const bool slot = lane < p.k;
-  const int e = slot ? p.topk_idx[tt * p.k + lane] : 0;
+  const int e = lane < p.k ? p.topk_idx[tt * p.k + lane] : -1;
+  const bool slot = static_cast<unsigned>(e) < static_cast<unsigned>(E);  // e addresses the row: a slot outside it counts as absent
   const float dg = slot ? p.scale * p.dgates[tt * p.k + lane] : 0.f;
   const float l = slot ? row[e] : -INFINITY;
   const bool full = !p.sigmoid && !p.renorm;

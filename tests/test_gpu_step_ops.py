@@ -119,6 +119,33 @@ def test_route_scored(gpu, T, E, k, kind, bias, groups, top, best, renorm, scale
               so.bias_update(ref["counts"], b, np.float32(0.01)), half("f32") * (np.abs(b) + 0.01))
 
 
+@pytest.mark.parametrize("E", [12, 37, 250])  # rows by vectors and by single values, whole and ragged
+@pytest.mark.parametrize("kind,renorm", [("softmax", True), ("softmax", False), ("sigmoid", True), ("sigmoid", False)])
+def test_route_scored_bwd_leaves_out_slots_outside_the_experts(gpu, kind, renorm, E):
+    gu.say(f"case route_scored_bwd marked slots E={E} {kind} renorm={renorm}")
+    rng = np.random.default_rng(E)
+    T, k, scale = 53, 5, 1.5
+    lg = (rng.standard_normal((T, E)) * 2).astype(np.float32)
+    dg = rng.standard_normal((T, k)).astype(np.float32)
+    idx = so.route_scored(lg, k, kind)["topk_idx"].astype(np.int64)
+    out = rng.random((T, k)) < 0.4
+    out[0], out[1], out[T - 1] = True, False, True  # none left, all there, none left in the last row
+    marked = np.where(out, rng.choice([-1, E, -2**31, 2**31 - 1], (T, k)), idx).astype(np.int32)
+    want, bound = np.zeros((T, E)), np.zeros((T, E))
+    for t in range(T):
+        own = ~out[t]
+        if not own.any():
+            continue
+        at, dgt = idx[t:t + 1, own], dg[t:t + 1, own]
+        want[t] = so.route_scored_bwd(lg[t:t + 1], at, dgt, kind, renorm, scale)
+        s = so.scores(lg[t:t + 1], kind)
+        S = s[0, at[0]].sum() if renorm else 1.0
+        bound[t] = 8e-6 * (np.abs(want[t]) + s[0] / S * np.abs(scale * dgt).max())  # as for whole rows
+    got = B.moe_route_scored_bwd(torch.from_numpy(lg).cuda(), torch.from_numpy(marked).cuda(), torch.from_numpy(dg).cuda(),
+                                 score=kind, renorm=renorm, scale=scale)
+    close("dlogits", got, want, bound)
+
+
 @pytest.mark.parametrize("kind", ["softmax", "sigmoid"])
 @pytest.mark.parametrize("groups,top,best", [(1, 1, 1), (4, 2, 2), (8, 3, 1)])
 def test_route_scored_ties(gpu, kind, groups, top, best):
