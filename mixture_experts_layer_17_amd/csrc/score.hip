@@ -519,7 +519,7 @@ __global__ __launch_bounds__(kSelThreads) void score_select_kernel(ScoreArgs p) 
 #pragma unroll
   for (int c = 0; c < C; ++c) on |= static_cast<uint32_t>(expert_of<VEC>(c, lane) < E) << c;
 
-  // scores in 32 bits; softmax's maximum and sum serve the gates too
+  // scores in 32 bits; softmax's maximum serves the gates too
   float s[C], m = 0.f, sum = 1.f, inv = 1.f;
   if (p.sigmoid) {
 #pragma unroll
@@ -545,13 +545,20 @@ __global__ __launch_bounds__(kSelThreads) void score_select_kernel(ScoreArgs p) 
   if (!choose_fast<C, VEC>(p, l, s, m, inv, on, reinterpret_cast<float*>(mine), lane, tok, row, my_e))
     my_e = choose_exact<C, VEC>(p, l, m, on, mine, lane, tok);
 
-  // the gate of lane j's expert, in 64 bits
+  // the gate of lane j's expert, in 64 bits; where the scores are gates as they are, so is softmax's sum (a sum of 32 bits
+  // would put several roundings into a gate)
+  double total = 0.0;
+  if (!p.sigmoid && !p.renorm) {
+#pragma unroll
+    for (int c = 0; c < C; ++c) total += (on >> c) & 1 ? softmax_part(l[c], m) : 0.0;
+    total = row_sum(total);
+  }
   const float lj = lane < p.k ? row[my_e] : -INFINITY;
   const float mj = p.renorm ? row_fmax(lj) : m;
   double gate = 0.0;
   if (lane < p.k) {
     if (p.sigmoid) gate = 1.0 / (1.0 + exp(-static_cast<double>(lj)));
-    else if (!p.renorm) gate = sum == 0.f ? 0.0 : softmax_part(lj, m) / sum;
+    else if (!p.renorm) gate = total == 0.0 ? 0.0 : softmax_part(lj, m) / total;
     else gate = sum != sum ? NAN : softmax_part(lj, mj);  // from the chosen logits alone: the sum divides out
   }
   if (p.renorm) {

@@ -1,0 +1,72 @@
+"""Routing by scores, the dense product and the AdamW step where few bits, the
+ends of fp32's range or long sums decide, against the fp64 oracle.
+
+Bounds are in steps of the stored type: `ulp` is the distance of neighbouring
+fp32 values at the result, of which one rounding costs half.
+"""
+import numpy as np
+import pytest
+import torch
+
+from mixture_experts_layer_17_amd import binding as B
+from oracle import step_ops_oracle as so
+
+import gpu_util as gu
+
+pytestmark = pytest.mark.gpu
+
+INF, NAN = float("inf"), float("nan")
+U = 2.0 ** -24                                           # half a step of fp32, relative
+
+
+def h64(t):
+    return t.detach().cpu().double().numpy()
+
+
+def half_ulp(x):
+    return np.spacing(np.abs(np.asarray(x)).astype(np.float32)).astype(np.float64) / 2
+
+
+def dev(a, dtype=np.float32):
+    return torch.from_numpy(np.ascontiguousarray(np.asarray(a, dtype))).cuda()
+
+
+def within(name, got, ref, bound):
+    over = np.abs(h64(got) - ref) - bound
+    assert np.isfinite(over).all(), name
+    assert over.max() <= 0, (name, over.max(), float((over > 0).mean()))
+
+
+# ------------------------------------------------------------------- routing by scores
+
+@pytest.mark.parametrize("kind,renorm", [("softmax", False), ("softmax", True), ("sigmoid", False), ("sigmoid", True)])
+@pytest.mark.parametrize("T,E,k,spread", [(300, 8, 2, 1), (2000, 60, 6, 2), (1500, 128, 4, 1), (700, 250, 8, 30), (65, 256, 3, 3)])
+def test_gates_are_rounded_once(gpu, T, E, k, spread, kind, renorm):
+    """Gates in 64 bits, to fp32 at the end: half a step, and 2^-40 for what 64 bits leave (exp's argument of at most 2^8
+    to 2^-53, sums of 256 terms)."""
+    gu.say(f"case gates once T={T} E={E} {kind} {renorm}")
+    rng = np.random.default_rng(E)
+    lg = (spread * rng.standard_normal((T, E))).astype(np.float32)
+    for scale in (1.0, 2.5):
+        got = B.moe_route_scored(dev(lg), k, score=kind, renorm=renorm, scale=scale)
+        ref = so.route_scored(lg, k, kind, renorm=renorm, scale=scale)
+        assert np.array_equal(got["topk_idx"].cpu().numpy(), ref["topk_idx"])
+        want = ref["gates"]
+        within("gates", got["gates"], want, (U + 2.0 ** -40) * np.abs(want) + 2.0 ** -150)
+
+
+# ------------------------------------------------------------------- dense product
+
+# ------------------------------------------------------------------- AdamW
+
+def adamw_one(w, g, lr, step=1, bits=32, master=False, m=None, v=None, dtype=torch.float32, weight_decay=0.0, **kw):
+    p = [dev(w).to(dtype)]
+    state = B.moe_adamw_state(p, bits=bits, master=master)
+    n = len(w)
+    if m is not None:
+        state["m"][:n], state["v"][:n] = dev(m), dev(v)
+    if master:
+        state["master"][:n] = dev(w)
+    B.moe_adamw_step(B.moe_adamw_plan(p, [dev(g).to(dtype)], state, weight_decay=weight_decay), lr, step, **kw)
+    torch.cuda.synchronize()
+    return (state["master"][:n] if master else p[0]), state
