@@ -169,7 +169,8 @@ int moe_route_scored(const float* logits, const float* bias, int64_t T, int32_t 
  * experts per token, as moe_route_scored wrote them for these logits; a slot whose
  * index is outside 0..E-1 (a caller's mark of padding) takes no part.  Experts that
  * were not chosen get zero, but under softmax without renorm, where every score
- * depends on all logits.  dlogits [T, E] is overwritten, or with accumulate != 0
+ * depends on all logits.  Under softmax a row with a NaN or +inf logit gives NaN to
+ * its chosen experts, as its gates are NaN.  dlogits [T, E] is overwritten, or with accumulate != 0
  * added to (so it joins the gradient of moe_balance_loss_bwd). */
 int moe_route_scored_bwd(const float* logits, const int32_t* topk_idx, const float* dgates, int64_t T, int32_t E,
                          int32_t k, int score, int renorm, float scale, int accumulate, float* dlogits, void* stream);

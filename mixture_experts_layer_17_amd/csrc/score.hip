@@ -676,10 +676,12 @@ __global__ __launch_bounds__(256) void score_scatter_kernel(const int32_t* __res
 //   softmax         dl_e = s_e (ds_e - sum_j ds_j s_j), where the sum is zero
 //                   for renormalised gates: then dl is zero elsewhere too, and
 //                   s / S is the softmax over the chosen logits alone
-// So only softmax without renormalising reads whole rows.  Sixteen lanes take a
-// token, lane j its slot j, the row in registers; what the slots add meets it in
-// LDS.  16384 x 128 without renormalising: 6.6 us, 2.5 TB/s of rows read and
-// written: too short for the rate of a large copy.
+// Softmax without renormalising needs whole rows; with it they are read all the
+// same: a NaN or +inf in them, also of an expert not chosen, makes the gates NaN,
+// and the gradient must not hide that.  Sixteen lanes take a token, lane j its
+// slot j, the row in registers; what the slots add meets it in LDS.  16384 x 128
+// without renormalising: 6.6 us, 2.5 TB/s of rows read and written: too short for
+// the rate of a large copy.
 // ---------------------------------------------------------------------------
 struct ScoreBwdArgs {
   const float* logits;
@@ -707,7 +709,7 @@ __global__ __launch_bounds__(256) void score_bwd_kernel(ScoreBwdArgs p) {
   const float l = slot ? row[e] : -INFINITY;
   const bool full = !p.sigmoid && !p.renorm;
 
-  float x[C], m = -INFINITY, inv = 0.f;
+  float x[C], m = -INFINITY, inv = 0.f, whole = 1.f;
   if (full) {
     load_row<C, VEC>(row, E, lane, -INFINITY, x);
 #pragma unroll
@@ -723,9 +725,14 @@ __global__ __launch_bounds__(256) void score_bwd_kernel(ScoreBwdArgs p) {
     inv = sum == 0.f ? 0.f : 1.0f / sum;
   } else if (!p.sigmoid) {
     m = row_fmax(l);
+    load_row<C, VEC>(row, E, lane, -INFINITY, x);
+    float bad = 0.f;  // a NaN or +inf anywhere leaves the row without scores: `whole` becomes NaN
+#pragma unroll
+    for (int c = 0; c < C; ++c) bad = x[c] < INFINITY ? bad : NAN;
+    whole = 1.f + row_sum(bad);
   }
   // the slot's score (of all experts, or of the chosen ones alone) and gradient, in 64 bits: a lane has one
-  double s = 0.0, ds = dg;
+  double s = 0.0, ds = dg * whole;
   if (slot) s = p.sigmoid ? 1.0 / (1.0 + exp(-static_cast<double>(l))) : softmax_part(l, m) * (full ? inv : 1.0);
   if (p.renorm) {
     const double tot = row_sum(s), w = tot == 0.0 ? 0.0 : 1.0 / tot;

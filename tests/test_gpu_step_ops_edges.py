@@ -55,6 +55,30 @@ def test_gates_are_rounded_once(gpu, T, E, k, spread, kind, renorm):
         within("gates", got["gates"], want, (U + 2.0 ** -40) * np.abs(want) + 2.0 ** -150)
 
 
+@pytest.mark.parametrize("E", [24, 37, 128, 250])
+@pytest.mark.parametrize("renorm", [False, True])
+def test_softmax_gradient_of_a_row_without_scores_is_nan(gpu, E, renorm):
+    """A NaN or +inf logit anywhere makes the row's scores, its gates and the gradients of its chosen experts NaN."""
+    gu.say(f"case NaN rows E={E} renorm={renorm}")
+    rng = np.random.default_rng(E)
+    T, k = 40, 3
+    lg = rng.standard_normal((T, E)).astype(np.float32)
+    clean = lg.copy()
+    bad = {2: (E - 1, NAN), 9: (k, NAN), 17: (E - 2, INF), 39: (E // 2, INF)}
+    for t, (e, v) in bad.items():
+        lg[t, e] = v
+    got = B.moe_route_scored(dev(lg), k, renorm=renorm)
+    dg = dev(rng.standard_normal((T, k)))
+    d = h64(B.moe_route_scored_bwd(dev(lg), got["topk_idx"], dg, renorm=renorm))
+    want = h64(B.moe_route_scored_bwd(dev(clean), got["topk_idx"], dg, renorm=renorm))
+    gates, idx = h64(got["gates"]), got["topk_idx"].cpu().numpy()
+    for t in range(T):
+        if t in bad:
+            assert np.isnan(gates[t]).all() and np.isnan(d[t, idx[t]]).all(), t
+        else:
+            assert np.isfinite(gates[t]).all() and np.array_equal(d[t], want[t]), t
+
+
 # ------------------------------------------------------------------- dense product
 
 # ------------------------------------------------------------------- AdamW
