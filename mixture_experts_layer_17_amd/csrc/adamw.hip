@@ -1,7 +1,7 @@
 // AdamW step of a list of tensors in few launches, and the values of 8-bit states.
 //
 // Per element, in fp32:  m' = b1 m + (1 - b1) g,  v' = b2 v + (1 - b2) g^2,
-//   w' = (1 - lr decay) w - lr / (1 - b1^t) m' / (sqrt(v') / sqrt(1 - b2^t) + eps)
+//   w' = w - (lr decay w + lr / (1 - b1^t) m' / (sqrt(v') / sqrt(1 - b2^t) + eps))
 // One pass: every operand read once and written once, which is what bounds it:
 // 50 M bf16 values with fp32 weights and states take 268 us (5.6 TB/s; a large copy
 // reaches 5.2).  268 M bf16 values with 8-bit states take 555 to 600 us (4.5 to 4.9
@@ -43,7 +43,7 @@ struct ListEntry {
   int64_t offset;  // of its states, in elements
   double lr;
   float rate;      // lr / (1 - beta1^step), for a step counted on the host
-  float keep;      // 1 - lr weight_decay
+  float decay;     // lr weight_decay
   uint32_t seed;
 };
 
@@ -293,7 +293,8 @@ __global__ __launch_bounds__(kThreads) void adamw_kernel(AdamArgs p) {
 #pragma unroll
     for (int j = 0; j < kPer; ++j) {
       if (EIGHT) v[j] = root[j];
-      w[j] = t.keep * w[j] - rate * (m[j] * __builtin_amdgcn_rcpf(root[j] * root2 + p.eps));
+      // the decay is part of what is subtracted: 1 - lr weight_decay in 32 bits would be a multiple of 2^-24
+      w[j] -= fmaf(t.decay, w[j], rate * (m[j] * __builtin_amdgcn_rcpf(root[j] * root2 + p.eps)));
     }
     // behind the tensor's end (its gradient reads as zero) states and master stay what they are made of: zero
     if (valid < kPer) {
@@ -412,7 +413,7 @@ extern "C" int moe_adamw_step(const moe_adamw_tensor* tensors, int32_t count, in
       if (units + more >= kMaxUnits) break;
       const double rate = lr * t.lr_scale;
       a.list[a.count] = ListEntry{t.w, t.g, t.w_out, t.n, t.offset, rate, static_cast<float>(rate / c1),
-                                  static_cast<float>(1.0 - rate * t.weight_decay), seed + kGolden * static_cast<uint32_t>(i)};
+                                  static_cast<float>(rate * t.weight_decay), seed + kGolden * static_cast<uint32_t>(i)};
       a.first[a.count++] = static_cast<int32_t>(units);
       units += more;
     }

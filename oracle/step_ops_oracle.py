@@ -204,7 +204,8 @@ def decode(codes, byte):
 def adamw(w, g, m, v, lr, step, betas=(0.9, 0.999), eps=1e-8, weight_decay=0.0, grad_scale=1.0):
     """w', m', v' of one tensor."""
     w, g, m, v = (np.asarray(a, np.float64) for a in (w, g, m, v))
-    b1, b2 = betas
+    # numbers of 64 bits: an np.float32 among them would round 1 - lr weight_decay to 32
+    lr, b1, b2, eps, weight_decay, grad_scale = map(float, (lr, *betas, eps, weight_decay, grad_scale))
     g = g * grad_scale
     m = b1 * m + (1 - b1) * g
     v = b2 * v + (1 - b2) * g * g

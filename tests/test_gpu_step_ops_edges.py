@@ -94,3 +94,29 @@ def adamw_one(w, g, lr, step=1, bits=32, master=False, m=None, v=None, dtype=tor
     B.moe_adamw_step(B.moe_adamw_plan(p, [dev(g).to(dtype)], state, weight_decay=weight_decay), lr, step, **kw)
     torch.cuda.synchronize()
     return (state["master"][:n] if master else p[0]), state
+
+
+@pytest.mark.parametrize("product", [1e-6, 1e-7, 3e-8, 1e-8])
+@pytest.mark.parametrize("bits,master", [(32, False), (32, True), (8, False), (8, True)])
+def test_adamw_decay_of_less_than_a_step(gpu, bits, master, product):
+    """lr weight_decay below 2^-24: the decay is part of what is subtracted, so a weight is off by its own rounding and 16
+    roundings of what is subtracted, and over many weights by nothing."""
+    gu.say(f"case small decay {bits} {master} {product}")
+    rng = np.random.default_rng(3)
+    n, lr = 100000, 1e-4
+    wd = np.float32(product / lr)
+    w = (1 + rng.random(n)).astype(np.float32)
+    g = (1e-3 * (0.5 + rng.random(n))).astype(np.float32)
+    dtype = torch.bfloat16 if master else torch.float32
+    g = h64(dev(g).to(dtype))
+    # eps of the gradients' size, so that the updates differ
+    got, _ = adamw_one(w, g, lr, bits=bits, master=master, dtype=dtype, weight_decay=float(wd), eps=1e-3)
+    z = np.zeros(n)
+    want = so.adamw(w, g, z, z, lr, 1, eps=1e-3, weight_decay=wd)[0]
+    within("w", got, want, half_ulp(want) + 16 * U * np.abs(want - w))
+    # a weight in [1, 2) is a multiple of 2^-23, so how w - s rounds goes by where s lies in a step, even over the steps:
+    # weights of one gradient share it (but for the decay), and n_i of each make the mean's variance 2^-46 / 12 times
+    # sum (n_i / n)^2.  bf16 gradients have some 190 values.  5 standard deviations, besides the 16 roundings above
+    mean = abs((h64(got) - want).mean())
+    share = np.unique(g, return_counts=True)[1] / n
+    assert mean < 5 * 2.0 ** -23 * np.sqrt((share * share).sum() / 12) + 16 * U * np.abs(want - w).mean(), mean
