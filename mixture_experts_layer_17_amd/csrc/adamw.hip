@@ -246,6 +246,7 @@ __global__ __launch_bounds__(kThreads) void adamw_kernel(AdamArgs p) {
   const float b1 = static_cast<float>(p.beta1), b2 = static_cast<float>(p.beta2);
   const float a1 = static_cast<float>(1.0 - p.beta1), a2 = static_cast<float>(1.0 - p.beta2);
   const float b1_low = static_cast<float>(p.beta1 - b1), a1_low = static_cast<float>(1.0 - p.beta1 - a1);
+  const float b2_low = static_cast<float>(p.beta2 - b2);
   float rate = t.rate, root2 = p.root2;
   if (p.step_dev) {
     rate = static_cast<float>(t.lr / (1.0 - int_pow(p.beta1, step)));
@@ -284,9 +285,11 @@ __global__ __launch_bounds__(kThreads) void adamw_kernel(AdamArgs p) {
         m[j] = fmaf(b1, m[j], t) + low;
         v[j] *= v[j];
       } else {
-        m[j] = b1 * m[j] + a1 * gg;
+        m[j] = fmaf(b1, m[j], fmaf(b1_low, fminf(fmaxf(m[j], -3.402823466e38f), 3.402823466e38f), a1 * gg));
       }
-      v[j] = b2 * v[j] + a2 * gg * gg;
+      // a beta in 32 bits is off by up to 2^-25, a large part of 1 - beta near 1 (at 0.99999 a thousandth, in the end all of
+      // it): the rest of it joins what is added (of the largest finite value at most, so that an infinite state stays one)
+      v[j] = fmaf(b2, v[j], fmaf(b2_low, fminf(v[j], 3.402823466e38f), a2 * gg * gg));
     }
     float root[kPer];
     square_roots(v, root);

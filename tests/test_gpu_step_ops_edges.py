@@ -120,3 +120,41 @@ def test_adamw_decay_of_less_than_a_step(gpu, bits, master, product):
     mean = abs((h64(got) - want).mean())
     share = np.unique(g, return_counts=True)[1] / n
     assert mean < 5 * 2.0 ** -23 * np.sqrt((share * share).sum() / 12) + 16 * U * np.abs(want - w).mean(), mean
+
+
+@pytest.mark.parametrize("betas", [(0.9, 0.999), (0.99, 0.99999), (0.9999, 0.999999), (0.0, 0.0), (0.3, 0.01)])
+def test_adamw_states_move_by_what_the_betas_leave(gpu, betas):
+    """m' and v' are off by their own rounding and few roundings of what is added, not by the rounding of beta, which is a
+    large part of 1 - beta near 1; infinite states stay infinite."""
+    gu.say(f"case betas {betas}")
+    rng = np.random.default_rng(7)
+    n = 4096
+    w = rng.standard_normal(n).astype(np.float32)
+    g = rng.standard_normal(n).astype(np.float32)
+    m, v = rng.standard_normal(n).astype(np.float32), (0.5 + rng.random(n)).astype(np.float32)
+    g[:n // 4] = 0.0
+    _, state = adamw_one(w, g, 1e-3, 5, m=m, v=v, betas=betas)
+    _, m2, v2 = so.adamw(w, g, m, v, 1e-3, 5, betas)
+    g64, m64, v64 = (a.astype(np.float64) for a in (g, m, v))
+    within("m", state["m"][:n], m2, half_ulp(m2) + 4.01 * U * (1 - betas[0]) * (np.abs(g64) + U * np.abs(m64)) + 2 * U * U * np.abs(m64))
+    within("v", state["v"][:n], v2, half_ulp(v2) + 4.01 * U * (1 - betas[1]) * (g64 * g64 + U * v64) + 2 * U * U * v64)
+    m[:], v[:] = 1.0, 1.0
+    m[3], v[5], m[6], v[6] = -INF, INF, INF, INF
+    _, state = adamw_one(w, g, 1e-3, 5, m=m, v=v, betas=betas)
+    if min(betas) > 0:
+        sm, sv = h64(state["m"][:n]), h64(state["v"][:n])
+        assert sm[3] == -INF and sm[6] == INF and sv[5] == sv[6] == INF
+        assert np.isfinite(np.delete(sm, [3, 6])).all() and np.isfinite(np.delete(sv, [5, 6])).all()
+    # 8 bits: the codes are the formula's
+    w8, st = [dev(w)], B.moe_adamw_state([dev(w)], bits=8)
+    for name, x, root in (("m", 0.3 * g64, False), ("v", np.abs(g64) + 0.1, True)):
+        codes, byte = so.encode(x, np.full(n, 32768), root)
+        st[name][:], st[name + "_scale"][:] = dev(codes, np.uint8), dev(byte, np.uint8)
+    m8, u8 = (so.decode(st[k].cpu().numpy(), st[k + "_scale"].cpu().numpy()) for k in ("m", "v"))
+    B.moe_adamw_step(B.moe_adamw_plan(w8, [dev(g)], st), 1e-3, 5, betas=betas, seed=11)
+    _, m2, v2 = so.adamw(w, g, m8, u8 * u8, 1e-3, 5, betas)
+    hi, lo = so.random_halves(11, 0, 5, n)
+    for name, x, r, root in (("m", m2, hi, False), ("v", np.sqrt(v2), lo, True)):
+        codes, byte = so.encode(x, r, root)
+        assert np.array_equal(st[name + "_scale"].cpu().numpy(), byte), name
+        assert np.array_equal(st[name].cpu().numpy(), codes), name
