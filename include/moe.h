@@ -506,6 +506,7 @@ int moe_linear_bwd(const void* dy, const void* x, const void* w, const void* z, 
  *            is (r + 1/2) / 2^16 with r the high (m) or low (root of v) half of
  *            hash(i 0x9E3779B9 + hash(hash(seed + j 0x9E3779B9) + t 0x9E3779B9)) for
  *            element i of tensor j, all modulo 2^32.  A root above 0 is at least the least code.
+ *            (Values below 2^-126 are taken as fp32 has them there, a root above 0 above 0.)
  * master (MOE_BF16 only, NULL: none): fp32 weights [state_len]; the step is theirs, and
  * w_out their rounding (w is not read).  All *_out buffers may be their inputs; no other
  * overlap, and no tensor twice.

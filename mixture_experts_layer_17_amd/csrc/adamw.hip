@@ -207,6 +207,28 @@ __device__ __forceinline__ void square_roots(const float (&v)[kPer], float (&r)[
   }
 }
 
+// The roots of 8-bit states have fp32's range, their squares have not: where v left it
+// (or is zero) the root is again(j), formed in 64 bits, and zero only if that is.  True
+// where a denominator root root2 + eps is not one that the hardware's reciprocal takes.
+// For lanes with a root or gradient that small or large; zeros do not count as small,
+// so that what has not been trained yet costs no more.  Looking for them: 268 M bf16
+// values 584 us a step, 572 without.
+template <class F>
+__device__ __forceinline__ bool wide_roots(const float (&v)[kPer], float (&r)[kPer], float root2, float eps, F&& again) {
+  bool far = false;
+#pragma unroll
+  for (int j = 0; j < kPer; ++j) {
+    if (!(v[j] >= 0x1p-100f && v[j] < INFINITY)) {
+      const double u = again(j);
+      r[j] = u > 0.0 && u < 0x1p-149 ? 0x1p-149f : static_cast<float>(u);
+      const float den = r[j] * root2 + eps;
+      far = far || (r[j] > 0.f && !(den >= 0x1p-126f && den <= 0x1p126f));
+    }
+    __builtin_amdgcn_sched_barrier(0);  // one value after the other: side by side they would take registers from the whole kernel
+  }
+  return far;
+}
+
 template <class T>
 __device__ __forceinline__ void load8(const T* p, int64_t i, int valid, float (&x)[kPer]) {
   if (valid == kPer) {
@@ -247,6 +269,8 @@ __global__ __launch_bounds__(kThreads) void adamw_kernel(AdamArgs p) {
   const float a1 = static_cast<float>(1.0 - p.beta1), a2 = static_cast<float>(1.0 - p.beta2);
   const float b1_low = static_cast<float>(p.beta1 - b1), a1_low = static_cast<float>(1.0 - p.beta1 - a1);
   const float b2_low = static_cast<float>(p.beta2 - b2);
+  // roots and gradients from here on have a v' of 2^-100 or more (as a float's bits)
+  const uint32_t least_root = __float_as_uint(0x1p-50f / sqrtf(fminf(a2, b2 > 0.f ? b2 : 1.f)));
   float rate = t.rate, root2 = p.root2;
   if (p.step_dev) {
     rate = static_cast<float>(t.lr / (1.0 - int_pow(p.beta1, step)));
@@ -271,6 +295,7 @@ __global__ __launch_bounds__(kThreads) void adamw_kernel(AdamArgs p) {
       load8(static_cast<const float*>(p.m), o, kPer, m);
       load8(static_cast<const float*>(p.v), o, kPer, v);
     }
+    uint32_t least = 0xFFFFFFFFu, most = 0;
 #pragma unroll
     for (int j = 0; j < kPer; ++j) {
       const float gg = g[j] * gs;
@@ -283,21 +308,49 @@ __global__ __launch_bounds__(kThreads) void adamw_kernel(AdamArgs p) {
         low = fmaf(a1_low, gg, low);
         low = fmaf(b1_low, m[j], low);
         m[j] = fmaf(b1, m[j], t) + low;
+        const uint32_t size = max(__float_as_uint(v[j]), __float_as_uint(gg) & 0x7FFFFFFFu);  // of the larger of the two
+        least = min(least, size - 1u);  // zeros pass
+        most = max(most, size);
         v[j] *= v[j];
       } else {
         m[j] = fmaf(b1, m[j], fmaf(b1_low, fminf(fmaxf(m[j], -3.402823466e38f), 3.402823466e38f), a1 * gg));
       }
       // a beta in 32 bits is off by up to 2^-25, a large part of 1 - beta near 1 (at 0.99999 a thousandth, in the end all of
-      // it): the rest of it joins what is added (of the largest finite value at most, so that an infinite state stays one)
-      v[j] = fmaf(b2, v[j], fmaf(b2_low, fminf(v[j], 3.402823466e38f), a2 * gg * gg));
+      // it): the rest of it joins what is added (of the largest finite value at most, so that an infinite state of 32 bits
+      // stays one)
+      v[j] = fmaf(b2, v[j], fmaf(b2_low, EIGHT ? v[j] : fminf(v[j], 3.402823466e38f), a2 * gg * gg));
     }
     float root[kPer];
-    square_roots(v, root);
+    bool far = false;
+    if constexpr (EIGHT) {
+#pragma unroll
+      for (int j = 0; j < kPer; ++j) root[j] = __builtin_amdgcn_sqrtf(v[j]);
+      if (least < least_root || most > 0x5D800000u) {  // 2^60
+        far = wide_roots(v, root, root2, p.eps, [&](int j) {
+          const double r = decode1(p.v, p.v_scale, o + j);
+          const double gg = j < valid ? static_cast<double>(Elem<T>::load1(t.g, i + j)) * gs : 0.0;
+          return sqrt(p.beta2 * r * r + (1.0 - p.beta2) * gg * gg);
+        });
+      }
+    } else {
+      square_roots(v, root);
+    }
 #pragma unroll
     for (int j = 0; j < kPer; ++j) {
       if (EIGHT) v[j] = root[j];
       // the decay is part of what is subtracted: 1 - lr weight_decay in 32 bits would be a multiple of 2^-24
       w[j] -= fmaf(t.decay, w[j], rate * (m[j] * __builtin_amdgcn_rcpf(root[j] * root2 + p.eps)));
+    }
+    // again from what is in memory, by a division (as a case of the loop above it cost 45 us of 573)
+    if (EIGHT && far) {
+#pragma unroll
+      for (int j = 0; j < kPer; ++j) {
+        float x = 0.f;
+        if constexpr (MASTER) x = p.master[o + j];
+        else x = j < valid ? Elem<T>::load1(t.w, i + j) : 0.f;
+        w[j] = x - fmaf(t.decay, x, rate * (m[j] / (root[j] * root2 + p.eps)));
+        __builtin_amdgcn_sched_barrier(0);
+      }
     }
     // behind the tensor's end (its gradient reads as zero) states and master stay what they are made of: zero
     if (valid < kPer) {

@@ -158,3 +158,58 @@ def test_adamw_states_move_by_what_the_betas_leave(gpu, betas):
         codes, byte = so.encode(x, r, root)
         assert np.array_equal(st[name + "_scale"].cpu().numpy(), byte), name
         assert np.array_equal(st[name].cpu().numpy(), codes), name
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("size", [3e-20, 1e-22, 1e-24, 1e-30, 2e-33, 1e19, 1e21, 1e30, 2e38])
+def test_adamw_roots_whose_squares_leave_the_range(gpu, size, dtype):
+    """8-bit states of gradients whose squares are below or above fp32's range: the root's codes are the formula's, now
+    and a step later without a gradient, and the step is lr in size (eps 0)."""
+    gu.say(f"case roots {size} {dtype}")
+    rng = np.random.default_rng(5)
+    n, dt = 352, torch.float32 if dtype == "f32" else torch.bfloat16
+    g = size * (0.5 + rng.random(n)) * rng.choice([-1.0, 1.0], n)
+    g[64:96] = 0.0                                       # a block of zeros, and zeros among others
+    g[100:130:3] = 0.0
+    g[200:210] = 1e-3                                    # ordinary ones beside them, in their block
+    gt = dev(g).to(dt)
+    g = h64(gt)
+    w = np.zeros(n)
+    wt, state = [dev(w).to(dt)], B.moe_adamw_state([dev(w)], bits=8)
+    z = np.zeros(n)
+    plan = B.moe_adamw_plan(wt, [gt], state)
+    old = z, z
+    for step in (1, 2):
+        B.moe_adamw_step(plan, 1e-3, step, eps=0.0 if step == 1 else 1e-8, seed=2)
+        torch.cuda.synchronize()
+        ww, m2, v2 = so.adamw(w, g, old[0], old[1] ** 2, 1e-3, step, eps=1e-300 if step == 1 else 1e-8)
+        if step == 1:
+            got, live = h64(wt[0]), g != 0
+            # a dozen roundings of lr, and the weight's
+            assert (np.abs(got - ww)[live] <= 1e-3 * (12 * U + (2.0 ** -8 if dtype == "bf16" else 0.0))).all()
+            assert np.isnan(got[~live]).all()            # 0 / 0 without an eps
+        hi, lo = so.random_halves(2, 0, step, n)
+        root = np.sqrt(v2)
+        codes, byte = so.encode(root, lo, root=True)
+        assert np.array_equal(state["v_scale"].cpu().numpy(), byte)
+        assert np.array_equal(state["v"].cpu().numpy(), codes)
+        assert (codes[root > 0] > 0).all()
+        old = tuple(so.decode(state[k].cpu().numpy(), state[k + "_scale"].cpu().numpy()) for k in ("m", "v"))
+        g = z
+        gt.zero_()
+
+
+def test_adamw_roots_below_the_normal_range(gpu):
+    """Gradients near and in fp32's subnormal range: a root above zero is stored above zero (its value there is as fp32 has
+    it, which may be another code than the formula's)."""
+    gu.say("case subnormal roots")
+    sizes = np.array([1e-36, 1e-38, 3e-40, 1e-43, 1.4e-45])
+    g = np.repeat(sizes, 32)
+    w, state = [torch.zeros(g.size, device="cuda")], B.moe_adamw_state([torch.zeros(g.size, device="cuda")], bits=8)
+    B.moe_adamw_step(B.moe_adamw_plan(w, [dev(g)], state), 1e-3, seed=1)
+    codes, byte = state["v"].cpu().numpy(), state["v_scale"].cpu().numpy()
+    assert (codes > 0).all() and torch.isfinite(w[0]).all()
+    want = np.sqrt(0.001) * g
+    least = 2.0 ** -136                                  # code 1 of the least scale
+    got = so.decode(codes, byte)
+    assert (np.abs(got - want) <= np.maximum(want / 8, least) * 1.001).all()
