@@ -436,14 +436,15 @@ extern "C" int moe_adamw_step(const moe_adamw_tensor* tensors, int32_t count, in
   int64_t end = 0;
   for (int32_t i = 0; i < count; ++i) {
     const moe_adamw_tensor& t = tensors[i];
-    if (t.n < 0 || t.offset < end || t.offset % 32 || t.offset > state_len || pad32(t.n) > state_len - t.offset)
+    if (t.n < 0 || t.offset < end || t.offset % 32 || t.offset > state_len ||
+        t.n > ((state_len - t.offset) & ~int64_t{31}))  // a tensor takes whole blocks (no sum that could pass 64 bits)
       return MOE_EINVAL;
     if (t.n > 0 && (!t.w || !t.g || !t.w_out)) return MOE_EINVAL;
     if (!aligned16(t.w) || !aligned16(t.g) || !aligned16(t.w_out)) return MOE_EINVAL;
     if (!std::isfinite(t.weight_decay) || !std::isfinite(t.lr_scale) || !std::isfinite(static_cast<float>(lr * t.lr_scale)) ||
         !std::isfinite(static_cast<float>(lr * t.lr_scale * t.weight_decay)))
       return MOE_EINVAL;
-    if (cdiv(t.n, 4 * kTurn) >= kMaxUnits) return MOE_EUNSUPPORTED;
+    if (t.n > (kMaxUnits - 1) * 4 * kTurn) return MOE_EUNSUPPORTED;
     end = t.offset + pad32(t.n);
   }
   hipStream_t s = static_cast<hipStream_t>(stream);
@@ -501,7 +502,7 @@ extern "C" int moe_adamw_state_values(const uint8_t* m, const uint8_t* m_scale, 
                         static_cast<const void*>(v_scale), static_cast<const void*>(m_values),
                         static_cast<const void*>(root_values)})
     if (!aligned16(q)) return MOE_EINVAL;
-  if (2 * cdiv(state_len, kTurn) >= kMaxUnits) return MOE_EUNSUPPORTED;
+  if (state_len > (kMaxUnits / 2 - 1) * kTurn) return MOE_EUNSUPPORTED;
   MOE_LAUNCH("adamw_state_values", state_values_kernel, dim3(static_cast<unsigned>(cdiv(state_len, kTurn)), 2), dim3(kThreads),
              0, static_cast<hipStream_t>(stream), m, m_scale, v, v_scale, state_len, static_cast<uint16_t*>(m_values),
              static_cast<uint16_t*>(root_values));

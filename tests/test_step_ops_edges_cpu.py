@@ -1,0 +1,42 @@
+"""Refusals of routing by scores, the dense product and the AdamW step at the
+ends of their arguments' ranges (CPU only: no call here reaches a launch)."""
+import ctypes
+import os
+import types
+
+import pytest
+import torch
+
+from mixture_experts_layer_17_amd import binding as B
+
+OK, EINVAL, EUNSUP = 0, 1, 2
+FAKE = ctypes.c_void_p(0x10000)
+BIG = 1 << 60
+NAN = float("nan")
+
+
+@pytest.fixture(scope="module")
+def L():
+    if not os.path.exists(B.LIB_PATH):
+        pytest.fail("libmoe.so not built: run __graft_entry__.build()")
+    return B.lib()
+
+
+def adamw(L, n=64, length=1 << 20, offset=0, eps=1e-8, bits=32, dtype=0):
+    t = (B._AdamwTensor * 1)(B._AdamwTensor(0x10000, 0x20000, 0x10000, n, offset, 0.1, 1.0))
+    scale = FAKE if bits == 8 else None
+    return L.moe_adamw_step(t, 1, dtype, bits, length, FAKE, FAKE, scale, scale, None, 1e-3, 0.9, 0.999, eps, 1, None, None, 7,
+                            FAKE, FAKE, scale, scale, None, None)
+
+
+def test_adamw_sizes_at_the_end_of_64_bits(L):
+    top = (1 << 63) - 1
+    for n in (top, top - 31, top - 30, top - 63):
+        for length in (top, 1 << 40):
+            assert adamw(L, n=n, length=length) in (EINVAL, EUNSUP), (n, length)
+    assert adamw(L, n=top, length=top) == EINVAL                      # its last block passes the states' end
+    assert adamw(L, n=top - 31, length=top) == EUNSUP
+    assert adamw(L, n=top - 63, length=top - 31, offset=64) == EINVAL
+    assert adamw(L, n=0, length=0) == OK
+    for n in (top - 31, top - 63, 1 << 62):
+        assert L.moe_adamw_state_values(FAKE, FAKE, FAKE, FAKE, n, FAKE, FAKE, None) == EUNSUP, n
