@@ -511,10 +511,10 @@ int moe_linear_bwd(const void* dy, const void* x, const void* w, const void* z, 
  * w_out their rounding (w is not read).  All *_out buffers may be their inputs; no other
  * overlap, and no tensor twice.
  * step_dev (NULL: `step` counts): t on the device, at least 1, for captured graphs.
- * MOE_EINVAL for betas outside [0, 1), a negative eps, scalars that are not finite (products
- * of lr, lr_scale and weight_decay among them), step < 1, n < 0 (0 is skipped), bad offsets, a
- * null or unaligned pointer, a master with MOE_F32; MOE_EUNSUPPORTED for 2^37 elements or more
- * in a tensor.  A launch takes 56 tensors. */
+ * MOE_EINVAL for betas outside [0, 1), an eps that is neither 0 nor within 2^-126 .. 2^100,
+ * scalars that are not finite (products of lr, lr_scale and weight_decay among them), step < 1,
+ * n < 0 (0 is skipped), bad offsets, a null or unaligned pointer, a master with MOE_F32;
+ * MOE_EUNSUPPORTED for 2^37 elements or more in a tensor.  A launch takes 56 tensors. */
 typedef struct {
   const void* w;
   const void* g;

@@ -421,7 +421,10 @@ extern "C" int moe_adamw_step(const moe_adamw_tensor* tensors, int32_t count, in
   if (!(beta1 >= 0.0 && beta1 < 1.0) || !(beta2 >= 0.0 && beta2 < 1.0) || !(eps >= 0.0) || !std::isfinite(eps) ||
       !std::isfinite(lr) || (!step_dev && step < 1))
     return MOE_EINVAL;
-  if (!std::isfinite(static_cast<float>(eps)) || !std::isfinite(static_cast<float>(lr))) return MOE_EINVAL;
+  if (!std::isfinite(static_cast<float>(lr))) return MOE_EINVAL;
+  // what the hardware's reciprocal takes: below, a value without gradient would become 0 times infinity, far above (from
+  // 2^126 on, with the root) it is zero
+  if (eps > 0.0 && !(eps >= 0x1p-126 && eps <= 0x1p100)) return MOE_EINVAL;
   if (dtype == MOE_F32 && (master || master_out)) return MOE_EINVAL;
   if (!master != !master_out) return MOE_EINVAL;
   if (count == 0) return MOE_OK;

@@ -213,3 +213,12 @@ def test_adamw_roots_below_the_normal_range(gpu):
     least = 2.0 ** -136                                  # code 1 of the least scale
     got = so.decode(codes, byte)
     assert (np.abs(got - want) <= np.maximum(want / 8, least) * 1.001).all()
+
+
+@pytest.mark.parametrize("bits", [32, 8])
+def test_adamw_least_eps_leaves_weights_without_gradients(gpu, bits):
+    gu.say(f"case least eps {bits}")
+    w, g = [torch.full((64,), 0.5, device="cuda")], [torch.zeros(64, device="cuda")]
+    state = B.moe_adamw_state(w, bits=bits)
+    B.moe_adamw_step(B.moe_adamw_plan(w, g, state), 1e-3, eps=2.0 ** -126)
+    assert (w[0] == 0.5).all()

@@ -40,3 +40,13 @@ def test_adamw_sizes_at_the_end_of_64_bits(L):
     assert adamw(L, n=0, length=0) == OK
     for n in (top - 31, top - 63, 1 << 62):
         assert L.moe_adamw_state_values(FAKE, FAKE, FAKE, FAKE, n, FAKE, FAKE, None) == EUNSUP, n
+
+
+def test_adamw_eps_outside_what_the_reciprocal_takes(L):
+    """The hardware's reciprocal takes subnormal values for zero and gives zero for a subnormal result: a positive eps lies
+    in 2^-126 .. 2^100."""
+    for bits in (32, 8):
+        for bad in (1e-39, 1e-50, 5e-324, 2.0 ** -127, 1e38, 1.01 * 2.0 ** 100):
+            assert adamw(L, eps=bad, bits=bits) == EINVAL, bad
+        for good in (0.0, 2.0 ** -126, 1e-12, 2.0 ** 100):
+            assert adamw(L, eps=good, n=0, bits=bits) == OK, good
