@@ -478,7 +478,8 @@ int moe_muon_step(const void* g, int dtype, int32_t E, int32_t rows, int32_t col
  * MOE_ACT_GELU is z Phi(z) with the error function; relu'(0) = 0.  For MOE_BF16 the products
  * take dz rounded to bf16 (db does not).  y may be residual; dx may be dres or in_z; no
  * other overlap.  M = 0 is allowed (dw and db become zero).  MOE_EUNSUPPORTED for K or N
- * past 2^20 and for more than 2^35 elements (rounded up to 8 columns). */
+ * past 2^20, for more than 2^35 elements (rounded up to 8 columns), and for rows of few columns
+ * from about 2^30 (fp32) or 2^31 (bf16) on, whose launch would hold 2^32 threads. */
 typedef enum { MOE_ACT_NONE = 0, MOE_ACT_RELU = 1, MOE_ACT_SILU = 2, MOE_ACT_GELU = 3 } moe_act;
 size_t moe_linear_workspace(int dtype, int64_t M, int32_t K, int32_t N, int is_bwd);
 int moe_linear(const void* x, const void* w, const void* bias, const void* residual, int dtype, int64_t M, int32_t K,

@@ -819,12 +819,22 @@ Buffers buffers(int dtype, int64_t M, int64_t K, int64_t N, bool bwd) {
   return b;
 }
 
-// 2^32 threads in one launch are too many: the widest one has a thread per eight elements.
-int linear_sizes(int dtype, int64_t M, int64_t K, int64_t N) {
+// Whether a product's launch stays below 2^32 threads (its tiles have two to four a row, so many rows of few columns do
+// not).
+bool product_fits(int dtype, int64_t rows, int64_t cols, int64_t depth) {
+  const Plan pl = plan_product(dtype, rows, cols, depth);
+  const int bt = kTiles[dtype == MOE_BF16][pl.wide].bt;
+  const int64_t threads = dtype == MOE_BF16 && pl.wide ? Wide::kThreads : 256;
+  return xcd_grid(cdiv(rows, bt) * cdiv(cols, bt) * pl.splits) * threads < (1ll << 32);
+}
+
+// 2^32 threads in one launch are too many: those beside the products have a thread per eight elements at most.
+int linear_sizes(int dtype, int64_t M, int64_t K, int64_t N, bool bwd) {
   if ((dtype != MOE_F32 && dtype != MOE_BF16) || M < 0 || K < 1 || N < 1) return MOE_EINVAL;
   if (M >= (1ll << 31) || K > kMaxWidth || N > kMaxWidth) return MOE_EUNSUPPORTED;
   const int64_t big = M > K ? M : K, side = K > N ? K : N;
   if (big * up8(side) / 8 >= (1ll << 32) - 256) return MOE_EUNSUPPORTED;
+  if (M >= (1ll << 28) && !product_fits(dtype, M, bwd ? K : N, bwd ? N : K)) return MOE_EUNSUPPORTED;  // (dw's is far below)
   return MOE_OK;
 }
 bool act_ok(int act) { return act >= kActNone && act <= kActGelu; }
@@ -916,13 +926,13 @@ int linear_bwd(const void* dy, const void* x, const void* w, const void* z, int6
 using namespace moe;
 
 extern "C" size_t moe_linear_workspace(int dtype, int64_t M, int32_t K, int32_t N, int is_bwd) {
-  if (linear_sizes(dtype, M, K, N) != MOE_OK) return 0;
+  if (linear_sizes(dtype, M, K, N, is_bwd != 0) != MOE_OK) return 0;
   return buffers(dtype, M, K, N, is_bwd != 0).total;
 }
 
 extern "C" int moe_linear(const void* x, const void* w, const void* bias, const void* residual, int dtype, int64_t M,
                           int32_t K, int32_t N, int act, void* y, void* z, void* ws, size_t ws_bytes, void* stream) {
-  const int st = linear_sizes(dtype, M, K, N);
+  const int st = linear_sizes(dtype, M, K, N, false);
   if (st != MOE_OK) return st;
   if (!act_ok(act)) return MOE_EINVAL;
   if (M == 0) return MOE_OK;
@@ -939,7 +949,7 @@ extern "C" int moe_linear(const void* x, const void* w, const void* bias, const 
 extern "C" int moe_linear_bwd(const void* dy, const void* x, const void* w, const void* z, int dtype, int64_t M,
                               int32_t K, int32_t N, int act, const void* in_z, int in_act, const void* dres, void* dx,
                               void* dw, void* db, void* ws, size_t ws_bytes, void* stream) {
-  const int st = linear_sizes(dtype, M, K, N);
+  const int st = linear_sizes(dtype, M, K, N, true);
   if (st != MOE_OK) return st;
   if (!act_ok(act) || !act_ok(in_act)) return MOE_EINVAL;
   if (!dx && (dres || in_act != kActNone)) return MOE_EINVAL;

@@ -50,3 +50,23 @@ def test_adamw_eps_outside_what_the_reciprocal_takes(L):
             assert adamw(L, eps=bad, bits=bits) == EINVAL, bad
         for good in (0.0, 2.0 ** -126, 1e-12, 2.0 ** 100):
             assert adamw(L, eps=good, n=0, bits=bits) == OK, good
+
+
+@pytest.mark.parametrize("dtype", [0, 1])
+def test_linear_sizes_whose_launch_would_pass_its_limit(L, dtype):
+    """A launch holds fewer than 2^32 threads: what would take more is refused, not left to fail."""
+    def fwd(M, K, N):
+        return L.moe_linear(FAKE, FAKE, None, None, dtype, M, K, N, 0, FAKE, None, FAKE, BIG, None)
+
+    def bwd(M, K, N):
+        return L.moe_linear_bwd(FAKE, FAKE, FAKE, None, dtype, M, K, N, 0, None, 0, None, FAKE, FAKE, None, FAKE, BIG, None)
+
+    top = (1 << 31) - 1
+    for M in (top, top - 126):
+        assert fwd(M, 8, 1) == EUNSUP and L.moe_linear_workspace(dtype, M, 8, 1, 0) == 0, M
+        assert bwd(M, 1, 8) == EUNSUP and L.moe_linear_workspace(dtype, M, 1, 8, 1) == 0, M
+    # what fits stays: 64-row tiles of fp32 take four threads a row, the bf16 ones two
+    M = (1 << 30) - 512
+    assert L.moe_linear_workspace(dtype, M, 8, 1, 0) > 0 and L.moe_linear_workspace(dtype, M, 1, 8, 1) > 0
+    if dtype == 1:
+        assert L.moe_linear_workspace(dtype, (1 << 31) - (1 << 16), 8, 1, 0) > 0
