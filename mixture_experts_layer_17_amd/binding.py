@@ -627,6 +627,8 @@ def moe_route_scored(logits, k, score="softmax", bias=None, groups=1, top_groups
     what, dev = "moe_route_scored", logits.device
     code = _named(what, "score", _SCORE, score)
     T, E = _route_sizes(what, logits, k)
+    if (groups | top_groups | group_best) >> 31:  # 32 bits: a larger number would be cut
+        raise MoeError(f"{what}: groups, top_groups, group_best = {groups}, {top_groups}, {group_best}")
     specs = (("logits", logits, (T, E), _F32), ("bias", bias, (E,), _F32)) + _ws_spec(ws)
     if out is not None:
         specs += (("topk_idx", out["topk_idx"], (T, k), _I32), ("gates", out["gates"], (T, k), _F32),
@@ -827,6 +829,8 @@ def moe_adamw_step(plan, lr, step=1, betas=(0.9, 0.999), eps=1e-8, seed=0, grad_
     """One AdamW step (step counts from 1; step_dev: an int64 tensor [1] on the device in its place); returns the
     updated (tensors, state)."""
     what = "moe_adamw_step"
+    if not -(1 << 63) <= step < 1 << 63:  # 64 bits: a larger number would be cut
+        raise MoeError(f"{what}: step = {step}")
     if [t.data_ptr() for t in plan.tensors] != plan.at:
         raise MoeError(f"{what}: a tensor of the plan has other memory now")
     _args(what, plan.device, (("grad_scale", grad_scale, (1,), _F32), ("step_dev", step_dev, (1,), torch.int64)))

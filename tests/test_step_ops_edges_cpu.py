@@ -70,3 +70,16 @@ def test_linear_sizes_whose_launch_would_pass_its_limit(L, dtype):
     assert L.moe_linear_workspace(dtype, M, 8, 1, 0) > 0 and L.moe_linear_workspace(dtype, M, 1, 8, 1) > 0
     if dtype == 1:
         assert L.moe_linear_workspace(dtype, (1 << 31) - (1 << 16), 8, 1, 0) > 0
+
+
+def test_binding_refuses_numbers_of_more_than_32_bits():
+    """The C ABI takes these in 32 bits: a larger one would be cut, and 2^32 + 4 groups taken for 4."""
+    lg = torch.zeros(4, 8)
+    for name in ("groups", "top_groups", "group_best"):
+        for bad in ((1 << 32) + 1, 1 << 31, -(1 << 32) + 1):
+            with pytest.raises(B.MoeError, match=name):
+                B.moe_route_scored(lg, 2, **{name: bad})
+    plan = types.SimpleNamespace(tensors=[], at=[], device=torch.device("cpu"))
+    for bad in ((1 << 64) + 1, 1 << 63, -(1 << 64) + 1):
+        with pytest.raises(B.MoeError, match="step ="):
+            B.moe_adamw_step(plan, 0.1, bad)
