@@ -29,6 +29,17 @@ def adamw(L, n=64, length=1 << 20, offset=0, eps=1e-8, bits=32, dtype=0):
                             FAKE, FAKE, scale, scale, None, None)
 
 
+def test_route_scored_bwd_refusals_one_by_one(L):
+    def bwd(T=10, E=16, k=2, score=0, scale=1.0):
+        return L.moe_route_scored_bwd(FAKE, FAKE, FAKE, T, E, k, score, 1, scale, 0, FAKE, None)
+
+    for bad in (dict(T=-1), dict(score=7), dict(score=-1), dict(scale=NAN), dict(scale=float("inf")), dict(k=0), dict(E=0),
+                dict(k=5, E=4)):
+        assert bwd(**bad) == EINVAL, bad
+    for bad in (dict(k=9), dict(k=17), dict(E=257), dict(T=1 << 28)):
+        assert bwd(**bad) == EUNSUP, bad
+
+
 def test_adamw_sizes_at_the_end_of_64_bits(L):
     top = (1 << 63) - 1
     for n in (top, top - 31, top - 30, top - 63):
