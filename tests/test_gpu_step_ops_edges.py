@@ -81,6 +81,22 @@ def test_softmax_gradient_of_a_row_without_scores_is_nan(gpu, E, renorm):
 
 # ------------------------------------------------------------------- dense product
 
+@pytest.mark.parametrize("M,N,dtype", [(20000, 64, "f32"), (16384, 768, "bf16"), (100003, 515, "bf16"), (65537, 1030, "f32"),
+                                       (30000, 9, "bf16")])
+def test_bias_gradient_of_many_rows_is_exact_for_whole_numbers(gpu, M, N, dtype):
+    """dy of whole numbers up to 3: every partial sum is one below 2^24, so db is exact before its rounding, and a row left
+    out or taken twice shows."""
+    gu.say(f"case db exact M={M} N={N} {dtype}")
+    dt = torch.bfloat16 if dtype == "bf16" else torch.float32
+    g = torch.Generator(device="cuda").manual_seed(M)
+    dy = torch.randint(-3, 4, (M, N), generator=g, device="cuda").to(dt)
+    x, w = torch.zeros((M, 8), dtype=dt, device="cuda"), torch.zeros((8, N), dtype=dt, device="cuda")
+    out = {"db": torch.full((N,), 7.0, dtype=dt, device="cuda")}
+    ws = B.moe_linear_workspace(x, w, bwd=True).fill_(255)
+    B.moe_linear_bwd(dy, x, w, out=out, ws=ws)
+    assert torch.equal(out["db"], dy.double().sum(0).to(dt))
+
+
 # ------------------------------------------------------------------- AdamW
 
 def adamw_one(w, g, lr, step=1, bits=32, master=False, m=None, v=None, dtype=torch.float32, weight_decay=0.0, **kw):
