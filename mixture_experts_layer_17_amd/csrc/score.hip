@@ -861,9 +861,12 @@ extern "C" int moe_route_scored(const float* logits, const float* bias, int64_t 
     else launch_score_select<16>(a, s);
   }
   if (nblk == 1) return launch_status();
-  // few counts: every workgroup can sum them for itself, which is a launch less (5003 x 60, 79 workgroups: 23.6 -> 21.0 us
-  // a call; with 256 x 256 counts they read 64 MB)
-  if (nblk > 0 && nblk * E <= 8192) {
+  // few counts: every workgroup can sum them for itself, which is a launch less.  A thread walks its expert's counts one
+  // after the other, so the number of workgroups decides, and for many experts what they all read.  Calls in a row, two
+  // launches against three: 128 workgroups and 1, 8, 32 or 60 experts 9.6, 10.1, 10.7, 11.5 against 9.9, 10.5, 11.2, 11.5
+  // us, 192 of them 11.0, 12.1, 12.5, 13.5 against 10.5, 11.1, 11.7, 12.0, 1024 with 8 experts 41 against 29; 128 experts
+  // 11.4 against 12.3 (96 workgroups) and 12.6 against 12.3 (128), 256 experts 11.5 against 12.6 (48) and 14.7 against 13.4 (96)
+  if (nblk > 0 && nblk <= 128 && nblk * E <= 12288) {
     MOE_LAUNCH("score_place", score_place_kernel, dim3(static_cast<unsigned>(nblk)), dim3(256), 0, s, topk_idx, rank, blk,
                nblk, R, k, E, counts, offsets, mx_blk_offsets, perm_src, perm_dst);
     return launch_status();

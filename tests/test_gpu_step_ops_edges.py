@@ -79,6 +79,27 @@ def test_softmax_gradient_of_a_row_without_scores_is_nan(gpu, E, renorm):
             assert np.isfinite(gates[t]).all() and np.array_equal(d[t], want[t]), t
 
 
+@pytest.mark.parametrize("T,E", [(128, 8), (8192, 8), (8200, 8), (65536, 8), (65600, 8), (131072, 4), (131200, 4), (200000, 1),
+                                 (524288, 1), (524400, 1), (8192, 64), (8256, 64), (6144, 128), (6208, 128), (3008, 256), (3136, 256)])
+def test_metadata_of_few_experts_and_many_tokens(gpu, T, E):
+    """Counts of many workgroups over few experts, at and next to where the ways of placing the tokens change over."""
+    gu.say(f"case metadata T={T} E={E}")
+    k = min(2, E)
+    lg = torch.randn((T, E), generator=torch.Generator(device="cuda").manual_seed(T + E), device="cuda")
+    ws = B._ws(B.lib().moe_route_scored_workspace(T, E, k), "cuda").fill_(255)
+    got = B.moe_route_scored(lg, k, score="sigmoid", ws=ws)
+    flat = got["topk_idx"].reshape(-1).long()
+    assert torch.equal(got["topk_idx"].long(), torch.sigmoid(lg.double()).sort(dim=1, descending=True, stable=True).indices[:, :k])
+    src = flat.sort(dim=0, stable=True).indices
+    counts = torch.bincount(flat, minlength=E)
+    zero = torch.zeros(1, dtype=torch.int64, device="cuda")
+    assert torch.equal(got["counts"].long(), counts)
+    assert torch.equal(got["offsets"].long(), torch.cat([zero, counts.cumsum(0)]))
+    assert torch.equal(got["mx_blk_offsets"].long(), torch.cat([zero, ((counts + 31) // 32).cumsum(0)]))
+    assert torch.equal(got["perm_src"].long(), src)
+    assert torch.equal(got["perm_dst"].long()[src], torch.arange(T * k, device="cuda"))
+
+
 # ------------------------------------------------------------------- dense product
 
 @pytest.mark.parametrize("M,N,dtype", [(20000, 64, "f32"), (16384, 768, "bf16"), (100003, 515, "bf16"), (65537, 1030, "f32"),
