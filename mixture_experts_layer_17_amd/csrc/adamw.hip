@@ -63,6 +63,9 @@ struct AdamArgs {
   uint8_t* v_scale_out;
   float* master_out;
   double beta1, beta2;
+  float b1, b1_low, a1, a1_low; // beta1 and 1 - beta1, each in two parts
+  float b2, b2_low, a2;
+  float least_root;             // roots and gradients from here on have a v' of 2^-100 or more
   float eps, root2;             // root2: 1 / sqrt(1 - beta2^step)
   int64_t step;
   const int64_t* step_dev;
@@ -211,20 +214,22 @@ __device__ __forceinline__ void square_roots(const float (&v)[kPer], float (&r)[
 // (or is zero) the root is again(j), formed in 64 bits, and zero only if that is.  True
 // where a denominator root root2 + eps is not one that the hardware's reciprocal takes.
 // For lanes with a root or gradient that small or large; zeros do not count as small,
-// so that what has not been trained yet costs no more.  Looking for them: 268 M bf16
-// values 584 us a step, 572 without.
+// so that what has not been trained yet costs no more.  Looking for them takes 2% of a
+// step (268 M bf16 values: 584 us, 572 without).
 template <class F>
 __device__ __forceinline__ bool wide_roots(const float (&v)[kPer], float (&r)[kPer], float root2, float eps, F&& again) {
   bool far = false;
+#pragma unroll 1
+  for (int j = 0; j < kPer; ++j) {  // a loop: side by side the eight would take registers and code from the whole kernel
+    float vj = 0.f;
 #pragma unroll
-  for (int j = 0; j < kPer; ++j) {
-    if (!(v[j] >= 0x1p-100f && v[j] < INFINITY)) {
-      const double u = again(j);
-      r[j] = u > 0.0 && u < 0x1p-149 ? 0x1p-149f : static_cast<float>(u);
-      const float den = r[j] * root2 + eps;
-      far = far || (r[j] > 0.f && !(den >= 0x1p-126f && den <= 0x1p126f));
-    }
-    __builtin_amdgcn_sched_barrier(0);  // one value after the other: side by side they would take registers from the whole kernel
+    for (int i = 0; i < kPer; ++i) vj = i == j ? v[i] : vj;
+    if (vj >= 0x1p-100f && vj < INFINITY) continue;
+    const double u = again(j);
+    const float x = u > 0.0 && u < 0x1p-149 ? 0x1p-149f : static_cast<float>(u), den = x * root2 + eps;
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) r[i] = i == j ? x : r[i];
+    far = far || (x > 0.f && !(den >= 0x1p-126f && den <= 0x1p126f));
   }
   return far;
 }
@@ -265,12 +270,7 @@ __global__ __launch_bounds__(kThreads) void adamw_kernel(AdamArgs p) {
   const ListEntry& t = p.list[lo];
   const int64_t n = t.n, base = static_cast<int64_t>(b - p.first[lo]) * p.turns * kTurn;
   const int64_t step = p.step_dev ? *p.step_dev : p.step;
-  const float b1 = static_cast<float>(p.beta1), b2 = static_cast<float>(p.beta2);
-  const float a1 = static_cast<float>(1.0 - p.beta1), a2 = static_cast<float>(1.0 - p.beta2);
-  const float b1_low = static_cast<float>(p.beta1 - b1), a1_low = static_cast<float>(1.0 - p.beta1 - a1);
-  const float b2_low = static_cast<float>(p.beta2 - b2);
-  // roots and gradients from here on have a v' of 2^-100 or more (as a float's bits)
-  const uint32_t least_root = __float_as_uint(0x1p-50f / sqrtf(fminf(a2, b2 > 0.f ? b2 : 1.f)));
+  const float b1 = p.b1, b1_low = p.b1_low, a1 = p.a1, a1_low = p.a1_low, b2 = p.b2, b2_low = p.b2_low, a2 = p.a2;
   float rate = t.rate, root2 = p.root2;
   if (p.step_dev) {
     rate = static_cast<float>(t.lr / (1.0 - int_pow(p.beta1, step)));
@@ -325,7 +325,7 @@ __global__ __launch_bounds__(kThreads) void adamw_kernel(AdamArgs p) {
     if constexpr (EIGHT) {
 #pragma unroll
       for (int j = 0; j < kPer; ++j) root[j] = __builtin_amdgcn_sqrtf(v[j]);
-      if (least < least_root || most > 0x5D800000u) {  // 2^60
+      if (least < __float_as_uint(p.least_root) || most > 0x5D800000u) {  // 2^60
         far = wide_roots(v, root, root2, p.eps, [&](int j) {
           const double r = decode1(p.v, p.v_scale, o + j);
           const double gg = j < valid ? static_cast<double>(Elem<T>::load1(t.g, i + j)) * gs : 0.0;
@@ -455,6 +455,10 @@ extern "C" int moe_adamw_step(const moe_adamw_tensor* tensors, int32_t count, in
   a.m = m; a.v = v; a.m_scale = m_scale; a.v_scale = v_scale; a.master = master;
   a.m_out = m_out; a.v_out = v_out; a.m_scale_out = m_scale_out; a.v_scale_out = v_scale_out; a.master_out = master_out;
   a.beta1 = beta1; a.beta2 = beta2; a.eps = static_cast<float>(eps);
+  a.b1 = static_cast<float>(beta1); a.b1_low = static_cast<float>(beta1 - a.b1);
+  a.a1 = static_cast<float>(1.0 - beta1); a.a1_low = static_cast<float>(1.0 - beta1 - a.a1);
+  a.b2 = static_cast<float>(beta2); a.b2_low = static_cast<float>(beta2 - a.b2); a.a2 = static_cast<float>(1.0 - beta2);
+  a.least_root = 0x1p-50f / std::sqrt(a.b2 > 0.f && a.b2 < a.a2 ? a.b2 : a.a2);
   const double c1 = step_dev ? 1.0 : 1.0 - int_pow(beta1, step);
   a.root2 = step_dev ? 1.0f : static_cast<float>(1.0 / std::sqrt(1.0 - int_pow(beta2, step)));
   // one turn a unit until four would still leave eight workgroups to a compute unit
