@@ -302,9 +302,9 @@ __device__ __forceinline__ int choose_exact(const ScoreArgs& p, const float (&l)
 // which cuts the value by up to 2^-19 of itself.  Where that does not tell (NaN,
 // infinities, more than 16 candidates, groups too near at their border) the wave
 // chooses by choose_exact.  16384 x 256 sigmoid scores, bias, 8 groups: 17 us
-// without a near pair, 21 like this, 28 with choose_exact for every wave that has one (some
+// without a near pair, 23 like this, 28 with choose_exact for every wave that has one (some
 // wave of every compute unit's 16 does, and the others wait for it), 34 all in
-// 64 bits, one after the other; 23 in a later trace of what stands here.
+// 64 bits, one after the other.
 // ---------------------------------------------------------------------------
 __device__ __forceinline__ uint32_t order_key32(float c) {
   const uint32_t b = __float_as_uint(c);
@@ -680,7 +680,7 @@ __global__ __launch_bounds__(256) void score_scatter_kernel(const int32_t* __res
 // same: a NaN or +inf in them, also of an expert not chosen, makes the gates NaN,
 // and the gradient must not hide that.  Sixteen lanes take a token, lane j its
 // slot j, the row in registers; what the slots add meets it in LDS.  16384 x 128
-// without renormalising: 6.6 us, 2.5 TB/s of rows read and written: too short for
+// without renormalising: 6.5 us, 2.6 TB/s of rows read and written: too short for
 // the rate of a large copy.
 // ---------------------------------------------------------------------------
 struct ScoreBwdArgs {

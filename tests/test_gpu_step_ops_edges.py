@@ -197,7 +197,7 @@ def test_adamw_states_move_by_what_the_betas_leave(gpu, betas):
         assert np.array_equal(st[name].cpu().numpy(), codes), name
 
 
-@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("dtype", ["f32", "bf16", "bf16 master"])
 @pytest.mark.parametrize("size", [3e-20, 1e-22, 1e-24, 1e-30, 2e-33, 1e19, 1e21, 1e30, 2e38])
 def test_adamw_roots_whose_squares_leave_the_range(gpu, size, dtype):
     """8-bit states of gradients whose squares are below or above fp32's range: the root's codes are the formula's, now
@@ -212,7 +212,7 @@ def test_adamw_roots_whose_squares_leave_the_range(gpu, size, dtype):
     gt = dev(g).to(dt)
     g = h64(gt)
     w = np.zeros(n)
-    wt, state = [dev(w).to(dt)], B.moe_adamw_state([dev(w)], bits=8)
+    wt, state = [dev(w).to(dt)], B.moe_adamw_state([dev(w)], bits=8, master=dtype == "bf16 master")
     z = np.zeros(n)
     plan = B.moe_adamw_plan(wt, [gt], state)
     old = z, z
@@ -221,7 +221,7 @@ def test_adamw_roots_whose_squares_leave_the_range(gpu, size, dtype):
         torch.cuda.synchronize()
         ww, m2, v2 = so.adamw(w, g, old[0], old[1] ** 2, 1e-3, step, eps=1e-300 if step == 1 else 1e-8)
         if step == 1:
-            got, live = h64(wt[0]), g != 0
+            got, live = h64(state.get("master", wt[0])), g != 0
             # a dozen roundings of lr, and the weight's
             assert (np.abs(got - ww)[live] <= 1e-3 * (12 * U + (2.0 ** -8 if dtype == "bf16" else 0.0))).all()
             assert np.isnan(got[~live]).all()            # 0 / 0 without an eps
